@@ -202,7 +202,7 @@ def encode(x, dither, floor=False):
     never stored as less than the smallest code."""
     x = x.view(-1, BLOCK)
     _, e = torch.frexp(x.abs().amax(1, keepdim=True))
-    e = torch.clamp(e - 8, -126, 119)
+    e = torch.clamp(e - 8, -126, 120)
     scale = torch.ldexp(torch.ones((), device=x.device), e)
     t = torch.ldexp(torch.ones((), device=x.device), -e) * x
     a = t.abs()
@@ -420,7 +420,7 @@ def exact(case, seed):
     for x, u, floor in ((m, low, False), (v.sqrt(), high, True)):
         x, u = x.view(-1, BLOCK), (u.view(-1, BLOCK).double() + 0.5) / 65536
         top = x.abs().amax(1, keepdim=True)
-        e = torch.where(top > 0, torch.log2(torch.where(top > 0, top, 1.0)).floor() - 7, -126.0).clamp_(-126, 119)
+        e = torch.where(top > 0, torch.log2(torch.where(top > 0, top, 1.0)).floor() - 7, -126.0).clamp_(-126, 120)
         a = x.abs() / torch.exp2(e)
         if floor:
             a = torch.where((a > 0) & (a < 2.0 ** -9), 2.0 ** -9, a)
