@@ -84,11 +84,16 @@ def code_tokens(text):
     return " ".join("".join(out).split())
 
 
+# The collective's kernels and the headers they are made of: what the recorded
+# DRAM traffic was taken on.
+COLLECTIVE_SOURCES = ("rr_allgather.cu", "rr_allreduce.cu", "rr_device.cuh", "rr_internal.h")
+
+
 def source_hash():
-    """Hash of the kernel sources' code (comments and layout ignored)."""
+    """Hash of the collective's kernel sources (comments and layout ignored)."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "allgather_rr_allreduce_gb300", "csrc")
-    for name in sorted(os.listdir(csrc)):
+    for name in COLLECTIVE_SOURCES:
         with open(os.path.join(csrc, name), encoding="utf-8") as f:
             h.update(name.encode() + code_tokens(f.read()).encode())
     return h.hexdigest()[:16]
