@@ -9,6 +9,7 @@ computes: if librr.so is missing, every call raises.
 """
 import ctypes
 import os
+import sys
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "librr.so")
@@ -33,6 +34,15 @@ OPTIONS = {
     "world_size": 20, "max_blocks_per_rank": 21,
 }
 _DTYPE_NAMES = {"bf16": RR_BF16, "fp16": RR_FP16, "fp32": RR_FP32, "int32": RR_INT32}
+
+
+RR_ADAMW8_BLOCK = 256
+
+
+class rr_adamw_hyper(ctypes.Structure):
+    """rr_adamw_hyper(lr, beta1, beta2, eps, weight_decay, step)."""
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("step", ctypes.c_int64)]
 
 
 class RRError(RuntimeError):
@@ -69,6 +79,15 @@ def lib():
             "rr_allgather_list": [_PP, _PP, i32, i64, i32, _vp, _vp],
             "rr_allreduce_oneshot_noalloc": [_PP, _PP, _PP, i32, i64, i32, i32, _vp],
             "rr_allreduce_oneshot_noalloc_status": [_vp],
+            "rr_layer_norm": [_vp] * 6 + [i64] * 4 + [ctypes.c_float, i32, i32, _vp],
+            "rr_layer_norm_backward": [_vp] * 8 + [i64] * 5 + [i32, i32, _vp, ctypes.c_size_t, _vp],
+            "rr_layer_norm_backward_workspace": [i64, i64, ctypes.POINTER(ctypes.c_size_t)],
+            "rr_grad_norm": [_PP, ctypes.POINTER(i64), i32, i32, ctypes.c_float, ctypes.c_float, _vp, _vp, _vp,
+                             ctypes.c_size_t, _vp],
+            "rr_grad_norm_workspace": [i32, ctypes.POINTER(ctypes.c_size_t)],
+            "rr_adamw": [_PP] * 5 + [ctypes.POINTER(i64), i32, i32, i32, ctypes.POINTER(rr_adamw_hyper), _vp, _vp],
+            "rr_adamw8": [_PP] * 7 + [ctypes.POINTER(i64), i32, i32, i32, ctypes.POINTER(rr_adamw_hyper),
+                                      ctypes.c_uint32, _vp, _vp],
         }
         for name, args in sig.items():
             f = getattr(l, name)
@@ -240,6 +259,84 @@ def rr_allgather_list(rank_bufs, output_lists, world_size, numel_per_rank, dtype
     _check(lib().rr_allgather_list(pointer_array(rank_bufs), pointer_array(flat), world_size,
                                    numel_per_rank, dtype_code(dtype), _pad_handle(pad),
                                    stream_handle(stream)))
+
+
+# ---------------------------------------------------------------- training step
+def _tensor_array(items, count, name):
+    """pointer_array for a list of `count` tensors or addresses (None: no list)."""
+    if items is None:
+        return None
+    if len(items) != count:
+        raise ValueError(f"{name} has {len(items)} entries, sizes has {count}")
+    torch = sys.modules.get("torch")
+    plain = torch.Tensor if torch is not None else ()
+    return (_vp * count)(*[x.data_ptr() if x.__class__ is plain and x.is_cuda else _addr(x) for x in items])
+
+
+def _sizes(sizes):
+    return (ctypes.c_int64 * len(sizes))(*sizes)
+
+
+def rr_layer_norm(x, weight, bias, y, mean, rstd, rows, cols, x_stride, y_stride, eps, dtype, weight_dtype,
+                  stream=None):
+    """y = layer norm of each row of x; weight, bias, mean and rstd may be None."""
+    _check(lib().rr_layer_norm(_addr(x), _addr(weight), _addr(bias), _addr(y), _addr(mean), _addr(rstd), rows, cols,
+                               x_stride, y_stride, eps, dtype_code(dtype), dtype_code(weight_dtype),
+                               stream_handle(stream)))
+
+
+def rr_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, rows, cols, dy_stride, x_stride, dx_stride,
+                           dtype, weight_dtype, workspace, workspace_bytes, stream=None):
+    """Gradients of rr_layer_norm; weight and any of dx, dweight, dbias may be None."""
+    _check(lib().rr_layer_norm_backward(_addr(dy), _addr(x), _addr(weight), _addr(mean), _addr(rstd), _addr(dx),
+                                        _addr(dweight), _addr(dbias), rows, cols, dy_stride, x_stride, dx_stride,
+                                        dtype_code(dtype), dtype_code(weight_dtype), _addr(workspace),
+                                        workspace_bytes, stream_handle(stream)))
+
+
+def rr_layer_norm_backward_workspace(rows, cols):
+    """Bytes of workspace for rr_layer_norm_backward."""
+    n = ctypes.c_size_t()
+    _check(lib().rr_layer_norm_backward_workspace(rows, cols, ctypes.byref(n)))
+    return n.value
+
+
+def rr_grad_norm(grads, sizes, dtype, inv_scale, max_norm, norm, scale, workspace, workspace_bytes, stream=None):
+    """Norm over a list of gradient tensors and the factor that clips it; norm or scale may be None."""
+    n = len(sizes)
+    _check(lib().rr_grad_norm(_tensor_array(grads, n, "grads"), _sizes(sizes), n, dtype_code(dtype), inv_scale,
+                              max_norm, _addr(norm), _addr(scale), _addr(workspace), workspace_bytes,
+                              stream_handle(stream)))
+
+
+def rr_grad_norm_workspace(num_tensors):
+    """Bytes of workspace for rr_grad_norm."""
+    n = ctypes.c_size_t()
+    _check(lib().rr_grad_norm_workspace(num_tensors, ctypes.byref(n)))
+    return n.value
+
+
+def rr_adamw(params, grads, exp_avg, exp_avg_sq, master, sizes, param_dtype, grad_dtype, hyper, grad_scale=None,
+             stream=None):
+    """One AdamW step over a list of tensors, states in binary32; master may be None."""
+    n = len(sizes)
+    _check(lib().rr_adamw(_tensor_array(params, n, "params"), _tensor_array(grads, n, "grads"),
+                          _tensor_array(exp_avg, n, "exp_avg"), _tensor_array(exp_avg_sq, n, "exp_avg_sq"),
+                          _tensor_array(master, n, "master"), _sizes(sizes), n, dtype_code(param_dtype),
+                          dtype_code(grad_dtype), hyper, _addr(grad_scale), stream_handle(stream)))
+
+
+def rr_adamw8(params, grads, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale, master, sizes, param_dtype,
+              grad_dtype, hyper, seed, grad_scale=None, stream=None):
+    """One AdamW step over a list of tensors, states in 8 bits; master may be None."""
+    n = len(sizes)
+    _check(lib().rr_adamw8(_tensor_array(params, n, "params"), _tensor_array(grads, n, "grads"),
+                           _tensor_array(exp_avg, n, "exp_avg"), _tensor_array(exp_avg_scale, n, "exp_avg_scale"),
+                           _tensor_array(exp_avg_sq, n, "exp_avg_sq"),
+                           _tensor_array(exp_avg_sq_scale, n, "exp_avg_sq_scale"),
+                           _tensor_array(master, n, "master"), _sizes(sizes), n, dtype_code(param_dtype),
+                           dtype_code(grad_dtype), hyper, seed & 0xFFFFFFFF, _addr(grad_scale),
+                           stream_handle(stream)))
 
 
 def bound_call(name, *args):

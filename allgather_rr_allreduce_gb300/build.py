@@ -18,7 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "librr.so")
-SOURCES = ("rr_api.cu", "rr_allreduce.cu", "rr_allgather.cu")
+SOURCES = ("rr_api.cu", "rr_allreduce.cu", "rr_allgather.cu", "rr_layer_norm.cu", "rr_optim.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

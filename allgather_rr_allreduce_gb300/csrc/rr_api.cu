@@ -13,6 +13,7 @@
 #include <utility>
 
 #include "rr_internal.h"
+#include "rr_step.h"
 
 struct rr_signal_pad {
     int device;
@@ -844,6 +845,21 @@ const char *rr_status_string(rr_status s)
 const char *rr_last_error(void) { return g_err; }
 
 }  // extern "C"
+
+namespace rr {
+
+rr_status step_fail(rr_status s, const char *fmt, ...)
+{
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_err, sizeof g_err, fmt, ap);
+    va_end(ap);
+    return s;
+}
+rr_status step_cuda_fail(cudaError_t e, const char *what) { return cuda_fail(e, what); }
+rr_status step_ok() { return ok(); }
+
+}  // namespace rr
 
 // ---------------------------------------------------------------- no-alloc one-shot
 // rr_allreduce_oneshot_noalloc: the one-shot allreduce for callers that may

@@ -1,0 +1,752 @@
+// Layer norm and its gradient (include/rr.h: rr_layer_norm,
+// rr_layer_norm_backward).
+//
+// Both are bound by HBM: a row is read once into registers, its statistics are
+// reduced over the warps that share it, and the result is written from the
+// same registers.  A row belongs to G warps of one block, EL elements to a
+// lane; with G = 1 the warps of a block work on rows of their own and meet
+// nowhere.  Blocks stay for many rows, so weights are loaded once and the
+// weight's gradient is summed in registers over a block's rows; the blocks'
+// partial sums go to the workspace and a second kernel adds them in order.
+#include <map>
+#include <mutex>
+#include <utility>
+
+#include "rr_step.h"
+
+namespace rr {
+
+namespace {
+
+constexpr int kMaxPartials = 608;  // blocks whose partial weight gradients are kept
+
+struct NormArgs {
+    const void *x, *w, *b;
+    void *y;
+    float *mean, *rstd;
+    int64_t rows, cols, xs, ys;
+    float eps;
+    int wdtype;
+};
+
+struct NormGradArgs {
+    const void *dy, *x, *w;
+    const float *mean, *rstd;
+    void *dx;
+    float *part;   // [2][P][cols] partial dweight, dbias; null: not wanted
+    float2 *coef;  // [rows], the two row means (columns kernel only)
+    int64_t rows, cols, dys, xs, dxs;
+    int wdtype;
+    int P;
+};
+
+// One lane's EL elements of a row.  VEC: 16-byte vectors, vector v of the
+// lane at column ((v * G + g) * 32 + lane) * EN; else single elements, element
+// k at column (k * G + g) * 32 + lane.  Columns past the row read as zero.
+template <class T, int EL, bool VEC>
+struct Slice {
+    static constexpr int EN = 16 / (int)sizeof(T);
+    static constexpr int NV = EL / EN;
+    Pack<T, EN> raw[NV];
+
+    static __device__ __forceinline__ int col(int k, int G, int g, int lane)
+    {
+        return VEC ? ((k / EN * G + g) * 32 + lane) * EN + k % EN : (k * G + g) * 32 + lane;
+    }
+    __device__ __forceinline__ void load(const T *row, int cols, int G, int g, int lane)
+    {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            if (VEC) {
+                const int c = col(v * EN, G, g, lane);
+                if (c < cols) {
+                    raw[v] = *reinterpret_cast<const Pack<T, EN> *>(row + c);
+                } else {
+                    *reinterpret_cast<uint4 *>(&raw[v]) = make_uint4(0, 0, 0, 0);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < EN; ++j) {
+                    const int c = col(v * EN + j, G, g, lane);
+                    raw[v].v[j] = c < cols ? row[c] : from_f32<T>(0.0f);
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ float at(int k) const { return to_f32(raw[k / EN].v[k % EN]); }
+    __device__ __forceinline__ void set(int k, float x) { raw[k / EN].v[k % EN] = from_f32<T>(x); }
+    __device__ __forceinline__ void store(T *row, int cols, int G, int g, int lane) const
+    {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            if (VEC) {
+                const int c = col(v * EN, G, g, lane);
+                if (c < cols) *reinterpret_cast<Pack<T, EN> *>(row + c) = raw[v];
+            } else {
+#pragma unroll
+                for (int j = 0; j < EN; ++j) {
+                    const int c = col(v * EN + j, G, g, lane);
+                    if (c < cols) row[c] = raw[v].v[j];
+                }
+            }
+        }
+    }
+};
+
+// Row statistics: each warp takes the sum of its part and the squares centred
+// on its own mean, and the warps' parts are joined around the common mean, so
+// nothing is subtracted from a large sum of squares and one barrier serves.
+// GROUP: the block's G warps share a row (else the warp has it alone).
+template <class T, int EL, bool VEC, bool GROUP>
+__global__ void __launch_bounds__(EL == 8 ? 1024 : 512) norm_rows_kernel(const __grid_constant__ NormArgs a)
+{
+    stream_order();
+    using S = Slice<T, EL, VEC>;
+    __shared__ float2 s_part[2][32];
+    __shared__ float s_count[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int G = GROUP ? blockDim.x >> 5 : 1, g = GROUP ? warp : 0;
+    const int64_t step = GROUP ? gridDim.x : (int64_t)gridDim.x * (blockDim.x >> 5);
+    int64_t row = GROUP ? blockIdx.x : (int64_t)blockIdx.x * (blockDim.x >> 5) + warp;
+    const int cols = (int)a.cols;
+
+    float w[EL], b[EL];
+    float mine = 0.0f;
+#pragma unroll
+    for (int k = 0; k < EL; ++k) {
+        const int c = S::col(k, G, g, lane);
+        const bool in = c < cols;
+        w[k] = in && a.w ? load_any(a.w, c, a.wdtype) : 1.0f;
+        b[k] = in && a.b ? load_any(a.b, c, a.wdtype) : 0.0f;
+        mine += in ? 1.0f : 0.0f;
+    }
+    const float count = warp_sum(mine);
+    const float inv_count = count > 0.0f ? 1.0f / count : 0.0f;
+    if (GROUP) {
+        if (lane == 0) s_count[g] = count;
+        __syncthreads();
+    }
+    const float n = (float)cols;
+
+    S next;
+    if (row < a.rows) next.load(static_cast<const T *>(a.x) + row * a.xs, cols, G, g, lane);
+    for (int it = 0; row < a.rows; row += step, it ^= 1) {
+        S cur = next;
+        if (row + step < a.rows) next.load(static_cast<const T *>(a.x) + (row + step) * a.xs, cols, G, g, lane);
+        float sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < EL; ++k) sum += cur.at(k);
+        sum = warp_sum(sum);
+        float mean = sum * inv_count;
+        float m2 = 0.0f;
+#pragma unroll
+        for (int k = 0; k < EL; ++k) {
+            const float d = S::col(k, G, g, lane) < cols ? cur.at(k) - mean : 0.0f;
+            m2 = fmaf(d, d, m2);
+        }
+        m2 = warp_sum(m2);
+        if (GROUP) {
+            if (lane == 0) s_part[it][g] = make_float2(sum, m2);
+            __syncthreads();
+            float total = 0.0f;
+            for (int i = 0; i < G; ++i) total += s_part[it][i].x;
+            mean = total / n;
+            m2 = 0.0f;
+            for (int i = 0; i < G; ++i) {
+                const float c = s_count[i];
+                const float2 p = s_part[it][i];
+                const float d = c > 0.0f ? p.x / c - mean : 0.0f;
+                m2 += fmaf(c * d, d, p.y);
+            }
+        }
+        const float rstd = 1.0f / sqrtf(m2 / n + a.eps);
+#pragma unroll
+        for (int k = 0; k < EL; ++k) cur.set(k, fmaf((cur.at(k) - mean) * rstd, w[k], b[k]));
+        cur.store(static_cast<T *>(a.y) + row * a.ys, cols, G, g, lane);
+        if (g == 0 && lane == 0) {
+            if (a.mean) a.mean[row] = mean;
+            if (a.rstd) a.rstd[row] = rstd;
+        }
+    }
+}
+
+// Rows too long for registers: a block per row, three passes over it (the
+// second and third come from L2 for rows up to a few MB).
+__device__ __forceinline__ float block_sum(float x, float *s)
+{
+    x = warp_sum(x);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = x;
+    __syncthreads();
+    float t = 0.0f;
+    for (int i = 0; i < (int)(blockDim.x >> 5); ++i) t += s[i];
+    return t;
+}
+
+template <class T>
+__global__ void __launch_bounds__(1024) norm_long_kernel(const __grid_constant__ NormArgs a)
+{
+    stream_order();
+    __shared__ float s[32];
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const T *x = static_cast<const T *>(a.x) + row * a.xs;
+        T *y = static_cast<T *>(a.y) + row * a.ys;
+        float sum = 0.0f;
+        for (int64_t c = threadIdx.x; c < a.cols; c += blockDim.x) sum += to_f32(x[c]);
+        const float mean = block_sum(sum, s) / (float)a.cols;
+        float m2 = 0.0f;
+        for (int64_t c = threadIdx.x; c < a.cols; c += blockDim.x) {
+            const float d = to_f32(x[c]) - mean;
+            m2 = fmaf(d, d, m2);
+        }
+        const float rstd = 1.0f / sqrtf(block_sum(m2, s) / (float)a.cols + a.eps);
+        for (int64_t c = threadIdx.x; c < a.cols; c += blockDim.x) {
+            const float w = a.w ? load_any(a.w, c, a.wdtype) : 1.0f;
+            const float b = a.b ? load_any(a.b, c, a.wdtype) : 0.0f;
+            y[c] = from_f32<T>(fmaf((to_f32(x[c]) - mean) * rstd, w, b));
+        }
+        if (threadIdx.x == 0) {
+            if (a.mean) a.mean[row] = mean;
+            if (a.rstd) a.rstd[row] = rstd;
+        }
+    }
+}
+
+// ---------------------------------------------------------------- gradient
+// Each row needs two sums over its columns, sum(w dy) and sum(w dy xhat),
+// before its dx; dweight and dbias are sums over rows and stay in registers.
+template <class T, int EL, bool VEC, bool GROUP>
+__global__ void __launch_bounds__(EL == 32 ? 256 : 512) norm_grad_rows_kernel(const __grid_constant__ NormGradArgs a)
+{
+    stream_order();
+    using S = Slice<T, EL, VEC>;
+    __shared__ float2 s_part[2][16];
+    extern __shared__ float s_acc[];  // [cols], joins the warps of a block (GROUP off)
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int G = GROUP ? blockDim.x >> 5 : 1, g = GROUP ? warp : 0;
+    const int64_t step = GROUP ? gridDim.x : (int64_t)gridDim.x * (blockDim.x >> 5);
+    int64_t row = GROUP ? blockIdx.x : (int64_t)blockIdx.x * (blockDim.x >> 5) + warp;
+    const int cols = (int)a.cols;
+    const float n = (float)cols;
+
+    float w[EL], dw[EL], db[EL];
+#pragma unroll
+    for (int k = 0; k < EL; ++k) {
+        const int c = S::col(k, G, g, lane);
+        w[k] = c < cols ? (a.w ? load_any(a.w, c, a.wdtype) : 1.0f) : 0.0f;
+        dw[k] = db[k] = 0.0f;
+    }
+    S ndy, nx;
+    float nmean = 0.0f, nrstd = 0.0f;
+    auto fetch = [&](int64_t r) {
+        ndy.load(static_cast<const T *>(a.dy) + r * a.dys, cols, G, g, lane);
+        nx.load(static_cast<const T *>(a.x) + r * a.xs, cols, G, g, lane);
+        nmean = a.mean[r];
+        nrstd = a.rstd[r];
+    };
+    if (row < a.rows) fetch(row);
+    for (int it = 0; row < a.rows; row += step, it ^= 1) {
+        S dy = ndy, x = nx;
+        const float mean = nmean, rstd = nrstd;
+        if (row + step < a.rows) fetch(row + step);
+        float c1 = 0.0f, c2 = 0.0f;
+#pragma unroll
+        for (int k = 0; k < EL; ++k) {
+            const float d = dy.at(k), xhat = (x.at(k) - mean) * rstd;
+            const float wd = w[k] * d;
+            c1 += wd;
+            c2 = fmaf(wd, xhat, c2);
+            // columns past the row read dy = 0 and are never written out
+            dw[k] = fmaf(d, xhat, dw[k]);
+            db[k] += d;
+        }
+        c1 = warp_sum(c1);
+        c2 = warp_sum(c2);
+        if (GROUP) {
+            if (lane == 0) s_part[it][g] = make_float2(c1, c2);
+            __syncthreads();
+            c1 = c2 = 0.0f;
+            for (int i = 0; i < G; ++i) {
+                const float2 p = s_part[it][i];
+                c1 += p.x;
+                c2 += p.y;
+            }
+        }
+        c1 /= n;
+        c2 /= n;
+        if (a.dx) {
+#pragma unroll
+            for (int k = 0; k < EL; ++k) {
+                const float xhat = (x.at(k) - mean) * rstd;
+                x.set(k, (w[k] * dy.at(k) - c1 - xhat * c2) * rstd);
+            }
+            x.store(static_cast<T *>(a.dx) + row * a.dxs, cols, G, g, lane);
+        }
+    }
+    if (!a.part) return;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        float *out = a.part + ((int64_t)which * a.P + blockIdx.x) * cols;
+        if (GROUP) {
+#pragma unroll
+            for (int k = 0; k < EL; ++k) {
+                const int c = S::col(k, G, g, lane);
+                if (c < cols) out[c] = which ? db[k] : dw[k];
+            }
+        } else {
+            for (int turn = 0; turn < (int)(blockDim.x >> 5); ++turn) {
+                if (warp == turn) {
+#pragma unroll
+                    for (int k = 0; k < EL; ++k) {
+                        const int c = S::col(k, G, g, lane);
+                        const float v = which ? db[k] : dw[k];
+                        if (c < cols) s_acc[c] = turn == 0 ? v : s_acc[c] + v;
+                    }
+                }
+                __syncthreads();
+            }
+            for (int c = threadIdx.x; c < cols; c += blockDim.x) out[c] = s_acc[c];
+            __syncthreads();
+        }
+    }
+}
+
+// Rows too long for registers: the two row means first ...
+template <class T>
+__global__ void __launch_bounds__(1024) norm_grad_means_kernel(const __grid_constant__ NormGradArgs a)
+{
+    stream_order();
+    __shared__ float s[32];
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const T *dy = static_cast<const T *>(a.dy) + row * a.dys;
+        const T *x = static_cast<const T *>(a.x) + row * a.xs;
+        const float mean = a.mean[row], rstd = a.rstd[row];
+        float c1 = 0.0f, c2 = 0.0f;
+        for (int64_t c = threadIdx.x; c < a.cols; c += blockDim.x) {
+            const float wd = (a.w ? load_any(a.w, c, a.wdtype) : 1.0f) * to_f32(dy[c]);
+            c1 += wd;
+            c2 = fmaf(wd, (to_f32(x[c]) - mean) * rstd, c2);
+        }
+        c1 = block_sum(c1, s);
+        c2 = block_sum(c2, s);
+        if (threadIdx.x == 0) a.coef[row] = make_float2(c1 / (float)a.cols, c2 / (float)a.cols);
+    }
+}
+
+// ... then dx and the weight's gradient by columns: block (cx, p) has kTile
+// columns and every P-th row.
+constexpr int kTile = 1024;
+template <class T>
+__global__ void __launch_bounds__(256) norm_grad_columns_kernel(const __grid_constant__ NormGradArgs a)
+{
+    stream_order();
+    constexpr int E = kTile / 256;
+    const int64_t tiles = (a.cols + kTile - 1) / kTile;
+    const int64_t tile = blockIdx.x % tiles;
+    const int p = (int)(blockIdx.x / tiles);
+    float w[E], dw[E], db[E];
+#pragma unroll
+    for (int k = 0; k < E; ++k) {
+        const int64_t c = tile * kTile + k * 256 + threadIdx.x;
+        w[k] = c < a.cols && a.w ? load_any(a.w, c, a.wdtype) : 1.0f;
+        dw[k] = db[k] = 0.0f;
+    }
+    for (int64_t row = p; row < a.rows; row += a.P) {
+        const float2 m = a.coef[row];
+        const float mean = a.mean[row], rstd = a.rstd[row];
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+            const int64_t c = tile * kTile + k * 256 + threadIdx.x;
+            if (c < a.cols) {
+                const float d = to_f32(static_cast<const T *>(a.dy)[row * a.dys + c]);
+                const float xhat = (to_f32(static_cast<const T *>(a.x)[row * a.xs + c]) - mean) * rstd;
+                dw[k] = fmaf(d, xhat, dw[k]);
+                db[k] += d;
+                if (a.dx)
+                    static_cast<T *>(a.dx)[row * a.dxs + c] = from_f32<T>((w[k] * d - m.x - xhat * m.y) * rstd);
+            }
+        }
+    }
+    if (!a.part) return;
+#pragma unroll
+    for (int k = 0; k < E; ++k) {
+        const int64_t c = tile * kTile + k * 256 + threadIdx.x;
+        if (c < a.cols) {
+            a.part[(int64_t)p * a.cols + c] = dw[k];
+            a.part[((int64_t)a.P + p) * a.cols + c] = db[k];
+        }
+    }
+}
+
+// The blocks' partial sums, added in order: 32 columns to a block, every
+// 16th partial to a warp, the warps' sums in order.
+struct NormJoinArgs {
+    const float *part;
+    void *dweight, *dbias;
+    int64_t cols;
+    int P, wdtype;
+};
+constexpr int kJoinWarps = 16;
+__global__ void __launch_bounds__(32 * kJoinWarps) norm_grad_join_kernel(const __grid_constant__ NormJoinArgs a)
+{
+    stream_order();
+    __shared__ float s[kJoinWarps][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+    for (int which = 0; which < 2; ++which) {
+        void *out = which ? a.dbias : a.dweight;
+        if (!out) continue;
+        float t = 0.0f;
+        if (c < a.cols)
+            for (int p = warp; p < a.P; p += kJoinWarps) t += a.part[((int64_t)which * a.P + p) * a.cols + c];
+        s[warp][lane] = t;
+        __syncthreads();
+        if (warp == 0 && c < a.cols) {
+            for (int i = 1; i < kJoinWarps; ++i) t += s[i][lane];
+            store_any(out, c, a.wdtype, t);
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------- host side
+std::mutex g_mu;
+std::map<int, int> g_sms;
+std::map<std::pair<const void *, std::pair<int, int>>, int> g_fit;
+
+// Blocks of this kernel that fit one SM.
+rr_status blocks_per_sm(const void *fn, int threads, int smem, int *out)
+{
+    std::lock_guard<std::mutex> lock(g_mu);
+    const auto key = std::make_pair(fn, std::make_pair(threads, smem));
+    auto it = g_fit.find(key);
+    if (it == g_fit.end()) {
+        int fit = 0;
+        cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, fn, threads, smem);
+        if (e != cudaSuccess) return step_cuda_fail(e, "cudaOccupancyMaxActiveBlocksPerMultiprocessor");
+        if (fit < 1) return step_fail(RR_ERR_CUDA, "a block of %d threads does not fit the device", threads);
+        it = g_fit.emplace(key, fit).first;
+    }
+    *out = it->second;
+    return RR_OK;
+}
+
+template <class T, bool VEC, bool GROUP>
+const void *norm_rows_fn(int el)
+{
+    if (el == 8) return (const void *)norm_rows_kernel<T, 8, VEC, GROUP>;
+    if (el == 16) return (const void *)norm_rows_kernel<T, 16, VEC, GROUP>;
+    return (const void *)norm_rows_kernel<T, 32, VEC, GROUP>;
+}
+template <class T>
+const void *norm_rows_fn(int el, bool vec, bool group)
+{
+    if (vec) return group ? norm_rows_fn<T, true, true>(el) : norm_rows_fn<T, true, false>(el);
+    return group ? norm_rows_fn<T, false, true>(el) : norm_rows_fn<T, false, false>(el);
+}
+template <class T, bool VEC, bool GROUP>
+const void *norm_grad_fn(int el)
+{
+    if (el == 8) return (const void *)norm_grad_rows_kernel<T, 8, VEC, GROUP>;
+    if (el == 16) return (const void *)norm_grad_rows_kernel<T, 16, VEC, GROUP>;
+    return (const void *)norm_grad_rows_kernel<T, 32, VEC, GROUP>;
+}
+template <class T>
+const void *norm_grad_fn(int el, bool vec, bool group)
+{
+    if (vec) return group ? norm_grad_fn<T, true, true>(el) : norm_grad_fn<T, true, false>(el);
+    return group ? norm_grad_fn<T, false, true>(el) : norm_grad_fn<T, false, false>(el);
+}
+
+// Elements to a lane and warps to a row: one warp while 32 elements a lane
+// hold the row, else 16 a lane (32 where that needs more than 512 threads).
+// With fewer rows than SMs nothing but one row's latency counts: 8 a lane.
+// warps > 0 where a kernel of that shape takes the row (most[]: the warps its
+// launch bounds allow with 8, 16 and 32 elements a lane), else 0.
+void row_shape(int64_t rows, int64_t cols, int sms, const int *most, int *el, int *warps)
+{
+    auto need = [&](int e) { return (cols + 32 * e - 1) / (32 * e); };
+    if (rows <= sms && need(8) <= most[0]) *el = 8;
+    else if (cols <= 256) *el = 8;
+    else if (cols <= 512) *el = 16;
+    else if (cols <= 1024) *el = 32;
+    else *el = need(16) <= most[1] ? 16 : 32;
+    const int64_t n = need(*el);
+    *warps = n <= most[*el == 8 ? 0 : *el == 16 ? 1 : 2] ? (int)n : 0;
+}
+
+constexpr int kNormWarps[3] = {32, 16, 16}, kNormGradWarps[3] = {16, 16, 8};
+
+struct Rows {
+    const char *name;
+    const void *p;
+    int64_t stride;
+};
+
+// Whether two row layouts (bytes) touch each other's elements.
+bool rows_touch(uintptr_t a, int64_t as, uintptr_t b, int64_t bs, int64_t rows, int64_t len)
+{
+    const uintptr_t a1 = a + (uintptr_t)((rows - 1) * as + len), b1 = b + (uintptr_t)((rows - 1) * bs + len);
+    if (a >= b1 || b >= a1) return false;
+    if (as != bs || as <= 0) return true;
+    const int64_t d = (int64_t)(a > b ? a - b : b - a) % as;  // interleaved rows of one buffer
+    return !(d >= len && as - d >= len);
+}
+bool ranges_touch(const void *a, int64_t an, const void *b, int64_t bn)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && an > 0 && bn > 0 && x < y + (uintptr_t)bn && y < x + (uintptr_t)an;
+}
+
+rr_status check_sizes(int64_t rows, int64_t cols, rr_dtype dtype, rr_dtype wdtype)
+{
+    if (!float_bytes(dtype)) return step_fail(RR_ERR_UNSUPPORTED_DTYPE, "dtype %d", (int)dtype);
+    if (!float_bytes(wdtype)) return step_fail(RR_ERR_UNSUPPORTED_DTYPE, "weight_dtype %d", (int)wdtype);
+    if (rows < 0 || rows > ((int64_t)1 << 40)) return step_fail(RR_ERR_INVALID_ARG, "rows %lld", (long long)rows);
+    if (cols < 1 || cols > ((int64_t)1 << 31)) return step_fail(RR_ERR_INVALID_ARG, "cols %lld", (long long)cols);
+    return RR_OK;
+}
+rr_status check_stride(const char *name, int64_t stride, int64_t rows, int64_t cols, bool written)
+{
+    if (stride < 0 || stride > ((int64_t)1 << 40) || (written && rows > 1 && stride < cols))
+        return step_fail(RR_ERR_INVALID_ARG, "%s %lld with cols %lld", name, (long long)stride, (long long)cols);
+    if (rows > 0 && stride > 0 && rows > ((int64_t)1 << 60) / stride)
+        return step_fail(RR_ERR_INVALID_ARG, "%s %lld with rows %lld", name, (long long)stride, (long long)rows);
+    return RR_OK;
+}
+rr_status check_element(const char *name, const void *p, int bytes)
+{
+    if (!aligned_to(p, bytes)) return step_fail(RR_ERR_ALIGNMENT, "%s not aligned to its %d-byte element", name, bytes);
+    return RR_OK;
+}
+
+#define RR_TRY(expr)                            \
+    do {                                        \
+        const rr_status st_ = (expr);           \
+        if (st_ != RR_OK) return st_;           \
+    } while (0)
+
+int64_t row_span(int64_t rows, int64_t stride, int64_t cols) { return (rows - 1) * stride + cols; }
+
+bool vector_rows(const void *p, int64_t stride, int64_t rows, int eb)
+{
+    return aligned_to(p, 16) && (rows <= 1 || stride * eb % 16 == 0);
+}
+
+}  // namespace
+
+rr_status step_sms(int *sms)
+{
+    int dev = -1;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return step_cuda_fail(e, "cudaGetDevice");
+    std::lock_guard<std::mutex> lock(g_mu);
+    auto it = g_sms.find(dev);
+    if (it == g_sms.end()) {
+        int n = 0;
+        e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return step_cuda_fail(e, "cudaDeviceGetAttribute(multiProcessorCount)");
+        it = g_sms.emplace(dev, n).first;
+    }
+    *sms = it->second;
+    return RR_OK;
+}
+
+rr_status step_launch(const void *fn, int64_t grid, int threads, int smem, void *args, cudaStream_t stream)
+{
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof cfg);
+    cfg.gridDim = dim3((unsigned)grid, 1, 1);
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    void *params[1] = {args};
+    cudaError_t e = cudaLaunchKernelExC(&cfg, fn, params);
+    if (e != cudaSuccess) return step_cuda_fail(e, "cudaLaunchKernelExC");
+    return RR_OK;
+}
+
+}  // namespace rr
+
+using namespace rr;
+
+extern "C" rr_status rr_layer_norm(const void *x, const void *weight, const void *bias, void *y, float *mean,
+                                   float *rstd, int64_t rows, int64_t cols, int64_t x_stride,
+                                   int64_t y_stride, float eps, rr_dtype dtype, rr_dtype weight_dtype,
+                                   cudaStream_t stream)
+{
+    RR_TRY(check_sizes(rows, cols, dtype, weight_dtype));
+    RR_TRY(check_stride("x_stride", x_stride, rows, cols, false));
+    RR_TRY(check_stride("y_stride", y_stride, rows, cols, true));
+    if (!(eps >= 0.0f)) return step_fail(RR_ERR_INVALID_ARG, "eps %g", (double)eps);
+    if (rows == 0) return step_ok();
+    if (!x || !y) return step_fail(RR_ERR_INVALID_ARG, "%s is NULL", x ? "y" : "x");
+    const int eb = float_bytes(dtype), wb = float_bytes(weight_dtype);
+    RR_TRY(check_element("x", x, eb));
+    RR_TRY(check_element("y", y, eb));
+    RR_TRY(check_element("weight", weight, wb));
+    RR_TRY(check_element("bias", bias, wb));
+    RR_TRY(check_element("mean", mean, 4));
+    RR_TRY(check_element("rstd", rstd, 4));
+    const int64_t ybytes = row_span(rows, y_stride, cols) * eb, xbytes = row_span(rows, x_stride, cols) * eb;
+    if (!(x == y && (x_stride == y_stride || rows == 1)) &&
+        rows_touch(reinterpret_cast<uintptr_t>(x), x_stride * eb, reinterpret_cast<uintptr_t>(y), y_stride * eb, rows,
+                   cols * eb))
+        return step_fail(RR_ERR_ALIAS, "y overlaps x");
+    if (ranges_touch(y, ybytes, weight, cols * wb) || ranges_touch(y, ybytes, bias, cols * wb) ||
+        ranges_touch(y, ybytes, mean, rows * 4) || ranges_touch(y, ybytes, rstd, rows * 4))
+        return step_fail(RR_ERR_ALIAS, "y overlaps another argument");
+    for (const float *stat : {mean, rstd})
+        if (ranges_touch(stat, rows * 4, x, xbytes) || ranges_touch(stat, rows * 4, weight, cols * wb) ||
+            ranges_touch(stat, rows * 4, bias, cols * wb))
+            return step_fail(RR_ERR_ALIAS, "a statistic overlaps an input");
+    if (ranges_touch(mean, rows * 4, rstd, rows * 4)) return step_fail(RR_ERR_ALIAS, "mean overlaps rstd");
+
+    int sms = 0;
+    RR_TRY(step_sms(&sms));
+    NormArgs a{x, weight, bias, y, mean, rstd, rows, cols, x_stride, y_stride, eps, (int)weight_dtype};
+    int el = 0, warps = 0;
+    row_shape(rows, cols, sms, kNormWarps, &el, &warps);
+    const void *fn;
+    int threads;
+    int64_t blocks;
+    if (warps == 0) {
+        fn = dtype == RR_FP32 ? (const void *)norm_long_kernel<float>
+             : dtype == RR_BF16 ? (const void *)norm_long_kernel<__nv_bfloat16> : (const void *)norm_long_kernel<__half>;
+        threads = 1024;
+        blocks = rows;
+    } else {
+        const bool vec = cols * eb % 16 == 0 && vector_rows(x, x_stride, rows, eb) && vector_rows(y, y_stride, rows, eb);
+        const bool group = warps > 1;
+        fn = dtype == RR_FP32 ? norm_rows_fn<float>(el, vec, group)
+             : dtype == RR_BF16 ? norm_rows_fn<__nv_bfloat16>(el, vec, group) : norm_rows_fn<__half>(el, vec, group);
+        const int64_t per = group ? 1 : rows >= 8 * (int64_t)sms ? 8 : (rows + sms - 1) / sms;  // rows a block has at once
+        threads = 32 * (group ? warps : (int)per);
+        blocks = (rows + per - 1) / per;
+    }
+    int fit = 0;
+    RR_TRY(blocks_per_sm(fn, threads, 0, &fit));
+    const int64_t most = (int64_t)fit * sms;
+    RR_TRY(step_launch(fn, blocks < most ? blocks : most, threads, 0, &a, stream));
+    return step_ok();
+}
+
+extern "C" rr_status rr_layer_norm_backward_workspace(int64_t rows, int64_t cols, size_t *bytes)
+{
+    if (!bytes) return step_fail(RR_ERR_INVALID_ARG, "bytes is NULL");
+    RR_TRY(check_sizes(rows, cols, RR_FP32, RR_FP32));
+    const int64_t P = rows < kMaxPartials ? rows : kMaxPartials;
+    *bytes = (size_t)(((rows * 8 + 15) & ~(int64_t)15) + 2 * P * cols * 4);
+    return step_ok();
+}
+
+extern "C" rr_status rr_layer_norm_backward(const void *dy, const void *x, const void *weight, const float *mean,
+                                            const float *rstd, void *dx, void *dweight, void *dbias,
+                                            int64_t rows, int64_t cols, int64_t dy_stride, int64_t x_stride,
+                                            int64_t dx_stride, rr_dtype dtype, rr_dtype weight_dtype,
+                                            void *workspace, size_t workspace_bytes, cudaStream_t stream)
+{
+    RR_TRY(check_sizes(rows, cols, dtype, weight_dtype));
+    RR_TRY(check_stride("dy_stride", dy_stride, rows, cols, false));
+    RR_TRY(check_stride("x_stride", x_stride, rows, cols, false));
+    if (dx) RR_TRY(check_stride("dx_stride", dx_stride, rows, cols, true));
+    if (!dx && !dweight && !dbias) return step_fail(RR_ERR_INVALID_ARG, "dx, dweight and dbias are all NULL");
+    if (rows > 0 && (!dy || !x || !mean || !rstd))
+        return step_fail(RR_ERR_INVALID_ARG, "%s is NULL", !dy ? "dy" : !x ? "x" : !mean ? "mean" : "rstd");
+    const int eb = float_bytes(dtype), wb = float_bytes(weight_dtype);
+    RR_TRY(check_element("dy", dy, eb));
+    RR_TRY(check_element("x", x, eb));
+    RR_TRY(check_element("dx", dx, eb));
+    RR_TRY(check_element("weight", weight, wb));
+    RR_TRY(check_element("dweight", dweight, wb));
+    RR_TRY(check_element("dbias", dbias, wb));
+    RR_TRY(check_element("mean", mean, 4));
+    RR_TRY(check_element("rstd", rstd, 4));
+    size_t need = 0;
+    RR_TRY(rr_layer_norm_backward_workspace(rows, cols, &need));
+    if (rows > 0) {
+        if (!workspace) return step_fail(RR_ERR_INVALID_ARG, "workspace is NULL");
+        if (!aligned_to(workspace, 16)) return step_fail(RR_ERR_ALIGNMENT, "workspace not 16-byte aligned");
+        if (workspace_bytes < need)
+            return step_fail(RR_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+        const int64_t len = cols * eb;
+        struct {
+            const char *name;
+            const void *p;
+            int64_t bytes;
+        } in[] = {{"weight", weight, cols * wb}, {"mean", mean, rows * 4}, {"rstd", rstd, rows * 4},
+                  {"dy", dy, row_span(rows, dy_stride, cols) * eb}, {"x", x, row_span(rows, x_stride, cols) * eb}},
+          out[] = {{"dweight", dweight, cols * wb}, {"dbias", dbias, cols * wb}, {"workspace", workspace, (int64_t)need},
+                   {"dx", dx, row_span(rows, dx_stride, cols) * eb}};
+        for (int i = 0; i < 4; ++i) {
+            for (int j = 0; j < (i == 3 ? 3 : 5); ++j)
+                if (ranges_touch(out[i].p, out[i].bytes, in[j].p, in[j].bytes))
+                    return step_fail(RR_ERR_ALIAS, "%s overlaps %s", out[i].name, in[j].name);
+            for (int j = 0; j < i; ++j)
+                if (ranges_touch(out[i].p, out[i].bytes, out[j].p, out[j].bytes))
+                    return step_fail(RR_ERR_ALIAS, "%s overlaps %s", out[i].name, out[j].name);
+        }
+        for (const Rows &r : {Rows{"dy", dy, dy_stride}, Rows{"x", x, x_stride}})
+            if (dx && !(dx == r.p && (dx_stride == r.stride || rows == 1)) &&
+                rows_touch(reinterpret_cast<uintptr_t>(dx), dx_stride * eb, reinterpret_cast<uintptr_t>(r.p),
+                           r.stride * eb, rows, len))
+                return step_fail(RR_ERR_ALIAS, "dx overlaps %s", r.name);
+    } else if (ranges_touch(dweight, cols * wb, dbias, cols * wb)) {
+        return step_fail(RR_ERR_ALIAS, "dbias overlaps dweight");
+    }
+    if (rows == 0 && !dweight && !dbias) return step_ok();
+
+    int sms = 0;
+    RR_TRY(step_sms(&sms));
+    const bool sums = dweight || dbias;
+    float2 *coef = static_cast<float2 *>(workspace);
+    float *part = sums ? reinterpret_cast<float *>(static_cast<char *>(workspace) + ((rows * 8 + 15) & ~(int64_t)15)) : nullptr;
+    NormGradArgs a{dy, x, weight, mean, rstd, dx, part, coef, rows, cols, dy_stride, x_stride, dx_stride,
+                   (int)weight_dtype, 0};
+    if (rows > 0) {
+        int el = 0, warps = 0;
+        row_shape(rows, cols, sms, kNormGradWarps, &el, &warps);
+        if (warps == 0) {
+            const void *means = dtype == RR_FP32 ? (const void *)norm_grad_means_kernel<float>
+                                : dtype == RR_BF16 ? (const void *)norm_grad_means_kernel<__nv_bfloat16>
+                                                   : (const void *)norm_grad_means_kernel<__half>;
+            const void *columns = dtype == RR_FP32 ? (const void *)norm_grad_columns_kernel<float>
+                                  : dtype == RR_BF16 ? (const void *)norm_grad_columns_kernel<__nv_bfloat16>
+                                                     : (const void *)norm_grad_columns_kernel<__half>;
+            const int64_t most = 2 * (int64_t)sms, tiles = (cols + kTile - 1) / kTile;
+            RR_TRY(step_launch(means, rows < most ? rows : most, 1024, 0, &a, stream));
+            int64_t P = (8 * (int64_t)sms + tiles - 1) / tiles;
+            if (P > rows) P = rows;
+            if (P > kMaxPartials) P = kMaxPartials;
+            a.P = (int)P;
+            RR_TRY(step_launch(columns, P * tiles, 256, 0, &a, stream));
+        } else {
+            const bool vec = cols * eb % 16 == 0 && vector_rows(dy, dy_stride, rows, eb) &&
+                             vector_rows(x, x_stride, rows, eb) && (!dx || vector_rows(dx, dx_stride, rows, eb));
+            const bool group = warps > 1;
+            const void *fn = dtype == RR_FP32 ? norm_grad_fn<float>(el, vec, group)
+                             : dtype == RR_BF16 ? norm_grad_fn<__nv_bfloat16>(el, vec, group)
+                                                : norm_grad_fn<__half>(el, vec, group);
+            const int64_t per = group ? 1 : rows >= 8 * (int64_t)sms ? 8 : (rows + sms - 1) / sms;
+            const int threads = 32 * (group ? warps : (int)per);
+            const int smem = group ? 0 : (int)cols * 4;
+            int fit = 0;
+            RR_TRY(blocks_per_sm(fn, threads, smem, &fit));
+            int64_t blocks = (rows + per - 1) / per;
+            if (blocks > (int64_t)fit * sms) blocks = (int64_t)fit * sms;
+            if (blocks > kMaxPartials) blocks = kMaxPartials;
+            a.P = (int)blocks;
+            RR_TRY(step_launch(fn, blocks, threads, smem, &a, stream));
+        }
+    }
+    if (sums) {
+        NormJoinArgs j{part, dweight, dbias, cols, a.P, (int)weight_dtype};
+        RR_TRY(step_launch((const void *)norm_grad_join_kernel, (cols + 31) / 32, 32 * kJoinWarps, 0, &j, stream));
+    }
+    return step_ok();
+}

@@ -1,0 +1,866 @@
+// Gradient norm and AdamW over lists of tensors (include/rr.h: rr_grad_norm,
+// rr_adamw, rr_adamw8).
+//
+// All three stream: every byte is touched once and HBM bounds them.  A launch
+// takes its list of tensors by value in the kernel's parameters (no table in
+// device memory to fill or keep), cut into chunks of elements that the blocks
+// deal out in turn; a block finds a chunk's tensor by bisection.
+#include <algorithm>
+#include <cmath>
+#include <vector>
+
+#include "rr_step.h"
+
+namespace rr {
+
+namespace {
+
+#define RR_TRY(expr)                  \
+    do {                              \
+        const rr_status st_ = (expr); \
+        if (st_ != RR_OK) return st_; \
+    } while (0)
+
+constexpr int kThreads = 256;
+constexpr int64_t kMaxSize = (int64_t)1 << 40;
+
+// The chunk table of a launch.  head: elements before the first one at which
+// every pointer of the tensor is aligned for a vector (kNoVector: there is none).
+constexpr int kNoVector = -1;
+template <int CAP>
+struct Chunks {
+    int64_t start[CAP + 1];  // first chunk of each tensor; start[count] = all
+    int64_t size[CAP];
+    int8_t head[CAP];
+    int count;
+    __device__ __forceinline__ int find(int64_t chunk) const
+    {
+        int lo = 0, hi = count;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (start[mid] <= chunk) lo = mid;
+            else hi = mid;
+        }
+        return lo;
+    }
+};
+
+// ---------------------------------------------------------------- gradient norm
+constexpr int kNormCapSmall = 32, kNormCap = 1200;
+constexpr int kNormUnroll = 8;
+constexpr int kNormBlocks = 1024;  // most blocks of one launch, one partial sum each
+
+template <int CAP>
+struct GradNormArgs {
+    Chunks<CAP> list;
+    const void *g[CAP];
+    double *part;  // this launch's partial sums
+};
+
+// Squares of values in [2^-50, 2^40] stay normal in binary32 and sums of 2^40
+// of them finite.  A vector whose largest magnitude lies outside (and is not
+// 0) goes to a binary64 sum; NaN fails the comparison and goes there too.
+__device__ __forceinline__ bool plain_range(float top) { return top <= 0x1p40f && !(top < 0x1p-50f && top > 0.0f); }
+
+template <class T, int CAP>
+__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ GradNormArgs<CAP> a)
+{
+    stream_order();
+    constexpr int E = 16 / (int)sizeof(T);
+    constexpr int64_t C = (int64_t)kThreads * E * kNormUnroll;
+    __shared__ double s[kThreads / 32];
+    float hi = 0.0f, lo = 0.0f;  // compensated sum of the chunks
+    double wide = 0.0;
+    const int64_t total = a.list.start[a.list.count];
+    for (int64_t chunk = blockIdx.x; chunk < total; chunk += gridDim.x) {
+        const int t = a.list.find(chunk);
+        const T *g = static_cast<const T *>(a.g[t]);
+        const int64_t n = a.list.size[t], c = chunk - a.list.start[t];
+        const int head = a.list.head[t];
+        float sum = 0.0f;
+        auto one = [&](float x) {
+            if (plain_range(fabsf(x))) sum = fmaf(x, x, sum);
+            else wide += (double)x * x;
+        };
+        if (c == 0 && (int)threadIdx.x < head && (int64_t)threadIdx.x < n) one(to_f32(g[threadIdx.x]));
+        const int64_t e0 = head + c * C + (int64_t)threadIdx.x * E;
+        Pack<T, E> v[kNormUnroll];
+#pragma unroll
+        for (int j = 0; j < kNormUnroll; ++j) {
+            const int64_t e = e0 + (int64_t)j * kThreads * E;
+            if (e + E <= n) {
+                v[j] = *reinterpret_cast<const Pack<T, E> *>(g + e);
+            } else {
+#pragma unroll
+                for (int k = 0; k < E; ++k) v[j].v[k] = e + k < n ? g[e + k] : from_f32<T>(0.0f);
+            }
+        }
+        float acc[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < kNormUnroll; ++j) {
+            float top = 0.0f;
+            bool bad = false;
+#pragma unroll
+            for (int k = 0; k < E; ++k) {
+                const float x = to_f32(v[j].v[k]);
+                bad |= x != x;
+                top = fmaxf(top, fabsf(x));
+            }
+            if (!bad && plain_range(top)) {
+#pragma unroll
+                for (int k = 0; k < E; ++k) {
+                    const float x = to_f32(v[j].v[k]);
+                    acc[k & 1] = fmaf(x, x, acc[k & 1]);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < E; ++k) wide += (double)to_f32(v[j].v[k]) * to_f32(v[j].v[k]);
+            }
+        }
+        sum += acc[0] + acc[1];
+        // hi + lo += sum without losing the low bits (Knuth's two-sum)
+        const float t0 = __fadd_rn(hi, sum), z = __fsub_rn(t0, hi);
+        lo += __fadd_rn(__fsub_rn(hi, __fsub_rn(t0, z)), __fsub_rn(sum, z));
+        hi = t0;
+    }
+    double d = wide + (double)hi + (double)lo;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = d;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        d = 0.0;
+        for (int i = 0; i < kThreads / 32; ++i) d += s[i];
+        a.part[blockIdx.x] = d;
+    }
+}
+
+struct GradNormEndArgs {
+    const double *part;
+    int64_t count;
+    float inv_scale, max_norm;
+    float *norm, *scale;
+};
+
+__global__ void __launch_bounds__(kThreads) grad_norm_end_kernel(const __grid_constant__ GradNormEndArgs a)
+{
+    stream_order();
+    __shared__ double s[kThreads / 32];
+    double d = 0.0;
+    for (int64_t i = threadIdx.x; i < a.count; i += kThreads) d += a.part[i];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = d;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        d = 0.0;
+        for (int i = 0; i < kThreads / 32; ++i) d += s[i];
+        const float norm = (float)(sqrt(d) * (double)a.inv_scale);
+        const float clip = a.max_norm / (norm + 1e-6f);
+        if (a.norm) *a.norm = norm;
+        if (a.scale) *a.scale = isfinite(norm) ? a.inv_scale * fminf(1.0f, clip) : __int_as_float(0x7fc00000);
+    }
+}
+
+// ---------------------------------------------------------------- AdamW
+constexpr int kAdamCapSmall = 32, kAdamCap = 400;
+constexpr int kUnit = 4;   // elements of a vector: 16 bytes of binary32, 8 of the 16-bit types
+constexpr int kUnits = 4;  // vectors of a thread in a chunk
+constexpr int64_t kAdamChunk = (int64_t)kThreads * kUnit * kUnits;
+
+struct AdamScalars {
+    float beta1, omb1, beta2, omb2;  // beta and 1 - beta
+    float decay;                     // 1 - lr * weight_decay
+    float inv_c2;                    // 1 / sqrt(1 - beta2^step)
+    float step_size;                 // lr / (1 - beta1^step)
+    float eps;
+    const float *scale;
+};
+
+template <int CAP>
+struct AdamArgs {
+    Chunks<CAP> list;
+    void *p[CAP];
+    const void *g[CAP];
+    float *m[CAP], *v[CAP], *w[CAP];
+    AdamScalars h;
+};
+
+// One element.  Every operation rounds by itself (no fused multiply-add), so
+// that the result is the formula's, operation by operation, whatever the
+// compiler contracts.
+__device__ __forceinline__ float adam_element(const AdamScalars &h, float scale, float w, float g, float &m, float &v,
+                                              float &root)
+{
+    g = __fmul_rn(g, scale);
+    m = __fadd_rn(__fmul_rn(m, h.beta1), __fmul_rn(g, h.omb1));
+    v = __fadd_rn(__fmul_rn(v, h.beta2), __fmul_rn(__fmul_rn(g, h.omb2), g));
+    root = __fsqrt_rn(v);
+    const float den = __fadd_rn(__fmul_rn(root, h.inv_c2), h.eps);
+    return __fsub_rn(__fmul_rn(w, h.decay), __fmul_rn(__fdiv_rn(m, den), h.step_size));
+}
+
+template <class P, class G, bool MASTER, int CAP>
+__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ AdamArgs<CAP> a)
+{
+    stream_order();
+    const AdamScalars &h = a.h;
+    const float scale = h.scale ? *h.scale : 1.0f;
+    if (scale != scale) return;
+    const int64_t total = a.list.start[a.list.count];
+    for (int64_t chunk = blockIdx.x; chunk < total; chunk += gridDim.x) {
+        const int t = a.list.find(chunk);
+        const int64_t n = a.list.size[t], c = chunk - a.list.start[t];
+        const int head = a.list.head[t];
+        P *p = static_cast<P *>(a.p[t]);
+        const G *g = static_cast<const G *>(a.g[t]);
+        float *m = a.m[t], *v = a.v[t], *w = MASTER ? a.w[t] : nullptr;
+        auto one = [&](int64_t e) {
+            float me = m[e], ve = v[e], root;
+            const float x = adam_element(h, scale, MASTER ? w[e] : to_f32(p[e]), to_f32(g[e]), me, ve, root);
+            m[e] = me;
+            v[e] = ve;
+            if (MASTER) w[e] = x;
+            p[e] = from_f32<P>(x);
+        };
+        if (head == kNoVector) {
+            const int64_t end = (c + 1) * kAdamChunk < n ? (c + 1) * kAdamChunk : n;
+#pragma unroll 4
+            for (int64_t e = c * kAdamChunk + threadIdx.x; e < end; e += kThreads) one(e);
+            continue;
+        }
+        if (c == 0 && (int)threadIdx.x < head && (int64_t)threadIdx.x < n) one(threadIdx.x);
+        const int64_t e0 = head + c * kAdamChunk + (int64_t)threadIdx.x * kUnit;
+        Pack<P, kUnit> pv[kUnits];
+        Pack<G, kUnit> gv[kUnits];
+        Pack<float, kUnit> mv[kUnits], vv[kUnits], wv[kUnits];
+#pragma unroll
+        for (int j = 0; j < kUnits; ++j) {
+            const int64_t e = e0 + (int64_t)j * kThreads * kUnit;
+            if (e + kUnit <= n) {
+                if (MASTER) wv[j] = *reinterpret_cast<const Pack<float, kUnit> *>(w + e);
+                else pv[j] = *reinterpret_cast<const Pack<P, kUnit> *>(p + e);
+                gv[j] = *reinterpret_cast<const Pack<G, kUnit> *>(g + e);
+                mv[j] = *reinterpret_cast<const Pack<float, kUnit> *>(m + e);
+                vv[j] = *reinterpret_cast<const Pack<float, kUnit> *>(v + e);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kUnits; ++j) {
+            const int64_t e = e0 + (int64_t)j * kThreads * kUnit;
+            if (e + kUnit <= n) {
+#pragma unroll
+                for (int k = 0; k < kUnit; ++k) {
+                    float root;
+                    const float x = adam_element(h, scale, MASTER ? wv[j].v[k] : to_f32(pv[j].v[k]), to_f32(gv[j].v[k]),
+                                                 mv[j].v[k], vv[j].v[k], root);
+                    if (MASTER) wv[j].v[k] = x;
+                    pv[j].v[k] = from_f32<P>(x);
+                }
+                if (MASTER) *reinterpret_cast<Pack<float, kUnit> *>(w + e) = wv[j];
+                *reinterpret_cast<Pack<P, kUnit> *>(p + e) = pv[j];
+                *reinterpret_cast<Pack<float, kUnit> *>(m + e) = mv[j];
+                *reinterpret_cast<Pack<float, kUnit> *>(v + e) = vv[j];
+            } else {
+                for (int64_t k = e; k < n; ++k) one(k);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- AdamW, 8-bit states
+// A warp has one block of 256 elements, 8 to a lane: the block's largest
+// magnitude is one warp-wide maximum, and states go from codes to codes in
+// registers.
+constexpr int kBlock = RR_ADAMW8_BLOCK;
+constexpr int kLane = kBlock / 32;
+
+template <int CAP>
+struct Adam8Args {
+    Chunks<CAP> list;  // chunk = block of kBlock elements
+    void *p[CAP];
+    const void *g[CAP];
+    uint8_t *m[CAP], *r[CAP];
+    float *ms[CAP], *rs[CAP], *w[CAP];
+    AdamScalars h;
+    uint32_t seed, first;  // first: index in the caller's list of this launch's first tensor
+};
+
+__host__ __device__ __forceinline__ uint32_t mix32(uint32_t x)
+{
+    x ^= x >> 16;
+    x *= 0x7FEB352Du;
+    x ^= x >> 15;
+    x *= 0x68E31DA5u;
+    return x ^ (x >> 16);
+}
+
+// Power-of-two scale of a block from the bits of its largest magnitude: the
+// magnitude over the scale lies in [128, 256).
+__device__ __forceinline__ int scale_exponent(uint32_t top)
+{
+    const int e = (int)(top >> 23) - 127 - 7;
+    return e < -126 ? -126 : e;
+}
+__device__ __forceinline__ float exp2_int(int e) { return __int_as_float((e + 127) << 23); }
+
+// |x| / scale on the code's grid, up or down by the 16 random bits u: adding
+// them just below the last kept mantissa bit and cutting there rounds up with
+// the probability of the part cut off.  Below 2^-6 the grid is even, as that
+// of values in [2^-6, 2^-5); lifting by 2^-6 makes it theirs.
+__device__ __forceinline__ float round_to_code(float t, uint32_t u)
+{
+    const float lift = t < 0x1p-6f ? 0x1p-6f : 0.0f;
+    const uint32_t bits = (__float_as_uint(__fadd_rn(t, lift)) + (u << 4) + 8u) & 0xFFF00000u;
+    return __fsub_rn(__uint_as_float(bits), lift);
+}
+__device__ __forceinline__ uint16_t to_codes(float lo, float hi)
+{
+    uint16_t c;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(hi), "f"(lo));
+    return c;
+}
+__device__ __forceinline__ float2 from_codes(uint16_t c)
+{
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+}
+
+// The lane's elements: 8 in a row (VEC) or every 32nd.
+template <bool VEC>
+__device__ __forceinline__ int lane_element(int k, int lane) { return VEC ? lane * kLane + k : k * 32 + lane; }
+
+template <class T, bool VEC>
+__device__ __forceinline__ void load_lane(float (&x)[kLane], const T *src, int lane, int left)
+{
+    if (VEC) {
+        constexpr int E = 16 / (int)sizeof(T) < kLane ? 16 / (int)sizeof(T) : kLane;
+#pragma unroll
+        for (int j = 0; j < kLane; j += E) {
+            const Pack<T, E> v = *reinterpret_cast<const Pack<T, E> *>(src + lane * kLane + j);
+#pragma unroll
+            for (int k = 0; k < E; ++k) x[j + k] = to_f32(v.v[k]);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < kLane; ++k) {
+            const int e = lane_element<false>(k, lane);
+            x[k] = e < left ? to_f32(src[e]) : 0.0f;
+        }
+    }
+}
+template <class T, bool VEC>
+__device__ __forceinline__ void store_lane(const float (&x)[kLane], T *dst, int lane, int left)
+{
+    if (VEC) {
+        constexpr int E = 16 / (int)sizeof(T) < kLane ? 16 / (int)sizeof(T) : kLane;
+#pragma unroll
+        for (int j = 0; j < kLane; j += E) {
+            Pack<T, E> v;
+#pragma unroll
+            for (int k = 0; k < E; ++k) v.v[k] = from_f32<T>(x[j + k]);
+            *reinterpret_cast<Pack<T, E> *>(dst + lane * kLane + j) = v;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < kLane; ++k) {
+            const int e = lane_element<false>(k, lane);
+            if (e < left) dst[e] = from_f32<T>(x[k]);
+        }
+    }
+}
+template <bool VEC>
+__device__ __forceinline__ void load_codes(float (&x)[kLane], const uint8_t *src, int lane, int left)
+{
+    uint16_t c[kLane / 2];
+    if (VEC) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(src + lane * kLane);
+        c[0] = (uint16_t)v.x;
+        c[1] = (uint16_t)(v.x >> 16);
+        c[2] = (uint16_t)v.y;
+        c[3] = (uint16_t)(v.y >> 16);
+    } else {
+#pragma unroll
+        for (int k = 0; k < kLane; k += 2) {
+            const int e = lane_element<false>(k, lane), f = lane_element<false>(k + 1, lane);
+            c[k / 2] = (uint16_t)((e < left ? src[e] : 0) | (f < left ? src[f] : 0) << 8);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kLane; k += 2) {
+        const float2 v = from_codes(c[k / 2]);
+        x[k] = v.x;
+        x[k + 1] = v.y;
+    }
+}
+template <bool VEC>
+__device__ __forceinline__ void store_codes(const float (&x)[kLane], uint8_t *dst, int lane, int left)
+{
+    uint16_t c[kLane / 2];
+#pragma unroll
+    for (int k = 0; k < kLane; k += 2) c[k / 2] = to_codes(x[k], x[k + 1]);
+    if (VEC) {
+        *reinterpret_cast<uint2 *>(dst + lane * kLane) =
+            make_uint2((uint32_t)c[0] | (uint32_t)c[1] << 16, (uint32_t)c[2] | (uint32_t)c[3] << 16);
+    } else {
+#pragma unroll
+        for (int k = 0; k < kLane; ++k) {
+            const int e = lane_element<false>(k, lane);
+            if (e < left) dst[e] = (uint8_t)(c[k / 2] >> (k & 1 ? 8 : 0));
+        }
+    }
+}
+
+__device__ __forceinline__ uint32_t warp_max(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
+
+template <class P, class G, bool MASTER, bool VEC, int CAP>
+__device__ __forceinline__ void adamw8_block(const Adam8Args<CAP> &a, float scale, int t, int64_t b, int lane, int left)
+{
+    const int64_t at = b * kBlock;
+    P *p = static_cast<P *>(a.p[t]) + at;
+    const G *g = static_cast<const G *>(a.g[t]) + at;
+    uint8_t *mc = a.m[t] + at, *rc = a.r[t] + at;
+    float *master = MASTER ? a.w[t] + at : nullptr;
+
+    float w[kLane], gr[kLane], m[kLane], r[kLane];
+    if (MASTER) load_lane<float, VEC>(w, master, lane, left);
+    else load_lane<P, VEC>(w, p, lane, left);
+    load_lane<G, VEC>(gr, g, lane, left);
+    load_codes<VEC>(m, mc, lane, left);
+    load_codes<VEC>(r, rc, lane, left);
+    const float ms = a.ms[t][b], rs = a.rs[t][b];
+    uint32_t mtop = 0, rtop = 0;
+#pragma unroll
+    for (int k = 0; k < kLane; ++k) {
+        m[k] = __fmul_rn(m[k], ms);
+        const float root = __fmul_rn(r[k], rs);
+        float v = __fmul_rn(root, root);
+        w[k] = adam_element(a.h, scale, w[k], gr[k], m[k], v, r[k]);
+        mtop = max(mtop, __float_as_uint(m[k]) & 0x7FFFFFFFu);
+        rtop = max(rtop, __float_as_uint(r[k]) & 0x7FFFFFFFu);
+    }
+    if (MASTER) store_lane<float, VEC>(w, master, lane, left);
+    store_lane<P, VEC>(w, p, lane, left);
+
+    mtop = warp_max(mtop);
+    rtop = warp_max(rtop);
+    const bool mfine = mtop < 0x7F800000u, rfine = rtop < 0x7F800000u;
+    const int me = scale_exponent(mtop), re = scale_exponent(rtop);
+    const float minv = mfine ? exp2_int(-me) : 0.0f, rinv = rfine ? exp2_int(-re) : 0.0f;
+    const uint32_t key = mix32(a.seed + (a.first + (uint32_t)t + 1u) * 0x9E3779B9u);
+#pragma unroll
+    for (int k = 0; k < kLane; ++k) {
+        uint32_t u = (uint32_t)(at + lane_element<VEC>(k, lane)) * 0x9E3779B1u + key;
+        u ^= u >> 16;
+        u *= 0x7FEB352Du;
+        u ^= u >> 15;
+        const float mt = round_to_code(fabsf(__fmul_rn(m[k], minv)), u & 0xFFFFu);
+        m[k] = mfine ? copysignf(mt, m[k]) : 0.0f;
+        float rt = __fmul_rn(r[k], rinv);
+        if (r[k] > 0.0f) rt = fmaxf(rt, 0x1p-9f);
+        r[k] = rfine ? round_to_code(rt, u >> 16) : 0.0f;
+    }
+    store_codes<VEC>(m, mc, lane, left);
+    store_codes<VEC>(r, rc, lane, left);
+    if (lane == 0) {
+        const float nan = __int_as_float(0x7fc00000);
+        a.ms[t][b] = mfine ? exp2_int(me) : nan;
+        a.rs[t][b] = rfine ? exp2_int(re) : nan;
+    }
+}
+
+template <class P, class G, bool MASTER, int CAP>
+__global__ void __launch_bounds__(kThreads) adamw8_kernel(const __grid_constant__ Adam8Args<CAP> a)
+{
+    stream_order();
+    const float scale = a.h.scale ? *a.h.scale : 1.0f;
+    if (scale != scale) return;
+    const int lane = threadIdx.x & 31;
+    const int64_t total = a.list.start[a.list.count];
+    const int64_t step = (int64_t)gridDim.x * (kThreads / 32);
+    for (int64_t chunk = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); chunk < total; chunk += step) {
+        const int t = a.list.find(chunk);
+        const int64_t b = chunk - a.list.start[t], left = a.list.size[t] - b * kBlock;
+        if (a.list.head[t] == 0 && left >= kBlock) adamw8_block<P, G, MASTER, true>(a, scale, t, b, lane, kBlock);
+        else adamw8_block<P, G, MASTER, false>(a, scale, t, b, lane, left < kBlock ? (int)left : kBlock);
+    }
+}
+
+// ---------------------------------------------------------------- host side
+// A span of device memory of one argument; written ones may touch nothing.
+struct Span {
+    uintptr_t lo, hi;
+    bool written;
+};
+struct Spans {
+    std::vector<Span> all;
+    void add(const void *p, int64_t bytes, bool written)
+    {
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+        if (p && bytes > 0) all.push_back(Span{lo, lo + (uintptr_t)bytes, written});
+    }
+    bool touch()
+    {
+        auto before = [](const Span &x, const Span &y) { return x.lo < y.lo; };
+        if (!std::is_sorted(all.begin(), all.end(), before)) std::sort(all.begin(), all.end(), before);
+        uintptr_t any = 0, written = 0;
+        for (const Span &s : all) {
+            if (s.lo < written || (s.written && s.lo < any)) return true;
+            any = std::max(any, s.hi);
+            if (s.written) written = std::max(written, s.hi);
+        }
+        return false;
+    }
+};
+
+rr_status check_list(const int64_t *sizes, int count)
+{
+    if (count < 0) return step_fail(RR_ERR_INVALID_ARG, "num_tensors %d", count);
+    if (count > 0 && !sizes) return step_fail(RR_ERR_INVALID_ARG, "sizes is NULL");
+    for (int i = 0; i < count; ++i)
+        if (sizes[i] < 0 || sizes[i] > kMaxSize)
+            return step_fail(RR_ERR_INVALID_ARG, "sizes[%d] is %lld", i, (long long)sizes[i]);
+    return RR_OK;
+}
+rr_status check_pointers(const char *name, const void *const *p, const int64_t *sizes, int count, int bytes)
+{
+    if (count > 0 && !p) return step_fail(RR_ERR_INVALID_ARG, "%s is NULL", name);
+    for (int i = 0; i < count; ++i) {
+        if (sizes[i] == 0) continue;
+        if (!p[i]) return step_fail(RR_ERR_INVALID_ARG, "%s[%d] is NULL", name, i);
+        if (!aligned_to(p[i], bytes))
+            return step_fail(RR_ERR_ALIGNMENT, "%s[%d] not aligned to its %d-byte element", name, i, bytes);
+    }
+    return RR_OK;
+}
+template <class T>
+const void *const *plain(T *const *p) { return reinterpret_cast<const void *const *>(p); }
+
+// Elements before p's first `unit`-element boundary.
+int elements_before(const void *p, int bytes, int unit)
+{
+    const int past = (int)(reinterpret_cast<uintptr_t>(p) % (uintptr_t)(bytes * unit));
+    return past == 0 ? 0 : (bytes * unit - past) / bytes;
+}
+
+rr_status check_hyper(const rr_adamw_hyper *h)
+{
+    if (!h) return step_fail(RR_ERR_INVALID_ARG, "hyper is NULL");
+    if (!(h->beta1 >= 0.0 && h->beta1 < 1.0)) return step_fail(RR_ERR_INVALID_ARG, "beta1 %g", h->beta1);
+    if (!(h->beta2 >= 0.0 && h->beta2 < 1.0)) return step_fail(RR_ERR_INVALID_ARG, "beta2 %g", h->beta2);
+    if (!(h->lr >= 0.0)) return step_fail(RR_ERR_INVALID_ARG, "lr %g", h->lr);
+    if (!(h->eps >= 0.0)) return step_fail(RR_ERR_INVALID_ARG, "eps %g", h->eps);
+    if (!(h->weight_decay >= 0.0)) return step_fail(RR_ERR_INVALID_ARG, "weight_decay %g", h->weight_decay);
+    if (h->step < 1) return step_fail(RR_ERR_INVALID_ARG, "step %lld: steps count from 1", (long long)h->step);
+    return RR_OK;
+}
+AdamScalars scalars(const rr_adamw_hyper &h, const float *scale)
+{
+    AdamScalars s;
+    s.beta1 = (float)h.beta1;
+    s.omb1 = (float)(1.0 - h.beta1);
+    s.beta2 = (float)h.beta2;
+    s.omb2 = (float)(1.0 - h.beta2);
+    s.decay = (float)(1.0 - h.lr * h.weight_decay);
+    s.inv_c2 = (float)(1.0 / std::sqrt(1.0 - std::pow(h.beta2, (double)h.step)));
+    s.step_size = (float)(h.lr / (1.0 - std::pow(h.beta1, (double)h.step)));
+    s.eps = (float)h.eps;
+    s.scale = scale;
+    return s;
+}
+
+int64_t chunks_of(int64_t size, int head, int64_t chunk)
+{
+    if (size == 0) return 0;
+    const int64_t body = size - (head > 0 ? head : 0);
+    return body <= 0 ? 1 : (body + chunk - 1) / chunk;
+}
+
+// Blocks that fit an SM for these kernels (256 threads, no shared memory to
+// speak of), by registers: the grid is at most this many waves' worth of one.
+constexpr int kNormPerSm = 8, kAdamPerSm = 4, kAdam8PerSm = 4;
+
+template <class T, int CAP>
+rr_status launch_norm(GradNormArgs<CAP> &a, int64_t grid, cudaStream_t stream)
+{
+    return step_launch((const void *)grad_norm_kernel<T, CAP>, grid, kThreads, 0, &a, stream);
+}
+
+template <int CAP>
+rr_status norm_lists(const void *const *grads, const int64_t *sizes, int count, rr_dtype dtype, int sms, double *part,
+                     int64_t *parts, cudaStream_t stream)
+{
+    const int eb = float_bytes(dtype), E = 16 / eb;
+    const int64_t chunk = (int64_t)kThreads * E * kNormUnroll;
+    GradNormArgs<CAP> a;
+    for (int i = 0; i < count;) {
+        int k = 0;
+        a.list.start[0] = 0;
+        for (; i < count && k < CAP; ++i) {
+            if (sizes[i] == 0) continue;
+            a.g[k] = grads[i];
+            a.list.size[k] = sizes[i];
+            a.list.head[k] = (int8_t)elements_before(grads[i], eb, E);
+            a.list.start[k + 1] = a.list.start[k] + chunks_of(sizes[i], a.list.head[k], chunk);
+            ++k;
+        }
+        if (k == 0) break;
+        a.list.count = k;
+        const int64_t most = std::min<int64_t>((int64_t)kNormPerSm * sms, kNormBlocks);
+        const int64_t grid = std::min(a.list.start[k], most);
+        a.part = part + *parts;
+        *parts += grid;
+        RR_TRY(dtype == RR_FP32 ? launch_norm<float>(a, grid, stream)
+               : dtype == RR_BF16 ? launch_norm<__nv_bfloat16>(a, grid, stream) : launch_norm<__half>(a, grid, stream));
+    }
+    return RR_OK;
+}
+
+// Kernels by parameter type, gradient type and master weights.
+template <class P, class G, int CAP>
+const void *adamw_fn(bool master)
+{
+    return master ? (const void *)adamw_kernel<P, G, true, CAP> : (const void *)adamw_kernel<P, G, false, CAP>;
+}
+template <class P, class G, int CAP>
+const void *adamw8_fn(bool master)
+{
+    return master ? (const void *)adamw8_kernel<P, G, true, CAP> : (const void *)adamw8_kernel<P, G, false, CAP>;
+}
+#define RR_BY_TYPES(fn)                                                                                    \
+    template <class P, int CAP>                                                                            \
+    const void *fn##_for(rr_dtype g, bool master)                                                          \
+    {                                                                                                      \
+        return g == RR_FP32   ? fn<P, float, CAP>(master)                                                  \
+               : g == RR_BF16 ? fn<P, __nv_bfloat16, CAP>(master) : fn<P, __half, CAP>(master);            \
+    }                                                                                                      \
+    template <int CAP>                                                                                     \
+    const void *fn##_for(rr_dtype p, rr_dtype g, bool master)                                              \
+    {                                                                                                      \
+        return p == RR_FP32   ? fn##_for<float, CAP>(g, master)                                            \
+               : p == RR_BF16 ? fn##_for<__nv_bfloat16, CAP>(g, master) : fn##_for<__half, CAP>(g, master); \
+    }
+RR_BY_TYPES(adamw_fn)
+RR_BY_TYPES(adamw8_fn)
+#undef RR_BY_TYPES
+
+template <int CAP>
+rr_status adamw_lists(void *const *params, const void *const *grads, float *const *m, float *const *v,
+                      float *const *master, const int64_t *sizes, int count, rr_dtype pd, rr_dtype gd,
+                      const AdamScalars &h, int sms, cudaStream_t stream)
+{
+    const int pb = float_bytes(pd), gb = float_bytes(gd);
+    AdamArgs<CAP> a;
+    a.h = h;
+    for (int i = 0; i < count;) {
+        int k = 0;
+        a.list.start[0] = 0;
+        for (; i < count && k < CAP; ++i) {
+            if (sizes[i] == 0) continue;
+            a.p[k] = params[i];
+            a.g[k] = grads[i];
+            a.m[k] = m[i];
+            a.v[k] = v[i];
+            a.w[k] = master ? master[i] : nullptr;
+            const int head = elements_before(params[i], pb, kUnit);
+            const bool together = elements_before(grads[i], gb, kUnit) == head && elements_before(m[i], 4, kUnit) == head &&
+                                  elements_before(v[i], 4, kUnit) == head &&
+                                  (!master || elements_before(master[i], 4, kUnit) == head);
+            a.list.head[k] = (int8_t)(together ? head : kNoVector);
+            a.list.size[k] = sizes[i];
+            a.list.start[k + 1] = a.list.start[k] + chunks_of(sizes[i], a.list.head[k], kAdamChunk);
+            ++k;
+        }
+        if (k == 0) break;
+        a.list.count = k;
+        const int64_t grid = std::min<int64_t>(a.list.start[k], (int64_t)kAdamPerSm * sms);
+        RR_TRY(step_launch(adamw_fn_for<CAP>(pd, gd, master != nullptr), grid, kThreads, 0, &a, stream));
+    }
+    return RR_OK;
+}
+
+template <int CAP>
+rr_status adamw8_lists(void *const *params, const void *const *grads, uint8_t *const *m, float *const *ms,
+                       uint8_t *const *r, float *const *rs, float *const *master, const int64_t *sizes, int count,
+                       rr_dtype pd, rr_dtype gd, const AdamScalars &h, uint32_t seed, int sms, cudaStream_t stream)
+{
+    Adam8Args<CAP> a;
+    a.h = h;
+    a.seed = seed;
+    // Tensors keep their place in the caller's list (it enters the random
+    // bits), so empty ones stay in the table with no chunks.
+    for (int i = 0; i < count;) {
+        int k = 0;
+        a.first = (uint32_t)i;
+        a.list.start[0] = 0;
+        for (; i < count && k < CAP; ++i, ++k) {
+            a.p[k] = params[i];
+            a.g[k] = grads[i];
+            a.m[k] = m[i];
+            a.ms[k] = ms[i];
+            a.r[k] = r[i];
+            a.rs[k] = rs[i];
+            a.w[k] = master ? master[i] : nullptr;
+            a.list.head[k] = (int8_t)(aligned_to(params[i], 16) && aligned_to(grads[i], 16) && aligned_to(m[i], 8) &&
+                                              aligned_to(r[i], 8) && (!master || aligned_to(master[i], 16))
+                                          ? 0 : kNoVector);
+            a.list.size[k] = sizes[i];
+            a.list.start[k + 1] = a.list.start[k] + (sizes[i] + kBlock - 1) / kBlock;
+        }
+        a.list.count = k;
+        if (a.list.start[k] == 0) continue;
+        const int64_t want = (a.list.start[k] + kThreads / 32 - 1) / (kThreads / 32);
+        const int64_t grid = std::min<int64_t>(want, (int64_t)kAdam8PerSm * sms);
+        RR_TRY(step_launch(adamw8_fn_for<CAP>(pd, gd, master != nullptr), grid, kThreads, 0, &a, stream));
+    }
+    return RR_OK;
+}
+
+int64_t norm_launches(int count) { return count <= kNormCap ? 1 : (count + kNormCap - 1) / kNormCap; }
+
+rr_status check_types(rr_dtype pd, rr_dtype gd)
+{
+    if (!float_bytes(pd)) return step_fail(RR_ERR_UNSUPPORTED_DTYPE, "param_dtype %d", (int)pd);
+    if (!float_bytes(gd)) return step_fail(RR_ERR_UNSUPPORTED_DTYPE, "grad_dtype %d", (int)gd);
+    return RR_OK;
+}
+
+bool nothing_to_do(const int64_t *sizes, int count)
+{
+    for (int i = 0; i < count; ++i)
+        if (sizes[i] > 0) return false;
+    return true;
+}
+
+}  // namespace
+
+}  // namespace rr
+
+using namespace rr;
+
+extern "C" rr_status rr_grad_norm_workspace(int num_tensors, size_t *bytes)
+{
+    if (!bytes) return step_fail(RR_ERR_INVALID_ARG, "bytes is NULL");
+    if (num_tensors < 0) return step_fail(RR_ERR_INVALID_ARG, "num_tensors %d", num_tensors);
+    *bytes = (size_t)(norm_launches(num_tensors) * kNormBlocks) * sizeof(double);
+    return step_ok();
+}
+
+extern "C" rr_status rr_grad_norm(const void *const *grads, const int64_t *sizes, int num_tensors, rr_dtype dtype,
+                                  float inv_scale, float max_norm, float *norm, float *scale, void *workspace,
+                                  size_t workspace_bytes, cudaStream_t stream)
+{
+    if (!float_bytes(dtype)) return step_fail(RR_ERR_UNSUPPORTED_DTYPE, "dtype %d", (int)dtype);
+    RR_TRY(check_list(sizes, num_tensors));
+    if (!(inv_scale > 0.0f && std::isfinite(inv_scale))) return step_fail(RR_ERR_INVALID_ARG, "inv_scale %g", (double)inv_scale);
+    if (!(max_norm >= 0.0f)) return step_fail(RR_ERR_INVALID_ARG, "max_norm %g", (double)max_norm);
+    if (!norm && !scale) return step_fail(RR_ERR_INVALID_ARG, "norm and scale are both NULL");
+    RR_TRY(check_pointers("grads", grads, sizes, num_tensors, float_bytes(dtype)));
+    if (!aligned_to(norm, 4)) return step_fail(RR_ERR_ALIGNMENT, "norm not 4-byte aligned");
+    if (!aligned_to(scale, 4)) return step_fail(RR_ERR_ALIGNMENT, "scale not 4-byte aligned");
+    if (!workspace) return step_fail(RR_ERR_INVALID_ARG, "workspace is NULL");
+    if (!aligned_to(workspace, 16)) return step_fail(RR_ERR_ALIGNMENT, "workspace not 16-byte aligned");
+    size_t need = 0;
+    RR_TRY(rr_grad_norm_workspace(num_tensors, &need));
+    if (workspace_bytes < need)
+        return step_fail(RR_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+    static thread_local Spans spans;
+    spans.all.clear();
+    for (int i = 0; i < num_tensors; ++i) spans.add(grads[i], sizes[i] * float_bytes(dtype), false);
+    spans.add(workspace, (int64_t)need, true);
+    spans.add(norm, 4, true);
+    spans.add(scale, 4, true);
+    if (spans.touch()) return step_fail(RR_ERR_ALIAS, "norm, scale or workspace overlaps another argument");
+
+    int sms = 0;
+    RR_TRY(step_sms(&sms));
+    double *part = static_cast<double *>(workspace);
+    int64_t parts = 0;
+    RR_TRY(num_tensors <= kNormCapSmall ? norm_lists<kNormCapSmall>(grads, sizes, num_tensors, dtype, sms, part, &parts, stream)
+                                        : norm_lists<kNormCap>(grads, sizes, num_tensors, dtype, sms, part, &parts, stream));
+    GradNormEndArgs e{part, parts, inv_scale, max_norm, norm, scale};
+    RR_TRY(step_launch((const void *)grad_norm_end_kernel, 1, kThreads, 0, &e, stream));
+    return step_ok();
+}
+
+extern "C" rr_status rr_adamw(void *const *params, const void *const *grads, float *const *exp_avg,
+                              float *const *exp_avg_sq, float *const *master, const int64_t *sizes,
+                              int num_tensors, rr_dtype param_dtype, rr_dtype grad_dtype,
+                              const rr_adamw_hyper *hyper, const float *grad_scale, cudaStream_t stream)
+{
+    RR_TRY(check_types(param_dtype, grad_dtype));
+    RR_TRY(check_list(sizes, num_tensors));
+    RR_TRY(check_hyper(hyper));
+    const int pb = float_bytes(param_dtype), gb = float_bytes(grad_dtype);
+    RR_TRY(check_pointers("params", plain(params), sizes, num_tensors, pb));
+    RR_TRY(check_pointers("grads", grads, sizes, num_tensors, gb));
+    RR_TRY(check_pointers("exp_avg", plain(exp_avg), sizes, num_tensors, 4));
+    RR_TRY(check_pointers("exp_avg_sq", plain(exp_avg_sq), sizes, num_tensors, 4));
+    if (master) RR_TRY(check_pointers("master", plain(master), sizes, num_tensors, 4));
+    if (!aligned_to(grad_scale, 4)) return step_fail(RR_ERR_ALIGNMENT, "grad_scale not 4-byte aligned");
+    static thread_local Spans spans;
+    spans.all.clear();
+    for (int i = 0; i < num_tensors; ++i) spans.add(params[i], sizes[i] * pb, true);
+    for (int i = 0; i < num_tensors; ++i) spans.add(grads[i], sizes[i] * gb, false);
+    for (int i = 0; i < num_tensors; ++i) spans.add(exp_avg[i], sizes[i] * 4, true);
+    for (int i = 0; i < num_tensors; ++i) spans.add(exp_avg_sq[i], sizes[i] * 4, true);
+    for (int i = 0; master && i < num_tensors; ++i) spans.add(master[i], sizes[i] * 4, true);
+    spans.add(grad_scale, 4, false);
+    if (spans.touch()) return step_fail(RR_ERR_ALIAS, "a parameter, state or master weight overlaps another argument");
+    if (nothing_to_do(sizes, num_tensors)) return step_ok();
+
+    int sms = 0;
+    RR_TRY(step_sms(&sms));
+    const AdamScalars h = scalars(*hyper, grad_scale);
+    RR_TRY(num_tensors <= kAdamCapSmall
+               ? adamw_lists<kAdamCapSmall>(params, grads, exp_avg, exp_avg_sq, master, sizes, num_tensors, param_dtype,
+                                            grad_dtype, h, sms, stream)
+               : adamw_lists<kAdamCap>(params, grads, exp_avg, exp_avg_sq, master, sizes, num_tensors, param_dtype,
+                                       grad_dtype, h, sms, stream));
+    return step_ok();
+}
+
+extern "C" rr_status rr_adamw8(void *const *params, const void *const *grads, uint8_t *const *exp_avg,
+                               float *const *exp_avg_scale, uint8_t *const *exp_avg_sq,
+                               float *const *exp_avg_sq_scale, float *const *master, const int64_t *sizes,
+                               int num_tensors, rr_dtype param_dtype, rr_dtype grad_dtype,
+                               const rr_adamw_hyper *hyper, uint32_t seed, const float *grad_scale,
+                               cudaStream_t stream)
+{
+    RR_TRY(check_types(param_dtype, grad_dtype));
+    RR_TRY(check_list(sizes, num_tensors));
+    RR_TRY(check_hyper(hyper));
+    const int pb = float_bytes(param_dtype), gb = float_bytes(grad_dtype);
+    RR_TRY(check_pointers("params", plain(params), sizes, num_tensors, pb));
+    RR_TRY(check_pointers("grads", grads, sizes, num_tensors, gb));
+    RR_TRY(check_pointers("exp_avg", plain(exp_avg), sizes, num_tensors, 1));
+    RR_TRY(check_pointers("exp_avg_scale", plain(exp_avg_scale), sizes, num_tensors, 4));
+    RR_TRY(check_pointers("exp_avg_sq", plain(exp_avg_sq), sizes, num_tensors, 1));
+    RR_TRY(check_pointers("exp_avg_sq_scale", plain(exp_avg_sq_scale), sizes, num_tensors, 4));
+    if (master) RR_TRY(check_pointers("master", plain(master), sizes, num_tensors, 4));
+    if (!aligned_to(grad_scale, 4)) return step_fail(RR_ERR_ALIGNMENT, "grad_scale not 4-byte aligned");
+    static thread_local Spans spans;
+    spans.all.clear();
+    auto blocks = [](int64_t n) { return (n + kBlock - 1) / kBlock; };
+    for (int i = 0; i < num_tensors; ++i) spans.add(params[i], sizes[i] * pb, true);
+    for (int i = 0; i < num_tensors; ++i) spans.add(grads[i], sizes[i] * gb, false);
+    for (int i = 0; i < num_tensors; ++i) spans.add(exp_avg[i], sizes[i], true);
+    for (int i = 0; i < num_tensors; ++i) spans.add(exp_avg_scale[i], blocks(sizes[i]) * 4, true);
+    for (int i = 0; i < num_tensors; ++i) spans.add(exp_avg_sq[i], sizes[i], true);
+    for (int i = 0; i < num_tensors; ++i) spans.add(exp_avg_sq_scale[i], blocks(sizes[i]) * 4, true);
+    for (int i = 0; master && i < num_tensors; ++i) spans.add(master[i], sizes[i] * 4, true);
+    spans.add(grad_scale, 4, false);
+    if (spans.touch()) return step_fail(RR_ERR_ALIAS, "a parameter, state or master weight overlaps another argument");
+    if (nothing_to_do(sizes, num_tensors)) return step_ok();
+
+    int sms = 0;
+    RR_TRY(step_sms(&sms));
+    const AdamScalars h = scalars(*hyper, grad_scale);
+    RR_TRY(num_tensors <= kAdamCapSmall
+               ? adamw8_lists<kAdamCapSmall>(params, grads, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale, master,
+                                             sizes, num_tensors, param_dtype, grad_dtype, h, seed, sms, stream)
+               : adamw8_lists<kAdamCap>(params, grads, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale, master,
+                                        sizes, num_tensors, param_dtype, grad_dtype, h, seed, sms, stream));
+    return step_ok();
+}

@@ -1,0 +1,83 @@
+// Shared by the training-step operators (rr_layer_norm.cu, rr_optim.cu):
+// errors, launches, element loads and reductions.  Not part of the public ABI.
+#pragma once
+
+#include <cstdint>
+#include <cstring>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "rr.h"
+
+namespace rr {
+
+// ---------------------------------------------------------------- host side
+// The calling thread's rr_last_error (rr_api.cu).
+rr_status step_fail(rr_status s, const char *fmt, ...);
+rr_status step_cuda_fail(cudaError_t e, const char *what);
+rr_status step_ok();
+
+inline int float_bytes(rr_dtype d) { return d == RR_FP32 ? 4 : d == RR_BF16 || d == RR_FP16 ? 2 : 0; }
+inline bool aligned_to(const void *p, int bytes) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)bytes == 0; }
+
+// SMs of the current device.
+rr_status step_sms(int *sms);
+
+// One programmatic launch: the grid may start while the previous kernel in
+// the stream drains; every kernel here begins with stream_order().
+rr_status step_launch(const void *fn, int64_t grid, int threads, int smem, void *args, cudaStream_t stream);
+
+#if defined(__CUDACC__)
+// ---------------------------------------------------------------- device side
+// Wait for the previous grid in the stream (its writes are visible after
+// this), then let the next one be scheduled early.  Every thread of every
+// kernel calls it before it touches memory or exits.
+__device__ __forceinline__ void stream_order()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <class T>
+__device__ __forceinline__ T from_f32(float x);
+template <>
+__device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// One element of a float type known only at run time.
+__device__ __forceinline__ float load_any(const void *p, int64_t i, int dtype)
+{
+    if (dtype == RR_FP32) return static_cast<const float *>(p)[i];
+    if (dtype == RR_BF16) return to_f32(static_cast<const __nv_bfloat16 *>(p)[i]);
+    return to_f32(static_cast<const __half *>(p)[i]);
+}
+__device__ __forceinline__ void store_any(void *p, int64_t i, int dtype, float x)
+{
+    if (dtype == RR_FP32) static_cast<float *>(p)[i] = x;
+    else if (dtype == RR_BF16) static_cast<__nv_bfloat16 *>(p)[i] = from_f32<__nv_bfloat16>(x);
+    else static_cast<__half *>(p)[i] = from_f32<__half>(x);
+}
+
+// N consecutive elements at an address aligned to their N * sizeof(T) bytes
+// (4, 8 or 16 bytes at a time).
+template <class T, int N>
+struct alignas(N * sizeof(T) > 16 ? 16 : N * sizeof(T)) Pack {
+    T v[N];
+};
+
+__device__ __forceinline__ float warp_sum(float x)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+#endif
+
+}  // namespace rr

@@ -395,6 +395,166 @@ rr_status rr_allreduce_oneshot_noalloc(const void *const *inputs, void *const *r
  */
 rr_status rr_allreduce_oneshot_noalloc_status(cudaStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The local half of a data-parallel training step: the operators between the
+ * collectives above.  A layer norm makes activations and, backwards, the
+ * gradients that an allreduce sums; the gradient norm and the AdamW step
+ * consume them on each rank's shard before an allgather hands the new weights
+ * out (examples/sharded_step.py runs the whole chain).
+ *
+ * They keep the conventions above except where stated here:
+ *  - They run no barrier and need no signal pad.  Each is one to three kernel
+ *    launches on `stream`, none cooperative, all programmatic; any number of
+ *    streams may run them at once.  Calls allocate nothing and may be captured
+ *    in a CUDA graph; scalars (learning rate, step number, ...) are then the
+ *    captured ones on every replay.
+ *  - Device pointers need only their element's alignment (RR_ERR_ALIGNMENT
+ *    otherwise): 4 bytes for binary32, 2 for bf16 and fp16, 1 for 8-bit codes.
+ *    16-byte aligned rows and tensors run faster.  Workspaces are 16-byte
+ *    aligned.
+ *  - A workspace is device memory of the caller's, at least as large as the
+ *    matching rr_..._workspace function says.  Its content before a call does
+ *    not matter and after it means nothing; two calls that may overlap on the
+ *    device need one each.
+ *  - Types are RR_BF16, RR_FP16 and RR_FP32 (RR_ERR_UNSUPPORTED_DTYPE for
+ *    RR_INT32).  Arithmetic, sums and statistics are in binary32 or more, with
+ *    one rounding to the element type at the end.
+ *  - Results do not depend on timing: every sum has a fixed order on a given
+ *    GPU model (no atomics).  NaN and infinities propagate as in the formulas.
+ * No passage on the pages covers these operators.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * rr_layer_norm -- y = (x - mean) * rstd * weight + bias over each row, with
+ * mean = sum(x) / cols, rstd = 1 / sqrt(sum((x - mean)^2) / cols + eps) (the
+ * squares are of centred values, not sum(x^2) - mean^2).
+ *
+ * x, y:      rows of `cols` elements of `dtype`, x_stride / y_stride elements
+ *            apart.  y == x with equal strides normalises in place; any other
+ *            overlap is RR_ERR_ALIAS, except slices of one buffer whose rows
+ *            interleave without touching (equal strides).
+ * weight, bias: `cols` elements of weight_dtype, or NULL (ones / zeros).
+ * mean, rstd: one binary32 each per row for the backward, or NULL.
+ * rows >= 0 (0 returns RR_OK without a launch), cols >= 1.  x_stride >= 0 (0
+ * reads one row again and again), y_stride >= cols.
+ */
+rr_status rr_layer_norm(const void *x, const void *weight, const void *bias, void *y, float *mean,
+                        float *rstd, int64_t rows, int64_t cols, int64_t x_stride, int64_t y_stride,
+                        float eps, rr_dtype dtype, rr_dtype weight_dtype, cudaStream_t stream);
+
+/*
+ * rr_layer_norm_backward -- the gradients of rr_layer_norm from dy, x and the
+ * forward's mean and rstd.  With xhat = (x - mean) * rstd:
+ *   dx      = rstd * (w dy - sum(w dy) / cols - xhat * sum(w dy xhat) / cols)
+ *   dweight = sum over rows of dy * xhat,  dbias = sum over rows of dy.
+ *
+ * dx, dweight, dbias: each may be NULL (not computed), not all three.  dweight
+ * and dbias hold `cols` elements of weight_dtype and are overwritten; with
+ * rows == 0 they become zeros.  weight may be NULL (ones).
+ * dx == dy or dx == x with equal strides works in place.  Strides as in
+ * rr_layer_norm (dy_stride 0: one row of gradients for every row).
+ * workspace: see rr_layer_norm_backward_workspace.
+ */
+rr_status rr_layer_norm_backward(const void *dy, const void *x, const void *weight, const float *mean,
+                                 const float *rstd, void *dx, void *dweight, void *dbias, int64_t rows,
+                                 int64_t cols, int64_t dy_stride, int64_t x_stride, int64_t dx_stride,
+                                 rr_dtype dtype, rr_dtype weight_dtype, void *workspace,
+                                 size_t workspace_bytes, cudaStream_t stream);
+
+/* Bytes of workspace rr_layer_norm_backward needs for this many rows and cols. */
+rr_status rr_layer_norm_backward_workspace(int64_t rows, int64_t cols, size_t *bytes);
+
+/*
+ * rr_grad_norm -- the Euclidean norm over a list of gradient tensors and the
+ * factor that clips it:
+ *   *norm  = inv_scale * sqrt(sum of g^2 over all tensors)
+ *   *scale = inv_scale * min(1, max_norm / (*norm + 1e-6)),
+ *            or NaN when *norm is not finite.
+ * inv_scale takes a loss scale or a sum over ranks out of the gradients (1 /
+ * scale, 1 / W); max_norm = INFINITY clips nothing.  Values whose squares
+ * leave binary32's range do not overflow or vanish: the sum is held in binary64.
+ *
+ * grads: HOST array of num_tensors (>= 0) device pointers; tensor i holds
+ * sizes[i] >= 0 elements of dtype (NULL allowed where sizes[i] is 0).  The
+ * host arrays are read during the call only.
+ * norm, scale: device binary32 words; either may be NULL, not both.
+ */
+rr_status rr_grad_norm(const void *const *grads, const int64_t *sizes, int num_tensors, rr_dtype dtype,
+                       float inv_scale, float max_norm, float *norm, float *scale, void *workspace,
+                       size_t workspace_bytes, cudaStream_t stream);
+
+/* Bytes of workspace rr_grad_norm needs for a list of this length. */
+rr_status rr_grad_norm_workspace(int num_tensors, size_t *bytes);
+
+/* Scalars of an AdamW step.  step counts from 1. */
+typedef struct {
+    double lr, beta1, beta2, eps, weight_decay;
+    int64_t step;
+} rr_adamw_hyper;
+
+/*
+ * rr_adamw -- one AdamW step over a list of tensors, in place.  For each
+ * element, with g = grad * (*grad_scale) (or grad where grad_scale is NULL)
+ * and w the master weight if there is one, else the parameter:
+ *   m = beta1 * m + (1 - beta1) * g
+ *   v = beta2 * v + (1 - beta2) * g^2
+ *   w = (1 - lr * weight_decay) * w
+ *       - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * and param = w rounded once to param_dtype.
+ *
+ * grad_scale: device binary32 word (rr_grad_norm's scale), or NULL.  When it
+ * holds NaN the step is skipped: nothing is written, so a step whose gradients
+ * are not finite costs no state.  Without it NaN gradients reach the states.
+ * params, grads: HOST arrays of num_tensors device pointers; exp_avg and
+ * exp_avg_sq: the states m and v, binary32; master: binary32 master weights,
+ * or NULL for none (the whole array).  Tensor i holds sizes[i] >= 0 elements
+ * (pointers may be NULL where it is 0).  Nothing written may overlap anything
+ * else (RR_ERR_ALIAS).  Lists of any length; a call is one launch for each 400
+ * tensors.
+ */
+rr_status rr_adamw(void *const *params, const void *const *grads, float *const *exp_avg,
+                   float *const *exp_avg_sq, float *const *master, const int64_t *sizes, int num_tensors,
+                   rr_dtype param_dtype, rr_dtype grad_dtype, const rr_adamw_hyper *hyper,
+                   const float *grad_scale, cudaStream_t stream);
+
+#define RR_ADAMW8_BLOCK 256 /* elements of an 8-bit state that share a scale */
+
+/*
+ * rr_adamw8 -- rr_adamw with the states held in 8 bits.
+ *
+ * exp_avg holds m and exp_avg_sq the square root of v, each as one 8-bit float
+ * per element (e4m3: 4 exponent bits, 3 mantissa bits, bias 7; 0x7F and 0xFF
+ * are NaN) and one binary32 scale for each RR_ADAMW8_BLOCK consecutive
+ * elements of a tensor, counted from its start (the last block may be short):
+ * value = code * scale.  Zero-filled codes and scales are the initial state.
+ * A step reads the states, computes as rr_adamw does in binary32, updates the
+ * weights from the unrounded states, and stores them as follows: scale is the
+ * power of two that brings the block's largest magnitude into [128, 256) (at
+ * least 2^-126, which a block of zeros has; NaN if the block holds a value that is not finite, which then
+ * reads back as NaN throughout), and |value| / scale is rounded to the code's
+ * grid up or down at random in proportion, so that slow averages, whose change
+ * in one step is far below the grid's spacing, still move on average.  A
+ * positive sqrt(v) is stored as no less than the smallest code (2^-9): a zero
+ * there would let m / (sqrt(v) + eps) explode.
+ *
+ * The random bits are a function of `seed` (pass another one each step), the
+ * tensor's index i in the list and the element's index k, modulo 2^32:
+ *   mix(x): x ^= x >> 16; x *= 0x7FEB352D; x ^= x >> 15; x *= 0x68E31DA5; x ^= x >> 16
+ *   h = k * 0x9E3779B1 + mix(seed + (i + 1) * 0x9E3779B9)
+ *   h ^= h >> 16; h *= 0x7FEB352D; h ^= h >> 15
+ * u = (h & 0xFFFF) for m, h >> 16 for sqrt(v); a value t = |value| / scale with
+ * grid spacing q (2^-9 below 2^-6) becomes floor(t / q + (u + 1/2) / 65536) * q.
+ *
+ * exp_avg_scale, exp_avg_sq_scale: HOST arrays of device pointers to
+ * ceil(sizes[i] / RR_ADAMW8_BLOCK) binary32 scales.  Other arguments as
+ * rr_adamw.
+ */
+rr_status rr_adamw8(void *const *params, const void *const *grads, uint8_t *const *exp_avg,
+                    float *const *exp_avg_scale, uint8_t *const *exp_avg_sq, float *const *exp_avg_sq_scale,
+                    float *const *master, const int64_t *sizes, int num_tensors, rr_dtype param_dtype,
+                    rr_dtype grad_dtype, const rr_adamw_hyper *hyper, uint32_t seed,
+                    const float *grad_scale, cudaStream_t stream);
+
 /* Name of a status code (static string). */
 const char *rr_status_string(rr_status s);
 
