@@ -7,7 +7,9 @@ torch dtypes; streams as integers, torch.cuda.Stream objects, or None for
 torch's current stream.  A non-zero rr_status raises RRError.  Nothing here
 computes: if librr.so is missing, every call raises.
 """
+import array
 import ctypes
+import operator
 import os
 import sys
 
@@ -52,13 +54,16 @@ class RRError(RuntimeError):
 
 
 _lib = None
+_tensor_class = None  # torch.Tensor, once torch has been imported by the caller
 _vp = ctypes.c_void_p
 _PP = ctypes.POINTER(ctypes.c_void_p)
 
 
 def lib():
     """Load librr.so (raises if it has not been built)."""
-    global _lib
+    global _lib, _tensor_class
+    if _tensor_class is None and "torch" in sys.modules:
+        _tensor_class = getattr(sys.modules["torch"], "Tensor", None)
     if _lib is None:
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(f"{LIB_PATH} is missing: build it with allgather_rr_allreduce_gb300.build.build()")
@@ -109,6 +114,8 @@ def _check(status):
 def _addr(x):
     if x is None:
         return 0
+    if x.__class__ is _tensor_class and x.is_cuda:
+        return x.data_ptr()
     if isinstance(x, int):
         return x
     if hasattr(x, "data_ptr"):
@@ -139,6 +146,8 @@ def dtype_code(dtype):
 def stream_handle(stream):
     if stream is None:
         import torch
+        if torch.cuda.is_initialized():  # the current stream without a Stream object
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -262,19 +271,27 @@ def rr_allgather_list(rank_bufs, output_lists, world_size, numel_per_rank, dtype
 
 
 # ---------------------------------------------------------------- training step
+_is_cuda, _data_ptr = operator.attrgetter("is_cuda"), operator.methodcaller("data_ptr")
+
+
 def _tensor_array(items, count, name):
     """pointer_array for a list of `count` tensors or addresses (None: no list)."""
     if items is None:
         return None
     if len(items) != count:
         raise ValueError(f"{name} has {len(items)} entries, sizes has {count}")
-    torch = sys.modules.get("torch")
-    plain = torch.Tensor if torch is not None else ()
-    return (_vp * count)(*[x.data_ptr() if x.__class__ is plain and x.is_cuda else _addr(x) for x in items])
+    if not count:
+        return (_vp * 0)()
+    try:  # CUDA tensors throughout, without a Python call for each
+        if all(map(_is_cuda, items)):
+            return (_vp * count).from_buffer(array.array("Q", map(_data_ptr, items)))
+    except AttributeError:
+        pass
+    return pointer_array(items)
 
 
 def _sizes(sizes):
-    return (ctypes.c_int64 * len(sizes))(*sizes)
+    return (ctypes.c_int64 * len(sizes)).from_buffer(array.array("q", sizes)) if len(sizes) else (ctypes.c_int64 * 0)()
 
 
 def rr_layer_norm(x, weight, bias, y, mean, rstd, rows, cols, x_stride, y_stride, eps, dtype, weight_dtype,

@@ -40,9 +40,10 @@ struct NormGradArgs {
     int P;
 };
 
-// One lane's EL elements of a row.  VEC: 16-byte vectors, vector v of the
-// lane at column ((v * G + g) * 32 + lane) * EN; else single elements, element
-// k at column (k * G + g) * 32 + lane.  Columns past the row read as zero.
+// One lane's EL elements of a row, in pairs.  VEC: 16-byte vectors, vector v
+// of the lane at column ((v * G + g) * 32 + lane) * EN; else single elements,
+// element k at column (k * G + g) * 32 + lane.  Columns past the row read as
+// zero and are not written.
 template <class T, int EL, bool VEC>
 struct Slice {
     static constexpr int EN = 16 / (int)sizeof(T);
@@ -73,8 +74,26 @@ struct Slice {
             }
         }
     }
-    __device__ __forceinline__ float at(int k) const { return to_f32(raw[k / EN].v[k % EN]); }
-    __device__ __forceinline__ void set(int k, float x) { raw[k / EN].v[k % EN] = from_f32<T>(x); }
+    // The same through a thread's own slots in shared memory (VEC only):
+    // slot v * threads of the stage.
+    static __device__ __forceinline__ void fetch(uint4 *slot, int threads, const T *row, int cols, int G, int g, int lane)
+    {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int c = col(v * EN, G, g, lane);
+            if (c < cols) fetch16(slot + v * threads, row + c);
+        }
+    }
+    __device__ __forceinline__ void take(const uint4 *slot, int threads, int cols, int G, int g, int lane)
+    {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const uint4 x = slot[v * threads];
+            *reinterpret_cast<uint4 *>(&raw[v]) = col(v * EN, G, g, lane) < cols ? x : make_uint4(0, 0, 0, 0);
+        }
+    }
+    __device__ __forceinline__ float2 pair(int k) const { return pair_f32(&raw[k / EN].v[k % EN]); }
+    __device__ __forceinline__ void set(int k, float2 x) { pair_set(&raw[k / EN].v[k % EN], x); }
     __device__ __forceinline__ void store(T *row, int cols, int G, int g, int lane) const
     {
 #pragma unroll
@@ -93,75 +112,124 @@ struct Slice {
     }
 };
 
+// A lane's pairs of a vector of weights as binary32.
+template <class S, int EL>
+__device__ __forceinline__ void load_weights(float2 (&w)[EL / 2], const void *p, int dtype, float absent, float past,
+                                             int cols, int G, int g, int lane)
+{
+#pragma unroll
+    for (int k = 0; k < EL; ++k) {
+        const int c = S::col(k, G, g, lane);
+        const float v = c < cols ? (p ? load_any(p, c, dtype) : absent) : past;
+        if (k & 1) w[k / 2].y = v;
+        else w[k / 2].x = v;
+    }
+}
+
+// Sum over a block's G warps of what lane i % (power of two >= G) holds for
+// warp i; every lane gets it.
+__device__ __forceinline__ float group_sum(float x, int half)
+{
+    for (int o = half; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+__device__ __forceinline__ int half_of(int G) { return G > 1 ? 1 << (31 - __clz(G - 1)) : 0; }
+
 // Row statistics: each warp takes the sum of its part and the squares centred
 // on its own mean, and the warps' parts are joined around the common mean, so
 // nothing is subtracted from a large sum of squares and one barrier serves.
 // GROUP: the block's G warps share a row (else the warp has it alone).
+// VEC: rows come through a ring of ring_rows() rows in shared memory, each
+// thread fetching and reading only its own vectors.
+__host__ __device__ constexpr int ring_rows(int el, int eb) { return el * eb > 64 ? 3 : 4; }  // 512 threads' rings fit an SM
 template <class T, int EL, bool VEC, bool GROUP>
 __global__ void __launch_bounds__(EL == 8 ? 1024 : 512) norm_rows_kernel(const __grid_constant__ NormArgs a)
 {
     stream_order();
     using S = Slice<T, EL, VEC>;
+    constexpr int kStages = ring_rows(EL, sizeof(T));
     __shared__ float2 s_part[2][32];
-    __shared__ float s_count[32];
+    __shared__ float2 s_count[32];  // columns of each warp and the reciprocal
+    extern __shared__ uint4 s_ring[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int G = GROUP ? blockDim.x >> 5 : 1, g = GROUP ? warp : 0;
     const int64_t step = GROUP ? gridDim.x : (int64_t)gridDim.x * (blockDim.x >> 5);
     int64_t row = GROUP ? blockIdx.x : (int64_t)blockIdx.x * (blockDim.x >> 5) + warp;
-    const int cols = (int)a.cols;
+    const int cols = (int)a.cols, threads = blockDim.x, half = half_of(G);
+    const T *x = static_cast<const T *>(a.x);
 
-    float w[EL], b[EL];
+    uint4 *slots = s_ring + threadIdx.x;
+    if (VEC) {
+#pragma unroll
+        for (int s = 0; s < kStages - 1; ++s) {
+            if (row + s * step < a.rows) S::fetch(slots + s * S::NV * threads, threads, x + (row + s * step) * a.xs, cols, G, g, lane);
+            fetch_commit();
+        }
+    }
+    float2 w[EL / 2], b[EL / 2];
+    load_weights<S, EL>(w, a.w, a.wdtype, 1.0f, 0.0f, cols, G, g, lane);
+    load_weights<S, EL>(b, a.b, a.wdtype, 0.0f, 0.0f, cols, G, g, lane);
     float mine = 0.0f;
 #pragma unroll
-    for (int k = 0; k < EL; ++k) {
-        const int c = S::col(k, G, g, lane);
-        const bool in = c < cols;
-        w[k] = in && a.w ? load_any(a.w, c, a.wdtype) : 1.0f;
-        b[k] = in && a.b ? load_any(a.b, c, a.wdtype) : 0.0f;
-        mine += in ? 1.0f : 0.0f;
-    }
+    for (int k = 0; k < EL; ++k) mine += S::col(k, G, g, lane) < cols ? 1.0f : 0.0f;
     const float count = warp_sum(mine);
-    const float inv_count = count > 0.0f ? 1.0f / count : 0.0f;
+    const float inv_count = count > 0.0f ? 1.0f / count : 0.0f, inv_n = 1.0f / (float)cols;
+    float2 part_count = make_float2(0.0f, 0.0f);
+    const int peer = half ? lane & (2 * half - 1) : 0;
     if (GROUP) {
-        if (lane == 0) s_count[g] = count;
+        if (lane == 0) s_count[g] = make_float2(count, inv_count);
         __syncthreads();
+        if (peer < G) part_count = s_count[peer];
     }
-    const float n = (float)cols;
 
     S next;
-    if (row < a.rows) next.load(static_cast<const T *>(a.x) + row * a.xs, cols, G, g, lane);
+    if (!VEC && row < a.rows) next.load(x + row * a.xs, cols, G, g, lane);
+    int stage = 0;
     for (int it = 0; row < a.rows; row += step, it ^= 1) {
-        S cur = next;
-        if (row + step < a.rows) next.load(static_cast<const T *>(a.x) + (row + step) * a.xs, cols, G, g, lane);
-        float sum = 0.0f;
-#pragma unroll
-        for (int k = 0; k < EL; ++k) sum += cur.at(k);
-        sum = warp_sum(sum);
-        float mean = sum * inv_count;
-        float m2 = 0.0f;
-#pragma unroll
-        for (int k = 0; k < EL; ++k) {
-            const float d = S::col(k, G, g, lane) < cols ? cur.at(k) - mean : 0.0f;
-            m2 = fmaf(d, d, m2);
+        S cur;
+        if (VEC) {
+            const int ahead = stage == 0 ? kStages - 1 : stage - 1;
+            const int64_t far = row + (kStages - 1) * step;
+            if (far < a.rows) S::fetch(slots + ahead * S::NV * threads, threads, x + far * a.xs, cols, G, g, lane);
+            fetch_commit();
+            fetch_wait<kStages - 1>();
+            cur.take(slots + stage * S::NV * threads, threads, cols, G, g, lane);
+            stage = stage == kStages - 1 ? 0 : stage + 1;
+        } else {
+            cur = next;
+            if (row + step < a.rows) next.load(x + (row + step) * a.xs, cols, G, g, lane);
         }
-        m2 = warp_sum(m2);
+        float2 acc = both(0.0f);
+#pragma unroll
+        for (int k = 0; k < EL; k += 2) acc = add2(acc, cur.pair(k));
+        const float sum = warp_sum(acc.x + acc.y);
+        float mean = sum * inv_count;
+        acc = both(0.0f);
+#pragma unroll
+        for (int k = 0; k < EL; k += 2) {
+            // whole vectors lie inside the row or past it
+            if (!VEC || S::col(k, G, g, lane) < cols) {
+                float2 d = add2(cur.pair(k), both(-mean));
+                if (!VEC) {
+                    if (S::col(k, G, g, lane) >= cols) d.x = 0.0f;
+                    if (S::col(k + 1, G, g, lane) >= cols) d.y = 0.0f;
+                }
+                acc = fma2(d, d, acc);
+            }
+        }
+        float m2 = warp_sum(acc.x + acc.y);
         if (GROUP) {
             if (lane == 0) s_part[it][g] = make_float2(sum, m2);
             __syncthreads();
-            float total = 0.0f;
-            for (int i = 0; i < G; ++i) total += s_part[it][i].x;
-            mean = total / n;
-            m2 = 0.0f;
-            for (int i = 0; i < G; ++i) {
-                const float c = s_count[i];
-                const float2 p = s_part[it][i];
-                const float d = c > 0.0f ? p.x / c - mean : 0.0f;
-                m2 += fmaf(c * d, d, p.y);
-            }
+            const float2 p = peer < G ? s_part[it][peer] : make_float2(0.0f, 0.0f);
+            mean = group_sum(p.x, half) * inv_n;
+            const float d = fmaf(p.x, part_count.y, -mean);
+            m2 = group_sum(fmaf(part_count.x * d, d, p.y), half);
         }
-        const float rstd = 1.0f / sqrtf(m2 / n + a.eps);
+        const float rstd = rsqrtf(fmaf(m2, inv_n, a.eps));
+        const float2 r2 = both(rstd), shift = both(-mean);
 #pragma unroll
-        for (int k = 0; k < EL; ++k) cur.set(k, fmaf((cur.at(k) - mean) * rstd, w[k], b[k]));
+        for (int k = 0; k < EL; k += 2) cur.set(k, fma2(mul2(add2(cur.pair(k), shift), r2), w[k / 2], b[k / 2]));
         cur.store(static_cast<T *>(a.y) + row * a.ys, cols, G, g, lane);
         if (g == 0 && lane == 0) {
             if (a.mean) a.mean[row] = mean;
@@ -213,6 +281,7 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const __grid_constant__
 }
 
 // ---------------------------------------------------------------- gradient
+constexpr int kGradStages = 3;
 // Each row needs two sums over its columns, sum(w dy) and sum(w dy xhat),
 // before its dx; dweight and dbias are sums over rows and stay in registers.
 template <class T, int EL, bool VEC, bool GROUP>
@@ -221,77 +290,103 @@ __global__ void __launch_bounds__(EL == 32 ? 256 : 512) norm_grad_rows_kernel(co
     stream_order();
     using S = Slice<T, EL, VEC>;
     __shared__ float2 s_part[2][16];
-    extern __shared__ float s_acc[];  // [cols], joins the warps of a block (GROUP off)
+    extern __shared__ uint4 s_ring[];  // the ring of rows; at the end [cols] sums that join a block's warps
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int G = GROUP ? blockDim.x >> 5 : 1, g = GROUP ? warp : 0;
     const int64_t step = GROUP ? gridDim.x : (int64_t)gridDim.x * (blockDim.x >> 5);
     int64_t row = GROUP ? blockIdx.x : (int64_t)blockIdx.x * (blockDim.x >> 5) + warp;
-    const int cols = (int)a.cols;
-    const float n = (float)cols;
+    const int cols = (int)a.cols, threads = blockDim.x, half = half_of(G);
+    const float inv_n = 1.0f / (float)cols;
+    const int peer = half ? lane & (2 * half - 1) : 0;
+    const T *gdy = static_cast<const T *>(a.dy), *gx = static_cast<const T *>(a.x);
 
-    float w[EL], dw[EL], db[EL];
+    uint4 *slots = s_ring + threadIdx.x;
+    auto fetch = [&](int s, int64_t r) {
+        S::fetch(slots + s * 2 * S::NV * threads, threads, gdy + r * a.dys, cols, G, g, lane);
+        S::fetch(slots + (s * 2 + 1) * S::NV * threads, threads, gx + r * a.xs, cols, G, g, lane);
+    };
+    if (VEC) {
 #pragma unroll
-    for (int k = 0; k < EL; ++k) {
-        const int c = S::col(k, G, g, lane);
-        w[k] = c < cols ? (a.w ? load_any(a.w, c, a.wdtype) : 1.0f) : 0.0f;
-        dw[k] = db[k] = 0.0f;
+        for (int s = 0; s < kGradStages - 1; ++s) {
+            if (row + s * step < a.rows) fetch(s, row + s * step);
+            fetch_commit();
+        }
     }
+    float2 w[EL / 2], dw[EL / 2], db[EL / 2];
+    load_weights<S, EL>(w, a.w, a.wdtype, 1.0f, 0.0f, cols, G, g, lane);
+#pragma unroll
+    for (int k = 0; k < EL / 2; ++k) dw[k] = db[k] = both(0.0f);
     S ndy, nx;
     float nmean = 0.0f, nrstd = 0.0f;
-    auto fetch = [&](int64_t r) {
-        ndy.load(static_cast<const T *>(a.dy) + r * a.dys, cols, G, g, lane);
-        nx.load(static_cast<const T *>(a.x) + r * a.xs, cols, G, g, lane);
+    auto ahead = [&](int64_t r) {
+        if (!VEC) {
+            ndy.load(gdy + r * a.dys, cols, G, g, lane);
+            nx.load(gx + r * a.xs, cols, G, g, lane);
+        }
         nmean = a.mean[r];
         nrstd = a.rstd[r];
     };
-    if (row < a.rows) fetch(row);
+    if (row < a.rows) ahead(row);
+    int stage = 0;
     for (int it = 0; row < a.rows; row += step, it ^= 1) {
-        S dy = ndy, x = nx;
+        S dy, x;
         const float mean = nmean, rstd = nrstd;
-        if (row + step < a.rows) fetch(row + step);
-        float c1 = 0.0f, c2 = 0.0f;
-#pragma unroll
-        for (int k = 0; k < EL; ++k) {
-            const float d = dy.at(k), xhat = (x.at(k) - mean) * rstd;
-            const float wd = w[k] * d;
-            c1 += wd;
-            c2 = fmaf(wd, xhat, c2);
-            // columns past the row read dy = 0 and are never written out
-            dw[k] = fmaf(d, xhat, dw[k]);
-            db[k] += d;
+        if (VEC) {
+            const int64_t far = row + (kGradStages - 1) * step;
+            if (far < a.rows) fetch(stage == 0 ? kGradStages - 1 : stage - 1, far);
+            fetch_commit();
+            fetch_wait<kGradStages - 1>();
+            dy.take(slots + stage * 2 * S::NV * threads, threads, cols, G, g, lane);
+            x.take(slots + (stage * 2 + 1) * S::NV * threads, threads, cols, G, g, lane);
+            stage = stage == kGradStages - 1 ? 0 : stage + 1;
+        } else {
+            dy = ndy;
+            x = nx;
         }
-        c1 = warp_sum(c1);
-        c2 = warp_sum(c2);
+        if (row + step < a.rows) ahead(row + step);
+        const float2 r2 = both(rstd), shift = both(-mean);
+        float2 s1 = both(0.0f), s2 = both(0.0f);
+#pragma unroll
+        for (int k = 0; k < EL; k += 2) {
+            // columns past the row read dy = 0 and are never written out
+            const float2 d = dy.pair(k), xhat = mul2(add2(x.pair(k), shift), r2), wd = mul2(w[k / 2], d);
+            s1 = add2(s1, wd);
+            s2 = fma2(wd, xhat, s2);
+            dw[k / 2] = fma2(d, xhat, dw[k / 2]);
+            db[k / 2] = add2(db[k / 2], d);
+        }
+        float c1 = warp_sum(s1.x + s1.y), c2 = warp_sum(s2.x + s2.y);
         if (GROUP) {
             if (lane == 0) s_part[it][g] = make_float2(c1, c2);
             __syncthreads();
-            c1 = c2 = 0.0f;
-            for (int i = 0; i < G; ++i) {
-                const float2 p = s_part[it][i];
-                c1 += p.x;
-                c2 += p.y;
-            }
+            const float2 p = peer < G ? s_part[it][peer] : make_float2(0.0f, 0.0f);
+            c1 = group_sum(p.x, half);
+            c2 = group_sum(p.y, half);
         }
-        c1 /= n;
-        c2 /= n;
         if (a.dx) {
+            // rstd * (w dy - c1 - xhat c2) as (w dy) rstd + (xhat * -c2 rstd + -c1 rstd)
+            const float2 k1 = both(-c1 * inv_n * rstd), k2 = both(-c2 * inv_n * rstd);
 #pragma unroll
-            for (int k = 0; k < EL; ++k) {
-                const float xhat = (x.at(k) - mean) * rstd;
-                x.set(k, (w[k] * dy.at(k) - c1 - xhat * c2) * rstd);
+            for (int k = 0; k < EL; k += 2) {
+                const float2 xhat = mul2(add2(x.pair(k), shift), r2);
+                x.set(k, fma2(mul2(w[k / 2], dy.pair(k)), r2, fma2(xhat, k2, k1)));
             }
             x.store(static_cast<T *>(a.dx) + row * a.dxs, cols, G, g, lane);
         }
     }
     if (!a.part) return;
+    if (VEC) fetch_wait<0>();
+    float *s_acc = reinterpret_cast<float *>(s_ring);
+    if (!GROUP) __syncthreads();
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
         float *out = a.part + ((int64_t)which * a.P + blockIdx.x) * cols;
+        const float2 *v = which ? db : dw;
         if (GROUP) {
 #pragma unroll
             for (int k = 0; k < EL; ++k) {
                 const int c = S::col(k, G, g, lane);
-                if (c < cols) out[c] = which ? db[k] : dw[k];
+                if (c < cols) out[c] = k & 1 ? v[k / 2].y : v[k / 2].x;
             }
         } else {
             for (int turn = 0; turn < (int)(blockDim.x >> 5); ++turn) {
@@ -299,8 +394,8 @@ __global__ void __launch_bounds__(EL == 32 ? 256 : 512) norm_grad_rows_kernel(co
 #pragma unroll
                     for (int k = 0; k < EL; ++k) {
                         const int c = S::col(k, G, g, lane);
-                        const float v = which ? db[k] : dw[k];
-                        if (c < cols) s_acc[c] = turn == 0 ? v : s_acc[c] + v;
+                        const float y = k & 1 ? v[k / 2].y : v[k / 2].x;
+                        if (c < cols) s_acc[c] = turn == 0 ? y : s_acc[c] + y;
                     }
                 }
                 __syncthreads();
@@ -414,6 +509,10 @@ std::mutex g_mu;
 std::map<int, int> g_sms;
 std::map<std::pair<const void *, std::pair<int, int>>, int> g_fit;
 
+// Most dynamic shared memory of a block: the 227 KB of an SM less room for
+// the kernels' few static words.
+constexpr int kMaxDynamic = 224 * 1024;
+
 // Blocks of this kernel that fit one SM.
 rr_status blocks_per_sm(const void *fn, int threads, int smem, int *out)
 {
@@ -422,7 +521,9 @@ rr_status blocks_per_sm(const void *fn, int threads, int smem, int *out)
     auto it = g_fit.find(key);
     if (it == g_fit.end()) {
         int fit = 0;
-        cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, fn, threads, smem);
+        cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamic);
+        if (e != cudaSuccess) return step_cuda_fail(e, "cudaFuncSetAttribute(maxDynamicSharedMemorySize)");
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, fn, threads, smem);
         if (e != cudaSuccess) return step_cuda_fail(e, "cudaOccupancyMaxActiveBlocksPerMultiprocessor");
         if (fit < 1) return step_fail(RR_ERR_CUDA, "a block of %d threads does not fit the device", threads);
         it = g_fit.emplace(key, fit).first;
@@ -459,17 +560,17 @@ const void *norm_grad_fn(int el, bool vec, bool group)
 }
 
 // Elements to a lane and warps to a row: one warp while 32 elements a lane
-// hold the row, else 16 a lane (32 where that needs more than 512 threads).
+// hold the row (16 where rows are not vectors: 32 and a row held ahead spill), else 16 a lane (32 where that needs more than 512 threads).
 // With fewer rows than SMs nothing but one row's latency counts: 8 a lane.
 // warps > 0 where a kernel of that shape takes the row (most[]: the warps its
 // launch bounds allow with 8, 16 and 32 elements a lane), else 0.
-void row_shape(int64_t rows, int64_t cols, int sms, const int *most, int *el, int *warps)
+void row_shape(int64_t rows, int64_t cols, bool vec, int sms, const int *most, int *el, int *warps)
 {
     auto need = [&](int e) { return (cols + 32 * e - 1) / (32 * e); };
     if (rows <= sms && need(8) <= most[0]) *el = 8;
     else if (cols <= 256) *el = 8;
     else if (cols <= 512) *el = 16;
-    else if (cols <= 1024) *el = 32;
+    else if (cols <= 1024 && vec) *el = 32;
     else *el = need(16) <= most[1] ? 16 : 32;
     const int64_t n = need(*el);
     *warps = n <= most[*el == 8 ? 0 : *el == 16 ? 1 : 2] ? (int)n : 0;
@@ -611,9 +712,10 @@ extern "C" rr_status rr_layer_norm(const void *x, const void *weight, const void
     RR_TRY(step_sms(&sms));
     NormArgs a{x, weight, bias, y, mean, rstd, rows, cols, x_stride, y_stride, eps, (int)weight_dtype};
     int el = 0, warps = 0;
-    row_shape(rows, cols, sms, kNormWarps, &el, &warps);
+    const bool vec = cols * eb % 16 == 0 && vector_rows(x, x_stride, rows, eb) && vector_rows(y, y_stride, rows, eb);
+    row_shape(rows, cols, vec, sms, kNormWarps, &el, &warps);
     const void *fn;
-    int threads;
+    int threads, smem = 0;
     int64_t blocks;
     if (warps == 0) {
         fn = dtype == RR_FP32 ? (const void *)norm_long_kernel<float>
@@ -621,18 +723,18 @@ extern "C" rr_status rr_layer_norm(const void *x, const void *weight, const void
         threads = 1024;
         blocks = rows;
     } else {
-        const bool vec = cols * eb % 16 == 0 && vector_rows(x, x_stride, rows, eb) && vector_rows(y, y_stride, rows, eb);
         const bool group = warps > 1;
         fn = dtype == RR_FP32 ? norm_rows_fn<float>(el, vec, group)
              : dtype == RR_BF16 ? norm_rows_fn<__nv_bfloat16>(el, vec, group) : norm_rows_fn<__half>(el, vec, group);
         const int64_t per = group ? 1 : rows >= 8 * (int64_t)sms ? 8 : (rows + sms - 1) / sms;  // rows a block has at once
         threads = 32 * (group ? warps : (int)per);
+        smem = vec ? ring_rows(el, eb) * threads * el * eb : 0;
         blocks = (rows + per - 1) / per;
     }
     int fit = 0;
-    RR_TRY(blocks_per_sm(fn, threads, 0, &fit));
+    RR_TRY(blocks_per_sm(fn, threads, smem, &fit));
     const int64_t most = (int64_t)fit * sms;
-    RR_TRY(step_launch(fn, blocks < most ? blocks : most, threads, 0, &a, stream));
+    RR_TRY(step_launch(fn, blocks < most ? blocks : most, threads, smem, &a, stream));
     return step_ok();
 }
 
@@ -710,7 +812,9 @@ extern "C" rr_status rr_layer_norm_backward(const void *dy, const void *x, const
                    (int)weight_dtype, 0};
     if (rows > 0) {
         int el = 0, warps = 0;
-        row_shape(rows, cols, sms, kNormGradWarps, &el, &warps);
+        const bool vec = cols * eb % 16 == 0 && vector_rows(dy, dy_stride, rows, eb) &&
+                         vector_rows(x, x_stride, rows, eb) && (!dx || vector_rows(dx, dx_stride, rows, eb));
+        row_shape(rows, cols, vec, sms, kNormGradWarps, &el, &warps);
         if (warps == 0) {
             const void *means = dtype == RR_FP32 ? (const void *)norm_grad_means_kernel<float>
                                 : dtype == RR_BF16 ? (const void *)norm_grad_means_kernel<__nv_bfloat16>
@@ -726,15 +830,14 @@ extern "C" rr_status rr_layer_norm_backward(const void *dy, const void *x, const
             a.P = (int)P;
             RR_TRY(step_launch(columns, P * tiles, 256, 0, &a, stream));
         } else {
-            const bool vec = cols * eb % 16 == 0 && vector_rows(dy, dy_stride, rows, eb) &&
-                             vector_rows(x, x_stride, rows, eb) && (!dx || vector_rows(dx, dx_stride, rows, eb));
             const bool group = warps > 1;
             const void *fn = dtype == RR_FP32 ? norm_grad_fn<float>(el, vec, group)
                              : dtype == RR_BF16 ? norm_grad_fn<__nv_bfloat16>(el, vec, group)
                                                 : norm_grad_fn<__half>(el, vec, group);
             const int64_t per = group ? 1 : rows >= 8 * (int64_t)sms ? 8 : (rows + sms - 1) / sms;
             const int threads = 32 * (group ? warps : (int)per);
-            const int smem = group ? 0 : (int)cols * 4;
+            const int ring = vec ? 2 * kGradStages * threads * el * eb : 0, sums_bytes = group ? 0 : (int)cols * 4;
+            const int smem = ring > sums_bytes ? ring : sums_bytes;
             int fit = 0;
             RR_TRY(blocks_per_sm(fn, threads, smem, &fit));
             int64_t blocks = (rows + per - 1) / per;

@@ -72,6 +72,63 @@ struct alignas(N * sizeof(T) > 16 ? 16 : N * sizeof(T)) Pack {
     T v[N];
 };
 
+// Two binary32 operations in one instruction, each rounded by itself.
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 d, a, b;\n\t"
+        "mov.b64 {%0, %1}, d;}" : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 d, a, b;\n\t"
+        "mov.b64 {%0, %1}, d;}" : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("{.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// Two neighbouring elements between memory's type and binary32.
+__device__ __forceinline__ float2 pair_f32(const float *p) { return make_float2(p[0], p[1]); }
+__device__ __forceinline__ float2 pair_f32(const __half *p) { return __half22float2(*reinterpret_cast<const __half2 *>(p)); }
+__device__ __forceinline__ float2 pair_f32(const __nv_bfloat16 *p)
+{
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(p));
+}
+__device__ __forceinline__ void pair_set(float *p, float2 x)
+{
+    p[0] = x.x;
+    p[1] = x.y;
+}
+__device__ __forceinline__ void pair_set(__half *p, float2 x) { *reinterpret_cast<__half2 *>(p) = __float22half2_rn(x); }
+__device__ __forceinline__ void pair_set(__nv_bfloat16 *p, float2 x)
+{
+    *reinterpret_cast<__nv_bfloat162 *>(p) = __float22bfloat162_rn(x);
+}
+
+// 16 bytes from global to shared memory, past the registers; groups complete
+// in order.  A thread reads back only what it fetched, so nothing else waits.
+__device__ __forceinline__ void fetch16(void *s, const void *g)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(s))),
+                 "l"(g) : "memory");
+}
+__device__ __forceinline__ void fetch_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void fetch_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 __device__ __forceinline__ float warp_sum(float x)
 {
 #pragma unroll
