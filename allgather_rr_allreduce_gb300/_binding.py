@@ -271,22 +271,25 @@ def rr_allgather_list(rank_bufs, output_lists, world_size, numel_per_rank, dtype
 
 
 # ---------------------------------------------------------------- training step
-_is_cuda, _data_ptr = operator.attrgetter("is_cuda"), operator.methodcaller("data_ptr")
+_is_cuda = operator.attrgetter("is_cuda")
 
 
 def _tensor_array(items, count, name):
-    """pointer_array for a list of `count` tensors or addresses (None: no list)."""
+    """pointer_array for a list of `count` tensors or addresses (None: no
+    list).  A pointer_array made before passes through, so that a loop over
+    the same tensors need not marshal them again."""
     if items is None:
         return None
     if len(items) != count:
         raise ValueError(f"{name} has {len(items)} entries, sizes has {count}")
-    if not count:
-        return (_vp * 0)()
-    try:  # CUDA tensors throughout, without a Python call for each
-        if all(map(_is_cuda, items)):
-            return (_vp * count).from_buffer(array.array("Q", map(_data_ptr, items)))
-    except AttributeError:
-        pass
+    if isinstance(items, ctypes.Array):
+        return items
+    if count and _tensor_class is not None:
+        try:  # CUDA tensors throughout, without a Python-level step for each
+            if all(map(_is_cuda, items)):
+                return (_vp * count).from_buffer(array.array("Q", map(_tensor_class.data_ptr, items)))
+        except (AttributeError, TypeError):
+            pass
     return pointer_array(items)
 
 
@@ -320,8 +323,8 @@ def rr_layer_norm_backward_workspace(rows, cols):
 
 def rr_grad_norm(grads, sizes, dtype, inv_scale, max_norm, norm, scale, workspace, workspace_bytes, stream=None):
     """Norm over a list of gradient tensors and the factor that clips it; norm or scale may be None."""
-    n = len(sizes)
-    _check(lib().rr_grad_norm(_tensor_array(grads, n, "grads"), _sizes(sizes), n, dtype_code(dtype), inv_scale,
+    n, l = len(sizes), lib()
+    _check(l.rr_grad_norm(_tensor_array(grads, n, "grads"), _sizes(sizes), n, dtype_code(dtype), inv_scale,
                               max_norm, _addr(norm), _addr(scale), _addr(workspace), workspace_bytes,
                               stream_handle(stream)))
 
@@ -336,8 +339,8 @@ def rr_grad_norm_workspace(num_tensors):
 def rr_adamw(params, grads, exp_avg, exp_avg_sq, master, sizes, param_dtype, grad_dtype, hyper, grad_scale=None,
              stream=None):
     """One AdamW step over a list of tensors, states in binary32; master may be None."""
-    n = len(sizes)
-    _check(lib().rr_adamw(_tensor_array(params, n, "params"), _tensor_array(grads, n, "grads"),
+    n, l = len(sizes), lib()
+    _check(l.rr_adamw(_tensor_array(params, n, "params"), _tensor_array(grads, n, "grads"),
                           _tensor_array(exp_avg, n, "exp_avg"), _tensor_array(exp_avg_sq, n, "exp_avg_sq"),
                           _tensor_array(master, n, "master"), _sizes(sizes), n, dtype_code(param_dtype),
                           dtype_code(grad_dtype), hyper, _addr(grad_scale), stream_handle(stream)))
@@ -346,8 +349,8 @@ def rr_adamw(params, grads, exp_avg, exp_avg_sq, master, sizes, param_dtype, gra
 def rr_adamw8(params, grads, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale, master, sizes, param_dtype,
               grad_dtype, hyper, seed, grad_scale=None, stream=None):
     """One AdamW step over a list of tensors, states in 8 bits; master may be None."""
-    n = len(sizes)
-    _check(lib().rr_adamw8(_tensor_array(params, n, "params"), _tensor_array(grads, n, "grads"),
+    n, l = len(sizes), lib()
+    _check(l.rr_adamw8(_tensor_array(params, n, "params"), _tensor_array(grads, n, "grads"),
                            _tensor_array(exp_avg, n, "exp_avg"), _tensor_array(exp_avg_scale, n, "exp_avg_scale"),
                            _tensor_array(exp_avg_sq, n, "exp_avg_sq"),
                            _tensor_array(exp_avg_sq_scale, n, "exp_avg_sq_scale"),

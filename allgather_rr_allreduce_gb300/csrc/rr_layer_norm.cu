@@ -40,97 +40,104 @@ struct NormGradArgs {
     int P;
 };
 
-// One lane's EL elements of a row, in pairs.  VEC: 16-byte vectors, vector v
-// of the lane at column ((v * G + g) * 32 + lane) * EN; else single elements,
-// element k at column (k * G + g) * 32 + lane.  Columns past the row read as
-// zero and are not written.
+// One lane's EL elements of a row.  Warp g of the row has columns
+// [g * 32 * EL, (g + 1) * 32 * EL).  VEC: its 16-byte vectors in turn, vector v
+// of the lane at column ((g * NV + v) * 32 + lane) * EN; else its single
+// elements in turn, element k at column (g * EL + k) * 32 + lane.  Columns past
+// the row read as zero and are not written.
 template <class T, int EL, bool VEC>
 struct Slice {
     static constexpr int EN = 16 / (int)sizeof(T);
     static constexpr int NV = EL / EN;
+    static constexpr int kStep = VEC ? 32 * EN : 32;  // columns from a lane's vector (element) to its next
+    static constexpr int kRing = NV * 32;             // 16-byte slots of a warp in one stage of a ring
     Pack<T, EN> raw[NV];
 
-    static __device__ __forceinline__ int col(int k, int G, int g, int lane)
+    // The lane's first column; column of its k-th element.
+    static __device__ __forceinline__ int first(int g, int lane) { return g * 32 * EL + (VEC ? lane * EN : lane); }
+    static __device__ __forceinline__ int col(int k, int g, int lane)
     {
-        return VEC ? ((k / EN * G + g) * 32 + lane) * EN + k % EN : (k * G + g) * 32 + lane;
+        return first(g, lane) + (VEC ? k / EN * kStep + k % EN : k * kStep);
     }
-    __device__ __forceinline__ void load(const T *row, int cols, int G, int g, int lane)
+    // p: address of the lane's first column; c: that column.
+    __device__ __forceinline__ void load(const T *p, int c, int cols)
     {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             if (VEC) {
-                const int c = col(v * EN, G, g, lane);
-                if (c < cols) {
-                    raw[v] = *reinterpret_cast<const Pack<T, EN> *>(row + c);
+                if (c + v * kStep < cols) {
+                    raw[v] = *reinterpret_cast<const Pack<T, EN> *>(p + v * kStep);
                 } else {
                     *reinterpret_cast<uint4 *>(&raw[v]) = make_uint4(0, 0, 0, 0);
                 }
             } else {
 #pragma unroll
                 for (int j = 0; j < EN; ++j) {
-                    const int c = col(v * EN + j, G, g, lane);
-                    raw[v].v[j] = c < cols ? row[c] : from_f32<T>(0.0f);
+                    const int k = v * EN + j;
+                    raw[v].v[j] = c + k * kStep < cols ? p[k * kStep] : from_f32<T>(0.0f);
                 }
             }
         }
     }
-    // The same through a thread's own slots in shared memory (VEC only):
-    // slot v * threads of the stage.
-    static __device__ __forceinline__ void fetch(uint4 *slot, int threads, const T *row, int cols, int G, int g, int lane)
+    // The same through the lane's own slots of a ring in shared memory (VEC
+    // only).  Slots past the row are zeroed once and never fetched.
+    static __device__ __forceinline__ void fetch(uint4 *slot, const T *p, int c, int cols)
     {
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const int c = col(v * EN, G, g, lane);
-            if (c < cols) fetch16(slot + v * threads, row + c);
-        }
+        for (int v = 0; v < NV; ++v)
+            if (c + v * kStep < cols) fetch16(slot + v * 32, p + v * kStep);
     }
-    __device__ __forceinline__ void take(const uint4 *slot, int threads, int cols, int G, int g, int lane)
+    static __device__ __forceinline__ void clear(uint4 *slot, int c, int cols)
     {
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const uint4 x = slot[v * threads];
-            *reinterpret_cast<uint4 *>(&raw[v]) = col(v * EN, G, g, lane) < cols ? x : make_uint4(0, 0, 0, 0);
-        }
+        for (int v = 0; v < NV; ++v)
+            if (c + v * kStep >= cols) slot[v * 32] = make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void take(const uint4 *slot)
+    {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) *reinterpret_cast<uint4 *>(&raw[v]) = slot[v * 32];
     }
     __device__ __forceinline__ float2 pair(int k) const { return pair_f32(&raw[k / EN].v[k % EN]); }
     __device__ __forceinline__ void set(int k, float2 x) { pair_set(&raw[k / EN].v[k % EN], x); }
-    __device__ __forceinline__ void store(T *row, int cols, int G, int g, int lane) const
+    __device__ __forceinline__ void store(T *p, int c, int cols) const
     {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             if (VEC) {
-                const int c = col(v * EN, G, g, lane);
-                if (c < cols) *reinterpret_cast<Pack<T, EN> *>(row + c) = raw[v];
+                if (c + v * kStep < cols) *reinterpret_cast<Pack<T, EN> *>(p + v * kStep) = raw[v];
             } else {
 #pragma unroll
                 for (int j = 0; j < EN; ++j) {
-                    const int c = col(v * EN + j, G, g, lane);
-                    if (c < cols) row[c] = raw[v].v[j];
+                    const int k = v * EN + j;
+                    if (c + k * kStep < cols) p[k * kStep] = raw[v].v[j];
                 }
             }
         }
     }
 };
 
-// A lane's pairs of a vector of weights as binary32.
+// A lane's pairs of a vector of weights as binary32; zero past the row.
 template <class S, int EL>
-__device__ __forceinline__ void load_weights(float2 (&w)[EL / 2], const void *p, int dtype, float absent, float past,
-                                             int cols, int G, int g, int lane)
+__device__ __forceinline__ void load_weights(float2 (&w)[EL / 2], const void *p, int dtype, float absent, int cols, int g,
+                                             int lane)
 {
 #pragma unroll
     for (int k = 0; k < EL; ++k) {
-        const int c = S::col(k, G, g, lane);
-        const float v = c < cols ? (p ? load_any(p, c, dtype) : absent) : past;
+        const int c = S::col(k, g, lane);
+        const float v = c < cols ? (p ? load_any(p, c, dtype) : absent) : 0.0f;
         if (k & 1) w[k / 2].y = v;
         else w[k / 2].x = v;
     }
 }
 
-// Sum over a block's G warps of what lane i % (power of two >= G) holds for
-// warp i; every lane gets it.
+// Sum over a block's G warps of what lane i % 2 * half holds for warp i (half:
+// the largest power of two below G, 0 for one warp); every lane gets it.
 __device__ __forceinline__ float group_sum(float x, int half)
 {
-    for (int o = half; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        if (half >= o) x += __shfl_xor_sync(0xffffffffu, x, o);
     return x;
 }
 __device__ __forceinline__ int half_of(int G) { return G > 1 ? 1 << (31 - __clz(G - 1)) : 0; }
@@ -151,27 +158,35 @@ __global__ void __launch_bounds__(EL == 8 ? 1024 : 512) norm_rows_kernel(const _
     __shared__ float2 s_part[2][32];
     __shared__ float2 s_count[32];  // columns of each warp and the reciprocal
     extern __shared__ uint4 s_ring[];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int G = GROUP ? blockDim.x >> 5 : 1, g = GROUP ? warp : 0;
-    const int64_t step = GROUP ? gridDim.x : (int64_t)gridDim.x * (blockDim.x >> 5);
-    int64_t row = GROUP ? blockIdx.x : (int64_t)blockIdx.x * (blockDim.x >> 5) + warp;
-    const int cols = (int)a.cols, threads = blockDim.x, half = half_of(G);
-    const T *x = static_cast<const T *>(a.x);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int G = GROUP ? warps : 1, g = GROUP ? warp : 0;
+    const int64_t step = GROUP ? gridDim.x : (int64_t)gridDim.x * warps;
+    int64_t row = GROUP ? blockIdx.x : (int64_t)blockIdx.x * warps + warp;
+    const int cols = (int)a.cols, half = half_of(G), c0 = S::first(g, lane);
 
-    uint4 *slots = s_ring + threadIdx.x;
+    // Ring: stage s of this lane at ring + s * round.
+    uint4 *const ring = s_ring + warp * S::kRing + lane;
+    const int round = warps * S::kRing;
+    int64_t left = row < a.rows ? (a.rows - row + step - 1) / step : 0, far = left;  // rows to come: to reduce, to fetch
+    const T *src = static_cast<const T *>(a.x) + row * a.xs + c0;
+    const int64_t src_step = step * a.xs;
     if (VEC) {
 #pragma unroll
+        for (int s = 0; s < kStages; ++s) S::clear(ring + s * round, c0, cols);
+#pragma unroll
         for (int s = 0; s < kStages - 1; ++s) {
-            if (row + s * step < a.rows) S::fetch(slots + s * S::NV * threads, threads, x + (row + s * step) * a.xs, cols, G, g, lane);
+            if (far > 0) S::fetch(ring + s * round, src, c0, cols);
             fetch_commit();
+            src += src_step;
+            --far;
         }
     }
     float2 w[EL / 2], b[EL / 2];
-    load_weights<S, EL>(w, a.w, a.wdtype, 1.0f, 0.0f, cols, G, g, lane);
-    load_weights<S, EL>(b, a.b, a.wdtype, 0.0f, 0.0f, cols, G, g, lane);
+    load_weights<S, EL>(w, a.w, a.wdtype, 1.0f, cols, g, lane);
+    load_weights<S, EL>(b, a.b, a.wdtype, 0.0f, cols, g, lane);
     float mine = 0.0f;
 #pragma unroll
-    for (int k = 0; k < EL; ++k) mine += S::col(k, G, g, lane) < cols ? 1.0f : 0.0f;
+    for (int k = 0; k < EL; ++k) mine += S::col(k, g, lane) < cols ? 1.0f : 0.0f;
     const float count = warp_sum(mine);
     const float inv_count = count > 0.0f ? 1.0f / count : 0.0f, inv_n = 1.0f / (float)cols;
     float2 part_count = make_float2(0.0f, 0.0f);
@@ -182,59 +197,70 @@ __global__ void __launch_bounds__(EL == 8 ? 1024 : 512) norm_rows_kernel(const _
         if (peer < G) part_count = s_count[peer];
     }
 
+    T *dst = static_cast<T *>(a.y) + row * a.ys + c0;
+    const int64_t dst_step = step * a.ys;
     S next;
-    if (!VEC && row < a.rows) next.load(x + row * a.xs, cols, G, g, lane);
+    if (!VEC && left > 0) next.load(src, c0, cols);
     int stage = 0;
-    for (int it = 0; row < a.rows; row += step, it ^= 1) {
+    for (int it = 0; left > 0; --left, it ^= 1) {
         S cur;
         if (VEC) {
-            const int ahead = stage == 0 ? kStages - 1 : stage - 1;
-            const int64_t far = row + (kStages - 1) * step;
-            if (far < a.rows) S::fetch(slots + ahead * S::NV * threads, threads, x + far * a.xs, cols, G, g, lane);
+            if (far > 0) S::fetch(ring + (stage == 0 ? kStages - 1 : stage - 1) * round, src, c0, cols);
             fetch_commit();
+            src += src_step;
+            --far;
             fetch_wait<kStages - 1>();
-            cur.take(slots + stage * S::NV * threads, threads, cols, G, g, lane);
+            cur.take(ring + stage * round);
             stage = stage == kStages - 1 ? 0 : stage + 1;
         } else {
             cur = next;
-            if (row + step < a.rows) next.load(x + (row + step) * a.xs, cols, G, g, lane);
+            src += src_step;
+            if (left > 1) next.load(src, c0, cols);
         }
+        float2 d[EL / 2];
         float2 acc = both(0.0f);
 #pragma unroll
-        for (int k = 0; k < EL; k += 2) acc = add2(acc, cur.pair(k));
+        for (int k = 0; k < EL / 2; ++k) {
+            d[k] = cur.pair(2 * k);
+            acc = add2(acc, d[k]);
+        }
         const float sum = warp_sum(acc.x + acc.y);
-        float mean = sum * inv_count;
+        float shift = sum * inv_count;  // the warp's mean
         acc = both(0.0f);
 #pragma unroll
-        for (int k = 0; k < EL; k += 2) {
-            // whole vectors lie inside the row or past it
-            if (!VEC || S::col(k, G, g, lane) < cols) {
-                float2 d = add2(cur.pair(k), both(-mean));
-                if (!VEC) {
-                    if (S::col(k, G, g, lane) >= cols) d.x = 0.0f;
-                    if (S::col(k + 1, G, g, lane) >= cols) d.y = 0.0f;
-                }
-                acc = fma2(d, d, acc);
+        for (int k = 0; k < EL / 2; ++k) {
+            d[k] = add2(d[k], both(-shift));
+            if (VEC) {  // whole vectors lie inside the row or past it
+                if (S::col(2 * k, g, lane) < cols) acc = fma2(d[k], d[k], acc);
+            } else {
+                float2 in = d[k];
+                if (S::col(2 * k, g, lane) >= cols) in.x = 0.0f;
+                if (S::col(2 * k + 1, g, lane) >= cols) in.y = 0.0f;
+                acc = fma2(in, in, acc);
             }
         }
-        float m2 = warp_sum(acc.x + acc.y);
+        float m2 = warp_sum(acc.x + acc.y), mean = shift;
         if (GROUP) {
             if (lane == 0) s_part[it][g] = make_float2(sum, m2);
             __syncthreads();
             const float2 p = peer < G ? s_part[it][peer] : make_float2(0.0f, 0.0f);
             mean = group_sum(p.x, half) * inv_n;
-            const float d = fmaf(p.x, part_count.y, -mean);
-            m2 = group_sum(fmaf(part_count.x * d, d, p.y), half);
+            const float off = fmaf(p.x, part_count.y, -mean);
+            m2 = group_sum(fmaf(part_count.x * off, off, p.y), half);
         }
+        // (x - mean) * rstd from x less the warp's mean: both terms are of the
+        // spread's size, however large the mean
         const float rstd = rsqrtf(fmaf(m2, inv_n, a.eps));
-        const float2 r2 = both(rstd), shift = both(-mean);
+        const float2 r2 = both(rstd), move = both((shift - mean) * rstd);
 #pragma unroll
-        for (int k = 0; k < EL; k += 2) cur.set(k, fma2(mul2(add2(cur.pair(k), shift), r2), w[k / 2], b[k / 2]));
-        cur.store(static_cast<T *>(a.y) + row * a.ys, cols, G, g, lane);
+        for (int k = 0; k < EL / 2; ++k) cur.set(2 * k, fma2(fma2(d[k], r2, move), w[k], b[k]));
+        cur.store(dst, c0, cols);
         if (g == 0 && lane == 0) {
             if (a.mean) a.mean[row] = mean;
             if (a.rstd) a.rstd[row] = rstd;
         }
+        dst += dst_step;
+        row += step;
     }
 }
 
@@ -290,70 +316,91 @@ __global__ void __launch_bounds__(EL == 32 ? 256 : 512) norm_grad_rows_kernel(co
     stream_order();
     using S = Slice<T, EL, VEC>;
     __shared__ float2 s_part[2][16];
-    extern __shared__ uint4 s_ring[];  // the ring of rows; at the end [cols] sums that join a block's warps
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int G = GROUP ? blockDim.x >> 5 : 1, g = GROUP ? warp : 0;
-    const int64_t step = GROUP ? gridDim.x : (int64_t)gridDim.x * (blockDim.x >> 5);
-    int64_t row = GROUP ? blockIdx.x : (int64_t)blockIdx.x * (blockDim.x >> 5) + warp;
-    const int cols = (int)a.cols, threads = blockDim.x, half = half_of(G);
+    extern __shared__ uint4 s_ring[];  // the ring of rows; at the end the sums that join a block's warps
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int G = GROUP ? warps : 1, g = GROUP ? warp : 0;
+    const int64_t step = GROUP ? gridDim.x : (int64_t)gridDim.x * warps;
+    int64_t row = GROUP ? blockIdx.x : (int64_t)blockIdx.x * warps + warp;
+    const int cols = (int)a.cols, half = half_of(G), c0 = S::first(g, lane);
     const float inv_n = 1.0f / (float)cols;
     const int peer = half ? lane & (2 * half - 1) : 0;
-    const T *gdy = static_cast<const T *>(a.dy), *gx = static_cast<const T *>(a.x);
 
-    uint4 *slots = s_ring + threadIdx.x;
-    auto fetch = [&](int s, int64_t r) {
-        S::fetch(slots + s * 2 * S::NV * threads, threads, gdy + r * a.dys, cols, G, g, lane);
-        S::fetch(slots + (s * 2 + 1) * S::NV * threads, threads, gx + r * a.xs, cols, G, g, lane);
+    uint4 *const ring = s_ring + warp * 2 * S::kRing + lane;  // dy's slots of a stage, then x's
+    const int round = warps * 2 * S::kRing;
+    int64_t left = row < a.rows ? (a.rows - row + step - 1) / step : 0, far = left;
+    const T *gdy = static_cast<const T *>(a.dy) + row * a.dys + c0, *gx = static_cast<const T *>(a.x) + row * a.xs + c0;
+    const int64_t dy_step = step * a.dys, x_step = step * a.xs;
+    auto fetch = [&](uint4 *slot) {
+        if (far > 0) {
+            S::fetch(slot, gdy, c0, cols);
+            S::fetch(slot + S::kRing, gx, c0, cols);
+        }
+        fetch_commit();
+        gdy += dy_step;
+        gx += x_step;
+        --far;
     };
     if (VEC) {
 #pragma unroll
-        for (int s = 0; s < kGradStages - 1; ++s) {
-            if (row + s * step < a.rows) fetch(s, row + s * step);
-            fetch_commit();
+        for (int s = 0; s < kGradStages; ++s) {
+            S::clear(ring + s * round, c0, cols);
+            S::clear(ring + s * round + S::kRing, c0, cols);
         }
+#pragma unroll
+        for (int s = 0; s < kGradStages - 1; ++s) fetch(ring + s * round);
     }
     float2 w[EL / 2], dw[EL / 2], db[EL / 2];
-    load_weights<S, EL>(w, a.w, a.wdtype, 1.0f, 0.0f, cols, G, g, lane);
+    load_weights<S, EL>(w, a.w, a.wdtype, 1.0f, cols, g, lane);
 #pragma unroll
     for (int k = 0; k < EL / 2; ++k) dw[k] = db[k] = both(0.0f);
+    T *dst = static_cast<T *>(a.dx) + (a.dx ? row * a.dxs + c0 : 0);
+    const int64_t dst_step = step * a.dxs;
     S ndy, nx;
     float nmean = 0.0f, nrstd = 0.0f;
     auto ahead = [&](int64_t r) {
         if (!VEC) {
-            ndy.load(gdy + r * a.dys, cols, G, g, lane);
-            nx.load(gx + r * a.xs, cols, G, g, lane);
+            ndy.load(gdy, c0, cols);
+            nx.load(gx, c0, cols);
+            gdy += dy_step;
+            gx += x_step;
         }
         nmean = a.mean[r];
         nrstd = a.rstd[r];
     };
-    if (row < a.rows) ahead(row);
+    if (left > 0) ahead(row);
     int stage = 0;
-    for (int it = 0; row < a.rows; row += step, it ^= 1) {
+    for (int it = 0; left > 0; --left, it ^= 1) {
         S dy, x;
         const float mean = nmean, rstd = nrstd;
         if (VEC) {
-            const int64_t far = row + (kGradStages - 1) * step;
-            if (far < a.rows) fetch(stage == 0 ? kGradStages - 1 : stage - 1, far);
-            fetch_commit();
+            fetch(ring + (stage == 0 ? kGradStages - 1 : stage - 1) * round);
             fetch_wait<kGradStages - 1>();
-            dy.take(slots + stage * 2 * S::NV * threads, threads, cols, G, g, lane);
-            x.take(slots + (stage * 2 + 1) * S::NV * threads, threads, cols, G, g, lane);
+            dy.take(ring + stage * round);
+            x.take(ring + stage * round + S::kRing);
             stage = stage == kGradStages - 1 ? 0 : stage + 1;
         } else {
             dy = ndy;
             x = nx;
         }
-        if (row + step < a.rows) ahead(row + step);
+        row += step;
+        if (left > 1) ahead(row);
+        // With u = x - mean and e = dy rstd: db += dy, dw += e u, and the row's
+        // sums are of w e and w e u, from which
+        //   dx = w e - sum(w e) / n - u rstd^2 sum(w e u) / n.
+        float2 u[EL / 2], e[EL / 2];
         const float2 r2 = both(rstd), shift = both(-mean);
         float2 s1 = both(0.0f), s2 = both(0.0f);
 #pragma unroll
-        for (int k = 0; k < EL; k += 2) {
+        for (int k = 0; k < EL / 2; ++k) {
             // columns past the row read dy = 0 and are never written out
-            const float2 d = dy.pair(k), xhat = mul2(add2(x.pair(k), shift), r2), wd = mul2(w[k / 2], d);
-            s1 = add2(s1, wd);
-            s2 = fma2(wd, xhat, s2);
-            dw[k / 2] = fma2(d, xhat, dw[k / 2]);
-            db[k / 2] = add2(db[k / 2], d);
+            const float2 d = dy.pair(2 * k);
+            u[k] = add2(x.pair(2 * k), shift);
+            e[k] = mul2(d, r2);
+            db[k] = add2(db[k], d);
+            dw[k] = fma2(e[k], u[k], dw[k]);
+            e[k] = mul2(w[k], e[k]);
+            s1 = add2(s1, e[k]);
+            s2 = fma2(e[k], u[k], s2);
         }
         float c1 = warp_sum(s1.x + s1.y), c2 = warp_sum(s2.x + s2.y);
         if (GROUP) {
@@ -364,44 +411,42 @@ __global__ void __launch_bounds__(EL == 32 ? 256 : 512) norm_grad_rows_kernel(co
             c2 = group_sum(p.y, half);
         }
         if (a.dx) {
-            // rstd * (w dy - c1 - xhat c2) as (w dy) rstd + (xhat * -c2 rstd + -c1 rstd)
-            const float2 k1 = both(-c1 * inv_n * rstd), k2 = both(-c2 * inv_n * rstd);
+            const float2 k1 = both(-c1 * inv_n), k2 = both(-c2 * inv_n * rstd * rstd);
 #pragma unroll
-            for (int k = 0; k < EL; k += 2) {
-                const float2 xhat = mul2(add2(x.pair(k), shift), r2);
-                x.set(k, fma2(mul2(w[k / 2], dy.pair(k)), r2, fma2(xhat, k2, k1)));
-            }
-            x.store(static_cast<T *>(a.dx) + row * a.dxs, cols, G, g, lane);
+            for (int k = 0; k < EL / 2; ++k) x.set(2 * k, add2(e[k], fma2(u[k], k2, k1)));
+            x.store(dst, c0, cols);
+            dst += dst_step;
         }
     }
     if (!a.part) return;
-    if (VEC) fetch_wait<0>();
-    float *s_acc = reinterpret_cast<float *>(s_ring);
-    if (!GROUP) __syncthreads();
+    float *out = a.part + (int64_t)blockIdx.x * cols;
+    const int64_t other = (int64_t)a.P * cols;  // from a column's dw to its db
+    if (GROUP) {
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        float *out = a.part + ((int64_t)which * a.P + blockIdx.x) * cols;
-        const float2 *v = which ? db : dw;
-        if (GROUP) {
-#pragma unroll
-            for (int k = 0; k < EL; ++k) {
-                const int c = S::col(k, G, g, lane);
-                if (c < cols) out[c] = k & 1 ? v[k / 2].y : v[k / 2].x;
+        for (int k = 0; k < EL; ++k) {
+            const int c = S::col(k, g, lane);
+            if (c < cols) {
+                out[c] = k & 1 ? dw[k / 2].y : dw[k / 2].x;
+                out[c + other] = k & 1 ? db[k / 2].y : db[k / 2].x;
             }
-        } else {
-            for (int turn = 0; turn < (int)(blockDim.x >> 5); ++turn) {
-                if (warp == turn) {
+        }
+    } else {
+        // join the block's warps in order: [warp][element][lane], the ring's memory
+        float2 *s_sum = reinterpret_cast<float2 *>(s_ring);
+        if (VEC) fetch_wait<0>();
+        __syncthreads();
 #pragma unroll
-                    for (int k = 0; k < EL; ++k) {
-                        const int c = S::col(k, G, g, lane);
-                        const float y = k & 1 ? v[k / 2].y : v[k / 2].x;
-                        if (c < cols) s_acc[c] = turn == 0 ? y : s_acc[c] + y;
-                    }
-                }
-                __syncthreads();
+        for (int k = 0; k < EL; ++k)
+            s_sum[(warp * EL + k) * 32 + lane] = k & 1 ? make_float2(dw[k / 2].y, db[k / 2].y) : make_float2(dw[k / 2].x, db[k / 2].x);
+        __syncthreads();
+        for (int k = warp; k < EL; k += warps) {
+            float2 t = s_sum[k * 32 + lane];
+            for (int i = 1; i < warps; ++i) t = add2(t, s_sum[(i * EL + k) * 32 + lane]);
+            const int c = S::col(k, 0, lane);
+            if (c < cols) {
+                out[c] = t.x;
+                out[c + other] = t.y;
             }
-            for (int c = threadIdx.x; c < cols; c += blockDim.x) out[c] = s_acc[c];
-            __syncthreads();
         }
     }
 }
@@ -474,33 +519,36 @@ __global__ void __launch_bounds__(256) norm_grad_columns_kernel(const __grid_con
 }
 
 // The blocks' partial sums, added in order: 32 columns to a block, every
-// 16th partial to a warp, the warps' sums in order.
+// kJoinWarps-th partial to a warp, then the warps' sums.
 struct NormJoinArgs {
     const float *part;
     void *dweight, *dbias;
     int64_t cols;
     int P, wdtype;
 };
-constexpr int kJoinWarps = 16;
+constexpr int kJoinWarps = 32;
 __global__ void __launch_bounds__(32 * kJoinWarps) norm_grad_join_kernel(const __grid_constant__ NormJoinArgs a)
 {
     stream_order();
-    __shared__ float s[kJoinWarps][32];
+    __shared__ float2 s[kJoinWarps][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + lane;
-    for (int which = 0; which < 2; ++which) {
-        void *out = which ? a.dbias : a.dweight;
-        if (!out) continue;
-        float t = 0.0f;
-        if (c < a.cols)
-            for (int p = warp; p < a.P; p += kJoinWarps) t += a.part[((int64_t)which * a.P + p) * a.cols + c];
-        s[warp][lane] = t;
-        __syncthreads();
-        if (warp == 0 && c < a.cols) {
-            for (int i = 1; i < kJoinWarps; ++i) t += s[i][lane];
-            store_any(out, c, a.wdtype, t);
-        }
-        __syncthreads();
+    float2 t = both(0.0f);
+    if (c < a.cols) {
+#pragma unroll 8
+        for (int p = warp; p < a.P; p += kJoinWarps)
+            t = add2(t, make_float2(a.part[(int64_t)p * a.cols + c], a.part[((int64_t)a.P + p) * a.cols + c]));
+    }
+    s[warp][lane] = t;
+    __syncthreads();
+    // column `warp` of the block by warp: its kJoinWarps sums in a fixed tree
+    t = s[lane][warp];
+    t.x = warp_sum(t.x);
+    t.y = warp_sum(t.y);
+    const int64_t mine = (int64_t)blockIdx.x * 32 + warp;
+    if (lane == 0 && mine < a.cols) {
+        if (a.dweight) store_any(a.dweight, mine, a.wdtype, t.x);
+        if (a.dbias) store_any(a.dbias, mine, a.wdtype, t.y);
     }
 }
 
@@ -567,11 +615,11 @@ const void *norm_grad_fn(int el, bool vec, bool group)
 void row_shape(int64_t rows, int64_t cols, bool vec, int sms, const int *most, int *el, int *warps)
 {
     auto need = [&](int e) { return (cols + 32 * e - 1) / (32 * e); };
-    if (rows <= sms && need(8) <= most[0]) *el = 8;
+    if ((rows <= sms || !vec) && need(8) <= most[0]) *el = 8;
     else if (cols <= 256) *el = 8;
     else if (cols <= 512) *el = 16;
     else if (cols <= 1024 && vec) *el = 32;
-    else *el = need(16) <= most[1] ? 16 : 32;
+    else *el = need(16) <= (vec ? 8 : most[1]) ? 16 : 32;
     const int64_t n = need(*el);
     *warps = n <= most[*el == 8 ? 0 : *el == 16 ? 1 : 2] ? (int)n : 0;
 }
@@ -836,7 +884,7 @@ extern "C" rr_status rr_layer_norm_backward(const void *dy, const void *x, const
                                                 : norm_grad_fn<__half>(el, vec, group);
             const int64_t per = group ? 1 : rows >= 8 * (int64_t)sms ? 8 : (rows + sms - 1) / sms;
             const int threads = 32 * (group ? warps : (int)per);
-            const int ring = vec ? 2 * kGradStages * threads * el * eb : 0, sums_bytes = group ? 0 : (int)cols * 4;
+            const int ring = vec ? 2 * kGradStages * threads * el * eb : 0, sums_bytes = group ? 0 : threads * el * 8;
             const int smem = ring > sums_bytes ? ring : sums_bytes;
             int fit = 0;
             RR_TRY(blocks_per_sm(fn, threads, smem, &fit));
