@@ -557,29 +557,6 @@ std::mutex g_mu;
 std::map<int, int> g_sms;
 std::map<std::pair<const void *, std::pair<int, int>>, int> g_fit;
 
-// Most dynamic shared memory of a block: the 227 KB of an SM less room for
-// the kernels' few static words.
-constexpr int kMaxDynamic = 224 * 1024;
-
-// Blocks of this kernel that fit one SM.
-rr_status blocks_per_sm(const void *fn, int threads, int smem, int *out)
-{
-    std::lock_guard<std::mutex> lock(g_mu);
-    const auto key = std::make_pair(fn, std::make_pair(threads, smem));
-    auto it = g_fit.find(key);
-    if (it == g_fit.end()) {
-        int fit = 0;
-        cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamic);
-        if (e != cudaSuccess) return step_cuda_fail(e, "cudaFuncSetAttribute(maxDynamicSharedMemorySize)");
-        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, fn, threads, smem);
-        if (e != cudaSuccess) return step_cuda_fail(e, "cudaOccupancyMaxActiveBlocksPerMultiprocessor");
-        if (fit < 1) return step_fail(RR_ERR_CUDA, "a block of %d threads does not fit the device", threads);
-        it = g_fit.emplace(key, fit).first;
-    }
-    *out = it->second;
-    return RR_OK;
-}
-
 template <class T, bool VEC, bool GROUP>
 const void *norm_rows_fn(int el)
 {
@@ -684,6 +661,28 @@ bool vector_rows(const void *p, int64_t stride, int64_t rows, int eb)
 
 }  // namespace
 
+// Most dynamic shared memory of a block: the 227 KB of an SM less room for
+// the kernels' few static words.
+constexpr int kMaxDynamic = 224 * 1024;
+
+rr_status step_fit(const void *fn, int threads, int smem, int *out)
+{
+    std::lock_guard<std::mutex> lock(g_mu);
+    const auto key = std::make_pair(fn, std::make_pair(threads, smem));
+    auto it = g_fit.find(key);
+    if (it == g_fit.end()) {
+        int fit = 0;
+        cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamic);
+        if (e != cudaSuccess) return step_cuda_fail(e, "cudaFuncSetAttribute(maxDynamicSharedMemorySize)");
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, fn, threads, smem);
+        if (e != cudaSuccess) return step_cuda_fail(e, "cudaOccupancyMaxActiveBlocksPerMultiprocessor");
+        if (fit < 1) return step_fail(RR_ERR_CUDA, "a block of %d threads does not fit the device", threads);
+        it = g_fit.emplace(key, fit).first;
+    }
+    *out = it->second;
+    return RR_OK;
+}
+
 rr_status step_sms(int *sms)
 {
     int dev = -1;
@@ -780,7 +779,7 @@ extern "C" rr_status rr_layer_norm(const void *x, const void *weight, const void
         blocks = (rows + per - 1) / per;
     }
     int fit = 0;
-    RR_TRY(blocks_per_sm(fn, threads, smem, &fit));
+    RR_TRY(step_fit(fn, threads, smem, &fit));
     const int64_t most = (int64_t)fit * sms;
     RR_TRY(step_launch(fn, blocks < most ? blocks : most, threads, smem, &a, stream));
     return step_ok();
@@ -887,7 +886,7 @@ extern "C" rr_status rr_layer_norm_backward(const void *dy, const void *x, const
             const int ring = vec ? 2 * kGradStages * threads * el * eb : 0, sums_bytes = group ? 0 : threads * el * 8;
             const int smem = ring > sums_bytes ? ring : sums_bytes;
             int fit = 0;
-            RR_TRY(blocks_per_sm(fn, threads, smem, &fit));
+            RR_TRY(step_fit(fn, threads, smem, &fit));
             int64_t blocks = (rows + per - 1) / per;
             if (blocks > (int64_t)fit * sms) blocks = (int64_t)fit * sms;
             if (blocks > kMaxPartials) blocks = kMaxPartials;

@@ -7,8 +7,10 @@
 // deal out in turn; a block finds a chunk's tensor by bisection.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 #include <vector>
 
+#include "rr_round.cuh"
 #include "rr_step.h"
 
 namespace rr {
@@ -57,10 +59,11 @@ struct GradNormArgs {
     double *part;  // this launch's partial sums
 };
 
-// Squares of values in [2^-50, 2^40] stay normal in binary32 and sums of 2^40
-// of them finite.  A vector whose largest magnitude lies outside (and is not
-// 0) goes to a binary64 sum; NaN fails the comparison and goes there too.
-__device__ __forceinline__ bool plain_range(float top) { return top <= 0x1p40f && !(top < 0x1p-50f && top > 0.0f); }
+// Sums of squares in [2^-90, 2^90] are sound in binary32: every square that
+// underflowed is below 2^-126 and lost in the sum's own rounding, and 2^30 such
+// sums stay finite.  A thread's sum of a chunk that lies outside (zeros aside)
+// is taken again in binary64; NaN fails the comparison and goes there too.
+__device__ __forceinline__ bool sound(float sum) { return sum >= 0x1p-90f && sum <= 0x1p90f; }
 
 template <class T, int CAP>
 __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ GradNormArgs<CAP> a)
@@ -77,47 +80,50 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
         const T *g = static_cast<const T *>(a.g[t]);
         const int64_t n = a.list.size[t], c = chunk - a.list.start[t];
         const int head = a.list.head[t];
-        float sum = 0.0f;
-        auto one = [&](float x) {
-            if (plain_range(fabsf(x))) sum = fmaf(x, x, sum);
-            else wide += (double)x * x;
-        };
-        if (c == 0 && (int)threadIdx.x < head && (int64_t)threadIdx.x < n) one(to_f32(g[threadIdx.x]));
         const int64_t e0 = head + c * C + (int64_t)threadIdx.x * E;
         Pack<T, E> v[kNormUnroll];
+        if (head + (c + 1) * C <= n) {
 #pragma unroll
-        for (int j = 0; j < kNormUnroll; ++j) {
-            const int64_t e = e0 + (int64_t)j * kThreads * E;
-            if (e + E <= n) {
-                v[j] = *reinterpret_cast<const Pack<T, E> *>(g + e);
-            } else {
+            for (int j = 0; j < kNormUnroll; ++j)
+                v[j] = *reinterpret_cast<const Pack<T, E> *>(g + e0 + j * kThreads * E);
+        } else {
 #pragma unroll
-                for (int k = 0; k < E; ++k) v[j].v[k] = e + k < n ? g[e + k] : from_f32<T>(0.0f);
+            for (int j = 0; j < kNormUnroll; ++j) {
+                const int64_t e = e0 + (int64_t)j * kThreads * E;
+                if (e + E <= n) {
+                    v[j] = *reinterpret_cast<const Pack<T, E> *>(g + e);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < E; ++k) v[j].v[k] = e + k < n ? g[e + k] : from_f32<T>(0.0f);
+                }
             }
         }
-        float acc[2] = {0.0f, 0.0f};
+        float2 acc[2] = {both(0.0f), both(0.0f)};
 #pragma unroll
         for (int j = 0; j < kNormUnroll; ++j) {
-            float top = 0.0f;
-            bool bad = false;
 #pragma unroll
-            for (int k = 0; k < E; ++k) {
-                const float x = to_f32(v[j].v[k]);
-                bad |= x != x;
-                top = fmaxf(top, fabsf(x));
+            for (int k = 0; k < E; k += 2) {
+                const float2 x = pair_f32(&v[j].v[k]);
+                acc[j & 1] = fma2(x, x, acc[j & 1]);
             }
-            if (!bad && plain_range(top)) {
+        }
+        acc[0] = add2(acc[0], acc[1]);
+        float sum = acc[0].x + acc[0].y;
+        if (!sound(sum)) {
+            sum = 0.0f;
+#pragma unroll
+            for (int j = 0; j < kNormUnroll; ++j) {
 #pragma unroll
                 for (int k = 0; k < E; ++k) {
                     const float x = to_f32(v[j].v[k]);
-                    acc[k & 1] = fmaf(x, x, acc[k & 1]);
+                    if (x != 0.0f) wide += (double)x * x;
                 }
-            } else {
-#pragma unroll
-                for (int k = 0; k < E; ++k) wide += (double)to_f32(v[j].v[k]) * to_f32(v[j].v[k]);
             }
         }
-        sum += acc[0] + acc[1];
+        if (c == 0 && (int)threadIdx.x < head && (int64_t)threadIdx.x < n) {
+            const float x = to_f32(g[threadIdx.x]);
+            wide += (double)x * x;
+        }
         // hi + lo += sum without losing the low bits (Knuth's two-sum)
         const float t0 = __fadd_rn(hi, sum), z = __fsub_rn(t0, hi);
         lo += __fadd_rn(__fsub_rn(hi, __fsub_rn(t0, z)), __fsub_rn(sum, z));
@@ -174,6 +180,7 @@ struct AdamScalars {
     float inv_c2;                    // 1 / sqrt(1 - beta2^step)
     float step_size;                 // lr / (1 - beta1^step)
     float eps;
+    float minus_zero;                // -0, for mul2_apart
     const float *scale;
 };
 
@@ -274,15 +281,17 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
 // registers.
 constexpr int kBlock = RR_ADAMW8_BLOCK;
 constexpr int kLane = kBlock / 32;
+constexpr int kAdam8Run = 16; // blocks of a chunk where there are many
 
 template <int CAP>
 struct Adam8Args {
-    Chunks<CAP> list;  // chunk = block of kBlock elements
+    Chunks<CAP> list;  // chunk = run of blocks of kBlock elements
     void *p[CAP];
     const void *g[CAP];
     uint8_t *m[CAP], *r[CAP];
     float *ms[CAP], *rs[CAP], *w[CAP];
     AdamScalars h;
+    int run;               // blocks of a chunk
     uint32_t seed, first;  // first: index in the caller's list of this launch's first tensor
 };
 
@@ -314,6 +323,21 @@ __device__ __forceinline__ float round_to_code(float t, uint32_t u)
     const uint32_t bits = (__float_as_uint(__fadd_rn(t, lift)) + (u << 4) + 8u) & 0xFFF00000u;
     return __fsub_rn(__uint_as_float(bits), lift);
 }
+// The same for |x| / scale of at least 2^-6, sign and all.
+__device__ __forceinline__ float cut_to_code(float t, uint32_t u)
+{
+    return __uint_as_float((__float_as_uint(t) + (u * 16u + 8u)) & 0xFFF00000u);
+}
+// A positive root is stored as no less than the smallest code.
+__device__ __forceinline__ float floor_code(float t) { return t > 0.0f ? fmaxf(t, 0x1p-9f) : t; }
+// 32 random bits of an element.
+__device__ __forceinline__ uint32_t dither(uint32_t element, uint32_t key)
+{
+    uint32_t u = element * 0x9E3779B1u + key;
+    u ^= u >> 16;
+    u *= 0x7FEB352Du;
+    return u ^ (u >> 15);
+}
 __device__ __forceinline__ uint16_t to_codes(float lo, float hi)
 {
     uint16_t c;
@@ -327,146 +351,188 @@ __device__ __forceinline__ float2 from_codes(uint16_t c)
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 
-// The lane's elements: 8 in a row (VEC) or every 32nd.
-template <bool VEC>
-__device__ __forceinline__ int lane_element(int k, int lane) { return VEC ? lane * kLane + k : k * 32 + lane; }
+// What a lane holds of a block: 8 elements in a row (VEC) or every 32nd, in
+// memory's types until they are used, so that the next block's loads cost few
+// registers.
+template <class W, class G, bool VEC>
+struct Lane8 {
+    Pack<W, kLane> w;
+    Pack<G, kLane> g;
+    uint2 m, r;
+    float ms, rs;
 
-template <class T, bool VEC>
-__device__ __forceinline__ void load_lane(float (&x)[kLane], const T *src, int lane, int left)
-{
-    if (VEC) {
-        constexpr int E = 16 / (int)sizeof(T) < kLane ? 16 / (int)sizeof(T) : kLane;
+    static __device__ __forceinline__ int element(int k, int lane) { return VEC ? lane * kLane + k : k * 32 + lane; }
+
+    template <class T>
+    static __device__ __forceinline__ void load(Pack<T, kLane> &x, const T *p, int lane, int left)
+    {
+        if (VEC) {
+            constexpr int E = 16 / (int)sizeof(T);
+            const Pack<T, E> *v = reinterpret_cast<const Pack<T, E> *>(p + lane * kLane);
 #pragma unroll
-        for (int j = 0; j < kLane; j += E) {
-            const Pack<T, E> v = *reinterpret_cast<const Pack<T, E> *>(src + lane * kLane + j);
+            for (int j = 0; j < kLane / E; ++j) reinterpret_cast<Pack<T, E> *>(&x)[j] = v[j];
+        } else {
 #pragma unroll
-            for (int k = 0; k < E; ++k) x[j + k] = to_f32(v.v[k]);
+            for (int k = 0; k < kLane; ++k) {
+                const int e = element(k, lane);
+                x.v[k] = e < left ? p[e] : from_f32<T>(0.0f);
+            }
         }
-    } else {
+    }
+    static __device__ __forceinline__ uint2 load(const uint8_t *p, int lane, int left)
+    {
+        if (VEC) return *reinterpret_cast<const uint2 *>(p + lane * kLane);
+        uint32_t c[2] = {0, 0};
 #pragma unroll
         for (int k = 0; k < kLane; ++k) {
-            const int e = lane_element<false>(k, lane);
-            x[k] = e < left ? to_f32(src[e]) : 0.0f;
+            const int e = element(k, lane);
+            c[k / 4] |= (e < left ? (uint32_t)p[e] : 0u) << 8 * (k % 4);
+        }
+        return make_uint2(c[0], c[1]);
+    }
+    template <class T>
+    static __device__ __forceinline__ void store(T *p, const float2 (&x)[kLane / 2], int lane, int left)
+    {
+        if (VEC) {
+            Pack<T, kLane> y;
+#pragma unroll
+            for (int k = 0; k < kLane; k += 2) pair_set(&y.v[k], x[k / 2]);
+            constexpr int E = 16 / (int)sizeof(T);
+            Pack<T, E> *v = reinterpret_cast<Pack<T, E> *>(p + lane * kLane);
+#pragma unroll
+            for (int j = 0; j < kLane / E; ++j) v[j] = reinterpret_cast<Pack<T, E> *>(&y)[j];
+        } else {
+#pragma unroll
+            for (int k = 0; k < kLane; ++k) {
+                const int e = element(k, lane);
+                if (e < left) p[e] = from_f32<T>(k & 1 ? x[k / 2].y : x[k / 2].x);
+            }
         }
     }
-}
-template <class T, bool VEC>
-__device__ __forceinline__ void store_lane(const float (&x)[kLane], T *dst, int lane, int left)
-{
-    if (VEC) {
-        constexpr int E = 16 / (int)sizeof(T) < kLane ? 16 / (int)sizeof(T) : kLane;
+    static __device__ __forceinline__ void store(uint8_t *p, const float2 (&x)[kLane / 2], int lane, int left)
+    {
+        uint16_t c[kLane / 2];
 #pragma unroll
-        for (int j = 0; j < kLane; j += E) {
-            Pack<T, E> v;
+        for (int k = 0; k < kLane / 2; ++k) c[k] = to_codes(x[k].x, x[k].y);
+        if (VEC) {
+            *reinterpret_cast<uint2 *>(p + lane * kLane) =
+                make_uint2((uint32_t)c[0] | (uint32_t)c[1] << 16, (uint32_t)c[2] | (uint32_t)c[3] << 16);
+        } else {
 #pragma unroll
-            for (int k = 0; k < E; ++k) v.v[k] = from_f32<T>(x[j + k]);
-            *reinterpret_cast<Pack<T, E> *>(dst + lane * kLane + j) = v;
-        }
-    } else {
-#pragma unroll
-        for (int k = 0; k < kLane; ++k) {
-            const int e = lane_element<false>(k, lane);
-            if (e < left) dst[e] = from_f32<T>(x[k]);
+            for (int k = 0; k < kLane; ++k) {
+                const int e = element(k, lane);
+                if (e < left) p[e] = (uint8_t)(c[k / 2] >> 8 * (k & 1));
+            }
         }
     }
-}
-template <bool VEC>
-__device__ __forceinline__ void load_codes(float (&x)[kLane], const uint8_t *src, int lane, int left)
-{
-    uint16_t c[kLane / 2];
-    if (VEC) {
-        const uint2 v = *reinterpret_cast<const uint2 *>(src + lane * kLane);
-        c[0] = (uint16_t)v.x;
-        c[1] = (uint16_t)(v.x >> 16);
-        c[2] = (uint16_t)v.y;
-        c[3] = (uint16_t)(v.y >> 16);
-    } else {
-#pragma unroll
-        for (int k = 0; k < kLane; k += 2) {
-            const int e = lane_element<false>(k, lane), f = lane_element<false>(k + 1, lane);
-            c[k / 2] = (uint16_t)((e < left ? src[e] : 0) | (f < left ? src[f] : 0) << 8);
-        }
+    // W is the master weight's type where there is one, else the parameter's.
+    __device__ __forceinline__ void load(const W *wp, const G *gp, const uint8_t *mp, const uint8_t *rp, const float *msp,
+                                         const float *rsp, int lane, int left)
+    {
+        load(w, wp, lane, left);
+        load(g, gp, lane, left);
+        m = load(mp, lane, left);
+        r = load(rp, lane, left);
+        ms = *msp;
+        rs = *rsp;
     }
-#pragma unroll
-    for (int k = 0; k < kLane; k += 2) {
-        const float2 v = from_codes(c[k / 2]);
-        x[k] = v.x;
-        x[k + 1] = v.y;
-    }
-}
-template <bool VEC>
-__device__ __forceinline__ void store_codes(const float (&x)[kLane], uint8_t *dst, int lane, int left)
-{
-    uint16_t c[kLane / 2];
-#pragma unroll
-    for (int k = 0; k < kLane; k += 2) c[k / 2] = to_codes(x[k], x[k + 1]);
-    if (VEC) {
-        *reinterpret_cast<uint2 *>(dst + lane * kLane) =
-            make_uint2((uint32_t)c[0] | (uint32_t)c[1] << 16, (uint32_t)c[2] | (uint32_t)c[3] << 16);
-    } else {
-#pragma unroll
-        for (int k = 0; k < kLane; ++k) {
-            const int e = lane_element<false>(k, lane);
-            if (e < left) dst[e] = (uint8_t)(c[k / 2] >> (k & 1 ? 8 : 0));
-        }
-    }
-}
+};
 
 __device__ __forceinline__ uint32_t warp_max(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
-
-template <class P, class G, bool MASTER, bool VEC, int CAP>
-__device__ __forceinline__ void adamw8_block(const Adam8Args<CAP> &a, float scale, int t, int64_t b, int lane, int left)
+__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+__device__ __forceinline__ float2 codes_of(uint2 c, int k)
 {
-    const int64_t at = b * kBlock;
-    P *p = static_cast<P *>(a.p[t]) + at;
-    const G *g = static_cast<const G *>(a.g[t]) + at;
-    uint8_t *mc = a.m[t] + at, *rc = a.r[t] + at;
-    float *master = MASTER ? a.w[t] + at : nullptr;
+    const uint32_t word = k < 2 ? c.x : c.y;
+    return from_codes((uint16_t)(k & 1 ? word >> 16 : word));
+}
 
-    float w[kLane], gr[kLane], m[kLane], r[kLane];
-    if (MASTER) load_lane<float, VEC>(w, master, lane, left);
-    else load_lane<P, VEC>(w, p, lane, left);
-    load_lane<G, VEC>(gr, g, lane, left);
-    load_codes<VEC>(m, mc, lane, left);
-    load_codes<VEC>(r, rc, lane, left);
-    const float ms = a.ms[t][b], rs = a.rs[t][b];
-    uint32_t mtop = 0, rtop = 0;
+// One block of one tensor, loaded before: its step, weights and states stored.
+template <class P, class W, class G, bool MASTER, bool VEC>
+__device__ __forceinline__ void adamw8_block(const AdamScalars &h, float scale, uint32_t key, const Lane8<W, G, VEC> &in,
+                                             P *p, float *master, uint8_t *mp, uint8_t *rp, float *msp, float *rsp,
+                                             uint32_t at, int lane, int left)
+{
+    using L = Lane8<W, G, VEC>;
+    float2 w[kLane / 2], m[kLane / 2], r[kLane / 2], v[kLane / 2];
+    const float2 ms = both(in.ms), rs = both(in.rs), b1 = both(h.beta1), b2 = both(h.beta2),
+                 nz = both(h.minus_zero);
+    uint32_t mtop = 0;
+    float vlow = 3e38f, vtop = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kLane; ++k) {
-        m[k] = __fmul_rn(m[k], ms);
-        const float root = __fmul_rn(r[k], rs);
-        float v = __fmul_rn(root, root);
-        w[k] = adam_element(a.h, scale, w[k], gr[k], m[k], v, r[k]);
-        mtop = max(mtop, __float_as_uint(m[k]) & 0x7FFFFFFFu);
-        rtop = max(rtop, __float_as_uint(r[k]) & 0x7FFFFFFFu);
+    for (int k = 0; k < kLane / 2; ++k) {
+        const float2 g = mul2(pair_f32(&in.g.v[2 * k]), both(scale));
+        m[k] = add2(mul2_apart(mul2(codes_of(in.m, k), ms), b1, nz), mul2_apart(g, both(h.omb1), nz));
+        r[k] = mul2(codes_of(in.r, k), rs);
+        v[k] = add2(mul2_apart(mul2(r[k], r[k]), b2, nz), mul2_apart(mul2(g, both(h.omb2)), g, nz));
+        mtop = max(mtop, max(magnitude(m[k].x), magnitude(m[k].y)));
+        vlow = fminf(vlow, fminf(v[k].x, v[k].y));
+        vtop = fmaxf(vtop, fmaxf(v[k].x, v[k].y));
+        w[k] = pair_f32(&in.w.v[2 * k]);
     }
-    if (MASTER) store_lane<float, VEC>(w, master, lane, left);
-    store_lane<P, VEC>(w, p, lane, left);
+    // The fast roots and quotients round as sqrt and / do while their operands
+    // keep away from binary32's ends; a lane with one that does not (a v of 0
+    // among them) takes sqrt and / for all 8.
+    const float2 decay = both(h.decay), size = both(-h.step_size);
+    if (vlow >= 0x1p-100f && vtop <= 0x1p100f && mtop <= 0x71800000u /* 2^100 */ && h.eps <= 0x1p60f) {
+        const float2 nc2 = both(-h.inv_c2), neps = both(-h.eps);
+#pragma unroll
+        for (int k = 0; k < kLane / 2; ++k) {
+            r[k] = root2(v[k], make_float2(-v[k].x, -v[k].y));
+            const float2 q = quotient2(m[k], add2(mul2_apart(r[k], nc2, nz), neps));
+            w[k] = add2(mul2_apart(w[k], decay, nz), mul2_apart(q, size, nz));
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < kLane / 2; ++k) {
+            r[k] = make_float2(__fsqrt_rn(v[k].x), __fsqrt_rn(v[k].y));
+            const float2 den = add2(mul2_apart(r[k], both(h.inv_c2), nz), both(h.eps));
+            w[k] = add2(mul2_apart(w[k], decay, nz), mul2_apart(make_float2(__fdiv_rn(m[k].x, den.x), __fdiv_rn(m[k].y, den.y)), size, nz));
+        }
+    }
+    uint32_t rtop = 0;
+#pragma unroll
+    for (int k = 0; k < kLane / 2; ++k) rtop = max(rtop, max(magnitude(r[k].x), magnitude(r[k].y)));
+    if (MASTER) L::store(master, w, lane, left);
+    L::store(p, w, lane, left);
 
     mtop = warp_max(mtop);
     rtop = warp_max(rtop);
     const bool mfine = mtop < 0x7F800000u, rfine = rtop < 0x7F800000u;
     const int me = scale_exponent(mtop), re = scale_exponent(rtop);
-    const float minv = mfine ? exp2_int(-me) : 0.0f, rinv = rfine ? exp2_int(-re) : 0.0f;
-    const uint32_t key = mix32(a.seed + (a.first + (uint32_t)t + 1u) * 0x9E3779B9u);
+    const float2 minv = both(mfine ? exp2_int(-me) : 0.0f), rinv = both(rfine ? exp2_int(-re) : 0.0f);
+    // (x / scale) on the code's grid: adding random bits just below the last
+    // kept mantissa bit and cutting there rounds up with the probability of the
+    // part cut off.  Signs stay out of it.
+    float low = 3e38f;
+    float2 mq[kLane / 2], rq[kLane / 2];
 #pragma unroll
-    for (int k = 0; k < kLane; ++k) {
-        uint32_t u = (uint32_t)(at + lane_element<VEC>(k, lane)) * 0x9E3779B1u + key;
-        u ^= u >> 16;
-        u *= 0x7FEB352Du;
-        u ^= u >> 15;
-        const float mt = round_to_code(fabsf(__fmul_rn(m[k], minv)), u & 0xFFFFu);
-        m[k] = mfine ? copysignf(mt, m[k]) : 0.0f;
-        float rt = __fmul_rn(r[k], rinv);
-        if (r[k] > 0.0f) rt = fmaxf(rt, 0x1p-9f);
-        r[k] = rfine ? round_to_code(rt, u >> 16) : 0.0f;
+    for (int k = 0; k < kLane / 2; ++k) {
+        m[k] = mul2(m[k], minv);
+        r[k] = mul2(r[k], rinv);
+        low = fminf(low, fminf(fminf(fabsf(m[k].x), fabsf(m[k].y)), fminf(r[k].x, r[k].y)));
+        const uint32_t u0 = dither(at + L::element(2 * k, lane), key), u1 = dither(at + L::element(2 * k + 1, lane), key);
+        mq[k] = make_float2(cut_to_code(m[k].x, u0 & 0xFFFFu), cut_to_code(m[k].y, u1 & 0xFFFFu));
+        rq[k] = make_float2(cut_to_code(r[k].x, u0 >> 16), cut_to_code(r[k].y, u1 >> 16));
     }
-    store_codes<VEC>(m, mc, lane, left);
-    store_codes<VEC>(r, rc, lane, left);
+    // Below 2^-6 the grid is even; a lane with such a value (or a block that is
+    // not finite) takes the long way.
+    if (!(low >= 0x1p-6f) || !mfine || !rfine) {
+#pragma unroll
+        for (int k = 0; k < kLane / 2; ++k) {
+            const uint32_t u0 = dither(at + L::element(2 * k, lane), key), u1 = dither(at + L::element(2 * k + 1, lane), key);
+            mq[k] = make_float2(copysignf(round_to_code(fabsf(m[k].x), u0 & 0xFFFFu), m[k].x),
+                                copysignf(round_to_code(fabsf(m[k].y), u1 & 0xFFFFu), m[k].y));
+            rq[k] = make_float2(round_to_code(floor_code(r[k].x), u0 >> 16), round_to_code(floor_code(r[k].y), u1 >> 16));
+            if (!mfine) mq[k] = both(0.0f);
+            if (!rfine) rq[k] = both(0.0f);
+        }
+    }
+    L::store(mp, mq, lane, left);
+    L::store(rp, rq, lane, left);
     if (lane == 0) {
         const float nan = __int_as_float(0x7fc00000);
-        a.ms[t][b] = mfine ? exp2_int(me) : nan;
-        a.rs[t][b] = rfine ? exp2_int(re) : nan;
+        *msp = mfine ? exp2_int(me) : nan;
+        *rsp = rfine ? exp2_int(re) : nan;
     }
 }
 
@@ -474,6 +540,7 @@ template <class P, class G, bool MASTER, int CAP>
 __global__ void __launch_bounds__(kThreads) adamw8_kernel(const __grid_constant__ Adam8Args<CAP> a)
 {
     stream_order();
+    using W = typename std::conditional<MASTER, float, P>::type;
     const float scale = a.h.scale ? *a.h.scale : 1.0f;
     if (scale != scale) return;
     const int lane = threadIdx.x & 31;
@@ -481,9 +548,34 @@ __global__ void __launch_bounds__(kThreads) adamw8_kernel(const __grid_constant_
     const int64_t step = (int64_t)gridDim.x * (kThreads / 32);
     for (int64_t chunk = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); chunk < total; chunk += step) {
         const int t = a.list.find(chunk);
-        const int64_t b = chunk - a.list.start[t], left = a.list.size[t] - b * kBlock;
-        if (a.list.head[t] == 0 && left >= kBlock) adamw8_block<P, G, MASTER, true>(a, scale, t, b, lane, kBlock);
-        else adamw8_block<P, G, MASTER, false>(a, scale, t, b, lane, left < kBlock ? (int)left : kBlock);
+        const int64_t b = (chunk - a.list.start[t]) * a.run, at = b * kBlock;
+        int64_t left = a.list.size[t] - at;
+        P *p = static_cast<P *>(a.p[t]) + at;
+        const G *g = static_cast<const G *>(a.g[t]) + at;
+        uint8_t *m = a.m[t] + at, *r = a.r[t] + at;
+        float *ms = a.ms[t] + b, *rs = a.rs[t] + b, *master = MASTER ? a.w[t] + at : nullptr;
+        const W *w = MASTER ? reinterpret_cast<const W *>(master) : reinterpret_cast<const W *>(p);
+        const uint32_t key = mix32(a.seed + (a.first + (uint32_t)t + 1u) * 0x9E3779B9u);
+        int i = 0;
+        if (a.list.head[t] == 0 && left >= kBlock) {  // whole blocks; the next one's loads run ahead
+            Lane8<W, G, true> cur, next;
+            cur.load(w, g, m, r, ms, rs, lane, kBlock);
+            for (; i < a.run && left >= kBlock; ++i, left -= kBlock) {
+                const int e = (i + 1) * kBlock;
+                if (i + 1 < a.run && left >= 2 * kBlock) next.load(w + e, g + e, m + e, r + e, ms + i + 1, rs + i + 1, lane, kBlock);
+                adamw8_block<P, W, G, MASTER, true>(a.h, scale, key, cur, p + i * kBlock, master + (MASTER ? i * kBlock : 0),
+                                                    m + i * kBlock, r + i * kBlock, ms + i, rs + i,
+                                                    (uint32_t)at + i * kBlock, lane, kBlock);
+                cur = next;
+            }
+        }
+        for (; i < a.run && left > 0; ++i, left -= kBlock) {
+            const int e = i * kBlock, n = left < kBlock ? (int)left : kBlock;
+            Lane8<W, G, false> cur;
+            cur.load(w + e, g + e, m + e, r + e, ms + i, rs + i, lane, n);
+            adamw8_block<P, W, G, MASTER, false>(a.h, scale, key, cur, p + e, master + (MASTER ? e : 0), m + e, r + e, ms + i,
+                                                 rs + i, (uint32_t)at + e, lane, n);
+        }
     }
 }
 
@@ -494,16 +586,33 @@ struct Span {
     bool written;
 };
 struct Spans {
-    std::vector<Span> all;
+    std::vector<Span> all, spare;
+    std::vector<size_t> cuts;
     void add(const void *p, int64_t bytes, bool written)
     {
         const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
         if (p && bytes > 0) all.push_back(Span{lo, lo + (uintptr_t)bytes, written});
     }
+    // Sorts by address, joining ascending stretches (a list over a flat buffer
+    // is one), and looks at neighbours.
     bool touch()
     {
         auto before = [](const Span &x, const Span &y) { return x.lo < y.lo; };
-        if (!std::is_sorted(all.begin(), all.end(), before)) std::sort(all.begin(), all.end(), before);
+        std::vector<size_t> &cut = cuts;
+        for (;;) {
+            cut.assign(1, 0);
+            for (size_t i = 1; i < all.size(); ++i)
+                if (before(all[i], all[i - 1])) cut.push_back(i);
+            cut.push_back(all.size());
+            if (cut.size() <= 2) break;
+            spare.resize(all.size());
+            for (size_t k = 0; k + 1 < cut.size(); k += 2) {
+                const size_t mid = cut[k + 1], end = k + 2 < cut.size() ? cut[k + 2] : mid;
+                std::merge(all.begin() + cut[k], all.begin() + mid, all.begin() + mid, all.begin() + end,
+                           spare.begin() + cut[k], before);
+            }
+            all.swap(spare);
+        }
         uintptr_t any = 0, written = 0;
         for (const Span &s : all) {
             if (s.lo < written || (s.written && s.lo < any)) return true;
@@ -566,6 +675,7 @@ AdamScalars scalars(const rr_adamw_hyper &h, const float *scale)
     s.inv_c2 = (float)(1.0 / std::sqrt(1.0 - std::pow(h.beta2, (double)h.step)));
     s.step_size = (float)(h.lr / (1.0 - std::pow(h.beta1, (double)h.step)));
     s.eps = (float)h.eps;
+    s.minus_zero = -0.0f;
     s.scale = scale;
     return s;
 }
@@ -577,22 +687,18 @@ int64_t chunks_of(int64_t size, int head, int64_t chunk)
     return body <= 0 ? 1 : (body + chunk - 1) / chunk;
 }
 
-// Blocks that fit an SM for these kernels (256 threads, no shared memory to
-// speak of), by registers: the grid is at most this many waves' worth of one.
-constexpr int kNormPerSm = 8, kAdamPerSm = 4, kAdam8PerSm = 4;
-
-template <class T, int CAP>
-rr_status launch_norm(GradNormArgs<CAP> &a, int64_t grid, cudaStream_t stream)
-{
-    return step_launch((const void *)grad_norm_kernel<T, CAP>, grid, kThreads, 0, &a, stream);
-}
-
 template <int CAP>
 rr_status norm_lists(const void *const *grads, const int64_t *sizes, int count, rr_dtype dtype, int sms, double *part,
                      int64_t *parts, cudaStream_t stream)
 {
     const int eb = float_bytes(dtype), E = 16 / eb;
     const int64_t chunk = (int64_t)kThreads * E * kNormUnroll;
+    const void *fn = dtype == RR_FP32   ? (const void *)grad_norm_kernel<float, CAP>
+                     : dtype == RR_BF16 ? (const void *)grad_norm_kernel<__nv_bfloat16, CAP>
+                                        : (const void *)grad_norm_kernel<__half, CAP>;
+    int fit = 0;
+    RR_TRY(step_fit(fn, kThreads, 0, &fit));
+    const int64_t most = std::min<int64_t>((int64_t)fit * sms, kNormBlocks);
     GradNormArgs<CAP> a;
     for (int i = 0; i < count;) {
         int k = 0;
@@ -607,12 +713,10 @@ rr_status norm_lists(const void *const *grads, const int64_t *sizes, int count, 
         }
         if (k == 0) break;
         a.list.count = k;
-        const int64_t most = std::min<int64_t>((int64_t)kNormPerSm * sms, kNormBlocks);
         const int64_t grid = std::min(a.list.start[k], most);
         a.part = part + *parts;
         *parts += grid;
-        RR_TRY(dtype == RR_FP32 ? launch_norm<float>(a, grid, stream)
-               : dtype == RR_BF16 ? launch_norm<__nv_bfloat16>(a, grid, stream) : launch_norm<__half>(a, grid, stream));
+        RR_TRY(step_launch(fn, grid, kThreads, 0, &a, stream));
     }
     return RR_OK;
 }
@@ -653,6 +757,9 @@ rr_status adamw_lists(void *const *params, const void *const *grads, float *cons
     const int pb = float_bytes(pd), gb = float_bytes(gd);
     AdamArgs<CAP> a;
     a.h = h;
+    const void *fn = adamw_fn_for<CAP>(pd, gd, master != nullptr);
+    int fit = 0;
+    RR_TRY(step_fit(fn, kThreads, 0, &fit));
     for (int i = 0; i < count;) {
         int k = 0;
         a.list.start[0] = 0;
@@ -674,8 +781,7 @@ rr_status adamw_lists(void *const *params, const void *const *grads, float *cons
         }
         if (k == 0) break;
         a.list.count = k;
-        const int64_t grid = std::min<int64_t>(a.list.start[k], (int64_t)kAdamPerSm * sms);
-        RR_TRY(step_launch(adamw_fn_for<CAP>(pd, gd, master != nullptr), grid, kThreads, 0, &a, stream));
+        RR_TRY(step_launch(fn, std::min<int64_t>(a.list.start[k], (int64_t)fit * sms), kThreads, 0, &a, stream));
     }
     return RR_OK;
 }
@@ -688,6 +794,13 @@ rr_status adamw8_lists(void *const *params, const void *const *grads, uint8_t *c
     Adam8Args<CAP> a;
     a.h = h;
     a.seed = seed;
+    const void *fn = adamw8_fn_for<CAP>(pd, gd, master != nullptr);
+    int fit = 0;
+    RR_TRY(step_fit(fn, kThreads, 0, &fit));
+    const int64_t warps = (int64_t)fit * sms * (kThreads / 32);
+    int64_t blocks = 0;
+    for (int i = 0; i < count; ++i) blocks += (sizes[i] + kBlock - 1) / kBlock;
+    a.run = blocks >= kAdam8Run * warps ? kAdam8Run : 1;
     // Tensors keep their place in the caller's list (it enters the random
     // bits), so empty ones stay in the table with no chunks.
     for (int i = 0; i < count;) {
@@ -706,13 +819,12 @@ rr_status adamw8_lists(void *const *params, const void *const *grads, uint8_t *c
                                               aligned_to(r[i], 8) && (!master || aligned_to(master[i], 16))
                                           ? 0 : kNoVector);
             a.list.size[k] = sizes[i];
-            a.list.start[k + 1] = a.list.start[k] + (sizes[i] + kBlock - 1) / kBlock;
+            a.list.start[k + 1] = a.list.start[k] + (sizes[i] + (int64_t)a.run * kBlock - 1) / ((int64_t)a.run * kBlock);
         }
         a.list.count = k;
         if (a.list.start[k] == 0) continue;
         const int64_t want = (a.list.start[k] + kThreads / 32 - 1) / (kThreads / 32);
-        const int64_t grid = std::min<int64_t>(want, (int64_t)kAdam8PerSm * sms);
-        RR_TRY(step_launch(adamw8_fn_for<CAP>(pd, gd, master != nullptr), grid, kThreads, 0, &a, stream));
+        RR_TRY(step_launch(fn, std::min<int64_t>(want, (int64_t)fit * sms), kThreads, 0, &a, stream));
     }
     return RR_OK;
 }

@@ -21,8 +21,9 @@ rr_status step_ok();
 inline int float_bytes(rr_dtype d) { return d == RR_FP32 ? 4 : d == RR_BF16 || d == RR_FP16 ? 2 : 0; }
 inline bool aligned_to(const void *p, int bytes) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)bytes == 0; }
 
-// SMs of the current device.
+// SMs of the current device; blocks of a kernel that fit one of them.
 rr_status step_sms(int *sms);
+rr_status step_fit(const void *fn, int threads, int smem, int *blocks);
 
 // One programmatic launch: the grid may start while the previous kernel in
 // the stream drains; every kernel here begins with stream_order().
@@ -72,7 +73,9 @@ struct alignas(N * sizeof(T) > 16 ? 16 : N * sizeof(T)) Pack {
     T v[N];
 };
 
-// Two binary32 operations in one instruction, each rounded by itself.
+// Two binary32 operations in one instruction.  The assembler contracts a mul2
+// whose result only an add2 takes into one fused operation, whatever its flags
+// say; where the product's own rounding matters, see mul2_apart.
 __device__ __forceinline__ float2 add2(float2 a, float2 b)
 {
     float2 d;
@@ -95,6 +98,10 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
         : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
     return d;
 }
+// A product rounded by itself: fused with an addend of -0 that the compiler
+// cannot see (a kernel argument), it equals the product, and no later addition
+// can be contracted with it.
+__device__ __forceinline__ float2 mul2_apart(float2 a, float2 b, float2 minus_zero) { return fma2(a, b, minus_zero); }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // Two neighbouring elements between memory's type and binary32.
