@@ -181,6 +181,7 @@ struct AdamScalars {
     float step_size;                 // lr / (1 - beta1^step)
     float eps;
     float minus_zero;                // -0, for mul2_apart
+    uint32_t one, sixteen;           // 1 and 16 where the compiler may not turn a multiply-add into shifts and adds
     const float *scale;
 };
 
@@ -281,7 +282,9 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
 // registers.
 constexpr int kBlock = RR_ADAMW8_BLOCK;
 constexpr int kLane = kBlock / 32;
-constexpr int kAdam8Run = 16; // blocks of a chunk where there are many
+constexpr int kAdam8Run = 32;    // most blocks of a run: one for each lane's scales
+constexpr int kAdam8Runs = 4;    // runs of a warp where there are enough blocks
+constexpr int kAdam8Stages = 4;  // blocks of a warp in flight or in use
 
 template <int CAP>
 struct Adam8Args {
@@ -323,10 +326,12 @@ __device__ __forceinline__ float round_to_code(float t, uint32_t u)
     const uint32_t bits = (__float_as_uint(__fadd_rn(t, lift)) + (u << 4) + 8u) & 0xFFF00000u;
     return __fsub_rn(__uint_as_float(bits), lift);
 }
-// The same for |x| / scale of at least 2^-6, sign and all.
-__device__ __forceinline__ float cut_to_code(float t, uint32_t u)
+// The same for |x| / scale of at least 2^-6, sign and all.  The sum is two
+// integer multiply-adds, which run beside the logic units that the rest of the
+// rounding keeps busy.
+__device__ __forceinline__ float cut_to_code(float t, uint32_t u, const AdamScalars &h)
 {
-    return __uint_as_float((__float_as_uint(t) + (u * 16u + 8u)) & 0xFFF00000u);
+    return __uint_as_float((u * h.sixteen + (__float_as_uint(t) * h.one + 8u)) & 0xFFF00000u);
 }
 // A positive root is stored as no less than the smallest code.
 __device__ __forceinline__ float floor_code(float t) { return t > 0.0f ? fmaxf(t, 0x1p-9f) : t; }
@@ -359,7 +364,6 @@ struct Lane8 {
     Pack<W, kLane> w;
     Pack<G, kLane> g;
     uint2 m, r;
-    float ms, rs;
 
     static __device__ __forceinline__ int element(int k, int lane) { return VEC ? lane * kLane + k : k * 32 + lane; }
 
@@ -426,20 +430,62 @@ struct Lane8 {
         }
     }
     // W is the master weight's type where there is one, else the parameter's.
-    __device__ __forceinline__ void load(const W *wp, const G *gp, const uint8_t *mp, const uint8_t *rp, const float *msp,
-                                         const float *rsp, int lane, int left)
+    __device__ __forceinline__ void load(const W *wp, const G *gp, const uint8_t *mp, const uint8_t *rp, int lane, int left)
     {
         load(w, wp, lane, left);
         load(g, gp, lane, left);
         m = load(mp, lane, left);
         r = load(rp, lane, left);
-        ms = *msp;
-        rs = *rsp;
+    }
+
+    // Whole blocks come through a ring in shared memory, kStages blocks of a
+    // warp's run deep: weights, gradients, codes, one after the other.
+    static constexpr int kW = kBlock * (int)sizeof(W), kG = kBlock * (int)sizeof(G), kStage = kW + kG + 2 * kBlock;
+    static __device__ __forceinline__ void fetch(char *s, const W *wp, const G *gp, const uint8_t *mp, const uint8_t *rp,
+                                                 int lane)
+    {
+#pragma unroll
+        for (int j = 0; j < kW; j += 512) fetch16(s + j + lane * 16, reinterpret_cast<const char *>(wp) + j + lane * 16);
+#pragma unroll
+        for (int j = 0; j < kG; j += 512) fetch16(s + kW + j + lane * 16, reinterpret_cast<const char *>(gp) + j + lane * 16);
+        fetch8(s + kW + kG + lane * 8, mp + lane * 8);
+        fetch8(s + kW + kG + kBlock + lane * 8, rp + lane * 8);
+    }
+    __device__ __forceinline__ void take(const char *s, int lane)
+    {
+        load(w, reinterpret_cast<const W *>(s), lane, kBlock);
+        load(g, reinterpret_cast<const G *>(s + kW), lane, kBlock);
+        m = load(reinterpret_cast<const uint8_t *>(s + kW + kG), lane, kBlock);
+        r = load(reinterpret_cast<const uint8_t *>(s + kW + kG + kBlock), lane, kBlock);
     }
 };
 
 __device__ __forceinline__ uint32_t warp_max(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
-__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+// max(|a|, |b|, |c|), NaN if one is; min(a, b, c) and max(a, b, c) of what is not NaN.
+__device__ __forceinline__ float top3(float a, float b, float c)
+{
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float low3(float a, float b, float c)
+{
+    float d;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float high3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float low3_abs(float a, float b, float c)
+{
+    float d;
+    asm("min.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 __device__ __forceinline__ float2 codes_of(uint2 c, int k)
 {
     const uint32_t word = k < 2 ? c.x : c.y;
@@ -449,35 +495,34 @@ __device__ __forceinline__ float2 codes_of(uint2 c, int k)
 // One block of one tensor, loaded before: its step, weights and states stored.
 template <class P, class W, class G, bool MASTER, bool VEC>
 __device__ __forceinline__ void adamw8_block(const AdamScalars &h, float scale, uint32_t key, const Lane8<W, G, VEC> &in,
-                                             P *p, float *master, uint8_t *mp, uint8_t *rp, float *msp, float *rsp,
+                                             float &mscale, float &rscale, P *p, float *master, uint8_t *mp, uint8_t *rp,
                                              uint32_t at, int lane, int left)
 {
     using L = Lane8<W, G, VEC>;
     float2 w[kLane / 2], m[kLane / 2], r[kLane / 2], v[kLane / 2];
-    const float2 ms = both(in.ms), rs = both(in.rs), b1 = both(h.beta1), b2 = both(h.beta2),
+    const float2 ms = both(mscale), rs = both(rscale), b1 = both(h.beta1), b2 = both(h.beta2),
                  nz = both(h.minus_zero);
-    uint32_t mtop = 0;
-    float vlow = 3e38f, vtop = 0.0f;
+    float mtop = 0.0f, rtop = 0.0f, vlow = 3e38f, vtop = 0.0f;
 #pragma unroll
     for (int k = 0; k < kLane / 2; ++k) {
         const float2 g = mul2(pair_f32(&in.g.v[2 * k]), both(scale));
         m[k] = add2(mul2_apart(mul2(codes_of(in.m, k), ms), b1, nz), mul2_apart(g, both(h.omb1), nz));
         r[k] = mul2(codes_of(in.r, k), rs);
         v[k] = add2(mul2_apart(mul2(r[k], r[k]), b2, nz), mul2_apart(mul2(g, both(h.omb2)), g, nz));
-        mtop = max(mtop, max(magnitude(m[k].x), magnitude(m[k].y)));
-        vlow = fminf(vlow, fminf(v[k].x, v[k].y));
-        vtop = fmaxf(vtop, fmaxf(v[k].x, v[k].y));
+        mtop = top3(mtop, m[k].x, m[k].y);
+        vlow = low3(vlow, v[k].x, v[k].y);
+        vtop = high3(vtop, v[k].x, v[k].y);
         w[k] = pair_f32(&in.w.v[2 * k]);
     }
     // The fast roots and quotients round as sqrt and / do while their operands
     // keep away from binary32's ends; a lane with one that does not (a v of 0
     // among them) takes sqrt and / for all 8.
     const float2 decay = both(h.decay), size = both(-h.step_size);
-    if (vlow >= 0x1p-100f && vtop <= 0x1p100f && mtop <= 0x71800000u /* 2^100 */ && h.eps <= 0x1p60f) {
+    if (vlow >= 0x1p-100f && vtop <= 0x1p100f && mtop <= 0x1p100f && h.eps <= 0x1p60f) {
         const float2 nc2 = both(-h.inv_c2), neps = both(-h.eps);
 #pragma unroll
         for (int k = 0; k < kLane / 2; ++k) {
-            r[k] = root2(v[k], make_float2(-v[k].x, -v[k].y));
+            r[k] = root2(v[k], mul2(v[k], both(-1.0f)));
             const float2 q = quotient2(m[k], add2(mul2_apart(r[k], nc2, nz), neps));
             w[k] = add2(mul2_apart(w[k], decay, nz), mul2_apart(q, size, nz));
         }
@@ -489,16 +534,15 @@ __device__ __forceinline__ void adamw8_block(const AdamScalars &h, float scale, 
             w[k] = add2(mul2_apart(w[k], decay, nz), mul2_apart(make_float2(__fdiv_rn(m[k].x, den.x), __fdiv_rn(m[k].y, den.y)), size, nz));
         }
     }
-    uint32_t rtop = 0;
 #pragma unroll
-    for (int k = 0; k < kLane / 2; ++k) rtop = max(rtop, max(magnitude(r[k].x), magnitude(r[k].y)));
+    for (int k = 0; k < kLane / 2; ++k) rtop = top3(rtop, r[k].x, r[k].y);
     if (MASTER) L::store(master, w, lane, left);
     L::store(p, w, lane, left);
 
-    mtop = warp_max(mtop);
-    rtop = warp_max(rtop);
-    const bool mfine = mtop < 0x7F800000u, rfine = rtop < 0x7F800000u;
-    const int me = scale_exponent(mtop), re = scale_exponent(rtop);
+    // bits of magnitudes order as they do, NaN above all
+    const uint32_t mbits = warp_max(__float_as_uint(mtop)), rbits = warp_max(__float_as_uint(rtop));
+    const bool mfine = mbits < 0x7F800000u, rfine = rbits < 0x7F800000u;
+    const int me = scale_exponent(mbits), re = scale_exponent(rbits);
     const float2 minv = both(mfine ? exp2_int(-me) : 0.0f), rinv = both(rfine ? exp2_int(-re) : 0.0f);
     // (x / scale) on the code's grid: adding random bits just below the last
     // kept mantissa bit and cutting there rounds up with the probability of the
@@ -509,10 +553,10 @@ __device__ __forceinline__ void adamw8_block(const AdamScalars &h, float scale, 
     for (int k = 0; k < kLane / 2; ++k) {
         m[k] = mul2(m[k], minv);
         r[k] = mul2(r[k], rinv);
-        low = fminf(low, fminf(fminf(fabsf(m[k].x), fabsf(m[k].y)), fminf(r[k].x, r[k].y)));
+        low = low3_abs(low3_abs(low, m[k].x, m[k].y), r[k].x, r[k].y);
         const uint32_t u0 = dither(at + L::element(2 * k, lane), key), u1 = dither(at + L::element(2 * k + 1, lane), key);
-        mq[k] = make_float2(cut_to_code(m[k].x, u0 & 0xFFFFu), cut_to_code(m[k].y, u1 & 0xFFFFu));
-        rq[k] = make_float2(cut_to_code(r[k].x, u0 >> 16), cut_to_code(r[k].y, u1 >> 16));
+        mq[k] = make_float2(cut_to_code(m[k].x, u0 & 0xFFFFu, h), cut_to_code(m[k].y, u1 & 0xFFFFu, h));
+        rq[k] = make_float2(cut_to_code(r[k].x, u0 >> 16, h), cut_to_code(r[k].y, u1 >> 16, h));
     }
     // Below 2^-6 the grid is even; a lane with such a value (or a block that is
     // not finite) takes the long way.
@@ -529,53 +573,81 @@ __device__ __forceinline__ void adamw8_block(const AdamScalars &h, float scale, 
     }
     L::store(mp, mq, lane, left);
     L::store(rp, rq, lane, left);
-    if (lane == 0) {
-        const float nan = __int_as_float(0x7fc00000);
-        *msp = mfine ? exp2_int(me) : nan;
-        *rsp = rfine ? exp2_int(re) : nan;
-    }
+    const float nan = __int_as_float(0x7fc00000);
+    mscale = mfine ? exp2_int(me) : nan;
+    rscale = rfine ? exp2_int(re) : nan;
 }
 
+// A warp takes runs of up to 32 blocks of one tensor.  Lane i holds the scales
+// of the run's block i, so that they are read and written together.
 template <class P, class G, bool MASTER, int CAP>
 __global__ void __launch_bounds__(kThreads) adamw8_kernel(const __grid_constant__ Adam8Args<CAP> a)
 {
     stream_order();
     using W = typename std::conditional<MASTER, float, P>::type;
+    using L = Lane8<W, G, true>;
+    extern __shared__ uint4 s_ring[];
     const float scale = a.h.scale ? *a.h.scale : 1.0f;
     if (scale != scale) return;
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    char *const ring = reinterpret_cast<char *>(s_ring) + warp * kAdam8Stages * L::kStage;
     const int64_t total = a.list.start[a.list.count];
     const int64_t step = (int64_t)gridDim.x * (kThreads / 32);
-    for (int64_t chunk = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); chunk < total; chunk += step) {
+    for (int64_t chunk = (int64_t)blockIdx.x * (kThreads / 32) + warp; chunk < total; chunk += step) {
         const int t = a.list.find(chunk);
-        const int64_t b = (chunk - a.list.start[t]) * a.run, at = b * kBlock;
-        int64_t left = a.list.size[t] - at;
+        const int64_t b = (chunk - a.list.start[t]) * a.run, at = b * kBlock, left = a.list.size[t] - at;
+        const int blocks = (int)min((int64_t)a.run, (left + kBlock - 1) / kBlock);
+        const int whole = a.list.head[t] == 0 ? (int)min((int64_t)a.run, left / kBlock) : 0;
         P *p = static_cast<P *>(a.p[t]) + at;
         const G *g = static_cast<const G *>(a.g[t]) + at;
         uint8_t *m = a.m[t] + at, *r = a.r[t] + at;
         float *ms = a.ms[t] + b, *rs = a.rs[t] + b, *master = MASTER ? a.w[t] + at : nullptr;
         const W *w = MASTER ? reinterpret_cast<const W *>(master) : reinterpret_cast<const W *>(p);
         const uint32_t key = mix32(a.seed + (a.first + (uint32_t)t + 1u) * 0x9E3779B9u);
-        int i = 0;
-        if (a.list.head[t] == 0 && left >= kBlock) {  // whole blocks; the next one's loads run ahead
-            Lane8<W, G, true> cur, next;
-            cur.load(w, g, m, r, ms, rs, lane, kBlock);
-            for (; i < a.run && left >= kBlock; ++i, left -= kBlock) {
-                const int e = (i + 1) * kBlock;
-                if (i + 1 < a.run && left >= 2 * kBlock) next.load(w + e, g + e, m + e, r + e, ms + i + 1, rs + i + 1, lane, kBlock);
-                adamw8_block<P, W, G, MASTER, true>(a.h, scale, key, cur, p + i * kBlock, master + (MASTER ? i * kBlock : 0),
-                                                    m + i * kBlock, r + i * kBlock, ms + i, rs + i,
-                                                    (uint32_t)at + i * kBlock, lane, kBlock);
-                cur = next;
+        float mscales = 0.0f, rscales = 0.0f;
+        if (lane < blocks) {
+            mscales = ms[lane];
+            rscales = rs[lane];
+        }
+        auto fetch = [&](int i) {
+            if (i < whole) {
+                const int e = i * kBlock;
+                L::fetch(ring + i % kAdam8Stages * L::kStage, w + e, g + e, m + e, r + e, lane);
+            }
+            fetch_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < kAdam8Stages - 1; ++i) fetch(i);
+        for (int i = 0; i < blocks; ++i) {
+            const int e = i * kBlock;
+            float msc = __shfl_sync(0xffffffffu, mscales, i), rsc = __shfl_sync(0xffffffffu, rscales, i);
+            float *const master_at = MASTER ? master + e : nullptr;
+            if (i < whole) {
+                // block i has landed for every lane, and every lane is done with block i - 1
+                fetch_wait<kAdam8Stages - 2>();
+                __syncwarp();
+                fetch(i + kAdam8Stages - 1);
+                L cur;
+                cur.take(ring + i % kAdam8Stages * L::kStage, lane);
+                adamw8_block<P, W, G, MASTER, true>(a.h, scale, key, cur, msc, rsc, p + e, master_at, m + e, r + e,
+                                                    (uint32_t)at + e, lane, kBlock);
+            } else {
+                const int n = left - e < kBlock ? (int)(left - e) : kBlock;
+                Lane8<W, G, false> cur;
+                cur.load(w + e, g + e, m + e, r + e, lane, n);
+                adamw8_block<P, W, G, MASTER, false>(a.h, scale, key, cur, msc, rsc, p + e, master_at, m + e, r + e,
+                                                     (uint32_t)at + e, lane, n);
+            }
+            if (lane == i) {
+                mscales = msc;
+                rscales = rsc;
             }
         }
-        for (; i < a.run && left > 0; ++i, left -= kBlock) {
-            const int e = i * kBlock, n = left < kBlock ? (int)left : kBlock;
-            Lane8<W, G, false> cur;
-            cur.load(w + e, g + e, m + e, r + e, ms + i, rs + i, lane, n);
-            adamw8_block<P, W, G, MASTER, false>(a.h, scale, key, cur, p + e, master + (MASTER ? e : 0), m + e, r + e, ms + i,
-                                                 rs + i, (uint32_t)at + e, lane, n);
+        if (lane < blocks) {
+            ms[lane] = mscales;
+            rs[lane] = rscales;
         }
+        __syncwarp();  // the next run refills the ring
     }
 }
 
@@ -676,6 +748,8 @@ AdamScalars scalars(const rr_adamw_hyper &h, const float *scale)
     s.step_size = (float)(h.lr / (1.0 - std::pow(h.beta1, (double)h.step)));
     s.eps = (float)h.eps;
     s.minus_zero = -0.0f;
+    s.one = 1;
+    s.sixteen = 16;
     s.scale = scale;
     return s;
 }
@@ -796,11 +870,14 @@ rr_status adamw8_lists(void *const *params, const void *const *grads, uint8_t *c
     a.seed = seed;
     const void *fn = adamw8_fn_for<CAP>(pd, gd, master != nullptr);
     int fit = 0;
-    RR_TRY(step_fit(fn, kThreads, 0, &fit));
+    const int wb = master ? 4 : float_bytes(pd);
+    const int smem = kThreads / 32 * kAdam8Stages * kBlock * (wb + float_bytes(gd) + 2);
+    RR_TRY(step_fit(fn, kThreads, smem, &fit));
+    // Runs as long as leave each warp a few of them.
     const int64_t warps = (int64_t)fit * sms * (kThreads / 32);
     int64_t blocks = 0;
     for (int i = 0; i < count; ++i) blocks += (sizes[i] + kBlock - 1) / kBlock;
-    a.run = blocks >= kAdam8Run * warps ? kAdam8Run : 1;
+    a.run = (int)std::min<int64_t>(kAdam8Run, std::max<int64_t>(1, blocks / (kAdam8Runs * warps)));
     // Tensors keep their place in the caller's list (it enters the random
     // bits), so empty ones stay in the table with no chunks.
     for (int i = 0; i < count;) {
@@ -824,7 +901,7 @@ rr_status adamw8_lists(void *const *params, const void *const *grads, uint8_t *c
         a.list.count = k;
         if (a.list.start[k] == 0) continue;
         const int64_t want = (a.list.start[k] + kThreads / 32 - 1) / (kThreads / 32);
-        RR_TRY(step_launch(fn, std::min<int64_t>(want, (int64_t)fit * sms), kThreads, 0, &a, stream));
+        RR_TRY(step_launch(fn, std::min<int64_t>(want, (int64_t)fit * sms), kThreads, smem, &a, stream));
     }
     return RR_OK;
 }
