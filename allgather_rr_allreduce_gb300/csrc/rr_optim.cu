@@ -181,7 +181,7 @@ struct AdamScalars {
     float step_size;                 // lr / (1 - beta1^step)
     float eps;
     float minus_zero;                // -0, for mul2_apart
-    uint32_t one, sixteen;           // 1 and 16 where the compiler may not turn a multiply-add into shifts and adds
+    uint32_t one;                    // 1, where a multiply-add may not become an addition
     const float *scale;
 };
 
@@ -326,19 +326,22 @@ __device__ __forceinline__ float round_to_code(float t, uint32_t u)
     const uint32_t bits = (__float_as_uint(__fadd_rn(t, lift)) + (u << 4) + 8u) & 0xFFF00000u;
     return __fsub_rn(__uint_as_float(bits), lift);
 }
-// The same for |x| / scale of at least 2^-6, sign and all.  The sum is two
-// integer multiply-adds, which run beside the logic units that the rest of the
-// rounding keeps busy.
-__device__ __forceinline__ float cut_to_code(float t, uint32_t u, const AdamScalars &h)
+// The same for |x| / scale of at least 2^-6, sign and all.  `half`: 0x10 adds
+// 16 times the low 16 bits of u, 0x1000 the high ones (a two-way dot product
+// picks the half, shifts and adds at once); the 8 comes through a multiply-add,
+// which runs beside the logic units that the rest of the rounding keeps busy.
+__device__ __forceinline__ float cut_to_code(float t, uint32_t u, uint32_t half, const AdamScalars &h)
 {
-    return __uint_as_float((u * h.sixteen + (__float_as_uint(t) * h.one + 8u)) & 0xFFF00000u);
+    return __uint_as_float(__dp2a_lo(u, half, __float_as_uint(t) * h.one + 8u) & 0xFFF00000u);
 }
 // A positive root is stored as no less than the smallest code.
 __device__ __forceinline__ float floor_code(float t) { return t > 0.0f ? fmaxf(t, 0x1p-9f) : t; }
-// 32 random bits of an element.
-__device__ __forceinline__ uint32_t dither(uint32_t element, uint32_t key)
+// 32 random bits of element `step` after the one whose product with kWeyl,
+// plus the tensor's key, is `base`.
+constexpr uint32_t kWeyl = 0x9E3779B1u;
+__device__ __forceinline__ uint32_t dither(uint32_t base, uint32_t step)
 {
-    uint32_t u = element * 0x9E3779B1u + key;
+    uint32_t u = base + step * kWeyl;
     u ^= u >> 16;
     u *= 0x7FEB352Du;
     return u ^ (u >> 15);
@@ -366,6 +369,7 @@ struct Lane8 {
     uint2 m, r;
 
     static __device__ __forceinline__ int element(int k, int lane) { return VEC ? lane * kLane + k : k * 32 + lane; }
+    static __device__ __forceinline__ uint32_t after(int k) { return VEC ? k : k * 32; }  // element(k) - element(0)
 
     template <class T>
     static __device__ __forceinline__ void load(Pack<T, kLane> &x, const T *p, int lane, int left)
@@ -440,23 +444,25 @@ struct Lane8 {
 
     // Whole blocks come through a ring in shared memory, kStages blocks of a
     // warp's run deep: weights, gradients, codes, one after the other.
-    static constexpr int kW = kBlock * (int)sizeof(W), kG = kBlock * (int)sizeof(G), kStage = kW + kG + 2 * kBlock;
+    static __device__ __forceinline__ constexpr int w_bytes() { return kBlock * (int)sizeof(W); }
+    static __device__ __forceinline__ constexpr int g_bytes() { return kBlock * (int)sizeof(G); }
+    static __device__ __forceinline__ constexpr int stage_bytes() { return w_bytes() + g_bytes() + 2 * kBlock; }
     static __device__ __forceinline__ void fetch(char *s, const W *wp, const G *gp, const uint8_t *mp, const uint8_t *rp,
                                                  int lane)
     {
 #pragma unroll
-        for (int j = 0; j < kW; j += 512) fetch16(s + j + lane * 16, reinterpret_cast<const char *>(wp) + j + lane * 16);
+        for (int j = 0; j < w_bytes(); j += 512) fetch16(s + j + lane * 16, reinterpret_cast<const char *>(wp) + j + lane * 16);
 #pragma unroll
-        for (int j = 0; j < kG; j += 512) fetch16(s + kW + j + lane * 16, reinterpret_cast<const char *>(gp) + j + lane * 16);
-        fetch8(s + kW + kG + lane * 8, mp + lane * 8);
-        fetch8(s + kW + kG + kBlock + lane * 8, rp + lane * 8);
+        for (int j = 0; j < g_bytes(); j += 512) fetch16(s + w_bytes() + j + lane * 16, reinterpret_cast<const char *>(gp) + j + lane * 16);
+        fetch8(s + w_bytes() + g_bytes() + lane * 8, mp + lane * 8);
+        fetch8(s + w_bytes() + g_bytes() + kBlock + lane * 8, rp + lane * 8);
     }
     __device__ __forceinline__ void take(const char *s, int lane)
     {
         load(w, reinterpret_cast<const W *>(s), lane, kBlock);
-        load(g, reinterpret_cast<const G *>(s + kW), lane, kBlock);
-        m = load(reinterpret_cast<const uint8_t *>(s + kW + kG), lane, kBlock);
-        r = load(reinterpret_cast<const uint8_t *>(s + kW + kG + kBlock), lane, kBlock);
+        load(g, reinterpret_cast<const G *>(s + w_bytes()), lane, kBlock);
+        m = load(reinterpret_cast<const uint8_t *>(s + w_bytes() + g_bytes()), lane, kBlock);
+        r = load(reinterpret_cast<const uint8_t *>(s + w_bytes() + g_bytes() + kBlock), lane, kBlock);
     }
 };
 
@@ -494,9 +500,9 @@ __device__ __forceinline__ float2 codes_of(uint2 c, int k)
 
 // One block of one tensor, loaded before: its step, weights and states stored.
 template <class P, class W, class G, bool MASTER, bool VEC>
-__device__ __forceinline__ void adamw8_block(const AdamScalars &h, float scale, uint32_t key, const Lane8<W, G, VEC> &in,
+__device__ __forceinline__ void adamw8_block(const AdamScalars &h, float scale, uint32_t base, const Lane8<W, G, VEC> &in,
                                              float &mscale, float &rscale, P *p, float *master, uint8_t *mp, uint8_t *rp,
-                                             uint32_t at, int lane, int left)
+                                             int lane, int left)
 {
     using L = Lane8<W, G, VEC>;
     float2 w[kLane / 2], m[kLane / 2], r[kLane / 2], v[kLane / 2];
@@ -554,16 +560,16 @@ __device__ __forceinline__ void adamw8_block(const AdamScalars &h, float scale, 
         m[k] = mul2(m[k], minv);
         r[k] = mul2(r[k], rinv);
         low = low3_abs(low3_abs(low, m[k].x, m[k].y), r[k].x, r[k].y);
-        const uint32_t u0 = dither(at + L::element(2 * k, lane), key), u1 = dither(at + L::element(2 * k + 1, lane), key);
-        mq[k] = make_float2(cut_to_code(m[k].x, u0 & 0xFFFFu, h), cut_to_code(m[k].y, u1 & 0xFFFFu, h));
-        rq[k] = make_float2(cut_to_code(r[k].x, u0 >> 16, h), cut_to_code(r[k].y, u1 >> 16, h));
+        const uint32_t u0 = dither(base, L::after(2 * k)), u1 = dither(base, L::after(2 * k + 1));
+        mq[k] = make_float2(cut_to_code(m[k].x, u0, 0x10u, h), cut_to_code(m[k].y, u1, 0x10u, h));
+        rq[k] = make_float2(cut_to_code(r[k].x, u0, 0x1000u, h), cut_to_code(r[k].y, u1, 0x1000u, h));
     }
     // Below 2^-6 the grid is even; a lane with such a value (or a block that is
     // not finite) takes the long way.
     if (!(low >= 0x1p-6f) || !mfine || !rfine) {
 #pragma unroll
         for (int k = 0; k < kLane / 2; ++k) {
-            const uint32_t u0 = dither(at + L::element(2 * k, lane), key), u1 = dither(at + L::element(2 * k + 1, lane), key);
+            const uint32_t u0 = dither(base, L::after(2 * k)), u1 = dither(base, L::after(2 * k + 1));
             mq[k] = make_float2(copysignf(round_to_code(fabsf(m[k].x), u0 & 0xFFFFu), m[k].x),
                                 copysignf(round_to_code(fabsf(m[k].y), u1 & 0xFFFFu), m[k].y));
             rq[k] = make_float2(round_to_code(floor_code(r[k].x), u0 >> 16), round_to_code(floor_code(r[k].y), u1 >> 16));
@@ -589,8 +595,9 @@ __global__ void __launch_bounds__(kThreads) adamw8_kernel(const __grid_constant_
     extern __shared__ uint4 s_ring[];
     const float scale = a.h.scale ? *a.h.scale : 1.0f;
     if (scale != scale) return;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    char *const ring = reinterpret_cast<char *>(s_ring) + warp * kAdam8Stages * L::kStage;
+    // one value in the warp, so that what follows from it is too
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+    char *const ring = reinterpret_cast<char *>(s_ring) + warp * kAdam8Stages * L::stage_bytes();
     const int64_t total = a.list.start[a.list.count];
     const int64_t step = (int64_t)gridDim.x * (kThreads / 32);
     for (int64_t chunk = (int64_t)blockIdx.x * (kThreads / 32) + warp; chunk < total; chunk += step) {
@@ -603,7 +610,7 @@ __global__ void __launch_bounds__(kThreads) adamw8_kernel(const __grid_constant_
         uint8_t *m = a.m[t] + at, *r = a.r[t] + at;
         float *ms = a.ms[t] + b, *rs = a.rs[t] + b, *master = MASTER ? a.w[t] + at : nullptr;
         const W *w = MASTER ? reinterpret_cast<const W *>(master) : reinterpret_cast<const W *>(p);
-        const uint32_t key = mix32(a.seed + (a.first + (uint32_t)t + 1u) * 0x9E3779B9u);
+        const uint32_t start = (uint32_t)at * kWeyl + mix32(a.seed + (a.first + (uint32_t)t + 1u) * 0x9E3779B9u);
         float mscales = 0.0f, rscales = 0.0f;
         if (lane < blocks) {
             mscales = ms[lane];
@@ -612,7 +619,7 @@ __global__ void __launch_bounds__(kThreads) adamw8_kernel(const __grid_constant_
         auto fetch = [&](int i) {
             if (i < whole) {
                 const int e = i * kBlock;
-                L::fetch(ring + i % kAdam8Stages * L::kStage, w + e, g + e, m + e, r + e, lane);
+                L::fetch(ring + i % kAdam8Stages * L::stage_bytes(), w + e, g + e, m + e, r + e, lane);
             }
             fetch_commit();
         };
@@ -628,15 +635,15 @@ __global__ void __launch_bounds__(kThreads) adamw8_kernel(const __grid_constant_
                 __syncwarp();
                 fetch(i + kAdam8Stages - 1);
                 L cur;
-                cur.take(ring + i % kAdam8Stages * L::kStage, lane);
-                adamw8_block<P, W, G, MASTER, true>(a.h, scale, key, cur, msc, rsc, p + e, master_at, m + e, r + e,
-                                                    (uint32_t)at + e, lane, kBlock);
+                cur.take(ring + i % kAdam8Stages * L::stage_bytes(), lane);
+                adamw8_block<P, W, G, MASTER, true>(a.h, scale, start + (e + L::element(0, lane)) * kWeyl, cur, msc, rsc, p + e,
+                                                    master_at, m + e, r + e, lane, kBlock);
             } else {
                 const int n = left - e < kBlock ? (int)(left - e) : kBlock;
                 Lane8<W, G, false> cur;
                 cur.load(w + e, g + e, m + e, r + e, lane, n);
-                adamw8_block<P, W, G, MASTER, false>(a.h, scale, key, cur, msc, rsc, p + e, master_at, m + e, r + e,
-                                                     (uint32_t)at + e, lane, n);
+                adamw8_block<P, W, G, MASTER, false>(a.h, scale, start + (e + Lane8<W, G, false>::element(0, lane)) * kWeyl,
+                                                     cur, msc, rsc, p + e, master_at, m + e, r + e, lane, n);
             }
             if (lane == i) {
                 mscales = msc;
@@ -749,7 +756,6 @@ AdamScalars scalars(const rr_adamw_hyper &h, const float *scale)
     s.eps = (float)h.eps;
     s.minus_zero = -0.0f;
     s.one = 1;
-    s.sixteen = 16;
     s.scale = scale;
     return s;
 }
