@@ -167,7 +167,8 @@ __global__ void __launch_bounds__(EL == 8 ? 1024 : 512) norm_rows_kernel(const _
     // Ring: stage s of this lane at ring + s * round.
     uint4 *const ring = s_ring + warp * S::kRing + lane;
     const int round = warps * S::kRing;
-    int64_t left = row < a.rows ? (a.rows - row + step - 1) / step : 0, far = left;  // rows to come: to reduce, to fetch
+    // rows to come, to reduce and to fetch: fewer than 2^31, as more than 2^31 rows fill the grid
+    int left = row < a.rows ? (int)((a.rows - row + step - 1) / step) : 0, far = left;
     const T *src = static_cast<const T *>(a.x) + row * a.xs + c0;
     const int64_t src_step = step * a.xs;
     if (VEC) {
@@ -307,48 +308,68 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const __grid_constant__
 }
 
 // ---------------------------------------------------------------- gradient
-constexpr int kGradStages = 3;
 // Each row needs two sums over its columns, sum(w dy) and sum(w dy xhat),
 // before its dx; dweight and dbias are sums over rows and stay in registers.
+//
+// What bounds a block is the chain of one row (load, sum, shuffles, barrier,
+// store), so a block has grad_rows() rows in it at once, whose chains overlap;
+// grad_stages() such steps fill the ring in shared memory.  Row statistics come
+// 32 rows at a time, one to a lane.
+__host__ __device__ constexpr int grad_rows(int el, bool vec) { return vec && el == 8 ? 2 : 1; }
+__host__ __device__ constexpr int grad_stages(int el) { return el == 8 ? 2 : 3; }
 template <class T, int EL, bool VEC, bool GROUP>
 __global__ void __launch_bounds__(EL == 32 ? 256 : 512) norm_grad_rows_kernel(const __grid_constant__ NormGradArgs a)
 {
     stream_order();
     using S = Slice<T, EL, VEC>;
-    __shared__ float2 s_part[2][16];
+    constexpr int R = grad_rows(EL, VEC), kStages = grad_stages(EL);
+    __shared__ float2 s_part[2][R][16];
     extern __shared__ uint4 s_ring[];  // the ring of rows; at the end the sums that join a block's warps
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int G = GROUP ? warps : 1, g = GROUP ? warp : 0;
     const int64_t step = GROUP ? gridDim.x : (int64_t)gridDim.x * warps;
-    int64_t row = GROUP ? blockIdx.x : (int64_t)blockIdx.x * warps + warp;
+    const int64_t row = GROUP ? blockIdx.x : (int64_t)blockIdx.x * warps + warp;
     const int cols = (int)a.cols, half = half_of(G), c0 = S::first(g, lane);
     const float inv_n = 1.0f / (float)cols;
     const int peer = half ? lane & (2 * half - 1) : 0;
 
-    uint4 *const ring = s_ring + warp * 2 * S::kRing + lane;  // dy's slots of a stage, then x's
+    uint4 *const ring = s_ring + warp * 2 * S::kRing + lane;  // of each row, dy's slots and then x's
     const int round = warps * 2 * S::kRing;
-    int64_t left = row < a.rows ? (a.rows - row + step - 1) / step : 0, far = left;
+    // rows of this group: fewer than 2^31, as more than 2^31 rows fill the grid
+    const int count = row < a.rows ? (int)((a.rows - row + step - 1) / step) : 0;
+    int far = count;
     const T *gdy = static_cast<const T *>(a.dy) + row * a.dys + c0, *gx = static_cast<const T *>(a.x) + row * a.xs + c0;
     const int64_t dy_step = step * a.dys, x_step = step * a.xs;
     auto fetch = [&](uint4 *slot) {
-        if (far > 0) {
-            S::fetch(slot, gdy, c0, cols);
-            S::fetch(slot + S::kRing, gx, c0, cols);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            if (far > i) {
+                S::fetch(slot + i * round, gdy, c0, cols);
+                S::fetch(slot + i * round + S::kRing, gx, c0, cols);
+            }
+            gdy += dy_step;
+            gx += x_step;
         }
         fetch_commit();
-        gdy += dy_step;
-        gx += x_step;
-        --far;
+        far -= R;
     };
     if (VEC) {
 #pragma unroll
-        for (int s = 0; s < kGradStages; ++s) {
+        for (int s = 0; s < kStages * R; ++s) {
             S::clear(ring + s * round, c0, cols);
             S::clear(ring + s * round + S::kRing, c0, cols);
         }
 #pragma unroll
-        for (int s = 0; s < kGradStages - 1; ++s) fetch(ring + s * round);
+        for (int s = 0; s < kStages - 1; ++s) fetch(ring + s * R * round);
     }
+    float means = 0.0f, rstds = 0.0f, next_means = 0.0f, next_rstds = 0.0f;  // of rows i .. i + 31, and the 32 after
+    auto statistics = [&](int i) {
+        if (i + lane < count) {
+            next_means = a.mean[row + (i + lane) * step];
+            next_rstds = a.rstd[row + (i + lane) * step];
+        }
+    };
+    statistics(0);
     float2 w[EL / 2], dw[EL / 2], db[EL / 2];
     load_weights<S, EL>(w, a.w, a.wdtype, 1.0f, cols, g, lane);
 #pragma unroll
@@ -356,66 +377,94 @@ __global__ void __launch_bounds__(EL == 32 ? 256 : 512) norm_grad_rows_kernel(co
     T *dst = static_cast<T *>(a.dx) + (a.dx ? row * a.dxs + c0 : 0);
     const int64_t dst_step = step * a.dxs;
     S ndy, nx;
-    float nmean = 0.0f, nrstd = 0.0f;
-    auto ahead = [&](int64_t r) {
-        if (!VEC) {
-            ndy.load(gdy, c0, cols);
-            nx.load(gx, c0, cols);
+    if (!VEC && count > 0) {
+        ndy.load(gdy, c0, cols);
+        nx.load(gx, c0, cols);
+    }
+    int stage = 0, it = 0;
+    for (int i = 0; i < count; i += R, it ^= 1) {
+        if ((i & 31) == 0) {
+            means = next_means;
+            rstds = next_rstds;
+            statistics(i + 32);
+        }
+        S dy[R], x[R];
+        if (VEC) {
+            fetch(ring + (stage == 0 ? kStages - 1 : stage - 1) * R * round);
+            fetch_wait<kStages - 1>();
+#pragma unroll
+            for (int j = 0; j < R; ++j) {
+                dy[j].take(ring + (stage * R + j) * round);
+                x[j].take(ring + (stage * R + j) * round + S::kRing);
+            }
+            stage = stage == kStages - 1 ? 0 : stage + 1;
+        } else {
+            dy[0] = ndy;
+            x[0] = nx;
             gdy += dy_step;
             gx += x_step;
+            if (i + 1 < count) {
+                ndy.load(gdy, c0, cols);
+                nx.load(gx, c0, cols);
+            }
         }
-        nmean = a.mean[r];
-        nrstd = a.rstd[r];
-    };
-    if (left > 0) ahead(row);
-    int stage = 0;
-    for (int it = 0; left > 0; --left, it ^= 1) {
-        S dy, x;
-        const float mean = nmean, rstd = nrstd;
-        if (VEC) {
-            fetch(ring + (stage == 0 ? kGradStages - 1 : stage - 1) * round);
-            fetch_wait<kGradStages - 1>();
-            dy.take(ring + stage * round);
-            x.take(ring + stage * round + S::kRing);
-            stage = stage == kGradStages - 1 ? 0 : stage + 1;
-        } else {
-            dy = ndy;
-            x = nx;
-        }
-        row += step;
-        if (left > 1) ahead(row);
         // With u = x - mean and e = dy rstd: db += dy, dw += e u, and the row's
         // sums are of w e and w e u, from which
         //   dx = w e - sum(w e) / n - u rstd^2 sum(w e u) / n.
-        float2 u[EL / 2], e[EL / 2];
-        const float2 r2 = both(rstd), shift = both(-mean);
-        float2 s1 = both(0.0f), s2 = both(0.0f);
+        float mean[R], rstd[R], c1[R], c2[R];
 #pragma unroll
-        for (int k = 0; k < EL / 2; ++k) {
-            // columns past the row read dy = 0 and are never written out
-            const float2 d = dy.pair(2 * k);
-            u[k] = add2(x.pair(2 * k), shift);
-            e[k] = mul2(d, r2);
-            db[k] = add2(db[k], d);
-            dw[k] = fma2(e[k], u[k], dw[k]);
-            e[k] = mul2(w[k], e[k]);
-            s1 = add2(s1, e[k]);
-            s2 = fma2(e[k], u[k], s2);
+        for (int j = 0; j < R; ++j) {
+            // past the last row, and past a row's columns, nothing is kept of e = 0
+            const bool in = R == 1 || i + j < count;
+            mean[j] = __shfl_sync(0xffffffffu, means, (i & 31) + j);
+            rstd[j] = in ? __shfl_sync(0xffffffffu, rstds, (i & 31) + j) : 0.0f;
+            const float2 r2 = both(rstd[j]), shift = both(-mean[j]);
+            float2 s1 = both(0.0f), s2 = both(0.0f);
+#pragma unroll
+            for (int k = 0; k < EL / 2; ++k) {
+                const float2 d = dy[j].pair(2 * k), u = add2(x[j].pair(2 * k), shift), e = mul2(d, r2), we = mul2(w[k], e);
+                if (in) db[k] = add2(db[k], d);
+                if (in) dw[k] = fma2(e, u, dw[k]);
+                s1 = add2(s1, we);
+                s2 = fma2(we, u, s2);
+            }
+            c1[j] = s1.x + s1.y;
+            c2[j] = s2.x + s2.y;
         }
-        float c1 = warp_sum(s1.x + s1.y), c2 = warp_sum(s2.x + s2.y);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+#pragma unroll
+            for (int j = 0; j < R; ++j) {
+                c1[j] += __shfl_xor_sync(0xffffffffu, c1[j], o);
+                c2[j] += __shfl_xor_sync(0xffffffffu, c2[j], o);
+            }
+        }
         if (GROUP) {
-            if (lane == 0) s_part[it][g] = make_float2(c1, c2);
+            if (lane == 0) {
+#pragma unroll
+                for (int j = 0; j < R; ++j) s_part[it][j][g] = make_float2(c1[j], c2[j]);
+            }
             __syncthreads();
-            const float2 p = peer < G ? s_part[it][peer] : make_float2(0.0f, 0.0f);
-            c1 = group_sum(p.x, half);
-            c2 = group_sum(p.y, half);
+#pragma unroll
+            for (int j = 0; j < R; ++j) {
+                const float2 p = peer < G ? s_part[it][j][peer] : make_float2(0.0f, 0.0f);
+                c1[j] = group_sum(p.x, half);
+                c2[j] = group_sum(p.y, half);
+            }
         }
         if (a.dx) {
-            const float2 k1 = both(-c1 * inv_n), k2 = both(-c2 * inv_n * rstd * rstd);
 #pragma unroll
-            for (int k = 0; k < EL / 2; ++k) x.set(2 * k, add2(e[k], fma2(u[k], k2, k1)));
-            x.store(dst, c0, cols);
-            dst += dst_step;
+            for (int j = 0; j < R; ++j) {
+                const float2 r2 = both(rstd[j]), shift = both(-mean[j]);
+                const float2 k1 = both(-c1[j] * inv_n), k2 = both(-c2[j] * inv_n * rstd[j] * rstd[j]);
+#pragma unroll
+                for (int k = 0; k < EL / 2; ++k) {
+                    const float2 u = add2(x[j].pair(2 * k), shift), we = mul2(w[k], mul2(dy[j].pair(2 * k), r2));
+                    x[j].set(2 * k, add2(we, fma2(u, k2, k1)));
+                }
+                if (R == 1 || i + j < count) x[j].store(dst, c0, cols);
+                dst += dst_step;
+            }
         }
     }
     if (!a.part) return;
@@ -883,7 +932,7 @@ extern "C" rr_status rr_layer_norm_backward(const void *dy, const void *x, const
                                                 : norm_grad_fn<__half>(el, vec, group);
             const int64_t per = group ? 1 : rows >= 8 * (int64_t)sms ? 8 : (rows + sms - 1) / sms;
             const int threads = 32 * (group ? warps : (int)per);
-            const int ring = vec ? 2 * kGradStages * threads * el * eb : 0, sums_bytes = group ? 0 : threads * el * 8;
+            const int ring = vec ? 2 * grad_stages(el) * grad_rows(el, vec) * threads * el * eb : 0, sums_bytes = group ? 0 : threads * el * 8;
             const int smem = ring > sums_bytes ? ring : sums_bytes;
             int fit = 0;
             RR_TRY(step_fit(fn, threads, smem, &fit));
