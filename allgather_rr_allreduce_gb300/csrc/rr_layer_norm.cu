@@ -150,7 +150,7 @@ __device__ __forceinline__ int half_of(int G) { return G > 1 ? 1 << (31 - __clz(
 // thread fetching and reading only its own vectors.
 __host__ __device__ constexpr int ring_rows(int el, int eb) { return el * eb > 64 ? 3 : 4; }  // 512 threads' rings fit an SM
 template <class T, int EL, bool VEC, bool GROUP>
-__global__ void __launch_bounds__(EL == 8 ? 1024 : 512) norm_rows_kernel(const __grid_constant__ NormArgs a)
+__global__ void __launch_bounds__(EL == 8 ? 1024 : EL == 16 ? 256 : 512, EL == 16 ? 3 : 1) norm_rows_kernel(const __grid_constant__ NormArgs a)
 {
     stream_order();
     using S = Slice<T, EL, VEC>;
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const __grid_constant__
 __host__ __device__ constexpr int grad_rows(int el, bool vec) { return vec && el == 8 ? 2 : 1; }
 __host__ __device__ constexpr int grad_stages(int el) { return el == 8 ? 2 : 3; }
 template <class T, int EL, bool VEC, bool GROUP>
-__global__ void __launch_bounds__(EL == 32 ? 256 : 512) norm_grad_rows_kernel(const __grid_constant__ NormGradArgs a)
+__global__ void __launch_bounds__(EL == 32 ? 256 : 512, EL == 8 ? 1 : 0) norm_grad_rows_kernel(const __grid_constant__ NormGradArgs a)
 {
     stream_order();
     using S = Slice<T, EL, VEC>;
@@ -645,12 +645,12 @@ void row_shape(int64_t rows, int64_t cols, bool vec, int sms, const int *most, i
     else if (cols <= 256) *el = 8;
     else if (cols <= 512) *el = 16;
     else if (cols <= 1024 && vec) *el = 32;
-    else *el = need(16) <= (vec ? 8 : most[1]) ? 16 : 32;
+    else *el = need(16) <= 8 ? 16 : 32;
     const int64_t n = need(*el);
     *warps = n <= most[*el == 8 ? 0 : *el == 16 ? 1 : 2] ? (int)n : 0;
 }
 
-constexpr int kNormWarps[3] = {32, 16, 16}, kNormGradWarps[3] = {16, 16, 8};
+constexpr int kNormWarps[3] = {32, 8, 16}, kNormGradWarps[3] = {16, 16, 8};
 
 struct Rows {
     const char *name;
