@@ -131,6 +131,34 @@ __device__ __forceinline__ void load_weights(float2 (&w)[EL / 2], const void *p,
     }
 }
 
+__device__ __forceinline__ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// E weights from column c on as binary32 (`aligned`: their address is a
+// multiple of 16 bytes wherever c is one of E).
+template <int E>
+__device__ __forceinline__ void weights_at(float (&w)[E], const void *p, int64_t c, int dtype, bool aligned, float absent)
+{
+    if (!p) {
+#pragma unroll
+        for (int k = 0; k < E; ++k) w[k] = absent;
+    } else if (E == 1 || !aligned) {
+#pragma unroll
+        for (int k = 0; k < E; ++k) w[k] = load_any(p, c + k, dtype);
+    } else if (dtype == RR_FP32) {
+        const Pack<float, E> v = *reinterpret_cast<const Pack<float, E> *>(static_cast<const float *>(p) + c);
+#pragma unroll
+        for (int k = 0; k < E; ++k) w[k] = v.v[k];
+    } else if (dtype == RR_BF16) {
+        const Pack<__nv_bfloat16, E> v = *reinterpret_cast<const Pack<__nv_bfloat16, E> *>(static_cast<const __nv_bfloat16 *>(p) + c);
+#pragma unroll
+        for (int k = 0; k < E; ++k) w[k] = to_f32(v.v[k]);
+    } else {
+        const Pack<__half, E> v = *reinterpret_cast<const Pack<__half, E> *>(static_cast<const __half *>(p) + c);
+#pragma unroll
+        for (int k = 0; k < E; ++k) w[k] = to_f32(v.v[k]);
+    }
+}
+
 // Sum over a block's G warps of what lane i % 2 * half holds for warp i (half:
 // the largest power of two below G, 0 for one warp); every lane gets it.
 __device__ __forceinline__ float group_sum(float x, int half)
@@ -265,8 +293,12 @@ __global__ void __launch_bounds__(EL == 8 ? 1024 : EL == 16 ? 256 : 512, EL == 1
     }
 }
 
-// Rows too long for registers: a block per row, three passes over it (the
-// second and third come from L2 for rows up to a few MB).
+// Rows too long for registers: a block per row, three passes over it, the
+// second and third out of L1 or L2.  EVEN: rows of whole, aligned 16-byte
+// vectors, E elements at a time; else one at a time.
+template <class T, bool EVEN>
+constexpr int kWidth = EVEN ? 16 / (int)sizeof(T) : 1;
+
 __device__ __forceinline__ float block_sum(float x, float *s)
 {
     x = warp_sum(x);
@@ -278,27 +310,48 @@ __device__ __forceinline__ float block_sum(float x, float *s)
     return t;
 }
 
-template <class T>
-__global__ void __launch_bounds__(1024) norm_long_kernel(const __grid_constant__ NormArgs a)
+// Vectors: 93 us for 4096 x 18944 bf16 forward with 512 threads, 134 with 1024;
+// single elements: 275 and 197 for 2000 x 40001.
+__host__ __device__ constexpr int long_threads(bool even) { return even ? 512 : 1024; }
+template <class T, bool EVEN>
+__global__ void __launch_bounds__(long_threads(EVEN)) norm_long_kernel(const __grid_constant__ NormArgs a)
 {
     stream_order();
+    constexpr int E = kWidth<T, EVEN>, kLongThreads = long_threads(EVEN);
     __shared__ float s[32];
+    const int64_t first = (int64_t)threadIdx.x * E, next = (int64_t)kLongThreads * E;
+    const bool waligned = aligned16(a.w), baligned = aligned16(a.b);
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const T *x = static_cast<const T *>(a.x) + row * a.xs;
         T *y = static_cast<T *>(a.y) + row * a.ys;
         float sum = 0.0f;
-        for (int64_t c = threadIdx.x; c < a.cols; c += blockDim.x) sum += to_f32(x[c]);
+#pragma unroll 4
+        for (int64_t c = first; c < a.cols; c += next) {
+            const Pack<T, E> v = *reinterpret_cast<const Pack<T, E> *>(x + c);
+#pragma unroll
+            for (int k = 0; k < E; ++k) sum += to_f32(v.v[k]);
+        }
         const float mean = block_sum(sum, s) / (float)a.cols;
         float m2 = 0.0f;
-        for (int64_t c = threadIdx.x; c < a.cols; c += blockDim.x) {
-            const float d = to_f32(x[c]) - mean;
-            m2 = fmaf(d, d, m2);
+#pragma unroll 4
+        for (int64_t c = first; c < a.cols; c += next) {
+            const Pack<T, E> v = *reinterpret_cast<const Pack<T, E> *>(x + c);
+#pragma unroll
+            for (int k = 0; k < E; ++k) {
+                const float d = to_f32(v.v[k]) - mean;
+                m2 = fmaf(d, d, m2);
+            }
         }
-        const float rstd = 1.0f / sqrtf(block_sum(m2, s) / (float)a.cols + a.eps);
-        for (int64_t c = threadIdx.x; c < a.cols; c += blockDim.x) {
-            const float w = a.w ? load_any(a.w, c, a.wdtype) : 1.0f;
-            const float b = a.b ? load_any(a.b, c, a.wdtype) : 0.0f;
-            y[c] = from_f32<T>(fmaf((to_f32(x[c]) - mean) * rstd, w, b));
+        const float rstd = rsqrtf(block_sum(m2, s) / (float)a.cols + a.eps);
+#pragma unroll 2
+        for (int64_t c = first; c < a.cols; c += next) {
+            Pack<T, E> v = *reinterpret_cast<const Pack<T, E> *>(x + c);
+            float w[E], b[E];
+            weights_at<E>(w, a.w, c, a.wdtype, waligned, 1.0f);
+            weights_at<E>(b, a.b, c, a.wdtype, baligned, 0.0f);
+#pragma unroll
+            for (int k = 0; k < E; ++k) v.v[k] = from_f32<T>(fmaf((to_f32(v.v[k]) - mean) * rstd, w[k], b[k]));
+            *reinterpret_cast<Pack<T, E> *>(y + c) = v;
         }
         if (threadIdx.x == 0) {
             if (a.mean) a.mean[row] = mean;
@@ -501,20 +554,29 @@ __global__ void __launch_bounds__(EL == 32 ? 256 : 512, EL == 8 ? 1 : 0) norm_gr
 }
 
 // Rows too long for registers: the two row means first ...
-template <class T>
-__global__ void __launch_bounds__(1024) norm_grad_means_kernel(const __grid_constant__ NormGradArgs a)
+template <class T, bool EVEN>
+__global__ void __launch_bounds__(long_threads(EVEN)) norm_grad_means_kernel(const __grid_constant__ NormGradArgs a)
 {
     stream_order();
+    constexpr int E = kWidth<T, EVEN>, kLongThreads = long_threads(EVEN);
     __shared__ float s[32];
+    const bool waligned = aligned16(a.w);
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const T *dy = static_cast<const T *>(a.dy) + row * a.dys;
         const T *x = static_cast<const T *>(a.x) + row * a.xs;
         const float mean = a.mean[row], rstd = a.rstd[row];
         float c1 = 0.0f, c2 = 0.0f;
-        for (int64_t c = threadIdx.x; c < a.cols; c += blockDim.x) {
-            const float wd = (a.w ? load_any(a.w, c, a.wdtype) : 1.0f) * to_f32(dy[c]);
-            c1 += wd;
-            c2 = fmaf(wd, (to_f32(x[c]) - mean) * rstd, c2);
+#pragma unroll 2
+        for (int64_t c = (int64_t)threadIdx.x * E; c < a.cols; c += (int64_t)kLongThreads * E) {
+            const Pack<T, E> d = *reinterpret_cast<const Pack<T, E> *>(dy + c), v = *reinterpret_cast<const Pack<T, E> *>(x + c);
+            float w[E];
+            weights_at<E>(w, a.w, c, a.wdtype, waligned, 1.0f);
+#pragma unroll
+            for (int k = 0; k < E; ++k) {
+                const float wd = w[k] * to_f32(d.v[k]);
+                c1 += wd;
+                c2 = fmaf(wd, (to_f32(v.v[k]) - mean) * rstd, c2);
+            }
         }
         c1 = block_sum(c1, s);
         c2 = block_sum(c2, s);
@@ -522,48 +584,53 @@ __global__ void __launch_bounds__(1024) norm_grad_means_kernel(const __grid_cons
     }
 }
 
-// ... then dx and the weight's gradient by columns: block (cx, p) has kTile
-// columns and every P-th row.
-constexpr int kTile = 1024;
-template <class T>
-__global__ void __launch_bounds__(256) norm_grad_columns_kernel(const __grid_constant__ NormGradArgs a)
+// ... then dx and the weight's gradient by columns: block p * tiles + i has
+// tile i of the columns, E to a thread, and every P-th row, kTileRows at once.
+constexpr int kTileThreads = 128, kTileRows = 4;
+template <class T, bool EVEN>
+__global__ void __launch_bounds__(kTileThreads) norm_grad_columns_kernel(const __grid_constant__ NormGradArgs a)
 {
     stream_order();
-    constexpr int E = kTile / 256;
-    const int64_t tiles = (a.cols + kTile - 1) / kTile;
-    const int64_t tile = blockIdx.x % tiles;
+    constexpr int E = kWidth<T, EVEN>;
+    const int64_t tiles = (a.cols + kTileThreads * E - 1) / (kTileThreads * E);
+    const int64_t c = (blockIdx.x % tiles * kTileThreads + threadIdx.x) * E;
     const int p = (int)(blockIdx.x / tiles);
+    if (c >= a.cols) return;
     float w[E], dw[E], db[E];
+    weights_at<E>(w, a.w, c, a.wdtype, false, 1.0f);
 #pragma unroll
-    for (int k = 0; k < E; ++k) {
-        const int64_t c = tile * kTile + k * 256 + threadIdx.x;
-        w[k] = c < a.cols && a.w ? load_any(a.w, c, a.wdtype) : 1.0f;
-        dw[k] = db[k] = 0.0f;
-    }
-    for (int64_t row = p; row < a.rows; row += a.P) {
-        const float2 m = a.coef[row];
-        const float mean = a.mean[row], rstd = a.rstd[row];
+    for (int k = 0; k < E; ++k) dw[k] = db[k] = 0.0f;
+    for (int64_t row = p; row < a.rows; row += (int64_t)kTileRows * a.P) {
+        Pack<T, E> d[kTileRows], x[kTileRows];
 #pragma unroll
-        for (int k = 0; k < E; ++k) {
-            const int64_t c = tile * kTile + k * 256 + threadIdx.x;
-            if (c < a.cols) {
-                const float d = to_f32(static_cast<const T *>(a.dy)[row * a.dys + c]);
-                const float xhat = (to_f32(static_cast<const T *>(a.x)[row * a.xs + c]) - mean) * rstd;
-                dw[k] = fmaf(d, xhat, dw[k]);
-                db[k] += d;
-                if (a.dx)
-                    static_cast<T *>(a.dx)[row * a.dxs + c] = from_f32<T>((w[k] * d - m.x - xhat * m.y) * rstd);
+        for (int j = 0; j < kTileRows; ++j) {
+            const int64_t r = row + (int64_t)j * a.P;
+            if (r < a.rows) {
+                d[j] = *reinterpret_cast<const Pack<T, E> *>(static_cast<const T *>(a.dy) + r * a.dys + c);
+                x[j] = *reinterpret_cast<const Pack<T, E> *>(static_cast<const T *>(a.x) + r * a.xs + c);
             }
+        }
+#pragma unroll
+        for (int j = 0; j < kTileRows; ++j) {
+            const int64_t r = row + (int64_t)j * a.P;
+            if (r >= a.rows) break;
+            const float2 m = a.coef[r];
+            const float mean = a.mean[r], rstd = a.rstd[r];
+#pragma unroll
+            for (int k = 0; k < E; ++k) {
+                const float g = to_f32(d[j].v[k]), xhat = (to_f32(x[j].v[k]) - mean) * rstd;
+                dw[k] = fmaf(g, xhat, dw[k]);
+                db[k] += g;
+                x[j].v[k] = from_f32<T>((w[k] * g - m.x - xhat * m.y) * rstd);
+            }
+            if (a.dx) *reinterpret_cast<Pack<T, E> *>(static_cast<T *>(a.dx) + r * a.dxs + c) = x[j];
         }
     }
     if (!a.part) return;
 #pragma unroll
     for (int k = 0; k < E; ++k) {
-        const int64_t c = tile * kTile + k * 256 + threadIdx.x;
-        if (c < a.cols) {
-            a.part[(int64_t)p * a.cols + c] = dw[k];
-            a.part[((int64_t)a.P + p) * a.cols + c] = db[k];
-        }
+        a.part[(int64_t)p * a.cols + c + k] = dw[k];
+        a.part[((int64_t)a.P + p) * a.cols + c + k] = db[k];
     }
 }
 
@@ -606,6 +673,19 @@ std::mutex g_mu;
 std::map<int, int> g_sms;
 std::map<std::pair<const void *, std::pair<int, int>>, int> g_fit;
 
+constexpr int kTileBlocks = 16;  // blocks of the columns kernel for each SM
+template <class T>
+const void *norm_long_fn(bool even)
+{
+    return even ? (const void *)norm_long_kernel<T, true> : (const void *)norm_long_kernel<T, false>;
+}
+template <class T>
+void norm_grad_long_fn(bool even, const void **means, const void **columns)
+{
+    *means = even ? (const void *)norm_grad_means_kernel<T, true> : (const void *)norm_grad_means_kernel<T, false>;
+    *columns = even ? (const void *)norm_grad_columns_kernel<T, true> : (const void *)norm_grad_columns_kernel<T, false>;
+}
+
 template <class T, bool VEC, bool GROUP>
 const void *norm_rows_fn(int el)
 {
@@ -634,17 +714,20 @@ const void *norm_grad_fn(int el, bool vec, bool group)
 }
 
 // Elements to a lane and warps to a row: one warp while 32 elements a lane
-// hold the row (16 where rows are not vectors: 32 and a row held ahead spill), else 16 a lane (32 where that needs more than 512 threads).
-// With fewer rows than SMs nothing but one row's latency counts: 8 a lane.
+// hold the row, else 16 a lane up to 8 warps, then 32.  `few`: 8 a lane where
+// that many warps fit, as with fewer rows than SMs, where nothing but one row's
+// latency counts.  Uneven rows take it too (32 a lane and a row held ahead
+// spill; 16 took 66 against 60 us for 8000 x 5001 bf16 forward), except the
+// gradient of 257 to 512 columns, one warp a row (65536 x 301: 55 against 81).
 // warps > 0 where a kernel of that shape takes the row (most[]: the warps its
 // launch bounds allow with 8, 16 and 32 elements a lane), else 0.
-void row_shape(int64_t rows, int64_t cols, bool vec, int sms, const int *most, int *el, int *warps)
+void row_shape(int64_t rows, int64_t cols, bool few, int sms, const int *most, int *el, int *warps)
 {
     auto need = [&](int e) { return (cols + 32 * e - 1) / (32 * e); };
-    if ((rows <= sms || !vec) && need(8) <= most[0]) *el = 8;
+    if ((rows <= sms || few) && need(8) <= most[0]) *el = 8;
     else if (cols <= 256) *el = 8;
     else if (cols <= 512) *el = 16;
-    else if (cols <= 1024 && vec) *el = 32;
+    else if (cols <= 1024) *el = 32;
     else *el = need(16) <= 8 ? 16 : 32;
     const int64_t n = need(*el);
     *warps = n <= most[*el == 8 ? 0 : *el == 16 ? 1 : 2] ? (int)n : 0;
@@ -809,14 +892,14 @@ extern "C" rr_status rr_layer_norm(const void *x, const void *weight, const void
     NormArgs a{x, weight, bias, y, mean, rstd, rows, cols, x_stride, y_stride, eps, (int)weight_dtype};
     int el = 0, warps = 0;
     const bool vec = cols * eb % 16 == 0 && vector_rows(x, x_stride, rows, eb) && vector_rows(y, y_stride, rows, eb);
-    row_shape(rows, cols, vec, sms, kNormWarps, &el, &warps);
+    row_shape(rows, cols, !vec, sms, kNormWarps, &el, &warps);
     const void *fn;
     int threads, smem = 0;
     int64_t blocks;
     if (warps == 0) {
-        fn = dtype == RR_FP32 ? (const void *)norm_long_kernel<float>
-             : dtype == RR_BF16 ? (const void *)norm_long_kernel<__nv_bfloat16> : (const void *)norm_long_kernel<__half>;
-        threads = 1024;
+        fn = dtype == RR_FP32   ? norm_long_fn<float>(vec)
+             : dtype == RR_BF16 ? norm_long_fn<__nv_bfloat16>(vec) : norm_long_fn<__half>(vec);
+        threads = long_threads(vec);
         blocks = rows;
     } else {
         const bool group = warps > 1;
@@ -910,21 +993,20 @@ extern "C" rr_status rr_layer_norm_backward(const void *dy, const void *x, const
         int el = 0, warps = 0;
         const bool vec = cols * eb % 16 == 0 && vector_rows(dy, dy_stride, rows, eb) &&
                          vector_rows(x, x_stride, rows, eb) && (!dx || vector_rows(dx, dx_stride, rows, eb));
-        row_shape(rows, cols, vec, sms, kNormGradWarps, &el, &warps);
+        row_shape(rows, cols, !vec && !(cols > 256 && cols <= 512), sms, kNormGradWarps, &el, &warps);
         if (warps == 0) {
-            const void *means = dtype == RR_FP32 ? (const void *)norm_grad_means_kernel<float>
-                                : dtype == RR_BF16 ? (const void *)norm_grad_means_kernel<__nv_bfloat16>
-                                                   : (const void *)norm_grad_means_kernel<__half>;
-            const void *columns = dtype == RR_FP32 ? (const void *)norm_grad_columns_kernel<float>
-                                  : dtype == RR_BF16 ? (const void *)norm_grad_columns_kernel<__nv_bfloat16>
-                                                     : (const void *)norm_grad_columns_kernel<__half>;
-            const int64_t most = 2 * (int64_t)sms, tiles = (cols + kTile - 1) / kTile;
-            RR_TRY(step_launch(means, rows < most ? rows : most, 1024, 0, &a, stream));
-            int64_t P = (8 * (int64_t)sms + tiles - 1) / tiles;
+            const void *means, *columns;
+            if (dtype == RR_FP32) norm_grad_long_fn<float>(vec, &means, &columns);
+            else if (dtype == RR_BF16) norm_grad_long_fn<__nv_bfloat16>(vec, &means, &columns);
+            else norm_grad_long_fn<__half>(vec, &means, &columns);
+            const int64_t most = 2 * (int64_t)sms;
+            const int64_t tile = kTileThreads * (vec ? 16 / eb : 1), tiles = (cols + tile - 1) / tile;
+            RR_TRY(step_launch(means, rows < most ? rows : most, long_threads(vec), 0, &a, stream));
+            int64_t P = (kTileBlocks * (int64_t)sms + tiles - 1) / tiles;
             if (P > rows) P = rows;
             if (P > kMaxPartials) P = kMaxPartials;
             a.P = (int)P;
-            RR_TRY(step_launch(columns, P * tiles, 256, 0, &a, stream));
+            RR_TRY(step_launch(columns, P * tiles, kTileThreads, 0, &a, stream));
         } else {
             const bool group = warps > 1;
             const void *fn = dtype == RR_FP32 ? norm_grad_fn<float>(el, vec, group)
