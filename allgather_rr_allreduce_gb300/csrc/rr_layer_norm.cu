@@ -686,46 +686,41 @@ void norm_grad_long_fn(bool even, const void **means, const void **columns)
     *columns = even ? (const void *)norm_grad_columns_kernel<T, true> : (const void *)norm_grad_columns_kernel<T, false>;
 }
 
-template <class T, bool VEC, bool GROUP>
-const void *norm_rows_fn(int el)
-{
-    if (el == 8) return (const void *)norm_rows_kernel<T, 8, VEC, GROUP>;
-    if (el == 16) return (const void *)norm_rows_kernel<T, 16, VEC, GROUP>;
-    return (const void *)norm_rows_kernel<T, 32, VEC, GROUP>;
-}
+// Kernels of the shapes that row_shape gives.
 template <class T>
 const void *norm_rows_fn(int el, bool vec, bool group)
 {
-    if (vec) return group ? norm_rows_fn<T, true, true>(el) : norm_rows_fn<T, true, false>(el);
-    return group ? norm_rows_fn<T, false, true>(el) : norm_rows_fn<T, false, false>(el);
-}
-template <class T, bool VEC, bool GROUP>
-const void *norm_grad_fn(int el)
-{
-    if (el == 8) return (const void *)norm_grad_rows_kernel<T, 8, VEC, GROUP>;
-    if (el == 16) return (const void *)norm_grad_rows_kernel<T, 16, VEC, GROUP>;
-    return (const void *)norm_grad_rows_kernel<T, 32, VEC, GROUP>;
+    if (!vec && el == 32) return (const void *)norm_rows_kernel<T, 32, false, true>;
+    if (!vec) return group ? (const void *)norm_rows_kernel<T, 8, false, true> : (const void *)norm_rows_kernel<T, 8, false, false>;
+    if (el == 8) return group ? (const void *)norm_rows_kernel<T, 8, true, true> : (const void *)norm_rows_kernel<T, 8, true, false>;
+    if (el == 16) return group ? (const void *)norm_rows_kernel<T, 16, true, true> : (const void *)norm_rows_kernel<T, 16, true, false>;
+    return group ? (const void *)norm_rows_kernel<T, 32, true, true> : (const void *)norm_rows_kernel<T, 32, true, false>;
 }
 template <class T>
 const void *norm_grad_fn(int el, bool vec, bool group)
 {
-    if (vec) return group ? norm_grad_fn<T, true, true>(el) : norm_grad_fn<T, true, false>(el);
-    return group ? norm_grad_fn<T, false, true>(el) : norm_grad_fn<T, false, false>(el);
+    if (!vec && el == 32) return (const void *)norm_grad_rows_kernel<T, 32, false, true>;
+    if (!vec && el == 16) return (const void *)norm_grad_rows_kernel<T, 16, false, false>;
+    if (!vec) return group ? (const void *)norm_grad_rows_kernel<T, 8, false, true> : (const void *)norm_grad_rows_kernel<T, 8, false, false>;
+    if (el == 8) return group ? (const void *)norm_grad_rows_kernel<T, 8, true, true> : (const void *)norm_grad_rows_kernel<T, 8, true, false>;
+    if (el == 16) return group ? (const void *)norm_grad_rows_kernel<T, 16, true, true> : (const void *)norm_grad_rows_kernel<T, 16, true, false>;
+    return group ? (const void *)norm_grad_rows_kernel<T, 32, true, true> : (const void *)norm_grad_rows_kernel<T, 32, true, false>;
 }
 
-// Elements to a lane and warps to a row: one warp while 32 elements a lane
-// hold the row, else 16 a lane up to 8 warps, then 32.  `few`: 8 a lane where
-// that many warps fit, as with fewer rows than SMs, where nothing but one row's
-// latency counts.  Uneven rows take it too (32 a lane and a row held ahead
-// spill; 16 took 66 against 60 us for 8000 x 5001 bf16 forward), except the
-// gradient of 257 to 512 columns, one warp a row (65536 x 301: 55 against 81).
-// warps > 0 where a kernel of that shape takes the row (most[]: the warps its
-// launch bounds allow with 8, 16 and 32 elements a lane), else 0.
-void row_shape(int64_t rows, int64_t cols, bool few, int sms, const int *most, int *el, int *warps)
+// Elements to a lane and warps to a row.  Even rows: one warp while 32 elements
+// a lane hold the row, else 16 a lane up to 8 warps, then 32; with fewer rows
+// than SMs, where nothing but one row's latency counts, 8 a lane.  Uneven rows
+// take 8 a lane while its warps allow (66 against 60 us for 8000 x 5001 bf16
+// forward with 16), except the gradient of 257 to 512 columns, one warp a row
+// with 16 (65536 x 301: 55 against 81), then 32 (it spills, but reads a row
+// once: 4000 x 12001 94 us, the long-row kernel 120).  warps > 0 where a kernel of
+// that shape takes the row (most[]: the warps its launch bounds allow with 8, 16
+// and 32 elements a lane), else 0.
+void row_shape(int64_t rows, int64_t cols, bool even, bool grad, int sms, const int *most, int *el, int *warps)
 {
     auto need = [&](int e) { return (cols + 32 * e - 1) / (32 * e); };
-    if ((rows <= sms || few) && need(8) <= most[0]) *el = 8;
-    else if (cols <= 256) *el = 8;
+    if (!even) *el = grad && cols > 256 && cols <= 512 ? 16 : need(8) <= most[0] ? 8 : 32;
+    else if (cols <= 256 || (rows <= sms && need(8) <= most[0])) *el = 8;
     else if (cols <= 512) *el = 16;
     else if (cols <= 1024) *el = 32;
     else *el = need(16) <= 8 ? 16 : 32;
@@ -892,7 +887,7 @@ extern "C" rr_status rr_layer_norm(const void *x, const void *weight, const void
     NormArgs a{x, weight, bias, y, mean, rstd, rows, cols, x_stride, y_stride, eps, (int)weight_dtype};
     int el = 0, warps = 0;
     const bool vec = cols * eb % 16 == 0 && vector_rows(x, x_stride, rows, eb) && vector_rows(y, y_stride, rows, eb);
-    row_shape(rows, cols, !vec, sms, kNormWarps, &el, &warps);
+    row_shape(rows, cols, vec, false, sms, kNormWarps, &el, &warps);
     const void *fn;
     int threads, smem = 0;
     int64_t blocks;
@@ -993,7 +988,7 @@ extern "C" rr_status rr_layer_norm_backward(const void *dy, const void *x, const
         int el = 0, warps = 0;
         const bool vec = cols * eb % 16 == 0 && vector_rows(dy, dy_stride, rows, eb) &&
                          vector_rows(x, x_stride, rows, eb) && (!dx || vector_rows(dx, dx_stride, rows, eb));
-        row_shape(rows, cols, !vec && !(cols > 256 && cols <= 512), sms, kNormGradWarps, &el, &warps);
+        row_shape(rows, cols, vec, true, sms, kNormGradWarps, &el, &warps);
         if (warps == 0) {
             const void *means, *columns;
             if (dtype == RR_FP32) norm_grad_long_fn<float>(vec, &means, &columns);
@@ -1020,6 +1015,11 @@ extern "C" rr_status rr_layer_norm_backward(const void *dy, const void *x, const
             RR_TRY(step_fit(fn, threads, smem, &fit));
             int64_t blocks = (rows + per - 1) / per;
             if (blocks > (int64_t)fit * sms) blocks = (int64_t)fit * sms;
+            // A block's partial sums are written and read again, so it should have
+            // 8 rows to itself where that leaves one block to an SM (1024 x 3584
+            // bf16: 14.8 us, with every block that fits 19.2).
+            const int64_t busy = rows / 8 / per > sms ? rows / 8 / per : sms;
+            if (blocks > busy) blocks = busy;
             if (blocks > kMaxPartials) blocks = kMaxPartials;
             a.P = (int)blocks;
             RR_TRY(step_launch(fn, blocks, threads, smem, &a, stream));

@@ -45,6 +45,9 @@ struct Chunks {
         }
         return lo;
     }
+    // Blocks take equal stretches of chunks, so that a block's search is one
+    // bisection and then a step now and then.
+    __device__ __forceinline__ int64_t stretch(int64_t i) const { return start[count] * i / gridDim.x; }
 };
 
 // ---------------------------------------------------------------- gradient norm
@@ -74,9 +77,10 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
     __shared__ double s[kThreads / 32];
     float hi = 0.0f, lo = 0.0f;  // compensated sum of the chunks
     double wide = 0.0;
-    const int64_t total = a.list.start[a.list.count];
-    for (int64_t chunk = blockIdx.x; chunk < total; chunk += gridDim.x) {
-        const int t = a.list.find(chunk);
+    const int64_t end = a.list.stretch(blockIdx.x + 1);
+    int64_t chunk = a.list.stretch(blockIdx.x);
+    for (int t = a.list.find(chunk); chunk < end; ++chunk) {
+        while (chunk >= a.list.start[t + 1]) ++t;
         const T *g = static_cast<const T *>(a.g[t]);
         const int64_t n = a.list.size[t], c = chunk - a.list.start[t];
         const int head = a.list.head[t];
@@ -111,18 +115,24 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
         float sum = acc[0].x + acc[0].y;
         if (!sound(sum)) {
             sum = 0.0f;
+            uint32_t any = 0;
 #pragma unroll
             for (int j = 0; j < kNormUnroll; ++j) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(&v[j]);
+                any |= x.x | x.y | x.z | x.w;
+            }
+            if (any & (sizeof(T) == 4 ? 0x7FFFFFFFu : 0x7FFF7FFFu)) {
 #pragma unroll
-                for (int k = 0; k < E; ++k) {
-                    const float x = to_f32(v[j].v[k]);
-                    if (x != 0.0f) wide += (double)x * x;
+                for (int j = 0; j < kNormUnroll; ++j) {
+#pragma unroll
+                    for (int k = 0; k < E; ++k) wide += (double)to_f32(v[j].v[k]) * to_f32(v[j].v[k]);
                 }
             }
         }
         if (c == 0 && (int)threadIdx.x < head && (int64_t)threadIdx.x < n) {
             const float x = to_f32(g[threadIdx.x]);
-            wide += (double)x * x;
+            if (sound(x * x)) sum = fmaf(x, x, sum);
+            else wide += (double)x * x;
         }
         // hi + lo += sum without losing the low bits (Knuth's two-sum)
         const float t0 = __fadd_rn(hi, sum), z = __fsub_rn(t0, hi);
