@@ -294,7 +294,10 @@ constexpr int kBlock = RR_ADAMW8_BLOCK;
 constexpr int kLane = kBlock / 32;
 constexpr int kAdam8Run = 32;    // most blocks of a run: one for each lane's scales
 constexpr int kAdam8Runs = 4;    // runs of a warp where there are enough blocks
-constexpr int kAdam8Stages = 4;  // blocks of a warp in flight or in use
+// Blocks of a warp in flight or in use.  With 4-byte weights the 6 leave one
+// thread block to an SM and are faster for it: 60M binary32 weights 160 us, with
+// 5 (two thread blocks) 168; a bf16 layer 435 with 5, 446 with 4 or 6.
+__host__ __device__ constexpr int adam8_stages(int weight_bytes) { return weight_bytes == 4 ? 6 : 5; }
 
 template <int CAP>
 struct Adam8Args {
@@ -477,7 +480,7 @@ struct Lane8 {
 };
 
 __device__ __forceinline__ uint32_t warp_max(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
-// max(|a|, |b|, |c|), NaN if one is; min(a, b, c) and max(a, b, c) of what is not NaN.
+// max(|a|, |b|, |c|), NaN if one is; min(a, b, c) and min(|a|, |b|, |c|) of what is not NaN.
 __device__ __forceinline__ float top3(float a, float b, float c)
 {
     float d;
@@ -488,12 +491,6 @@ __device__ __forceinline__ float low3(float a, float b, float c)
 {
     float d;
     asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-__device__ __forceinline__ float high3(float a, float b, float c)
-{
-    float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
 __device__ __forceinline__ float low3_abs(float a, float b, float c)
@@ -516,42 +513,43 @@ __device__ __forceinline__ void adamw8_block(const AdamScalars &h, float scale, 
 {
     using L = Lane8<W, G, VEC>;
     float2 w[kLane / 2], m[kLane / 2], r[kLane / 2], v[kLane / 2];
-    const float2 ms = both(mscale), rs = both(rscale), b1 = both(h.beta1), b2 = both(h.beta2),
-                 nz = both(h.minus_zero);
-    float mtop = 0.0f, rtop = 0.0f, vlow = 3e38f, vtop = 0.0f;
+    // A code times a power-of-two scale is exact, so the scale goes with beta1.
+    const float2 mb1 = both(mscale * h.beta1), rs = both(rscale), b2 = both(h.beta2), nz = both(h.minus_zero);
+    float mtop = 0.0f, rtop = 0.0f, rlow = 3e38f;
 #pragma unroll
     for (int k = 0; k < kLane / 2; ++k) {
         const float2 g = mul2(pair_f32(&in.g.v[2 * k]), both(scale));
-        m[k] = add2(mul2_apart(mul2(codes_of(in.m, k), ms), b1, nz), mul2_apart(g, both(h.omb1), nz));
+        m[k] = add2(mul2_apart(codes_of(in.m, k), mb1, nz), mul2_apart(g, both(h.omb1), nz));
         r[k] = mul2(codes_of(in.r, k), rs);
         v[k] = add2(mul2_apart(mul2(r[k], r[k]), b2, nz), mul2_apart(mul2(g, both(h.omb2)), g, nz));
         mtop = top3(mtop, m[k].x, m[k].y);
-        vlow = low3(vlow, v[k].x, v[k].y);
-        vtop = high3(vtop, v[k].x, v[k].y);
         w[k] = pair_f32(&in.w.v[2 * k]);
+        r[k] = root2(v[k], mul2(v[k], both(-1.0f)));
+        rtop = top3(rtop, r[k].x, r[k].y);
+        rlow = low3(rlow, r[k].x, r[k].y);
     }
     // The fast roots and quotients round as sqrt and / do while their operands
-    // keep away from binary32's ends; a lane with one that does not (a v of 0
-    // among them) takes sqrt and / for all 8.
+    // keep away from binary32's ends (a root that does not comes out as NaN,
+    // below 2^-50 or above 2^50); a lane with one that does not, a v of 0 among
+    // them, takes sqrt and / for all 8.
     const float2 decay = both(h.decay), size = both(-h.step_size);
-    if (vlow >= 0x1p-100f && vtop <= 0x1p100f && mtop <= 0x1p100f && h.eps <= 0x1p60f) {
+    if (rlow >= 0x1p-50f && rtop <= 0x1p50f && mtop <= 0x1p100f && h.eps <= 0x1p60f) {
         const float2 nc2 = both(-h.inv_c2), neps = both(-h.eps);
 #pragma unroll
         for (int k = 0; k < kLane / 2; ++k) {
-            r[k] = root2(v[k], mul2(v[k], both(-1.0f)));
             const float2 q = quotient2(m[k], add2(mul2_apart(r[k], nc2, nz), neps));
             w[k] = add2(mul2_apart(w[k], decay, nz), mul2_apart(q, size, nz));
         }
     } else {
+        rtop = 0.0f;
 #pragma unroll
         for (int k = 0; k < kLane / 2; ++k) {
             r[k] = make_float2(__fsqrt_rn(v[k].x), __fsqrt_rn(v[k].y));
+            rtop = top3(rtop, r[k].x, r[k].y);
             const float2 den = add2(mul2_apart(r[k], both(h.inv_c2), nz), both(h.eps));
             w[k] = add2(mul2_apart(w[k], decay, nz), mul2_apart(make_float2(__fdiv_rn(m[k].x, den.x), __fdiv_rn(m[k].y, den.y)), size, nz));
         }
     }
-#pragma unroll
-    for (int k = 0; k < kLane / 2; ++k) rtop = top3(rtop, r[k].x, r[k].y);
     if (MASTER) L::store(master, w, lane, left);
     L::store(p, w, lane, left);
 
@@ -602,6 +600,7 @@ __global__ void __launch_bounds__(kThreads) adamw8_kernel(const __grid_constant_
     stream_order();
     using W = typename std::conditional<MASTER, float, P>::type;
     using L = Lane8<W, G, true>;
+    constexpr int kAdam8Stages = adam8_stages(sizeof(W));
     extern __shared__ uint4 s_ring[];
     const float scale = a.h.scale ? *a.h.scale : 1.0f;
     if (scale != scale) return;
@@ -887,7 +886,7 @@ rr_status adamw8_lists(void *const *params, const void *const *grads, uint8_t *c
     const void *fn = adamw8_fn_for<CAP>(pd, gd, master != nullptr);
     int fit = 0;
     const int wb = master ? 4 : float_bytes(pd);
-    const int smem = kThreads / 32 * kAdam8Stages * kBlock * (wb + float_bytes(gd) + 2);
+    const int smem = kThreads / 32 * adam8_stages(wb) * kBlock * (wb + float_bytes(gd) + 2);
     RR_TRY(step_fit(fn, kThreads, smem, &fit));
     // Runs as long as leave each warp a few of them.
     const int64_t warps = (int64_t)fit * sms * (kThreads / 32);
