@@ -310,6 +310,16 @@ def test_adamw_on_a_stream_and_in_a_graph(rr):
     check_adamw(L, old, "bf16", 1.0, H)
 
 
+def test_pointer_arrays_made_before(rr):
+    """Lists marshalled once, as a loop over the same tensors keeps them."""
+    sizes = [3000, 17]
+    L = lists(sizes, [0, 0], 10, "fp32", "fp32", False)
+    old = snapshot(L)
+    arrays = [rr.pointer_array(tensors(L[k])) for k in ("p", "g", "m", "v")]
+    rr.rr_adamw(*arrays, None, sizes, "fp32", "fp32", hyper(rr))
+    check_adamw(L, old, "fp32", 1.0, H)
+
+
 def test_adamw_past_32_bit_offsets(rr):
     n = (1 << 31) + 5000
     p = torch.zeros(n, device="cuda", dtype=torch.bfloat16)
