@@ -87,12 +87,10 @@ def lib():
             "rr_layer_norm": [_vp] * 6 + [i64] * 4 + [ctypes.c_float, i32, i32, _vp],
             "rr_layer_norm_backward": [_vp] * 8 + [i64] * 5 + [i32, i32, _vp, ctypes.c_size_t, _vp],
             "rr_layer_norm_backward_workspace": [i64, i64, ctypes.POINTER(ctypes.c_size_t)],
-            "rr_grad_norm": [_PP, ctypes.POINTER(i64), i32, i32, ctypes.c_float, ctypes.c_float, _vp, _vp, _vp,
-                             ctypes.c_size_t, _vp],
+            "rr_grad_norm": [_vp, _vp, i32, i32, ctypes.c_float, ctypes.c_float, _vp, _vp, _vp, ctypes.c_size_t, _vp],
             "rr_grad_norm_workspace": [i32, ctypes.POINTER(ctypes.c_size_t)],
-            "rr_adamw": [_PP] * 5 + [ctypes.POINTER(i64), i32, i32, i32, ctypes.POINTER(rr_adamw_hyper), _vp, _vp],
-            "rr_adamw8": [_PP] * 7 + [ctypes.POINTER(i64), i32, i32, i32, ctypes.POINTER(rr_adamw_hyper),
-                                      ctypes.c_uint32, _vp, _vp],
+            "rr_adamw": [_vp] * 6 + [i32, i32, i32, ctypes.POINTER(rr_adamw_hyper), _vp, _vp],
+            "rr_adamw8": [_vp] * 8 + [i32, i32, i32, ctypes.POINTER(rr_adamw_hyper), ctypes.c_uint32, _vp, _vp],
         }
         for name, args in sig.items():
             f = getattr(l, name)
@@ -274,27 +272,29 @@ def rr_allgather_list(rank_bufs, output_lists, world_size, numel_per_rank, dtype
 _is_cuda = operator.attrgetter("is_cuda")
 
 
-def _tensor_array(items, count, name):
-    """pointer_array for a list of `count` tensors or addresses (None: no
-    list).  A pointer_array made before passes through, so that a loop over
-    the same tensors need not marshal them again."""
+def _pointers(items, count, name):
+    """A buffer of `count` device addresses for a list of tensors or addresses;
+    None for None.  A pointer_array made before passes through, so that a loop
+    over the same tensors need not marshal them again."""
     if items is None:
         return None
     if len(items) != count:
         raise ValueError(f"{name} has {len(items)} entries, sizes has {count}")
     if isinstance(items, ctypes.Array):
         return items
-    if count and _tensor_class is not None:
-        try:  # CUDA tensors throughout, without a Python-level step for each
-            if all(map(_is_cuda, items)):
-                return (_vp * count).from_buffer(array.array("Q", map(_tensor_class.data_ptr, items)))
-        except (AttributeError, TypeError):
-            pass
+    try:  # CUDA tensors throughout, without a Python-level step for each
+        if all(map(_is_cuda, items)):
+            return array.array("Q", map(_tensor_class.data_ptr, items))
+    except (AttributeError, TypeError):
+        pass
     return pointer_array(items)
 
 
-def _sizes(sizes):
-    return (ctypes.c_int64 * len(sizes)).from_buffer(array.array("q", sizes)) if len(sizes) else (ctypes.c_int64 * 0)()
+def _at(buffer):
+    """Where a buffer's first element lies."""
+    if buffer is None:
+        return 0
+    return buffer.buffer_info()[0] if buffer.__class__ is array.array else ctypes.addressof(buffer)
 
 
 def rr_layer_norm(x, weight, bias, y, mean, rstd, rows, cols, x_stride, y_stride, eps, dtype, weight_dtype,
@@ -323,10 +323,10 @@ def rr_layer_norm_backward_workspace(rows, cols):
 
 def rr_grad_norm(grads, sizes, dtype, inv_scale, max_norm, norm, scale, workspace, workspace_bytes, stream=None):
     """Norm over a list of gradient tensors and the factor that clips it; norm or scale may be None."""
-    n, l = len(sizes), lib()
-    _check(l.rr_grad_norm(_tensor_array(grads, n, "grads"), _sizes(sizes), n, dtype_code(dtype), inv_scale,
-                              max_norm, _addr(norm), _addr(scale), _addr(workspace), workspace_bytes,
-                              stream_handle(stream)))
+    l, n = lib(), len(sizes)
+    s, g = array.array("q", sizes), _pointers(grads, n, "grads")
+    _check(l.rr_grad_norm(_at(g), _at(s), n, dtype_code(dtype), inv_scale, max_norm, _addr(norm), _addr(scale),
+                          _addr(workspace), workspace_bytes, stream_handle(stream)))
 
 
 def rr_grad_norm_workspace(num_tensors):
@@ -339,24 +339,24 @@ def rr_grad_norm_workspace(num_tensors):
 def rr_adamw(params, grads, exp_avg, exp_avg_sq, master, sizes, param_dtype, grad_dtype, hyper, grad_scale=None,
              stream=None):
     """One AdamW step over a list of tensors, states in binary32; master may be None."""
-    n, l = len(sizes), lib()
-    _check(l.rr_adamw(_tensor_array(params, n, "params"), _tensor_array(grads, n, "grads"),
-                          _tensor_array(exp_avg, n, "exp_avg"), _tensor_array(exp_avg_sq, n, "exp_avg_sq"),
-                          _tensor_array(master, n, "master"), _sizes(sizes), n, dtype_code(param_dtype),
-                          dtype_code(grad_dtype), hyper, _addr(grad_scale), stream_handle(stream)))
+    l, n = lib(), len(sizes)
+    s, p, g = array.array("q", sizes), _pointers(params, n, "params"), _pointers(grads, n, "grads")
+    m, v = _pointers(exp_avg, n, "exp_avg"), _pointers(exp_avg_sq, n, "exp_avg_sq")
+    w = _pointers(master, n, "master")
+    _check(l.rr_adamw(_at(p), _at(g), _at(m), _at(v), _at(w), _at(s), n, dtype_code(param_dtype),
+                      dtype_code(grad_dtype), hyper, _addr(grad_scale), stream_handle(stream)))
 
 
 def rr_adamw8(params, grads, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale, master, sizes, param_dtype,
               grad_dtype, hyper, seed, grad_scale=None, stream=None):
     """One AdamW step over a list of tensors, states in 8 bits; master may be None."""
-    n, l = len(sizes), lib()
-    _check(l.rr_adamw8(_tensor_array(params, n, "params"), _tensor_array(grads, n, "grads"),
-                           _tensor_array(exp_avg, n, "exp_avg"), _tensor_array(exp_avg_scale, n, "exp_avg_scale"),
-                           _tensor_array(exp_avg_sq, n, "exp_avg_sq"),
-                           _tensor_array(exp_avg_sq_scale, n, "exp_avg_sq_scale"),
-                           _tensor_array(master, n, "master"), _sizes(sizes), n, dtype_code(param_dtype),
-                           dtype_code(grad_dtype), hyper, seed & 0xFFFFFFFF, _addr(grad_scale),
-                           stream_handle(stream)))
+    l, n = lib(), len(sizes)
+    s, p, g = array.array("q", sizes), _pointers(params, n, "params"), _pointers(grads, n, "grads")
+    m, ms = _pointers(exp_avg, n, "exp_avg"), _pointers(exp_avg_scale, n, "exp_avg_scale")
+    v, vs = _pointers(exp_avg_sq, n, "exp_avg_sq"), _pointers(exp_avg_sq_scale, n, "exp_avg_sq_scale")
+    w = _pointers(master, n, "master")
+    _check(l.rr_adamw8(_at(p), _at(g), _at(m), _at(ms), _at(v), _at(vs), _at(w), _at(s), n, dtype_code(param_dtype),
+                       dtype_code(grad_dtype), hyper, seed & 0xFFFFFFFF, _addr(grad_scale), stream_handle(stream)))
 
 
 def bound_call(name, *args):

@@ -11,6 +11,7 @@
 #include <vector>
 
 #include "rr_round.cuh"
+#include "rr_spans.h"
 #include "rr_step.h"
 
 namespace rr {
@@ -668,49 +669,6 @@ __global__ void __launch_bounds__(kThreads) adamw8_kernel(const __grid_constant_
 }
 
 // ---------------------------------------------------------------- host side
-// A span of device memory of one argument; written ones may touch nothing.
-struct Span {
-    uintptr_t lo, hi;
-    bool written;
-};
-struct Spans {
-    std::vector<Span> all, spare;
-    std::vector<size_t> cuts;
-    void add(const void *p, int64_t bytes, bool written)
-    {
-        const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-        if (p && bytes > 0) all.push_back(Span{lo, lo + (uintptr_t)bytes, written});
-    }
-    // Sorts by address, joining ascending stretches (a list over a flat buffer
-    // is one), and looks at neighbours.
-    bool touch()
-    {
-        auto before = [](const Span &x, const Span &y) { return x.lo < y.lo; };
-        std::vector<size_t> &cut = cuts;
-        for (;;) {
-            cut.assign(1, 0);
-            for (size_t i = 1; i < all.size(); ++i)
-                if (before(all[i], all[i - 1])) cut.push_back(i);
-            cut.push_back(all.size());
-            if (cut.size() <= 2) break;
-            spare.resize(all.size());
-            for (size_t k = 0; k + 1 < cut.size(); k += 2) {
-                const size_t mid = cut[k + 1], end = k + 2 < cut.size() ? cut[k + 2] : mid;
-                std::merge(all.begin() + cut[k], all.begin() + mid, all.begin() + mid, all.begin() + end,
-                           spare.begin() + cut[k], before);
-            }
-            all.swap(spare);
-        }
-        uintptr_t any = 0, written = 0;
-        for (const Span &s : all) {
-            if (s.lo < written || (s.written && s.lo < any)) return true;
-            any = std::max(any, s.hi);
-            if (s.written) written = std::max(written, s.hi);
-        }
-        return false;
-    }
-};
-
 rr_status check_list(const int64_t *sizes, int count)
 {
     if (count < 0) return step_fail(RR_ERR_INVALID_ARG, "num_tensors %d", count);

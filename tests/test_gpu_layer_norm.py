@@ -75,7 +75,8 @@ def check_forward(x, w, b, eps, y, mean, rstd, dtype, what):
 
 SHAPES = [(1, 1), (3, 2), (5, 7), (2, 8), (40, 31), (1, 64), (153, 64), (9, 255), (2000, 256), (7, 257), (1300, 512),
           (160, 513), (33, 1000), (1217, 1024), (5, 1027), (300, 1027), (1, 3584), (8, 3584), (700, 3584), (155, 8192),
-          (4, 8193), (160, 8200), (3, 16384), (2, 16385), (3, 18944), (2, 40001)]
+          (4, 8193), (160, 8200), (3, 16384), (2, 16385), (3, 18944), (2, 40001), (400, 18944), (330, 9001), (170, 20003),
+          (90, 32768), (160, 32776)]
 
 
 @pytest.mark.parametrize("rows,cols", SHAPES)
@@ -118,7 +119,7 @@ def test_forward_without_weight_and_bias_and_other_types(rr):
     check_forward(x, None, b, 1e-5, y, None, None, "bf16", "bias of another type")
 
 
-@pytest.mark.parametrize("rows,cols", [(17, 100), (400, 1024), (30, 3584), (3, 20000)])
+@pytest.mark.parametrize("rows,cols", [(17, 100), (400, 1024), (30, 3584), (3, 20000), (200, 24000)])
 def test_forward_in_place_and_interleaved(rr, rows, cols):
     x = make_x(rows, cols, "bf16", 11)
     keep = x.clone()
@@ -268,7 +269,7 @@ def test_backward_strided_and_misaligned(rr, rows, cols, dtype, shift, wide):
         g.check()
 
 
-@pytest.mark.parametrize("rows,cols", [(40, 200), (1300, 1024), (200, 3584), (6, 9000)])
+@pytest.mark.parametrize("rows,cols", [(40, 200), (1300, 1024), (200, 3584), (6, 9000), (300, 17000), (60, 33000)])
 def test_backward_parts_in_place_and_broadcast(rr, rows, cols):
     x = make_x(rows, cols, "bf16", 30)
     dy = make_x(rows, cols, "bf16", 31)

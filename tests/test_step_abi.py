@@ -1,8 +1,13 @@
 """Refusals of the training-step operators that need no GPU: arguments are
 checked before any CUDA call, and the message names what was wrong."""
 import ctypes
+import os
+import shutil
+import subprocess
 
 import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 OK = 4096  # an address that passes the alignment checks and is never read
 
@@ -193,3 +198,16 @@ def test_lists_that_hold_nothing_need_no_gpu(rr):
 def test_lists_of_unequal_length_are_refused_by_the_binding(rr):
     with pytest.raises(ValueError, match="grads"):
         adamw(rr, False, grads=[OK])
+
+
+def test_alias_rule_against_every_pair(tmp_path):
+    """rr_spans.h compiled for the host and compared with brute force."""
+    gxx = shutil.which("g++")
+    if gxx is None:
+        pytest.skip("no g++")
+    exe = tmp_path / "spans_check"
+    subprocess.run([gxx, "-std=c++17", "-O2", "-Wall", "-Wextra", "-Werror", "-I",
+                    os.path.join(ROOT, "allgather_rr_allreduce_gb300", "csrc"),
+                    os.path.join(ROOT, "tests", "native", "spans_check.cpp"), "-o", str(exe)], check=True)
+    res = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
+    assert res.returncode == 0, res.stdout + res.stderr
