@@ -10,7 +10,7 @@
 // partial sums go to the workspace and a second kernel adds them in order.
 #include <map>
 #include <mutex>
-#include <utility>
+#include <tuple>
 
 #include "rr_step.h"
 
@@ -695,7 +695,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) norm_grad_join_kernel(const _
 // ---------------------------------------------------------------- host side
 std::mutex g_mu;
 std::map<int, int> g_sms;
-std::map<std::pair<const void *, std::pair<int, int>>, int> g_fit;
+std::map<std::tuple<int, const void *, int, int>, int> g_fit;  // device, kernel, threads, shared memory
 
 // Blocks of the columns kernel for each SM: what fits at once with vectors (4096
 // x 18944 bf16, both kernels: 210 us, with 8 blocks 227), more with single
@@ -821,12 +821,15 @@ constexpr int kMaxDynamic = 224 * 1024;
 
 rr_status step_fit(const void *fn, int threads, int smem, int *out)
 {
+    int dev = -1;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return step_cuda_fail(e, "cudaGetDevice");
     std::lock_guard<std::mutex> lock(g_mu);
-    const auto key = std::make_pair(fn, std::make_pair(threads, smem));
+    const auto key = std::make_tuple(dev, fn, threads, smem);
     auto it = g_fit.find(key);
     if (it == g_fit.end()) {
         int fit = 0;
-        cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamic);
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamic);
         if (e != cudaSuccess) return step_cuda_fail(e, "cudaFuncSetAttribute(maxDynamicSharedMemorySize)");
         e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, fn, threads, smem);
         if (e != cudaSuccess) return step_cuda_fail(e, "cudaOccupancyMaxActiveBlocksPerMultiprocessor");
@@ -881,7 +884,7 @@ extern "C" rr_status rr_layer_norm(const void *x, const void *weight, const void
                                    float *rstd, int64_t rows, int64_t cols, int64_t x_stride,
                                    int64_t y_stride, float eps, rr_dtype dtype, rr_dtype weight_dtype,
                                    cudaStream_t stream)
-{
+try {
     RR_TRY(check_sizes(rows, cols, dtype, weight_dtype));
     RR_TRY(check_stride("x_stride", x_stride, rows, cols, false));
     RR_TRY(check_stride("y_stride", y_stride, rows, cols, true));
@@ -937,6 +940,8 @@ extern "C" rr_status rr_layer_norm(const void *x, const void *weight, const void
     const int64_t most = (int64_t)fit * sms;
     RR_TRY(step_launch(fn, blocks < most ? blocks : most, threads, smem, &a, stream));
     return step_ok();
+} catch (...) {
+    return step_no_memory();
 }
 
 extern "C" rr_status rr_layer_norm_backward_workspace(int64_t rows, int64_t cols, size_t *bytes)
@@ -953,7 +958,7 @@ extern "C" rr_status rr_layer_norm_backward(const void *dy, const void *x, const
                                             int64_t rows, int64_t cols, int64_t dy_stride, int64_t x_stride,
                                             int64_t dx_stride, rr_dtype dtype, rr_dtype weight_dtype,
                                             void *workspace, size_t workspace_bytes, cudaStream_t stream)
-{
+try {
     RR_TRY(check_sizes(rows, cols, dtype, weight_dtype));
     RR_TRY(check_stride("dy_stride", dy_stride, rows, cols, false));
     RR_TRY(check_stride("x_stride", x_stride, rows, cols, false));
@@ -1057,4 +1062,6 @@ extern "C" rr_status rr_layer_norm_backward(const void *dy, const void *x, const
         RR_TRY(step_launch((const void *)norm_grad_join_kernel, (cols + 31) / 32, 32 * kJoinWarps, 0, &j, stream));
     }
     return step_ok();
+} catch (...) {
+    return step_no_memory();
 }

@@ -912,7 +912,7 @@ extern "C" rr_status rr_grad_norm_workspace(int num_tensors, size_t *bytes)
 extern "C" rr_status rr_grad_norm(const void *const *grads, const int64_t *sizes, int num_tensors, rr_dtype dtype,
                                   float inv_scale, float max_norm, float *norm, float *scale, void *workspace,
                                   size_t workspace_bytes, cudaStream_t stream)
-{
+try {
     if (!float_bytes(dtype)) return step_fail(RR_ERR_UNSUPPORTED_DTYPE, "dtype %d", (int)dtype);
     RR_TRY(check_list(sizes, num_tensors));
     if (!(inv_scale > 0.0f && std::isfinite(inv_scale))) return step_fail(RR_ERR_INVALID_ARG, "inv_scale %g", (double)inv_scale);
@@ -944,13 +944,15 @@ extern "C" rr_status rr_grad_norm(const void *const *grads, const int64_t *sizes
     GradNormEndArgs e{part, parts, inv_scale, max_norm, norm, scale};
     RR_TRY(step_launch((const void *)grad_norm_end_kernel, 1, kThreads, 0, &e, stream));
     return step_ok();
+} catch (...) {
+    return step_no_memory();
 }
 
 extern "C" rr_status rr_adamw(void *const *params, const void *const *grads, float *const *exp_avg,
                               float *const *exp_avg_sq, float *const *master, const int64_t *sizes,
                               int num_tensors, rr_dtype param_dtype, rr_dtype grad_dtype,
                               const rr_adamw_hyper *hyper, const float *grad_scale, cudaStream_t stream)
-{
+try {
     RR_TRY(check_types(param_dtype, grad_dtype));
     RR_TRY(check_list(sizes, num_tensors));
     RR_TRY(check_hyper(hyper));
@@ -981,6 +983,8 @@ extern "C" rr_status rr_adamw(void *const *params, const void *const *grads, flo
                : adamw_lists<kAdamCap>(params, grads, exp_avg, exp_avg_sq, master, sizes, num_tensors, param_dtype,
                                        grad_dtype, h, sms, stream));
     return step_ok();
+} catch (...) {
+    return step_no_memory();
 }
 
 extern "C" rr_status rr_adamw8(void *const *params, const void *const *grads, uint8_t *const *exp_avg,
@@ -989,7 +993,7 @@ extern "C" rr_status rr_adamw8(void *const *params, const void *const *grads, ui
                                int num_tensors, rr_dtype param_dtype, rr_dtype grad_dtype,
                                const rr_adamw_hyper *hyper, uint32_t seed, const float *grad_scale,
                                cudaStream_t stream)
-{
+try {
     RR_TRY(check_types(param_dtype, grad_dtype));
     RR_TRY(check_list(sizes, num_tensors));
     RR_TRY(check_hyper(hyper));
@@ -1025,4 +1029,6 @@ extern "C" rr_status rr_adamw8(void *const *params, const void *const *grads, ui
                : adamw8_lists<kAdamCap>(params, grads, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale, master,
                                         sizes, num_tensors, param_dtype, grad_dtype, h, seed, sms, stream));
     return step_ok();
+} catch (...) {
+    return step_no_memory();
 }

@@ -17,6 +17,8 @@ namespace rr {
 rr_status step_fail(rr_status s, const char *fmt, ...);
 rr_status step_cuda_fail(cudaError_t e, const char *what);
 rr_status step_ok();
+// What a C entry returns for a C++ exception, which can only be host memory's.
+inline rr_status step_no_memory() { return step_fail(RR_ERR_CUDA, "host memory ran out"); }
 
 inline int float_bytes(rr_dtype d) { return d == RR_FP32 ? 4 : d == RR_BF16 || d == RR_FP16 ? 2 : 0; }
 inline bool aligned_to(const void *p, int bytes) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)bytes == 0; }

@@ -3,8 +3,8 @@
 Tolerances are bounds on the rounding errors, derived before the first run.
 u is the rounding unit of the output's type, e = 2^-24 that of binary32.  A
 sum of a row goes through at most D = 80 + cols / 1024 additions in sequence
-(32 to a lane, 5 of a warp, 32 warps, and for rows too long for registers one
-for each 1024 columns), so its error is at most D e times the sum of
+(32 to a lane, 5 of a warp, 32 warps; for rows too long for registers at least
+512 threads have them, which D covers up to 60000 columns), so its error is at most D e times the sum of
 magnitudes; a sum over rows through at most R = 100 + rows / 100 (a block has
 at most rows / 152 rows, the joins add 8 warps, 38 partials and 16 warps).
 """
