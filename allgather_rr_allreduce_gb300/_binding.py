@@ -55,6 +55,7 @@ class RRError(RuntimeError):
 
 _lib = None
 _tensor_class = None  # torch.Tensor, once torch has been imported by the caller
+_raw_stream = _device = None  # torch's current stream and device, once CUDA has been started
 _vp = ctypes.c_void_p
 _PP = ctypes.POINTER(ctypes.c_void_p)
 
@@ -132,10 +133,10 @@ def pointer_array(items):
 
 
 def dtype_code(dtype):
-    if isinstance(dtype, int):
-        return dtype
     if isinstance(dtype, str):
         return _DTYPE_NAMES[dtype]
+    if isinstance(dtype, int):
+        return dtype
     import torch
     return {torch.bfloat16: RR_BF16, torch.float16: RR_FP16, torch.float32: RR_FP32,
             torch.int32: RR_INT32}[dtype]
@@ -143,10 +144,15 @@ def dtype_code(dtype):
 
 def stream_handle(stream):
     if stream is None:
+        if _raw_stream is not None:  # the current stream without a Stream object
+            return _raw_stream(_device())
         import torch
-        if torch.cuda.is_initialized():  # the current stream without a Stream object
-            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-        return torch.cuda.current_stream().cuda_stream
+        current = torch.cuda.current_stream().cuda_stream  # starts CUDA
+        globals().update(_raw_stream=getattr(torch._C, "_cuda_getCurrentRawStream", None),
+                         _device=torch.cuda.current_device)
+        if hasattr(torch._C, "_cuda_getDevice"):
+            globals().update(_device=torch._C._cuda_getDevice)
+        return current
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -735,8 +735,10 @@ const void *norm_grad_fn(int el, bool vec, bool group)
 }
 
 // Elements to a lane and warps to a row.  Even rows: one warp while 32 elements
-// a lane hold the row, else 16 a lane up to 8 warps, then 32; with fewer rows
-// than SMs, where nothing but one row's latency counts, 8 a lane.  Uneven rows
+// a lane hold the row (two with 16 from 513 columns on where there are fewer
+// than 8 rows for each SM: the gradient of 257 x 1024 binary32 5.9 against 7.6
+// us), else 16 a lane up to 8 warps, then 32; with fewer rows than SMs, where
+// nothing but one row's latency counts, 8 a lane.  Uneven rows
 // take 8 a lane while its warps allow (66 against 60 us for 8000 x 5001 bf16
 // forward with 16), except the gradient of 257 to 512 columns, one warp a row
 // with 16 (65536 x 301: 55 against 81), then 32 (it spills, but reads a row
@@ -749,7 +751,7 @@ void row_shape(int64_t rows, int64_t cols, bool even, bool grad, int sms, const 
     if (!even) *el = grad && cols > 256 && cols <= 512 ? 16 : need(8) <= most[0] ? 8 : 32;
     else if (cols <= 256 || (rows <= sms && need(8) <= most[0])) *el = 8;
     else if (cols <= 512) *el = 16;
-    else if (cols <= 1024) *el = 32;
+    else if (cols <= 1024) *el = rows < 8 * sms ? 16 : 32;
     else *el = need(16) <= 8 ? 16 : 32;
     const int64_t n = need(*el);
     *warps = n <= most[*el == 8 ? 0 : *el == 16 ? 1 : 2] ? (int)n : 0;

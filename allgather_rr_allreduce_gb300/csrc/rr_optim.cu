@@ -55,12 +55,32 @@ struct Chunks {
 constexpr int kNormCapSmall = 32, kNormCap = 1200;
 constexpr int kNormUnroll = 8;
 constexpr int kNormBlocks = 1024;  // most blocks of one launch, one partial sum each
+// Up to so many chunks one block takes the list and finishes the norm itself.
+constexpr int kNormAlone = 2;
+
+struct GradNormEndArgs {
+    const double *part;
+    int64_t count;
+    float inv_scale, max_norm;
+    float *norm, *scale;
+};
+
+// Norm and scale from the sum of squares (one thread).
+__device__ __forceinline__ void grad_norm_finish(const GradNormEndArgs &a, double sum)
+{
+    const float norm = (float)(sqrt(sum) * (double)a.inv_scale);
+    const float clip = a.max_norm / (norm + 1e-6f);
+    if (a.norm) *a.norm = norm;
+    if (a.scale) *a.scale = isfinite(norm) ? a.inv_scale * fminf(1.0f, clip) : __int_as_float(0x7fc00000);
+}
 
 template <int CAP>
 struct GradNormArgs {
     Chunks<CAP> list;
     const void *g[CAP];
     double *part;  // this launch's partial sums
+    bool alone;    // its one block has the whole list: it finishes the norm itself
+    GradNormEndArgs end;
 };
 
 // Sums of squares in [2^-90, 2^90] are sound in binary32: every square that
@@ -148,16 +168,10 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
     if (threadIdx.x == 0) {
         d = 0.0;
         for (int i = 0; i < kThreads / 32; ++i) d += s[i];
-        a.part[blockIdx.x] = d;
+        if (a.alone) grad_norm_finish(a.end, d);
+        else a.part[blockIdx.x] = d;
     }
 }
-
-struct GradNormEndArgs {
-    const double *part;
-    int64_t count;
-    float inv_scale, max_norm;
-    float *norm, *scale;
-};
 
 __global__ void __launch_bounds__(kThreads) grad_norm_end_kernel(const __grid_constant__ GradNormEndArgs a)
 {
@@ -172,10 +186,7 @@ __global__ void __launch_bounds__(kThreads) grad_norm_end_kernel(const __grid_co
     if (threadIdx.x == 0) {
         d = 0.0;
         for (int i = 0; i < kThreads / 32; ++i) d += s[i];
-        const float norm = (float)(sqrt(d) * (double)a.inv_scale);
-        const float clip = a.max_norm / (norm + 1e-6f);
-        if (a.norm) *a.norm = norm;
-        if (a.scale) *a.scale = isfinite(norm) ? a.inv_scale * fminf(1.0f, clip) : __int_as_float(0x7fc00000);
+        grad_norm_finish(a, d);
     }
 }
 
@@ -735,8 +746,8 @@ int64_t chunks_of(int64_t size, int head, int64_t chunk)
 }
 
 template <int CAP>
-rr_status norm_lists(const void *const *grads, const int64_t *sizes, int count, rr_dtype dtype, int sms, double *part,
-                     int64_t *parts, cudaStream_t stream)
+rr_status norm_lists(const void *const *grads, const int64_t *sizes, int count, rr_dtype dtype, int sms,
+                     GradNormEndArgs &end, double *part, cudaStream_t stream)
 {
     const int eb = float_bytes(dtype), E = 16 / eb;
     const int64_t chunk = (int64_t)kThreads * E * kNormUnroll;
@@ -760,12 +771,15 @@ rr_status norm_lists(const void *const *grads, const int64_t *sizes, int count, 
         }
         if (k == 0) break;
         a.list.count = k;
-        const int64_t grid = std::min(a.list.start[k], most);
-        a.part = part + *parts;
-        *parts += grid;
+        a.alone = i == count && end.count == 0 && a.list.start[k] <= kNormAlone;
+        const int64_t grid = a.alone ? 1 : std::min(a.list.start[k], most);
+        a.part = part + end.count;
+        a.end = end;
         RR_TRY(step_launch(fn, grid, kThreads, 0, &a, stream));
+        if (a.alone) return RR_OK;
+        end.count += grid;
     }
-    return RR_OK;
+    return step_launch((const void *)grad_norm_end_kernel, 1, kThreads, 0, &end, stream);
 }
 
 // Kernels by parameter type, gradient type and master weights.
@@ -938,11 +952,9 @@ try {
     int sms = 0;
     RR_TRY(step_sms(&sms));
     double *part = static_cast<double *>(workspace);
-    int64_t parts = 0;
-    RR_TRY(num_tensors <= kNormCapSmall ? norm_lists<kNormCapSmall>(grads, sizes, num_tensors, dtype, sms, part, &parts, stream)
-                                        : norm_lists<kNormCap>(grads, sizes, num_tensors, dtype, sms, part, &parts, stream));
-    GradNormEndArgs e{part, parts, inv_scale, max_norm, norm, scale};
-    RR_TRY(step_launch((const void *)grad_norm_end_kernel, 1, kThreads, 0, &e, stream));
+    GradNormEndArgs end{part, 0, inv_scale, max_norm, norm, scale};
+    RR_TRY(num_tensors <= kNormCapSmall ? norm_lists<kNormCapSmall>(grads, sizes, num_tensors, dtype, sms, end, part, stream)
+                                        : norm_lists<kNormCap>(grads, sizes, num_tensors, dtype, sms, end, part, stream));
     return step_ok();
 } catch (...) {
     return step_no_memory();
