@@ -553,7 +553,108 @@ __global__ void __launch_bounds__(EL == 32 ? 256 : 512, EL == 8 ? 1 : 0) norm_gr
     }
 }
 
-// Rows too long for registers: the two row means first ...
+// Even rows of more than a block's registers hold beside the sums: a block per
+// row and two passes over it, the second out of L1, the weight's gradient in
+// registers, EL columns to a thread.  While a row's second pass runs, the next
+// row comes into L2.
+constexpr int kWideThreads = 512;
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+template <class T, int EL>
+__global__ void __launch_bounds__(kWideThreads) norm_grad_wide_kernel(const __grid_constant__ NormGradArgs a)
+{
+    stream_order();
+    constexpr int E = 16 / (int)sizeof(T), NV = EL / E, kWarps = kWideThreads / 32;
+    constexpr int kAtOnce = NV % 2 ? 1 : 2;  // vectors whose loads run together
+    __shared__ float2 s[2][kWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cols = (int)a.cols;
+    const float inv_n = 1.0f / (float)cols;
+    const bool waligned = aligned16(a.w);
+    const int c0 = threadIdx.x * E;
+    constexpr int kNext = kWideThreads * E;  // columns from a thread's vector to its next
+    float2 dw[EL / 2], db[EL / 2];
+#pragma unroll
+    for (int k = 0; k < EL / 2; ++k) dw[k] = db[k] = both(0.0f);
+    int it = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, it ^= 1) {
+        const T *dy = static_cast<const T *>(a.dy) + row * a.dys + c0, *x = static_cast<const T *>(a.x) + row * a.xs + c0;
+        const float mean = a.mean[row], rstd = a.rstd[row];
+        const float2 r2 = both(rstd), shift = both(-mean);
+        Pack<T, E> d[kAtOnce], xv[kAtOnce];
+        float w[kAtOnce][E];
+        auto load = [&](int v0) {
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+                const int c = (v0 + j) * kNext;
+                if (c0 + c < cols) {
+                    d[j] = *reinterpret_cast<const Pack<T, E> *>(dy + c);
+                    xv[j] = *reinterpret_cast<const Pack<T, E> *>(x + c);
+                    weights_at<E>(w[j], a.w, c0 + c, a.wdtype, waligned, 1.0f);
+                } else {
+                    *reinterpret_cast<uint4 *>(&d[j]) = *reinterpret_cast<uint4 *>(&xv[j]) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int k = 0; k < E; ++k) w[j][k] = 0.0f;
+                }
+            }
+        };
+        float2 s1 = both(0.0f), s2 = both(0.0f);
+#pragma unroll
+        for (int v = 0; v < NV; v += kAtOnce) {
+            load(v);
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+#pragma unroll
+                for (int k = 0; k < E; k += 2) {
+                    const float2 we = mul2(make_float2(w[j][k], w[j][k + 1]), mul2(pair_f32(&d[j].v[k]), r2));
+                    s1 = add2(s1, we);
+                    s2 = fma2(we, add2(pair_f32(&xv[j].v[k]), shift), s2);
+                }
+            }
+        }
+        float c1 = warp_sum(s1.x + s1.y), c2 = warp_sum(s2.x + s2.y);
+        if (lane == 0) s[it][warp] = make_float2(c1, c2);
+        __syncthreads();
+        const float2 p = s[it][lane % kWarps];
+        const float2 k1 = both(-group_sum(p.x, kWarps / 2) * inv_n), k2 = both(-group_sum(p.y, kWarps / 2) * inv_n * rstd * rstd);
+        if (row + gridDim.x < a.rows) {  // the next row, a 128-byte line to a thread
+            const char *fd = reinterpret_cast<const char *>(dy - c0 + gridDim.x * a.dys);
+            const char *fx = reinterpret_cast<const char *>(x - c0 + gridDim.x * a.xs);
+            for (int l = threadIdx.x * 128; l < cols * (int)sizeof(T); l += kWideThreads * 128) {
+                prefetch_l2(fd + l);
+                prefetch_l2(fx + l);
+            }
+        }
+        T *dx = static_cast<T *>(a.dx) + (a.dx ? row * a.dxs + c0 : 0);
+#pragma unroll
+        for (int v = 0; v < NV; v += kAtOnce) {
+            load(v);
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+#pragma unroll
+                for (int k = 0; k < E; k += 2) {
+                    const int i = ((v + j) * E + k) / 2;
+                    const float2 g = pair_f32(&d[j].v[k]), u = add2(pair_f32(&xv[j].v[k]), shift), e = mul2(g, r2);
+                    db[i] = add2(db[i], g);
+                    dw[i] = fma2(e, u, dw[i]);
+                    pair_set(&xv[j].v[k], fma2(make_float2(w[j][k], w[j][k + 1]), e, fma2(u, k2, k1)));
+                }
+                if (a.dx && c0 + (v + j) * kNext < cols) *reinterpret_cast<Pack<T, E> *>(dx + (v + j) * kNext) = xv[j];
+            }
+        }
+    }
+    if (!a.part) return;
+    float *out = a.part + (int64_t)blockIdx.x * cols;
+    const int64_t other = (int64_t)a.P * cols;
+#pragma unroll
+    for (int k = 0; k < EL; ++k) {
+        const int c = c0 + k / E * kNext + k % E;
+        if (c < cols) {
+            out[c] = k & 1 ? dw[k / 2].y : dw[k / 2].x;
+            out[c + other] = k & 1 ? db[k / 2].y : db[k / 2].x;
+        }
+    }
+}
+
+// Rows too long for that: the two row means first ...
 template <class T, bool EVEN>
 __global__ void __launch_bounds__(long_threads(EVEN)) norm_grad_means_kernel(const __grid_constant__ NormGradArgs a)
 {
@@ -711,6 +812,13 @@ void norm_grad_long_fn(bool even, const void **means, const void **columns)
 {
     *means = even ? (const void *)norm_grad_means_kernel<T, true> : (const void *)norm_grad_means_kernel<T, false>;
     *columns = even ? (const void *)norm_grad_columns_kernel<T, true> : (const void *)norm_grad_columns_kernel<T, false>;
+}
+
+template <class T>
+const void *norm_grad_wide_fn(int el)
+{
+    return el == 32   ? (const void *)norm_grad_wide_kernel<T, 32>
+           : el == 40 ? (const void *)norm_grad_wide_kernel<T, 40> : (const void *)norm_grad_wide_kernel<T, 48>;
 }
 
 // Kernels of the shapes that row_shape gives.
@@ -1023,7 +1131,15 @@ try {
         const bool vec = cols * eb % 16 == 0 && vector_rows(dy, dy_stride, rows, eb) &&
                          vector_rows(x, x_stride, rows, eb) && (!dx || vector_rows(dx, dx_stride, rows, eb));
         row_shape(rows, cols, vec, true, sms, kNormGradWarps, &el, &warps);
-        if (warps == 0) {
+        // Long even rows: one pass over HBM once each SM has a few of them (4096 x
+        // 18944 bf16 149 us, 64 rows 32; the two-pass kernels 215 and 14).
+        if (warps == 0 && vec && cols <= kWideThreads * 48 && rows >= 4 * (int64_t)sms) {
+            const int wide = cols <= kWideThreads * 32 ? 32 : cols <= kWideThreads * 40 ? 40 : 48;
+            const void *fn = dtype == RR_FP32   ? norm_grad_wide_fn<float>(wide)
+                             : dtype == RR_BF16 ? norm_grad_wide_fn<__nv_bfloat16>(wide) : norm_grad_wide_fn<__half>(wide);
+            a.P = sms < kMaxPartials ? sms : kMaxPartials;
+            RR_TRY(step_launch(fn, a.P, kWideThreads, 0, &a, stream));
+        } else if (warps == 0) {
             const void *means, *columns;
             if (dtype == RR_FP32) norm_grad_long_fn<float>(vec, &means, &columns);
             else if (dtype == RR_BF16) norm_grad_long_fn<__nv_bfloat16>(vec, &means, &columns);
