@@ -553,24 +553,24 @@ __global__ void __launch_bounds__(EL == 32 ? 256 : 512, EL == 8 ? 1 : 0) norm_gr
     }
 }
 
-// Even rows of more than a block's registers hold beside the sums: a block per
-// row and two passes over it, the second out of L1, the weight's gradient in
-// registers, EL columns to a thread.  While a row's second pass runs, the next
-// row comes into L2.
-constexpr int kWideThreads = 512;
+// Rows of more than a block's registers hold beside the sums: a block per row
+// and two passes over it, the second out of L1, the weight's gradient in
+// registers, EL columns to a thread, kAtOnce of them loaded together.  While a
+// row's second pass runs, the next row comes into L2.
+constexpr int kWideThreads = 512, kAtOnce = 8;
 __device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
-template <class T, int EL>
+template <class T, int EL, bool EVEN>
 __global__ void __launch_bounds__(kWideThreads) norm_grad_wide_kernel(const __grid_constant__ NormGradArgs a)
 {
     stream_order();
-    constexpr int E = 16 / (int)sizeof(T), NV = EL / E, kWarps = kWideThreads / 32;
-    constexpr int kAtOnce = NV % 2 ? 1 : 2;  // vectors whose loads run together
+    constexpr int E = kWidth<T, EVEN>, kWarps = kWideThreads / 32;
     __shared__ float2 s[2][kWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cols = (int)a.cols;
     const float inv_n = 1.0f / (float)cols;
     const bool waligned = aligned16(a.w);
+    // element k of the thread is at column c0 + column(k)
     const int c0 = threadIdx.x * E;
-    constexpr int kNext = kWideThreads * E;  // columns from a thread's vector to its next
+    auto column = [](int k) { return k / E * (kWideThreads * E) + k % E; };
     float2 dw[EL / 2], db[EL / 2];
 #pragma unroll
     for (int k = 0; k < EL / 2; ++k) dw[k] = db[k] = both(0.0f);
@@ -579,35 +579,51 @@ __global__ void __launch_bounds__(kWideThreads) norm_grad_wide_kernel(const __gr
         const T *dy = static_cast<const T *>(a.dy) + row * a.dys + c0, *x = static_cast<const T *>(a.x) + row * a.xs + c0;
         const float mean = a.mean[row], rstd = a.rstd[row];
         const float2 r2 = both(rstd), shift = both(-mean);
-        Pack<T, E> d[kAtOnce], xv[kAtOnce];
-        float w[kAtOnce][E];
-        auto load = [&](int v0) {
+        float g[kAtOnce], xv[kAtOnce], w[kAtOnce];  // elements k0 and on; dy = w = 0 past the row
+        auto load = [&](int k0) {
+            Pack<T, E> pd[kAtOnce / E], px[kAtOnce / E];
 #pragma unroll
-            for (int j = 0; j < kAtOnce; ++j) {
-                const int c = (v0 + j) * kNext;
+            for (int j = 0; j < kAtOnce / E; ++j) {
+                const int c = column(k0 + j * E);
+                float wj[E];
+#pragma unroll
+                for (int k = 0; k < E; ++k) {
+                    pd[j].v[k] = px[j].v[k] = from_f32<T>(0.0f);
+                    wj[k] = 0.0f;
+                }
                 if (c0 + c < cols) {
-                    d[j] = *reinterpret_cast<const Pack<T, E> *>(dy + c);
-                    xv[j] = *reinterpret_cast<const Pack<T, E> *>(x + c);
-                    weights_at<E>(w[j], a.w, c0 + c, a.wdtype, waligned, 1.0f);
-                } else {
-                    *reinterpret_cast<uint4 *>(&d[j]) = *reinterpret_cast<uint4 *>(&xv[j]) = make_uint4(0, 0, 0, 0);
+                    pd[j] = *reinterpret_cast<const Pack<T, E> *>(dy + c);
+                    px[j] = *reinterpret_cast<const Pack<T, E> *>(x + c);
+                    weights_at<E>(wj, a.w, c0 + c, a.wdtype, waligned, 1.0f);
+                }
 #pragma unroll
-                    for (int k = 0; k < E; ++k) w[j][k] = 0.0f;
+                for (int k = 0; k < E; ++k) w[j * E + k] = wj[k];
+            }
+#pragma unroll
+            for (int k = 0; k < kAtOnce; k += 2) {
+                if (E > 1) {
+                    const float2 gk = pair_f32(&pd[k / E].v[k % E]), xk = pair_f32(&px[k / E].v[k % E]);
+                    g[k] = gk.x;
+                    g[k + 1] = gk.y;
+                    xv[k] = xk.x;
+                    xv[k + 1] = xk.y;
+                } else {
+                    g[k] = to_f32(pd[k / E].v[k % E]);
+                    g[k + 1] = to_f32(pd[(k + 1) / E].v[(k + 1) % E]);
+                    xv[k] = to_f32(px[k / E].v[k % E]);
+                    xv[k + 1] = to_f32(px[(k + 1) / E].v[(k + 1) % E]);
                 }
             }
         };
         float2 s1 = both(0.0f), s2 = both(0.0f);
 #pragma unroll
-        for (int v = 0; v < NV; v += kAtOnce) {
-            load(v);
+        for (int k0 = 0; k0 < EL; k0 += kAtOnce) {
+            load(k0);
 #pragma unroll
-            for (int j = 0; j < kAtOnce; ++j) {
-#pragma unroll
-                for (int k = 0; k < E; k += 2) {
-                    const float2 we = mul2(make_float2(w[j][k], w[j][k + 1]), mul2(pair_f32(&d[j].v[k]), r2));
-                    s1 = add2(s1, we);
-                    s2 = fma2(we, add2(pair_f32(&xv[j].v[k]), shift), s2);
-                }
+            for (int k = 0; k < kAtOnce; k += 2) {
+                const float2 we = mul2(make_float2(w[k], w[k + 1]), mul2(make_float2(g[k], g[k + 1]), r2));
+                s1 = add2(s1, we);
+                s2 = fma2(we, add2(make_float2(xv[k], xv[k + 1]), shift), s2);
             }
         }
         float c1 = warp_sum(s1.x + s1.y), c2 = warp_sum(s2.x + s2.y);
@@ -615,7 +631,7 @@ __global__ void __launch_bounds__(kWideThreads) norm_grad_wide_kernel(const __gr
         __syncthreads();
         const float2 p = s[it][lane % kWarps];
         const float2 k1 = both(-group_sum(p.x, kWarps / 2) * inv_n), k2 = both(-group_sum(p.y, kWarps / 2) * inv_n * rstd * rstd);
-        if (row + gridDim.x < a.rows) {  // the next row, a 128-byte line to a thread
+        if (row + gridDim.x < a.rows) {  // the next row, 128 bytes to a thread
             const char *fd = reinterpret_cast<const char *>(dy - c0 + gridDim.x * a.dys);
             const char *fx = reinterpret_cast<const char *>(x - c0 + gridDim.x * a.xs);
             for (int l = threadIdx.x * 128; l < cols * (int)sizeof(T); l += kWideThreads * 128) {
@@ -625,19 +641,29 @@ __global__ void __launch_bounds__(kWideThreads) norm_grad_wide_kernel(const __gr
         }
         T *dx = static_cast<T *>(a.dx) + (a.dx ? row * a.dxs + c0 : 0);
 #pragma unroll
-        for (int v = 0; v < NV; v += kAtOnce) {
-            load(v);
+        for (int k0 = 0; k0 < EL; k0 += kAtOnce) {
+            load(k0);
+            Pack<T, E> out[kAtOnce / E];
 #pragma unroll
-            for (int j = 0; j < kAtOnce; ++j) {
-#pragma unroll
-                for (int k = 0; k < E; k += 2) {
-                    const int i = ((v + j) * E + k) / 2;
-                    const float2 g = pair_f32(&d[j].v[k]), u = add2(pair_f32(&xv[j].v[k]), shift), e = mul2(g, r2);
-                    db[i] = add2(db[i], g);
-                    dw[i] = fma2(e, u, dw[i]);
-                    pair_set(&xv[j].v[k], fma2(make_float2(w[j][k], w[j][k + 1]), e, fma2(u, k2, k1)));
+            for (int k = 0; k < kAtOnce; k += 2) {
+                const int i = (k0 + k) / 2;
+                const float2 gk = make_float2(g[k], g[k + 1]), u = add2(make_float2(xv[k], xv[k + 1]), shift), e = mul2(gk, r2);
+                db[i] = add2(db[i], gk);
+                dw[i] = fma2(e, u, dw[i]);
+                const float2 y = fma2(make_float2(w[k], w[k + 1]), e, fma2(u, k2, k1));
+                if (E > 1) {
+                    pair_set(&out[k / E].v[k % E], y);
+                } else {
+                    out[k / E].v[k % E] = from_f32<T>(y.x);
+                    out[(k + 1) / E].v[(k + 1) % E] = from_f32<T>(y.y);
                 }
-                if (a.dx && c0 + (v + j) * kNext < cols) *reinterpret_cast<Pack<T, E> *>(dx + (v + j) * kNext) = xv[j];
+            }
+            if (a.dx) {
+#pragma unroll
+                for (int j = 0; j < kAtOnce / E; ++j) {
+                    const int c = column(k0 + j * E);
+                    if (c0 + c < cols) *reinterpret_cast<Pack<T, E> *>(dx + c) = out[j];
+                }
             }
         }
     }
@@ -646,7 +672,7 @@ __global__ void __launch_bounds__(kWideThreads) norm_grad_wide_kernel(const __gr
     const int64_t other = (int64_t)a.P * cols;
 #pragma unroll
     for (int k = 0; k < EL; ++k) {
-        const int c = c0 + k / E * kNext + k % E;
+        const int c = c0 + column(k);
         if (c < cols) {
             out[c] = k & 1 ? dw[k / 2].y : dw[k / 2].x;
             out[c + other] = k & 1 ? db[k / 2].y : db[k / 2].x;
@@ -814,11 +840,16 @@ void norm_grad_long_fn(bool even, const void **means, const void **columns)
     *columns = even ? (const void *)norm_grad_columns_kernel<T, true> : (const void *)norm_grad_columns_kernel<T, false>;
 }
 
-template <class T>
+template <class T, bool EVEN>
 const void *norm_grad_wide_fn(int el)
 {
-    return el == 32   ? (const void *)norm_grad_wide_kernel<T, 32>
-           : el == 40 ? (const void *)norm_grad_wide_kernel<T, 40> : (const void *)norm_grad_wide_kernel<T, 48>;
+    return el == 32   ? (const void *)norm_grad_wide_kernel<T, 32, EVEN>
+           : el == 40 ? (const void *)norm_grad_wide_kernel<T, 40, EVEN> : (const void *)norm_grad_wide_kernel<T, 48, EVEN>;
+}
+template <class T>
+const void *norm_grad_wide_fn(int el, bool even)
+{
+    return even ? norm_grad_wide_fn<T, true>(el) : norm_grad_wide_fn<T, false>(el);
 }
 
 // Kernels of the shapes that row_shape gives.
@@ -1131,12 +1162,13 @@ try {
         const bool vec = cols * eb % 16 == 0 && vector_rows(dy, dy_stride, rows, eb) &&
                          vector_rows(x, x_stride, rows, eb) && (!dx || vector_rows(dx, dx_stride, rows, eb));
         row_shape(rows, cols, vec, true, sms, kNormGradWarps, &el, &warps);
-        // Long even rows: one pass over HBM once each SM has a few of them (4096 x
-        // 18944 bf16 149 us, 64 rows 32; the two-pass kernels 215 and 14).
-        if (warps == 0 && vec && cols <= kWideThreads * 48 && rows >= 4 * (int64_t)sms) {
+        // Long rows: one pass over HBM once each SM has a few of them (4096 x 18944
+        // bf16 150 us, 64 rows 32, uneven 2000 x 12001 73; the two-pass kernels 215,
+        // 14 and 120).
+        if (warps == 0 && cols <= kWideThreads * 48 && rows >= 4 * (int64_t)sms) {
             const int wide = cols <= kWideThreads * 32 ? 32 : cols <= kWideThreads * 40 ? 40 : 48;
-            const void *fn = dtype == RR_FP32   ? norm_grad_wide_fn<float>(wide)
-                             : dtype == RR_BF16 ? norm_grad_wide_fn<__nv_bfloat16>(wide) : norm_grad_wide_fn<__half>(wide);
+            const void *fn = dtype == RR_FP32   ? norm_grad_wide_fn<float>(wide, vec)
+                             : dtype == RR_BF16 ? norm_grad_wide_fn<__nv_bfloat16>(wide, vec) : norm_grad_wide_fn<__half>(wide, vec);
             a.P = sms < kMaxPartials ? sms : kMaxPartials;
             RR_TRY(step_launch(fn, a.P, kWideThreads, 0, &a, stream));
         } else if (warps == 0) {
