@@ -1,10 +1,12 @@
 // Gradient norm and AdamW over lists of tensors (include/rr.h: rr_grad_norm,
 // rr_adamw, rr_adamw8).
 //
-// All three stream: every byte is touched once and HBM bounds them.  A launch
-// takes its list of tensors by value in the kernel's parameters (no table in
-// device memory to fill or keep), cut into chunks of elements that the blocks
-// deal out in turn; a block finds a chunk's tensor by bisection.
+// All three stream: every byte is touched once.  A launch takes its list of
+// tensors by value in the kernel's parameters (no table in device memory to fill
+// or keep; a small and a large table, as parameters are copied at each launch),
+// cut into chunks of elements; a block finds a chunk's tensor by bisection.
+//
+// Times below are of one GB300 (152 SMs, measured copy 6.7 TB/s).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -83,10 +85,19 @@ struct GradNormArgs {
     GradNormEndArgs end;
 };
 
+// The sum of squares.  A thread takes 8 vectors of a chunk at once; their sum
+// goes to a compensated sum, the threads' sums to binary64, the blocks' partial
+// sums, in order, to a last block.
+//
 // Sums of squares in [2^-90, 2^90] are sound in binary32: every square that
 // underflowed is below 2^-126 and lost in the sum's own rounding, and 2^30 such
 // sums stay finite.  A thread's sum of a chunk that lies outside (zeros aside)
 // is taken again in binary64; NaN fails the comparison and goes there too.
+//
+// Bound: HBM.  A layer of 233M bf16 gradients 69.7 us, the measured copy peak
+// (with a range check for each vector and chunks dealt out in turn 120 and 74);
+// 60M in 100 odd tensors 23 us (77 %: partial chunks at the tensors' ends); two
+// tensors of 3584 4.4 us (latency, one launch).
 __device__ __forceinline__ bool sound(float sum) { return sum >= 0x1p-90f && sum <= 0x1p90f; }
 
 template <class T, int CAP>
@@ -230,6 +241,12 @@ __device__ __forceinline__ float adam_element(const AdamScalars &h, float scale,
     return __fsub_rn(__fmul_rn(w, h.decay), __fmul_rn(__fdiv_rn(m, den), h.step_size));
 }
 
+// A thread has four vectors of four elements of a chunk; the loads of all streams
+// are issued before the first is used.  Tensors whose pointers are not aligned
+// alike go element by element.  Bound: HBM (7 streams with master weights).  One
+// rank's shard of a layer, 29M bf16 weights with masters, 130 us, 6.3 TB/s, 93 % of
+// the copy peak; 30M binary32 138 us (91 %); 7M in 61 tensors packed at any element
+// 34.6 us (84 %).  Two vectors a thread took 160 us for the shard.
 template <class P, class G, bool MASTER, int CAP>
 __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ AdamArgs<CAP> a)
 {
@@ -606,6 +623,13 @@ __device__ __forceinline__ void adamw8_block(const AdamScalars &h, float scale, 
 
 // A warp takes runs of up to 32 blocks of one tensor.  Lane i holds the scales
 // of the run's block i, so that they are read and written together.
+//
+// Bound: instruction issue (74 % of the slots in use, about 55 instructions an
+// element), then HBM.  A layer of 233M bf16 weights 434 us, 5.4 TB/s, 81 % of the
+// copy peak: with sqrt and / of their own, one operation at a time, 906; those two
+// at a time and corrected 594; longer runs 514; the ring 455; the dither's halves
+// by a dot product 446.  60M bf16 weights with masters 181 us (89 %), 60M binary32
+// 161 us (89 %).
 template <class P, class G, bool MASTER, int CAP>
 __global__ void __launch_bounds__(kThreads) adamw8_kernel(const __grid_constant__ Adam8Args<CAP> a)
 {
