@@ -187,7 +187,7 @@ __device__ __forceinline__ int half_of(int G) { return G > 1 ? 1 << (31 - __clz(
 // by instructions, an element to each load and store: 20011 x 1027 fp16 28.8 us.
 __host__ __device__ constexpr int ring_rows(int el, int eb) { return el * eb > 64 ? 3 : 4; }  // 512 threads' rings fit an SM
 template <class T, int EL, bool VEC, bool GROUP>
-__global__ void __launch_bounds__(EL == 8 ? 1024 : EL == 16 ? 256 : 512, EL == 16 ? 3 : 1) norm_rows_kernel(const __grid_constant__ NormArgs a)
+__global__ void __launch_bounds__(EL == 8 ? 1024 : EL == 16 ? 256 : 512, EL == 16 ? (VEC ? 3 : 2) : 1) norm_rows_kernel(const __grid_constant__ NormArgs a)
 {
     stream_order();
     using S = Slice<T, EL, VEC>;
@@ -875,6 +875,7 @@ template <class T>
 const void *norm_rows_fn(int el, bool vec, bool group)
 {
     if (!vec && el == 32) return (const void *)norm_rows_kernel<T, 32, false, true>;
+    if (!vec && el == 16) return (const void *)norm_rows_kernel<T, 16, false, false>;
     if (!vec) return group ? (const void *)norm_rows_kernel<T, 8, false, true> : (const void *)norm_rows_kernel<T, 8, false, false>;
     if (el == 8) return group ? (const void *)norm_rows_kernel<T, 8, true, true> : (const void *)norm_rows_kernel<T, 8, true, false>;
     if (el == 16) return group ? (const void *)norm_rows_kernel<T, 16, true, true> : (const void *)norm_rows_kernel<T, 16, true, false>;
@@ -897,15 +898,15 @@ const void *norm_grad_fn(int el, bool vec, bool group)
 // us), else 16 a lane up to 8 warps, then 32; with fewer rows than SMs, where
 // nothing but one row's latency counts, 8 a lane.  Uneven rows
 // take 8 a lane while its warps allow (66 against 60 us for 8000 x 5001 bf16
-// forward with 16), except the gradient of 257 to 512 columns, one warp a row
-// with 16 (65536 x 301: 55 against 81), then 32 (it spills, but reads a row
+// forward with 16), except one warp a row with 16 for 257 to 512 columns (65536 x
+// 301 bf16: 30 against 35, gradient 55 against 81), then 32 (it spills, but reads a row
 // once: 4000 x 12001 94 us, the long-row kernel 120).  warps > 0 where a kernel of
 // that shape takes the row (most[]: the warps its launch bounds allow with 8, 16
 // and 32 elements a lane), else 0.
-void row_shape(int64_t rows, int64_t cols, bool even, bool grad, int sms, const int *most, int *el, int *warps)
+void row_shape(int64_t rows, int64_t cols, bool even, int sms, const int *most, int *el, int *warps)
 {
     auto need = [&](int e) { return (cols + 32 * e - 1) / (32 * e); };
-    if (!even) *el = grad && cols > 256 && cols <= 512 ? 16 : need(8) <= most[0] ? 8 : 32;
+    if (!even) *el = cols > 256 && cols <= 512 ? 16 : need(8) <= most[0] ? 8 : 32;
     else if (cols <= 256 || (rows <= sms && need(8) <= most[0])) *el = 8;
     else if (cols <= 512) *el = 16;
     else if (cols <= 1024) *el = rows < 8 * sms ? 16 : 32;
@@ -1076,7 +1077,7 @@ try {
     NormArgs a{x, weight, bias, y, mean, rstd, rows, cols, x_stride, y_stride, eps, (int)weight_dtype};
     int el = 0, warps = 0;
     const bool vec = cols * eb % 16 == 0 && vector_rows(x, x_stride, rows, eb) && vector_rows(y, y_stride, rows, eb);
-    row_shape(rows, cols, vec, false, sms, kNormWarps, &el, &warps);
+    row_shape(rows, cols, vec, sms, kNormWarps, &el, &warps);
     const void *fn;
     int threads, smem = 0;
     int64_t blocks;
@@ -1179,7 +1180,7 @@ try {
         int el = 0, warps = 0;
         const bool vec = cols * eb % 16 == 0 && vector_rows(dy, dy_stride, rows, eb) &&
                          vector_rows(x, x_stride, rows, eb) && (!dx || vector_rows(dx, dx_stride, rows, eb));
-        row_shape(rows, cols, vec, true, sms, kNormGradWarps, &el, &warps);
+        row_shape(rows, cols, vec, sms, kNormGradWarps, &el, &warps);
         // Long rows: one pass over HBM once each SM has a few of them (4096 x 18944
         // bf16 150 us, 64 rows 32, uneven 2000 x 12001 73; the two-pass kernels 215,
         // 14 and 120).
