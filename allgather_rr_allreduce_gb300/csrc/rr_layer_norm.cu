@@ -305,7 +305,8 @@ __global__ void __launch_bounds__(EL == 8 ? 1024 : EL == 16 ? 256 : 512, EL == 1
 // Rows too long for registers: a block per row, three passes over it, the
 // second and third out of L1 or L2.  EVEN: rows of whole, aligned 16-byte
 // vectors, E elements at a time; else one at a time.  Bound by the latency of the
-// passes and their two block sums: 4096 x 18944 bf16 93 us (50 % of the copy peak).
+// passes and their two block sums: 4096 x 18944 bf16 83 us (56 % of the copy peak;
+// 92 without the next row's way to L2).
 template <class T, bool EVEN>
 constexpr int kWidth = EVEN ? 16 / (int)sizeof(T) : 1;
 
@@ -320,8 +321,8 @@ __device__ __forceinline__ float block_sum(float x, float *s)
     return t;
 }
 
-// Vectors: 93 us for 4096 x 18944 bf16 forward with 512 threads, 134 with 1024;
-// single elements: 275 and 197 for 2000 x 40001.
+// Vectors: 83 us for 4096 x 18944 bf16 forward with 512 threads, 119 with 1024;
+// single elements: 275 and 197 for 2000 x 40001 (before rows were brought to L2).
 __host__ __device__ constexpr int long_threads(bool even) { return even ? 512 : 1024; }
 template <class T, bool EVEN>
 __global__ void __launch_bounds__(long_threads(EVEN)) norm_long_kernel(const __grid_constant__ NormArgs a)
@@ -341,6 +342,10 @@ __global__ void __launch_bounds__(long_threads(EVEN)) norm_long_kernel(const __g
 #pragma unroll
             for (int k = 0; k < E; ++k) sum += to_f32(v.v[k]);
         }
+        if (row + gridDim.x < a.rows) {  // the next row into L2, 128 bytes to a thread
+            const char *far = reinterpret_cast<const char *>(x + gridDim.x * a.xs);
+            for (int64_t l = threadIdx.x * 128; l < a.cols * (int64_t)sizeof(T); l += kLongThreads * 128) prefetch_l2(far + l);
+        }
         const float mean = block_sum(sum, s) / (float)a.cols;
         float m2 = 0.0f;
 #pragma unroll 4
@@ -353,7 +358,7 @@ __global__ void __launch_bounds__(long_threads(EVEN)) norm_long_kernel(const __g
             }
         }
         const float rstd = rsqrtf(block_sum(m2, s) / (float)a.cols + a.eps);
-#pragma unroll 2
+#pragma unroll 4
         for (int64_t c = first; c < a.cols; c += next) {
             Pack<T, E> v = *reinterpret_cast<const Pack<T, E> *>(x + c);
             float w[E], b[E];
@@ -575,7 +580,6 @@ __global__ void __launch_bounds__(EL == 32 ? 256 : 512, EL == 8 ? 1 : 0) norm_gr
 // 47 % of the copy peak; without that 190).  One block of 16 warps to an SM: bound by
 // the latency of its loads and by instructions.
 constexpr int kWideThreads = 512, kAtOnce = 8;
-__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 template <class T, int EL, bool EVEN>
 __global__ void __launch_bounds__(kWideThreads) norm_grad_wide_kernel(const __grid_constant__ NormGradArgs a)
 {
