@@ -321,8 +321,7 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
 // registers.
 constexpr int kBlock = RR_ADAMW8_BLOCK;
 constexpr int kLane = kBlock / 32;
-constexpr int kAdam8Run = 32;    // most blocks of a run: one for each lane's scales
-constexpr int kAdam8Runs = 4;    // runs of a warp where there are enough blocks
+constexpr int kAdam8Run = 16;  // most blocks of a run
 // Blocks of a warp in flight or in use.  With 4-byte weights the 6 leave one
 // thread block to an SM and are faster for it: 60M binary32 weights 160 us, with
 // 5 (two thread blocks) 168; a bf16 layer 435 with 5, 446 with 4 or 6.
@@ -330,13 +329,12 @@ __host__ __device__ constexpr int adam8_stages(int weight_bytes) { return weight
 
 template <int CAP>
 struct Adam8Args {
-    Chunks<CAP> list;  // chunk = run of blocks of kBlock elements
+    Chunks<CAP> list;  // chunk = block of kBlock elements
     void *p[CAP];
     const void *g[CAP];
     uint8_t *m[CAP], *r[CAP];
     float *ms[CAP], *rs[CAP], *w[CAP];
     AdamScalars h;
-    int run;               // blocks of a chunk
     uint32_t seed, first;  // first: index in the caller's list of this launch's first tensor
 };
 
@@ -349,14 +347,11 @@ __host__ __device__ __forceinline__ uint32_t mix32(uint32_t x)
     return x ^ (x >> 16);
 }
 
-// Power-of-two scale of a block from the bits of its largest magnitude: the
-// magnitude over the scale lies in [128, 256).
-__device__ __forceinline__ int scale_exponent(uint32_t top)
-{
-    const int e = (int)(top >> 23) - 127 - 7;
-    return e < -126 ? -126 : e;
-}
-__device__ __forceinline__ float exp2_int(int e) { return __int_as_float((e + 127) << 23); }
+// Power-of-two scale of a block from the bits of its largest magnitude, as bits:
+// the magnitude over the scale lies in [128, 256), or the scale is 2^-126.  Its
+// reciprocal has the mirrored exponent.
+__device__ __forceinline__ uint32_t scale_bits(uint32_t top) { return max(top & 0x7F800000u, 0x04000000u) - 0x03800000u; }
+__device__ __forceinline__ float reciprocal(uint32_t scale) { return __uint_as_float(0x7F000000u - scale); }
 
 // |x| / scale on the code's grid, up or down by the 16 random bits u: adding
 // them just below the last kept mantissa bit and cutting there rounds up with
@@ -585,8 +580,8 @@ __device__ __forceinline__ void adamw8_block(const AdamScalars &h, float scale, 
     // bits of magnitudes order as they do, NaN above all
     const uint32_t mbits = warp_max(__float_as_uint(mtop)), rbits = warp_max(__float_as_uint(rtop));
     const bool mfine = mbits < 0x7F800000u, rfine = rbits < 0x7F800000u;
-    const int me = scale_exponent(mbits), re = scale_exponent(rbits);
-    const float2 minv = both(mfine ? exp2_int(-me) : 0.0f), rinv = both(rfine ? exp2_int(-re) : 0.0f);
+    const uint32_t me = scale_bits(mbits), re = scale_bits(rbits);
+    const float2 minv = both(reciprocal(me)), rinv = both(reciprocal(re));
     // (x / scale) on the code's grid: adding random bits just below the last
     // kept mantissa bit and cutting there rounds up with the probability of the
     // part cut off.  Signs stay out of it.
@@ -617,19 +612,20 @@ __device__ __forceinline__ void adamw8_block(const AdamScalars &h, float scale, 
     L::store(mp, mq, lane, left);
     L::store(rp, rq, lane, left);
     const float nan = __int_as_float(0x7fc00000);
-    mscale = mfine ? exp2_int(me) : nan;
-    rscale = rfine ? exp2_int(re) : nan;
+    mscale = mfine ? __uint_as_float(me) : nan;
+    rscale = rfine ? __uint_as_float(re) : nan;
 }
 
-// A warp takes runs of up to 32 blocks of one tensor.  Lane i holds the scales
-// of the run's block i, so that they are read and written together.
+// Warps take equal stretches of the list's blocks, in runs of up to kAdam8Run of
+// one tensor.  Lane i holds the scales of the run's block i, so that they are read
+// and written together.
 //
 // Bound: instruction issue (74 % of the slots in use, about 55 instructions an
-// element), then HBM.  A layer of 233M bf16 weights 434 us, 5.4 TB/s, 81 % of the
+// element), then HBM.  A layer of 233M bf16 weights 436 us, 5.4 TB/s, 80 % of the
 // copy peak: with sqrt and / of their own, one operation at a time, 906; those two
-// at a time and corrected 594; longer runs 514; the ring 455; the dither's halves
-// by a dot product 446.  60M bf16 weights with masters 181 us (89 %), 60M binary32
-// 161 us (89 %).
+// at a time and corrected 594; the ring 455; the dither's halves by a dot product
+// 446.  60M bf16 weights with masters 178 us (91 %), 60M binary32 154 us (93 %);
+// runs of 32 dealt out in turn, uneven at the end, 185 and 161.
 template <class P, class G, bool MASTER, int CAP>
 __global__ void __launch_bounds__(kThreads) adamw8_kernel(const __grid_constant__ Adam8Args<CAP> a)
 {
@@ -643,13 +639,15 @@ __global__ void __launch_bounds__(kThreads) adamw8_kernel(const __grid_constant_
     // one value in the warp, so that what follows from it is too
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     char *const ring = reinterpret_cast<char *>(s_ring) + warp * kAdam8Stages * L::stage_bytes();
-    const int64_t total = a.list.start[a.list.count];
-    const int64_t step = (int64_t)gridDim.x * (kThreads / 32);
-    for (int64_t chunk = (int64_t)blockIdx.x * (kThreads / 32) + warp; chunk < total; chunk += step) {
-        const int t = a.list.find(chunk);
-        const int64_t b = (chunk - a.list.start[t]) * a.run, at = b * kBlock, left = a.list.size[t] - at;
-        const int blocks = (int)min((int64_t)a.run, (left + kBlock - 1) / kBlock);
-        const int whole = a.list.head[t] == 0 ? (int)min((int64_t)a.run, left / kBlock) : 0;
+    const int64_t total = a.list.start[a.list.count], warps = (int64_t)gridDim.x * (kThreads / 32);
+    const int64_t mine = (int64_t)blockIdx.x * (kThreads / 32) + warp, end = total * (mine + 1) / warps;
+    int64_t from = total * mine / warps;
+    for (int t = a.list.find(from); from < end;) {
+        while (from >= a.list.start[t + 1]) ++t;
+        const int64_t b = from - a.list.start[t], at = b * kBlock, left = a.list.size[t] - at;
+        const int blocks = (int)min((int64_t)kAdam8Run, min(end, a.list.start[t + 1]) - from);
+        const int whole = a.list.head[t] == 0 ? (int)min((int64_t)blocks, left / kBlock) : 0;
+        from += blocks;
         P *p = static_cast<P *>(a.p[t]) + at;
         const G *g = static_cast<const G *>(a.g[t]) + at;
         uint8_t *m = a.m[t] + at, *r = a.r[t] + at;
@@ -884,11 +882,6 @@ rr_status adamw8_lists(void *const *params, const void *const *grads, uint8_t *c
     const int wb = master ? 4 : float_bytes(pd);
     const int smem = kThreads / 32 * adam8_stages(wb) * kBlock * (wb + float_bytes(gd) + 2);
     RR_TRY(step_fit(fn, kThreads, smem, &fit));
-    // Runs as long as leave each warp a few of them.
-    const int64_t warps = (int64_t)fit * sms * (kThreads / 32);
-    int64_t blocks = 0;
-    for (int i = 0; i < count; ++i) blocks += (sizes[i] + kBlock - 1) / kBlock;
-    a.run = (int)std::min<int64_t>(kAdam8Run, std::max<int64_t>(1, blocks / (kAdam8Runs * warps)));
     // Tensors keep their place in the caller's list (it enters the random
     // bits), so empty ones stay in the table with no chunks.
     for (int i = 0; i < count;) {
@@ -907,7 +900,7 @@ rr_status adamw8_lists(void *const *params, const void *const *grads, uint8_t *c
                                               aligned_to(r[i], 8) && (!master || aligned_to(master[i], 16))
                                           ? 0 : kNoVector);
             a.list.size[k] = sizes[i];
-            a.list.start[k + 1] = a.list.start[k] + (sizes[i] + (int64_t)a.run * kBlock - 1) / ((int64_t)a.run * kBlock);
+            a.list.start[k + 1] = a.list.start[k] + (sizes[i] + kBlock - 1) / kBlock;
         }
         a.list.count = k;
         if (a.list.start[k] == 0) continue;
