@@ -472,7 +472,8 @@ rr_status rr_layer_norm_backward_workspace(int64_t rows, int64_t cols, size_t *b
  *            or NaN when *norm is not finite.
  * inv_scale takes a loss scale or a sum over ranks out of the gradients (1 /
  * scale, 1 / W); max_norm = INFINITY clips nothing.  Values whose squares
- * leave binary32's range do not overflow or vanish: the sum is held in binary64.
+ * leave binary32's range do not overflow or vanish: such parts of the sum, and
+ * the sum of the parts, are held in binary64.
  *
  * grads: HOST array of num_tensors (>= 0) device pointers; tensor i holds
  * sizes[i] >= 0 elements of dtype (NULL allowed where sizes[i] is 0).  The
