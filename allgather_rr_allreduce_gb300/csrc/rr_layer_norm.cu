@@ -899,7 +899,8 @@ const void *norm_grad_fn(int el, bool vec, bool group)
 // Elements to a lane and warps to a row.  Even rows: one warp while 32 elements
 // a lane hold the row (two with 16 from 513 columns on where there are fewer
 // than 8 rows for each SM: the gradient of 257 x 1024 binary32 5.9 against 7.6
-// us), else 16 a lane up to 8 warps, then 32; with fewer rows than SMs, where
+// us), else 16 a lane up to 8 warps (12 for the gradient: 8192 x 5120 bf16 60 us,
+// with 32 68; 8192 x 8192 85 and 78), then 32; with fewer rows than SMs, where
 // nothing but one row's latency counts, 8 a lane.  Uneven rows
 // take 8 a lane while its warps allow (66 against 60 us for 8000 x 5001 bf16
 // forward with 16), except one warp a row with 16 for 257 to 512 columns (65536 x
@@ -914,12 +915,12 @@ void row_shape(int64_t rows, int64_t cols, bool even, int sms, const int *most, 
     else if (cols <= 256 || (rows <= sms && need(8) <= most[0])) *el = 8;
     else if (cols <= 512) *el = 16;
     else if (cols <= 1024) *el = rows < 8 * sms ? 16 : 32;
-    else *el = need(16) <= 8 ? 16 : 32;
+    else *el = need(16) <= most[1] ? 16 : 32;
     const int64_t n = need(*el);
     *warps = n <= most[*el == 8 ? 0 : *el == 16 ? 1 : 2] ? (int)n : 0;
 }
 
-constexpr int kNormWarps[3] = {32, 8, 16}, kNormGradWarps[3] = {16, 16, 8};
+constexpr int kNormWarps[3] = {32, 8, 16}, kNormGradWarps[3] = {16, 12, 8};
 
 struct Rows {
     const char *name;

@@ -77,7 +77,7 @@ SHAPES = [(1, 1), (3, 2), (5, 7), (2, 8), (40, 31), (1, 64), (153, 64), (9, 255)
           (160, 513), (33, 1000), (1217, 1024), (5, 1027), (300, 1027), (1, 3584), (8, 3584), (700, 3584), (155, 8192),
           (4, 8193), (160, 8200), (3, 16384), (2, 16385), (3, 18944), (2, 40001), (400, 18944), (330, 9001), (170, 20003),
           (90, 32768), (160, 32776),
-          (700, 18944), (609, 24576), (620, 9008), (650, 16384)]
+          (200, 5120), (180, 6150), (700, 18944), (609, 24576), (620, 9008), (650, 16384)]
 
 
 @pytest.mark.parametrize("rows,cols", SHAPES)
