@@ -201,8 +201,8 @@ def encode(x, dither, floor=False):
     proportion; None rounds to the nearest.  `floor`: a positive value is
     never stored as less than the smallest code."""
     x = x.view(-1, BLOCK)
-    top = x.abs().amax(1, keepdim=True)
-    e = torch.where(top > 0, torch.frexp(top)[1] - 8, -126).clamp_(-126, 120)
+    _, e = torch.frexp(x.abs().amax(1, keepdim=True))
+    e = torch.clamp(e - 8, -126, 120)
     scale = torch.ldexp(torch.ones((), device=x.device), e)
     t = torch.ldexp(torch.ones((), device=x.device), -e) * x
     a = t.abs()
