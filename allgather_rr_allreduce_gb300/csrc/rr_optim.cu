@@ -215,6 +215,7 @@ struct AdamScalars {
     float eps;
     float minus_zero;                // -0, for mul2_apart
     uint32_t one;                    // 1, where a multiply-add may not become an addition
+    float root_most;                 // largest sqrt(v) of adamw8_block's fast quotients (-1: none)
     const float *scale;
 };
 
@@ -537,16 +538,17 @@ __device__ __forceinline__ void adamw8_block(const AdamScalars &h, float scale, 
 {
     using L = Lane8<W, G, VEC>;
     float2 w[kLane / 2], m[kLane / 2], r[kLane / 2], v[kLane / 2];
-    // A code times a power-of-two scale is exact, so the scale goes with beta1.
-    const float2 mb1 = both(mscale * h.beta1), rs = both(rscale), b2 = both(h.beta2), nz = both(h.minus_zero);
-    float mtop = 0.0f, rtop = 0.0f, rlow = 3e38f;
+    // A code times its power-of-two scale is exact.
+    const float2 ms = both(mscale), rs = both(rscale), b1 = both(h.beta1), b2 = both(h.beta2), nz = both(h.minus_zero);
+    float mtop = 0.0f, mlow = 3e38f, rtop = 0.0f, rlow = 3e38f;
 #pragma unroll
     for (int k = 0; k < kLane / 2; ++k) {
         const float2 g = mul2(pair_f32(&in.g.v[2 * k]), both(scale));
-        m[k] = add2(mul2_apart(codes_of(in.m, k), mb1, nz), mul2_apart(g, both(h.omb1), nz));
+        m[k] = add2(mul2_apart(mul2(codes_of(in.m, k), ms), b1, nz), mul2_apart(g, both(h.omb1), nz));
         r[k] = mul2(codes_of(in.r, k), rs);
         v[k] = add2(mul2_apart(mul2(r[k], r[k]), b2, nz), mul2_apart(mul2(g, both(h.omb2)), g, nz));
         mtop = top3(mtop, m[k].x, m[k].y);
+        mlow = low3_abs(mlow, m[k].x, m[k].y);
         w[k] = pair_f32(&in.w.v[2 * k]);
         r[k] = root2(v[k], mul2(v[k], both(-1.0f)));
         rtop = top3(rtop, r[k].x, r[k].y);
@@ -554,10 +556,19 @@ __device__ __forceinline__ void adamw8_block(const AdamScalars &h, float scale, 
     }
     // The fast roots and quotients round as sqrt and / do while their operands
     // keep away from binary32's ends (a root that does not comes out as NaN,
-    // below 2^-50 or above 2^50); a lane with one that does not, a v of 0 among
-    // them, takes sqrt and / for all 8.
+    // below 2^-50 or above 2^50) and the quotient is normal: it is at most m over
+    // the root, and at least 2^-100 over 2^25.  A lane with an operand that does
+    // not, a v of 0 among them, takes sqrt and / for all 8.
+    if (mlow < 0x1p-100f) {  // an m of 0 is no small one: its quotient is 0
+        mlow = 3e38f;
+#pragma unroll
+        for (int k = 0; k < kLane / 2; ++k) {
+            if (m[k].x != 0.0f) mlow = fminf(mlow, fabsf(m[k].x));
+            if (m[k].y != 0.0f) mlow = fminf(mlow, fabsf(m[k].y));
+        }
+    }
     const float2 decay = both(h.decay), size = both(-h.step_size);
-    if (rlow >= 0x1p-50f && rtop <= 0x1p50f && mtop <= 0x1p100f && h.eps <= 0x1p60f) {
+    if (rlow >= 0x1p-50f && rtop <= h.root_most && mlow >= 0x1p-100f && mtop <= fminf(rlow, 1.0f) * 0x1p100f) {
         const float2 nc2 = both(-h.inv_c2), neps = both(-h.eps);
 #pragma unroll
         for (int k = 0; k < kLane / 2; ++k) {
@@ -621,11 +632,13 @@ __device__ __forceinline__ void adamw8_block(const AdamScalars &h, float scale, 
 // and written together.
 //
 // Bound: instruction issue (74 % of the slots in use, about 55 instructions an
-// element), then HBM.  A layer of 233M bf16 weights 436 us, 5.4 TB/s, 80 % of the
+// element), then HBM.  A layer of 233M bf16 weights 437 us, 5.4 TB/s, 80 % of the
 // copy peak: with sqrt and / of their own, one operation at a time, 906; those two
 // at a time and corrected 594; the ring 455; the dither's halves by a dot product
-// 446.  60M bf16 weights with masters 178 us (91 %), 60M binary32 154 us (93 %);
-// runs of 32 dealt out in turn, uneven at the end, 185 and 161.
+// 446; runs in equal stretches 435; a look at the least m, and its code's scale
+// apart from beta1, 2 more.  60M bf16 weights with masters 178 us (91 %), 60M
+// binary32 156 us (92 %); runs of 32 dealt out in turn, uneven at the end, 185 and
+// 161 (before that look).
 template <class P, class G, bool MASTER, int CAP>
 __global__ void __launch_bounds__(kThreads) adamw8_kernel(const __grid_constant__ Adam8Args<CAP> a)
 {
@@ -756,6 +769,8 @@ AdamScalars scalars(const rr_adamw_hyper &h, const float *scale)
     s.eps = (float)h.eps;
     s.minus_zero = -0.0f;
     s.one = 1;
+    // keeps sqrt(v) * inv_c2 + eps at 2^25 or below
+    s.root_most = s.eps <= 0x1p24f ? std::fmin(0x1p50f, 0x1p24f / s.inv_c2) : -1.0f;
     s.scale = scale;
     return s;
 }

@@ -32,8 +32,9 @@ __device__ __forceinline__ float2 root2(float2 v, float2 nv)
 }
 
 // m / d rounded to nearest for d in [2^-100, 2^100] and m = 0 or |m| in [2^-100,
-// 2^100] with a normal quotient below 2^127 (a smaller m or quotient may be off
-// by a few of the smallest subnormals); nd = -d.
+// 2^100] with a normal quotient below 2^127; nd = -d.  Nothing else is sound: the
+// remainder of a smaller m underflows and leaves the quotient off by a unit in
+// its last place, a smaller quotient is rounded twice, a larger one is NaN.
 // y = 1 / d refined once, q = m * y, q + (m - d * q) * y.
 __device__ __forceinline__ float2 quotient2(float2 m, float2 nd)
 {
