@@ -384,10 +384,18 @@ __global__ void __launch_bounds__(long_threads(EVEN)) norm_long_kernel(const __g
 // fill the ring in shared memory.  Row statistics come 32 rows at a time, one to
 // a lane: fetched row by row they cost about 10 us of 128.
 //
-// 32768 x 3584 bf16 115.7 us, 6.1 TB/s, 91 % of the copy peak with the join (two
+// 32768 x 3584 bf16 114 us, 6.2 TB/s, 92 % of the copy peak with the join (two
 // rows at once spill and take 130; three blocks to an SM spill, 163).  65536 x
-// 1024 68 us (89 %), 8192 x 8192 78 us (77 %: one block of 255 registers to an SM),
+// 1024 68 us (89 %), 8192 x 8192 79 us (76 %: one block of 227 registers to an SM),
 // 131072 x 256 37 us (83 %), 1024 x 3584 14.5 us (the chain, and partial sums).
+//
+// Past its end a row reads as x = dy = 0, which leaves 0 * infinity in sum(w dy
+// xhat) where mean * rstd overflows; such a row's sum is taken again without
+// those columns.
+__device__ __forceinline__ bool product_overflows(float mean, float rstd)
+{
+    return !(fabsf(mean * rstd) < __int_as_float(0x7f800000));
+}
 __host__ __device__ constexpr int grad_rows(int el, bool vec) { return vec && el == 8 ? 2 : 1; }
 __host__ __device__ constexpr int grad_stages(int el) { return el == 8 ? 2 : 3; }
 template <class T, int EL, bool VEC, bool GROUP>
@@ -481,13 +489,15 @@ __global__ void __launch_bounds__(EL == 32 ? 256 : 512, EL == 8 ? 1 : 0) norm_gr
                 nx.load(gx, c0, cols);
             }
         }
-        // With u = x - mean and e = dy rstd: db += dy, dw += e u, and the row's
-        // sums are of w e and w e u, from which
-        //   dx = w e - sum(w e) / n - u rstd^2 sum(w e u) / n.
+        // With xhat = (x - mean) rstd: db += dy, dw += dy xhat, and the row's sums
+        // are c1 of w dy and c2 of w dy xhat, from which
+        //   dx = w dy rstd - (c1 rstd / n + xhat c2 rstd / n).
+        // Neither rstd^2 nor dy rstd is taken by itself: they may leave binary32's
+        // range where dx and dw do not.
         float mean[R], rstd[R], c1[R], c2[R];
 #pragma unroll
         for (int j = 0; j < R; ++j) {
-            // past the last row, and past a row's columns, nothing is kept of e = 0
+            // past the last row nothing is kept; past a row's columns dy = w = 0
             const bool in = R == 1 || i + j < count;
             mean[j] = __shfl_sync(0xffffffffu, means, (i & 31) + j);
             rstd[j] = in ? __shfl_sync(0xffffffffu, rstds, (i & 31) + j) : 0.0f;
@@ -495,11 +505,20 @@ __global__ void __launch_bounds__(EL == 32 ? 256 : 512, EL == 8 ? 1 : 0) norm_gr
             float2 s1 = both(0.0f), s2 = both(0.0f);
 #pragma unroll
             for (int k = 0; k < EL / 2; ++k) {
-                const float2 d = dy[j].pair(2 * k), u = add2(x[j].pair(2 * k), shift), e = mul2(d, r2), we = mul2(w[k], e);
+                const float2 d = dy[j].pair(2 * k), xhat = mul2(add2(x[j].pair(2 * k), shift), r2), wd = mul2(w[k], d);
                 if (in) db[k] = add2(db[k], d);
-                if (in) dw[k] = fma2(e, u, dw[k]);
-                s1 = add2(s1, we);
-                s2 = fma2(we, u, s2);
+                if (in) dw[k] = fma2(d, xhat, dw[k]);
+                s1 = add2(s1, wd);
+                s2 = fma2(wd, xhat, s2);
+            }
+            if (product_overflows(mean[j], rstd[j])) {  // without the columns past the row
+                s2 = both(0.0f);
+#pragma unroll
+                for (int k = 0; k < EL / 2; ++k) {
+                    const float2 xhat = mul2(add2(x[j].pair(2 * k), shift), r2), wd = mul2(w[k], dy[j].pair(2 * k));
+                    if (S::col(2 * k, g, lane) < cols) s2.x = fmaf(wd.x, xhat.x, s2.x);
+                    if (S::col(2 * k + 1, g, lane) < cols) s2.y = fmaf(wd.y, xhat.y, s2.y);
+                }
             }
             c1[j] = s1.x + s1.y;
             c2[j] = s2.x + s2.y;
@@ -529,11 +548,11 @@ __global__ void __launch_bounds__(EL == 32 ? 256 : 512, EL == 8 ? 1 : 0) norm_gr
 #pragma unroll
             for (int j = 0; j < R; ++j) {
                 const float2 r2 = both(rstd[j]), shift = both(-mean[j]);
-                const float2 k1 = both(-c1[j] * inv_n), k2 = both(-c2[j] * inv_n * rstd[j] * rstd[j]);
+                const float2 k1 = both(-c1[j] * inv_n * rstd[j]), k2 = both(-c2[j] * inv_n * rstd[j]);
 #pragma unroll
                 for (int k = 0; k < EL / 2; ++k) {
-                    const float2 u = add2(x[j].pair(2 * k), shift), we = mul2(w[k], mul2(dy[j].pair(2 * k), r2));
-                    x[j].set(2 * k, add2(we, fma2(u, k2, k1)));
+                    const float2 xhat = mul2(add2(x[j].pair(2 * k), shift), r2), wd = mul2(w[k], dy[j].pair(2 * k));
+                    x[j].set(2 * k, fma2(wd, r2, fma2(xhat, k2, k1)));
                 }
                 if (R == 1 || i + j < count) x[j].store(dst, c0, cols);
                 dst += dst_step;
@@ -600,7 +619,7 @@ __global__ void __launch_bounds__(kWideThreads) norm_grad_wide_kernel(const __gr
         const T *dy = static_cast<const T *>(a.dy) + row * a.dys + c0, *x = static_cast<const T *>(a.x) + row * a.xs + c0;
         const float mean = a.mean[row], rstd = a.rstd[row];
         const float2 r2 = both(rstd), shift = both(-mean);
-        float g[kAtOnce], xv[kAtOnce], w[kAtOnce];  // elements k0 and on; dy = w = 0 past the row
+        float g[kAtOnce], xv[kAtOnce], w[kAtOnce];  // elements k0 and on; 0 past the row
         auto load = [&](int k0) {
             Pack<T, E> pd[kAtOnce / E], px[kAtOnce / E];
 #pragma unroll
@@ -642,16 +661,22 @@ __global__ void __launch_bounds__(kWideThreads) norm_grad_wide_kernel(const __gr
             load(k0);
 #pragma unroll
             for (int k = 0; k < kAtOnce; k += 2) {
-                const float2 we = mul2(make_float2(w[k], w[k + 1]), mul2(make_float2(g[k], g[k + 1]), r2));
-                s1 = add2(s1, we);
-                s2 = fma2(we, add2(make_float2(xv[k], xv[k + 1]), shift), s2);
+                const float2 wd = mul2(make_float2(w[k], w[k + 1]), make_float2(g[k], g[k + 1]));
+                s1 = add2(s1, wd);
+                s2 = fma2(wd, mul2(add2(make_float2(xv[k], xv[k + 1]), shift), r2), s2);
             }
+        }
+        if (product_overflows(mean, rstd)) {  // without the columns past the row
+            s2 = both(0.0f);
+#pragma unroll 1
+            for (int c = threadIdx.x; c < cols; c += kWideThreads)
+                s2.x = fmaf((a.w ? load_any(a.w, c, a.wdtype) : 1.0f) * to_f32(dy[c - c0]), (to_f32(x[c - c0]) - mean) * rstd, s2.x);
         }
         float c1 = warp_sum(s1.x + s1.y), c2 = warp_sum(s2.x + s2.y);
         if (lane == 0) s[it][warp] = make_float2(c1, c2);
         __syncthreads();
         const float2 p = s[it][lane % kWarps];
-        const float2 k1 = both(-group_sum(p.x, kWarps / 2) * inv_n), k2 = both(-group_sum(p.y, kWarps / 2) * inv_n * rstd * rstd);
+        const float2 k1 = both(-group_sum(p.x, kWarps / 2) * inv_n * rstd), k2 = both(-group_sum(p.y, kWarps / 2) * inv_n * rstd);
         if (row + gridDim.x < a.rows) {  // the next row, 128 bytes to a thread
             const char *fd = reinterpret_cast<const char *>(dy - c0 + gridDim.x * a.dys);
             const char *fx = reinterpret_cast<const char *>(x - c0 + gridDim.x * a.xs);
@@ -668,10 +693,10 @@ __global__ void __launch_bounds__(kWideThreads) norm_grad_wide_kernel(const __gr
 #pragma unroll
             for (int k = 0; k < kAtOnce; k += 2) {
                 const int i = (k0 + k) / 2;
-                const float2 gk = make_float2(g[k], g[k + 1]), u = add2(make_float2(xv[k], xv[k + 1]), shift), e = mul2(gk, r2);
+                const float2 gk = make_float2(g[k], g[k + 1]), xhat = mul2(add2(make_float2(xv[k], xv[k + 1]), shift), r2);
                 db[i] = add2(db[i], gk);
-                dw[i] = fma2(e, u, dw[i]);
-                const float2 y = fma2(make_float2(w[k], w[k + 1]), e, fma2(u, k2, k1));
+                dw[i] = fma2(gk, xhat, dw[i]);
+                const float2 y = fma2(mul2(make_float2(w[k], w[k + 1]), gk), r2, fma2(xhat, k2, k1));
                 if (E > 1) {
                     pair_set(&out[k / E].v[k % E], y);
                 } else {
@@ -899,12 +924,12 @@ const void *norm_grad_fn(int el, bool vec, bool group)
 // Elements to a lane and warps to a row.  Even rows: one warp while 32 elements
 // a lane hold the row (two with 16 from 513 columns on where there are fewer
 // than 8 rows for each SM: the gradient of 257 x 1024 binary32 5.9 against 7.6
-// us), else 16 a lane up to 8 warps (12 for the gradient: 8192 x 5120 bf16 60 us,
-// with 32 68; 8192 x 8192 85 and 78), then 32; with fewer rows than SMs, where
+// us), else 16 a lane up to 8 warps (12 for the gradient: 8192 x 5120 bf16 58 us,
+// with 32 68; 8192 x 8192 85 and 79), then 32; with fewer rows than SMs, where
 // nothing but one row's latency counts, 8 a lane.  Uneven rows
 // take 8 a lane while its warps allow (66 against 60 us for 8000 x 5001 bf16
 // forward with 16), except one warp a row with 16 for 257 to 512 columns (65536 x
-// 301 bf16: 30 against 35, gradient 55 against 81), then 32 (it spills, but reads a row
+// 301 bf16: 30 against 35, gradient 49 against 81), then 32 (it spills, but reads a row
 // once: 4000 x 12001 94 us, the long-row kernel 120).  warps > 0 where a kernel of
 // that shape takes the row (most[]: the warps its launch bounds allow with 8, 16
 // and 32 elements a lane), else 0.
