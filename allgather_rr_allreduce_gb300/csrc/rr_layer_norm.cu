@@ -307,8 +307,12 @@ __global__ void __launch_bounds__(EL == 8 ? 1024 : EL == 16 ? 256 : 512, EL == 1
 // vectors, E elements at a time; else one at a time.  Bound by the latency of the
 // passes and their two block sums: 4096 x 18944 bf16 83 us (56 % of the copy peak;
 // 92 without the next row's way to L2).
+//
+// A thread's sums go to a compensated one after each kPart elements: the rounding
+// of a row's sums does not grow with its length.
 template <class T, bool EVEN>
 constexpr int kWidth = EVEN ? 16 / (int)sizeof(T) : 1;
+constexpr int kPart = 64;
 
 __device__ __forceinline__ float block_sum(float x, float *s)
 {
@@ -321,6 +325,19 @@ __device__ __forceinline__ float block_sum(float x, float *s)
     return t;
 }
 
+// A thread's sum of a row from column c on: `sum` of each stretch, the stretches by
+// a compensated sum.  Rows of one stretch (up to 32768 columns of vectors, 65536
+// single ones) take `sum` alone: 83 us for 4096 x 18944 bf16, in one loop over the
+// stretches 89.
+template <class F>
+__device__ __forceinline__ float in_parts(int64_t c, int64_t cols, int64_t stretch, F sum)
+{
+    if (cols - c <= stretch) return sum(c, cols);
+    Compensated all;
+    for (; c < cols; c += stretch) all.add(sum(c, min(cols, c + stretch)));
+    return all.value();
+}
+
 // Vectors: 83 us for 4096 x 18944 bf16 forward with 512 threads, 119 with 1024;
 // single elements: 275 and 197 for 2000 x 40001 (before rows were brought to L2).
 __host__ __device__ constexpr int long_threads(bool even) { return even ? 512 : 1024; }
@@ -330,33 +347,39 @@ __global__ void __launch_bounds__(long_threads(EVEN)) norm_long_kernel(const __g
     stream_order();
     constexpr int E = kWidth<T, EVEN>, kLongThreads = long_threads(EVEN);
     __shared__ float s[32];
-    const int64_t first = (int64_t)threadIdx.x * E, next = (int64_t)kLongThreads * E;
+    const int64_t first = (int64_t)threadIdx.x * E, next = (int64_t)kLongThreads * E, stretch = kPart / E * next;
     const bool waligned = aligned16(a.w), baligned = aligned16(a.b);
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const T *x = static_cast<const T *>(a.x) + row * a.xs;
         T *y = static_cast<T *>(a.y) + row * a.ys;
-        float sum = 0.0f;
+        const float sum = in_parts(first, a.cols, stretch, [&](int64_t c, int64_t end) {
+            float part = 0.0f;
 #pragma unroll 4
-        for (int64_t c = first; c < a.cols; c += next) {
-            const Pack<T, E> v = *reinterpret_cast<const Pack<T, E> *>(x + c);
+            for (; c < end; c += next) {
+                const Pack<T, E> v = *reinterpret_cast<const Pack<T, E> *>(x + c);
 #pragma unroll
-            for (int k = 0; k < E; ++k) sum += to_f32(v.v[k]);
-        }
+                for (int k = 0; k < E; ++k) part += to_f32(v.v[k]);
+            }
+            return part;
+        });
         if (row + gridDim.x < a.rows) {  // the next row into L2, 128 bytes to a thread
             const char *far = reinterpret_cast<const char *>(x + gridDim.x * a.xs);
             for (int64_t l = threadIdx.x * 128; l < a.cols * (int64_t)sizeof(T); l += kLongThreads * 128) prefetch_l2(far + l);
         }
         const float mean = block_sum(sum, s) / (float)a.cols;
-        float m2 = 0.0f;
+        const float m2 = in_parts(first, a.cols, stretch, [&](int64_t c, int64_t end) {
+            float part = 0.0f;
 #pragma unroll 4
-        for (int64_t c = first; c < a.cols; c += next) {
-            const Pack<T, E> v = *reinterpret_cast<const Pack<T, E> *>(x + c);
+            for (; c < end; c += next) {
+                const Pack<T, E> v = *reinterpret_cast<const Pack<T, E> *>(x + c);
 #pragma unroll
-            for (int k = 0; k < E; ++k) {
-                const float d = to_f32(v.v[k]) - mean;
-                m2 = fmaf(d, d, m2);
+                for (int k = 0; k < E; ++k) {
+                    const float d = to_f32(v.v[k]) - mean;
+                    part = fmaf(d, d, part);
+                }
             }
-        }
+            return part;
+        });
         const float rstd = rsqrtf(block_sum(m2, s) / (float)a.cols + a.eps);
 #pragma unroll 4
         for (int64_t c = first; c < a.cols; c += next) {
@@ -734,26 +757,32 @@ __global__ void __launch_bounds__(long_threads(EVEN)) norm_grad_means_kernel(con
     constexpr int E = kWidth<T, EVEN>, kLongThreads = long_threads(EVEN);
     __shared__ float2 s[2][32];
     const bool waligned = aligned16(a.w);
+    const int64_t next = (int64_t)kLongThreads * E, stretch = kPart / E * next;
     int it = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, it ^= 1) {
         const T *dy = static_cast<const T *>(a.dy) + row * a.dys;
         const T *x = static_cast<const T *>(a.x) + row * a.xs;
         const float mean = a.mean[row], rstd = a.rstd[row];
-        float c1 = 0.0f, c2 = 0.0f;
+        Compensated sum1, sum2;
+        for (int64_t c0 = (int64_t)threadIdx.x * E; c0 < a.cols; c0 += stretch) {
+            const int64_t end = min(a.cols, c0 + stretch);
+            float part1 = 0.0f, part2 = 0.0f;
 #pragma unroll 4
-        for (int64_t c = (int64_t)threadIdx.x * E; c < a.cols; c += (int64_t)kLongThreads * E) {
-            const Pack<T, E> d = *reinterpret_cast<const Pack<T, E> *>(dy + c), v = *reinterpret_cast<const Pack<T, E> *>(x + c);
-            float w[E];
-            weights_at<E>(w, a.w, c, a.wdtype, waligned, 1.0f);
+            for (int64_t c = c0; c < end; c += next) {
+                const Pack<T, E> d = *reinterpret_cast<const Pack<T, E> *>(dy + c), v = *reinterpret_cast<const Pack<T, E> *>(x + c);
+                float w[E];
+                weights_at<E>(w, a.w, c, a.wdtype, waligned, 1.0f);
 #pragma unroll
-            for (int k = 0; k < E; ++k) {
-                const float wd = w[k] * to_f32(d.v[k]);
-                c1 += wd;
-                c2 = fmaf(wd, (to_f32(v.v[k]) - mean) * rstd, c2);
+                for (int k = 0; k < E; ++k) {
+                    const float wd = w[k] * to_f32(d.v[k]);
+                    part1 += wd;
+                    part2 = fmaf(wd, (to_f32(v.v[k]) - mean) * rstd, part2);
+                }
             }
+            sum1.add(part1);
+            sum2.add(part2);
         }
-        c1 = warp_sum(c1);
-        c2 = warp_sum(c2);
+        float c1 = warp_sum(sum1.value()), c2 = warp_sum(sum2.value());
         if ((threadIdx.x & 31) == 0) s[it][threadIdx.x >> 5] = make_float2(c1, c2);
         __syncthreads();
         if (threadIdx.x < 32) {

@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
     constexpr int E = 16 / (int)sizeof(T);
     constexpr int64_t C = (int64_t)kThreads * E * kNormUnroll;
     __shared__ double s[kThreads / 32];
-    float hi = 0.0f, lo = 0.0f;  // compensated sum of the chunks
+    Compensated chunks;
     double wide = 0.0;
     const int64_t end = a.list.stretch(blockIdx.x + 1);
     int64_t chunk = a.list.stretch(blockIdx.x);
@@ -166,12 +166,9 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
             if (sound(x * x)) sum = fmaf(x, x, sum);
             else wide += (double)x * x;
         }
-        // hi + lo += sum without losing the low bits (Knuth's two-sum)
-        const float t0 = __fadd_rn(hi, sum), z = __fsub_rn(t0, hi);
-        lo += __fadd_rn(__fsub_rn(hi, __fsub_rn(t0, z)), __fsub_rn(sum, z));
-        hi = t0;
+        chunks.add(sum);
     }
-    double d = wide + (double)hi + (double)lo;
+    double d = wide + (double)chunks.hi + (double)chunks.lo;
 #pragma unroll
     for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
     if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = d;

@@ -144,6 +144,20 @@ __device__ __forceinline__ void fetch_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// A sum that keeps what each addition rounds off (Knuth's two-sum), so that its
+// own rounding does not grow with the number of parts.
+struct Compensated {
+    float hi = 0.0f, lo = 0.0f;
+    __device__ __forceinline__ void add(float x)
+    {
+        const float t = __fadd_rn(hi, x), z = __fsub_rn(t, hi);
+        lo += __fadd_rn(__fsub_rn(hi, __fsub_rn(t, z)), __fsub_rn(x, z));
+        hi = t;
+    }
+    // Of a sum that is not finite nothing was rounded off.
+    __device__ __forceinline__ float value() const { return fabsf(hi) < __int_as_float(0x7f800000) ? hi + lo : hi; }
+};
+
 __device__ __forceinline__ float warp_sum(float x)
 {
 #pragma unroll
