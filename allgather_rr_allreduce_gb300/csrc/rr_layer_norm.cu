@@ -325,17 +325,21 @@ __device__ __forceinline__ float block_sum(float x, float *s)
     return t;
 }
 
-// A thread's sum of a row from column c on: `sum` of each stretch, the stretches by
-// a compensated sum.  Rows of one stretch (up to 32768 columns of vectors, 65536
-// single ones) take `sum` alone: 83 us for 4096 x 18944 bf16, in one loop over the
-// stretches 89.
+// A thread's two sums of a row from column c on: `sum` of each stretch, the
+// stretches by compensated sums.  Rows of one stretch (up to 32768 columns of
+// vectors, 65536 single ones) take `sum` alone: 83 us for 4096 x 18944 bf16, in one
+// loop over the stretches 89.
 template <class F>
-__device__ __forceinline__ float in_parts(int64_t c, int64_t cols, int64_t stretch, F sum)
+__device__ __forceinline__ float2 in_parts(int64_t c, int64_t cols, int64_t stretch, F sum)
 {
-    if (cols - c <= stretch) return sum(c, cols);
-    Compensated all;
-    for (; c < cols; c += stretch) all.add(sum(c, min(cols, c + stretch)));
-    return all.value();
+    if (cols <= stretch) return sum(c, cols);
+    Compensated x, y;
+    for (; c < cols; c += stretch) {
+        const float2 part = sum(c, min(cols, c + stretch));
+        x.add(part.x);
+        y.add(part.y);
+    }
+    return make_float2(x.value(), y.value());
 }
 
 // Vectors: 83 us for 4096 x 18944 bf16 forward with 512 threads, 119 with 1024;
@@ -360,8 +364,8 @@ __global__ void __launch_bounds__(long_threads(EVEN)) norm_long_kernel(const __g
 #pragma unroll
                 for (int k = 0; k < E; ++k) part += to_f32(v.v[k]);
             }
-            return part;
-        });
+            return make_float2(part, 0.0f);
+        }).x;
         if (row + gridDim.x < a.rows) {  // the next row into L2, 128 bytes to a thread
             const char *far = reinterpret_cast<const char *>(x + gridDim.x * a.xs);
             for (int64_t l = threadIdx.x * 128; l < a.cols * (int64_t)sizeof(T); l += kLongThreads * 128) prefetch_l2(far + l);
@@ -378,8 +382,8 @@ __global__ void __launch_bounds__(long_threads(EVEN)) norm_long_kernel(const __g
                     part = fmaf(d, d, part);
                 }
             }
-            return part;
-        });
+            return make_float2(part, 0.0f);
+        }).x;
         const float rstd = rsqrtf(block_sum(m2, s) / (float)a.cols + a.eps);
 #pragma unroll 4
         for (int64_t c = first; c < a.cols; c += next) {
@@ -749,9 +753,10 @@ __global__ void __launch_bounds__(kWideThreads) norm_grad_wide_kernel(const __gr
     }
 }
 
-// Rows too long for that: the two row means first ...
+// Rows too long for that: the two row means first (two blocks to an SM: 2000 x
+// 40001 bf16, both kernels 342 us, with one 440) ...
 template <class T, bool EVEN>
-__global__ void __launch_bounds__(long_threads(EVEN)) norm_grad_means_kernel(const __grid_constant__ NormGradArgs a)
+__global__ void __launch_bounds__(long_threads(EVEN), 2) norm_grad_means_kernel(const __grid_constant__ NormGradArgs a)
 {
     stream_order();
     constexpr int E = kWidth<T, EVEN>, kLongThreads = long_threads(EVEN);
@@ -763,26 +768,23 @@ __global__ void __launch_bounds__(long_threads(EVEN)) norm_grad_means_kernel(con
         const T *dy = static_cast<const T *>(a.dy) + row * a.dys;
         const T *x = static_cast<const T *>(a.x) + row * a.xs;
         const float mean = a.mean[row], rstd = a.rstd[row];
-        Compensated sum1, sum2;
-        for (int64_t c0 = (int64_t)threadIdx.x * E; c0 < a.cols; c0 += stretch) {
-            const int64_t end = min(a.cols, c0 + stretch);
-            float part1 = 0.0f, part2 = 0.0f;
+        const float2 sums = in_parts((int64_t)threadIdx.x * E, a.cols, stretch, [&](int64_t c, int64_t end) {
+            float2 part = both(0.0f);
 #pragma unroll 4
-            for (int64_t c = c0; c < end; c += next) {
+            for (; c < end; c += next) {
                 const Pack<T, E> d = *reinterpret_cast<const Pack<T, E> *>(dy + c), v = *reinterpret_cast<const Pack<T, E> *>(x + c);
                 float w[E];
                 weights_at<E>(w, a.w, c, a.wdtype, waligned, 1.0f);
 #pragma unroll
                 for (int k = 0; k < E; ++k) {
                     const float wd = w[k] * to_f32(d.v[k]);
-                    part1 += wd;
-                    part2 = fmaf(wd, (to_f32(v.v[k]) - mean) * rstd, part2);
+                    part.x += wd;
+                    part.y = fmaf(wd, (to_f32(v.v[k]) - mean) * rstd, part.y);
                 }
             }
-            sum1.add(part1);
-            sum2.add(part2);
-        }
-        float c1 = warp_sum(sum1.value()), c2 = warp_sum(sum2.value());
+            return part;
+        });
+        float c1 = warp_sum(sums.x), c2 = warp_sum(sums.y);
         if ((threadIdx.x & 31) == 0) s[it][threadIdx.x >> 5] = make_float2(c1, c2);
         __syncthreads();
         if (threadIdx.x < 32) {
