@@ -754,7 +754,7 @@ __global__ void __launch_bounds__(kWideThreads) norm_grad_wide_kernel(const __gr
 }
 
 // Rows too long for that: the two row means first (two blocks to an SM: 2000 x
-// 40001 bf16, both kernels 342 us, with one 440) ...
+// 40001 bf16, both kernels 348 us, with one 440) ...
 template <class T, bool EVEN>
 __global__ void __launch_bounds__(long_threads(EVEN), 2) norm_grad_means_kernel(const __grid_constant__ NormGradArgs a)
 {
@@ -798,7 +798,11 @@ __global__ void __launch_bounds__(long_threads(EVEN), 2) norm_grad_means_kernel(
 
 // ... then dx and the weight's gradient by columns: block p * tiles + i has
 // tile i of the columns, E to a thread, and every P-th row, kTileRows at once
-// and the next ones' loads under way.
+// and the next ones' loads under way.  There are fewer P the longer the rows, so
+// a thread's sums go to a compensated sum after each kPart rows, in shared
+// memory (20000 x 32776 bf16, both kernels 2530 us; in registers, which leave two
+// blocks to an SM in place of three, 3334).  Single elements go two steps at a time
+// (2000 x 40001 348 us, one by one 366).
 constexpr int kTileThreads = 128, kTileRows = 4;
 template <class T, bool EVEN>
 struct TileRows {
@@ -822,7 +826,7 @@ struct TileRows {
     }
 };
 template <class T, bool EVEN>
-__global__ void __launch_bounds__(kTileThreads) norm_grad_columns_kernel(const __grid_constant__ NormGradArgs a)
+__global__ void __launch_bounds__(kTileThreads, EVEN ? 3 : 6) norm_grad_columns_kernel(const __grid_constant__ NormGradArgs a)
 {
     stream_order();
     constexpr int E = kWidth<T, EVEN>;
@@ -834,31 +838,50 @@ __global__ void __launch_bounds__(kTileThreads) norm_grad_columns_kernel(const _
     weights_at<E>(w, a.w, c, a.wdtype, false, 1.0f);
 #pragma unroll
     for (int k = 0; k < E; ++k) dw[k] = db[k] = 0.0f;
+    __shared__ float2 s_all[2 * E][kTileThreads];  // each thread its own
+#pragma unroll
+    for (int k = 0; k < 2 * E; ++k) s_all[k][threadIdx.x] = make_float2(0.0f, 0.0f);
+    auto flush = [&](float &x, float2 &all) {
+        Compensated t{all.x, all.y};
+        t.add(x);
+        all = make_float2(t.hi, t.lo);
+        x = 0.0f;
+        return t.value();
+    };
     TileRows<T, EVEN> cur, next;
     const int64_t step = (int64_t)kTileRows * a.P;
     next.load(a, p, c);
-    for (int64_t row = p; row < a.rows; row += step) {
-        cur = next;
-        next.load(a, row + step, c);
+    for (int64_t row = p; row < a.rows;) {
+        const int64_t end = min(a.rows, row + kPart / kTileRows * step);
+#pragma unroll (EVEN ? 1 : 2)
+        for (; row < end; row += step) {
+            cur = next;
+            next.load(a, row + step, c);
 #pragma unroll
-        for (int j = 0; j < kTileRows; ++j) {
-            const int64_t r = row + (int64_t)j * a.P;
-            if (r >= a.rows) break;
+            for (int j = 0; j < kTileRows; ++j) {
+                const int64_t r = row + (int64_t)j * a.P;
+                if (r >= a.rows) break;
 #pragma unroll
-            for (int k = 0; k < E; ++k) {
-                const float g = to_f32(cur.d[j].v[k]), xhat = (to_f32(cur.x[j].v[k]) - cur.mean[j]) * cur.rstd[j];
-                dw[k] = fmaf(g, xhat, dw[k]);
-                db[k] += g;
-                cur.x[j].v[k] = from_f32<T>((w[k] * g - cur.m[j].x - xhat * cur.m[j].y) * cur.rstd[j]);
+                for (int k = 0; k < E; ++k) {
+                    const float g = to_f32(cur.d[j].v[k]), xhat = (to_f32(cur.x[j].v[k]) - cur.mean[j]) * cur.rstd[j];
+                    dw[k] = fmaf(g, xhat, dw[k]);
+                    db[k] += g;
+                    cur.x[j].v[k] = from_f32<T>((w[k] * g - cur.m[j].x - xhat * cur.m[j].y) * cur.rstd[j]);
+                }
+                if (a.dx) *reinterpret_cast<Pack<T, E> *>(static_cast<T *>(a.dx) + r * a.dxs + c) = cur.x[j];
             }
-            if (a.dx) *reinterpret_cast<Pack<T, E> *>(static_cast<T *>(a.dx) + r * a.dxs + c) = cur.x[j];
+        }
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+            flush(dw[k], s_all[k][threadIdx.x]);
+            flush(db[k], s_all[E + k][threadIdx.x]);
         }
     }
     if (!a.part) return;
 #pragma unroll
     for (int k = 0; k < E; ++k) {
-        a.part[(int64_t)p * a.cols + c + k] = dw[k];
-        a.part[((int64_t)a.P + p) * a.cols + c + k] = db[k];
+        a.part[(int64_t)p * a.cols + c + k] = flush(dw[k], s_all[k][threadIdx.x]);
+        a.part[((int64_t)a.P + p) * a.cols + c + k] = flush(db[k], s_all[E + k][threadIdx.x]);
     }
 }
 
