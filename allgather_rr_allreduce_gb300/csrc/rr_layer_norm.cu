@@ -21,6 +21,7 @@ namespace rr {
 namespace {
 
 constexpr int kMaxPartials = 608;  // blocks whose partial weight gradients are kept
+constexpr int kWidePartials = 152;  // of them, of the kernels of long rows
 
 struct NormArgs {
     const void *x, *w, *b;
@@ -1050,6 +1051,28 @@ rr_status check_element(const char *name, const void *p, int bytes)
         if (st_ != RR_OK) return st_;           \
     } while (0)
 
+// Most partial weight gradients of a call: what the workspace has room for, so a
+// function of the sizes alone.  Up to the 8192 columns that row_shape has warps for,
+// a block's; of longer rows one for each SM of a GB300 where norm_grad_wide_kernel
+// may take them, else what gives norm_grad_columns_kernel tile_blocks() to each of
+// those SMs.  A device with more SMs leaves some of them without.
+int64_t most_partials(int64_t rows, int64_t cols)
+{
+    int64_t most = kMaxPartials;
+    if (cols > kNormGradWarps[2] * 1024) {
+        most = kWidePartials;
+        if (cols > kWideThreads * 48) {
+            most = 1;
+            for (int e : {1, 4, 8}) {  // single elements, vectors of binary32, of the 16-bit types
+                const int64_t tiles = (cols + kTileThreads * e - 1) / (kTileThreads * e);
+                const int64_t p = (tile_blocks(e > 1) * (int64_t)kWidePartials + tiles - 1) / tiles;
+                if (p > most) most = p;
+            }
+        }
+    }
+    return rows < most ? rows : most;
+}
+
 int64_t row_span(int64_t rows, int64_t stride, int64_t cols) { return (rows - 1) * stride + cols; }
 
 bool vector_rows(const void *p, int64_t stride, int64_t rows, int eb)
@@ -1192,8 +1215,7 @@ extern "C" rr_status rr_layer_norm_backward_workspace(int64_t rows, int64_t cols
 {
     if (!bytes) return step_fail(RR_ERR_INVALID_ARG, "bytes is NULL");
     RR_TRY(check_sizes(rows, cols, RR_FP32, RR_FP32));
-    const int64_t P = rows < kMaxPartials ? rows : kMaxPartials;
-    *bytes = (size_t)(((rows * 8 + 15) & ~(int64_t)15) + 2 * P * cols * 4);
+    *bytes = (size_t)(((rows * 8 + 15) & ~(int64_t)15) + 2 * most_partials(rows, cols) * cols * 4);
     return step_ok();
 }
 
@@ -1265,6 +1287,7 @@ try {
         const bool vec = cols * eb % 16 == 0 && vector_rows(dy, dy_stride, rows, eb) &&
                          vector_rows(x, x_stride, rows, eb) && (!dx || vector_rows(dx, dx_stride, rows, eb));
         row_shape(rows, cols, vec, sms, kNormGradWarps, &el, &warps);
+        const int64_t most = most_partials(rows, cols);
         // Long rows: one pass over HBM once each SM has a few of them (4096 x 18944
         // bf16 150 us, 64 rows 32, uneven 2000 x 12001 73; the two-pass kernels 215,
         // 14 and 120).
@@ -1272,19 +1295,18 @@ try {
             const int wide = cols <= kWideThreads * 32 ? 32 : cols <= kWideThreads * 40 ? 40 : 48;
             const void *fn = dtype == RR_FP32   ? norm_grad_wide_fn<float>(wide, vec)
                              : dtype == RR_BF16 ? norm_grad_wide_fn<__nv_bfloat16>(wide, vec) : norm_grad_wide_fn<__half>(wide, vec);
-            a.P = sms < kMaxPartials ? sms : kMaxPartials;
+            a.P = (int)(sms < most ? sms : most);
             RR_TRY(step_launch(fn, a.P, kWideThreads, 0, &a, stream));
         } else if (warps == 0) {
             const void *means, *columns;
             if (dtype == RR_FP32) norm_grad_long_fn<float>(vec, &means, &columns);
             else if (dtype == RR_BF16) norm_grad_long_fn<__nv_bfloat16>(vec, &means, &columns);
             else norm_grad_long_fn<__half>(vec, &means, &columns);
-            const int64_t most = 2 * (int64_t)sms;
+            const int64_t two = 2 * (int64_t)sms;
             const int64_t tile = kTileThreads * (vec ? 16 / eb : 1), tiles = (cols + tile - 1) / tile;
-            RR_TRY(step_launch(means, rows < most ? rows : most, long_threads(vec), 0, &a, stream));
+            RR_TRY(step_launch(means, rows < two ? rows : two, long_threads(vec), 0, &a, stream));
             int64_t P = (tile_blocks(vec) * (int64_t)sms + tiles - 1) / tiles;
-            if (P > rows) P = rows;
-            if (P > kMaxPartials) P = kMaxPartials;
+            if (P > most) P = most;
             a.P = (int)P;
             RR_TRY(step_launch(columns, P * tiles, kTileThreads, 0, &a, stream));
         } else {
@@ -1305,7 +1327,7 @@ try {
             // bf16: 14.8 us, with every block that fits 19.2).
             const int64_t busy = rows / 8 / per > sms ? rows / 8 / per : sms;
             if (blocks > busy) blocks = busy;
-            if (blocks > kMaxPartials) blocks = kMaxPartials;
+            if (blocks > most) blocks = most;
             a.P = (int)blocks;
             RR_TRY(step_launch(fn, blocks, threads, smem, &a, stream));
         }
