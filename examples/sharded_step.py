@@ -10,7 +10,8 @@ One step, with the calls in the order a training program makes them:
   allreduce   rr_allreduce_twoshot sums the gradients of all ranks
   clip        rr_grad_norm: the norm of the mean gradient and its clip factor
   update      rr_adamw or rr_adamw8 on the rank's shard: its W-th of every
-              weight, binary32 master weights and states only for that
+              weight (W divides the width), binary32 master weights and states
+              only for that
   allgather   rr_allgather_param_contiguous hands the new weights to all
 
 The model is a small residual network, x <- x + norm(x) V for each layer, fitted
@@ -66,6 +67,8 @@ class Step:
     def __init__(self, world=4, width=256, layers=3, states=8, lr=2e-3, max_norm=1.0, seed=0):
         self.world, self.width, self.layers, self.eight = world, width, layers, states == 8
         self.lr, self.max_norm, self.steps = lr, max_norm, 0
+        if width % world:  # every parameter holds width or width^2 elements
+            raise ValueError(f"width {width}: {world} ranks do not divide it, and each has an equal piece of every weight")
         g = torch.Generator(device="cuda").manual_seed(seed)
 
         def network():
