@@ -9,7 +9,6 @@ computes: if librr.so is missing, every call raises.
 """
 import array
 import ctypes
-import operator
 import os
 import sys
 
@@ -55,16 +54,20 @@ class RRError(RuntimeError):
 
 _lib = None
 _tensor_class = None  # torch.Tensor, once torch has been imported by the caller
-_raw_stream = _device = None  # torch's current stream and device, once CUDA has been started
+_device = None                # torch's current device, from then on
+_raw_stream = None            # torch's current stream, once CUDA has been started
 _vp = ctypes.c_void_p
 _PP = ctypes.POINTER(ctypes.c_void_p)
 
 
 def lib():
     """Load librr.so (raises if it has not been built)."""
-    global _lib, _tensor_class
+    global _lib, _tensor_class, _device
     if _tensor_class is None and "torch" in sys.modules:
-        _tensor_class = getattr(sys.modules["torch"], "Tensor", None)
+        torch = sys.modules["torch"]
+        _tensor_class = getattr(torch, "Tensor", None)
+        if _tensor_class is not None:
+            _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     if _lib is None:
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(f"{LIB_PATH} is missing: build it with allgather_rr_allreduce_gb300.build.build()")
@@ -142,16 +145,15 @@ def dtype_code(dtype):
             torch.int32: RR_INT32}[dtype]
 
 
-def stream_handle(stream):
+def stream_handle(stream, device=None):
+    """A stream as the C entries take it; `device`: the current one, where the caller knows it."""
     if stream is None:
         if _raw_stream is not None:  # the current stream without a Stream object
-            return _raw_stream(_device())
+            return _raw_stream(_device() if device is None else device)
         import torch
         current = torch.cuda.current_stream().cuda_stream  # starts CUDA
-        globals().update(_raw_stream=getattr(torch._C, "_cuda_getCurrentRawStream", None),
-                         _device=torch.cuda.current_device)
-        if hasattr(torch._C, "_cuda_getDevice"):
-            globals().update(_device=torch._C._cuda_getDevice)
+        if _device is not None:
+            globals().update(_raw_stream=getattr(torch._C, "_cuda_getCurrentRawStream", None))
         return current
     if isinstance(stream, int):
         return stream
@@ -275,10 +277,38 @@ def rr_allgather_list(rank_bufs, output_lists, world_size, numel_per_rank, dtype
 
 
 # ---------------------------------------------------------------- training step
-_is_cuda = operator.attrgetter("is_cuda")
+# Kernels run on the current device, so tensors have to be there.  _here() is that
+# device, None until a CUDA tensor has been seen (then CUDA has been started).
+_current = None
 
 
-def _pointers(items, count, name):
+def _here():
+    return None if _current is None else _current()
+
+
+def _near(x, here):
+    """_addr of a buffer on the current device."""
+    if x is None:
+        return 0
+    if x.__class__ is _tensor_class and x.get_device() == here:
+        return x.data_ptr()
+    return _look(x)
+
+
+def _look(x):
+    """_near of what is not known to be a tensor of the current device."""
+    global _current
+    if _device is not None and hasattr(x, "get_device"):
+        device = x.get_device()
+        if device < 0:
+            raise ValueError("device buffers must be CUDA tensors or device addresses")
+        _current, here = _device, _device()
+        if device != here:
+            raise RRError(RR_ERR_WRONG_DEVICE, f"a tensor is on device {device}, the current device is {here}")
+    return _addr(x)
+
+
+def _pointers(items, here, count, name):
     """A buffer of `count` device addresses for a list of tensors or addresses;
     None for None.  A pointer_array made before passes through, so that a loop
     over the same tensors need not marshal them again."""
@@ -288,12 +318,12 @@ def _pointers(items, count, name):
         raise ValueError(f"{name} has {len(items)} entries, sizes has {count}")
     if isinstance(items, ctypes.Array):
         return items
-    try:  # CUDA tensors throughout, without a Python-level step for each
-        if all(map(_is_cuda, items)):
+    try:  # tensors of the current device throughout, without a Python-level step for each
+        if {here}.issuperset(map(_tensor_class.get_device, items)):
             return array.array("Q", map(_tensor_class.data_ptr, items))
     except (AttributeError, TypeError):
         pass
-    return pointer_array(items)
+    return array.array("Q", map(_look, items))
 
 
 def _at(buffer):
@@ -306,18 +336,20 @@ def _at(buffer):
 def rr_layer_norm(x, weight, bias, y, mean, rstd, rows, cols, x_stride, y_stride, eps, dtype, weight_dtype,
                   stream=None):
     """y = layer norm of each row of x; weight, bias, mean and rstd may be None."""
-    _check(lib().rr_layer_norm(_addr(x), _addr(weight), _addr(bias), _addr(y), _addr(mean), _addr(rstd), rows, cols,
-                               x_stride, y_stride, eps, dtype_code(dtype), dtype_code(weight_dtype),
-                               stream_handle(stream)))
+    l, here = lib(), _here()
+    _check(l.rr_layer_norm(_near(x, here), _near(weight, here), _near(bias, here), _near(y, here), _near(mean, here),
+                           _near(rstd, here), rows, cols, x_stride, y_stride, eps, dtype_code(dtype),
+                           dtype_code(weight_dtype), stream_handle(stream, here)))
 
 
 def rr_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, rows, cols, dy_stride, x_stride, dx_stride,
                            dtype, weight_dtype, workspace, workspace_bytes, stream=None):
     """Gradients of rr_layer_norm; weight and any of dx, dweight, dbias may be None."""
-    _check(lib().rr_layer_norm_backward(_addr(dy), _addr(x), _addr(weight), _addr(mean), _addr(rstd), _addr(dx),
-                                        _addr(dweight), _addr(dbias), rows, cols, dy_stride, x_stride, dx_stride,
-                                        dtype_code(dtype), dtype_code(weight_dtype), _addr(workspace),
-                                        workspace_bytes, stream_handle(stream)))
+    l, here = lib(), _here()
+    _check(l.rr_layer_norm_backward(_near(dy, here), _near(x, here), _near(weight, here), _near(mean, here),
+                                    _near(rstd, here), _near(dx, here), _near(dweight, here), _near(dbias, here), rows,
+                                    cols, dy_stride, x_stride, dx_stride, dtype_code(dtype), dtype_code(weight_dtype),
+                                    _near(workspace, here), workspace_bytes, stream_handle(stream, here)))
 
 
 def rr_layer_norm_backward_workspace(rows, cols):
@@ -329,10 +361,10 @@ def rr_layer_norm_backward_workspace(rows, cols):
 
 def rr_grad_norm(grads, sizes, dtype, inv_scale, max_norm, norm, scale, workspace, workspace_bytes, stream=None):
     """Norm over a list of gradient tensors and the factor that clips it; norm or scale may be None."""
-    l, n = lib(), len(sizes)
-    s, g = array.array("q", sizes), _pointers(grads, n, "grads")
-    _check(l.rr_grad_norm(_at(g), _at(s), n, dtype_code(dtype), inv_scale, max_norm, _addr(norm), _addr(scale),
-                          _addr(workspace), workspace_bytes, stream_handle(stream)))
+    l, n, here = lib(), len(sizes), _here()
+    s, g = array.array("q", sizes), _pointers(grads, here, n, "grads")
+    _check(l.rr_grad_norm(_at(g), _at(s), n, dtype_code(dtype), inv_scale, max_norm, _near(norm, here),
+                          _near(scale, here), _near(workspace, here), workspace_bytes, stream_handle(stream, here)))
 
 
 def rr_grad_norm_workspace(num_tensors):
@@ -345,24 +377,25 @@ def rr_grad_norm_workspace(num_tensors):
 def rr_adamw(params, grads, exp_avg, exp_avg_sq, master, sizes, param_dtype, grad_dtype, hyper, grad_scale=None,
              stream=None):
     """One AdamW step over a list of tensors, states in binary32; master may be None."""
-    l, n = lib(), len(sizes)
-    s, p, g = array.array("q", sizes), _pointers(params, n, "params"), _pointers(grads, n, "grads")
-    m, v = _pointers(exp_avg, n, "exp_avg"), _pointers(exp_avg_sq, n, "exp_avg_sq")
-    w = _pointers(master, n, "master")
+    l, n, here = lib(), len(sizes), _here()
+    s, p, g = array.array("q", sizes), _pointers(params, here, n, "params"), _pointers(grads, here, n, "grads")
+    m, v = _pointers(exp_avg, here, n, "exp_avg"), _pointers(exp_avg_sq, here, n, "exp_avg_sq")
+    w = _pointers(master, here, n, "master")
     _check(l.rr_adamw(_at(p), _at(g), _at(m), _at(v), _at(w), _at(s), n, dtype_code(param_dtype),
-                      dtype_code(grad_dtype), hyper, _addr(grad_scale), stream_handle(stream)))
+                      dtype_code(grad_dtype), hyper, _near(grad_scale, here), stream_handle(stream, here)))
 
 
 def rr_adamw8(params, grads, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale, master, sizes, param_dtype,
               grad_dtype, hyper, seed, grad_scale=None, stream=None):
     """One AdamW step over a list of tensors, states in 8 bits; master may be None."""
-    l, n = lib(), len(sizes)
-    s, p, g = array.array("q", sizes), _pointers(params, n, "params"), _pointers(grads, n, "grads")
-    m, ms = _pointers(exp_avg, n, "exp_avg"), _pointers(exp_avg_scale, n, "exp_avg_scale")
-    v, vs = _pointers(exp_avg_sq, n, "exp_avg_sq"), _pointers(exp_avg_sq_scale, n, "exp_avg_sq_scale")
-    w = _pointers(master, n, "master")
+    l, n, here = lib(), len(sizes), _here()
+    s, p, g = array.array("q", sizes), _pointers(params, here, n, "params"), _pointers(grads, here, n, "grads")
+    m, ms = _pointers(exp_avg, here, n, "exp_avg"), _pointers(exp_avg_scale, here, n, "exp_avg_scale")
+    v, vs = _pointers(exp_avg_sq, here, n, "exp_avg_sq"), _pointers(exp_avg_sq_scale, here, n, "exp_avg_sq_scale")
+    w = _pointers(master, here, n, "master")
     _check(l.rr_adamw8(_at(p), _at(g), _at(m), _at(ms), _at(v), _at(vs), _at(w), _at(s), n, dtype_code(param_dtype),
-                       dtype_code(grad_dtype), hyper, seed & 0xFFFFFFFF, _addr(grad_scale), stream_handle(stream)))
+                       dtype_code(grad_dtype), hyper, seed & 0xFFFFFFFF, _near(grad_scale, here),
+                       stream_handle(stream, here)))
 
 
 def bound_call(name, *args):

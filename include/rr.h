@@ -408,6 +408,9 @@ rr_status rr_allreduce_oneshot_noalloc_status(cudaStream_t stream);
  *    streams may run them at once.  Calls allocate nothing and may be captured
  *    in a CUDA graph; scalars (learning rate, step number, ...) are then the
  *    captured ones on every replay.
+ *  - They run on the current device and take its memory; the C entries do not
+ *    look pointers up (the Python binding refuses tensors of another device
+ *    with RR_ERR_WRONG_DEVICE).
  *  - Device pointers need only their element's alignment (RR_ERR_ALIGNMENT
  *    otherwise): 4 bytes for binary32, 2 for bf16 and fp16, 1 for 8-bit codes.
  *    16-byte aligned rows and tensors run faster.  Workspaces are 16-byte
