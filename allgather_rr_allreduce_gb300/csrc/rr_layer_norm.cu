@@ -624,8 +624,9 @@ __global__ void __launch_bounds__(EL == 32 ? 256 : 512, EL == 8 ? 1 : 0) norm_gr
 // and two passes over it, the second out of L1, the weight's gradient in
 // registers, EL columns to a thread, kAtOnce of them loaded together.  While a
 // row's second pass runs, the next row comes into L2 (4096 x 18944 bf16 150 us,
-// 47 % of the copy peak; without that 190).  One block of 16 warps to an SM: bound by
-// the latency of its loads and by instructions.
+// 46 % of the copy peak; without that 190).  One block of 16 warps to an SM: bound by
+// the latency of its loads and by instructions; 48 columns to a thread spill 16 to
+// 104 bytes of its 128 registers.
 constexpr int kWideThreads = 512, kAtOnce = 8;
 template <class T, int EL, bool EVEN>
 __global__ void __launch_bounds__(kWideThreads) norm_grad_wide_kernel(const __grid_constant__ NormGradArgs a)
@@ -926,9 +927,9 @@ std::mutex g_mu;
 std::map<int, int> g_sms;
 std::map<std::tuple<int, const void *, int, int>, int> g_fit;  // device, kernel, threads, shared memory
 
-// Blocks of the columns kernel for each SM: what fits at once with vectors (4096
-// x 18944 bf16, both kernels: 210 us, with 8 blocks 227), more with single
-// elements (2000 x 12001: 118 us, with 3 blocks 171).
+// Blocks of the columns kernel for each SM: what fits at once with vectors, more
+// with single elements (before the sums in stretches, both kernels: 4096 x 18944
+// bf16 210 us, with 8 blocks 227; 2000 x 12001 118, with 3 blocks 171).
 constexpr int tile_blocks(bool even) { return even ? 3 : 16; }
 template <class T>
 const void *norm_long_fn(bool even)
@@ -976,15 +977,19 @@ const void *norm_grad_fn(int el, bool vec, bool group)
     return group ? (const void *)norm_grad_rows_kernel<T, 32, true, true> : (const void *)norm_grad_rows_kernel<T, 32, true, false>;
 }
 
-// Elements to a lane and warps to a row.  Even rows: one warp while 32 elements
-// a lane hold the row (two with 16 from 513 columns on where there are fewer
-// than 8 rows for each SM: the gradient of 257 x 1024 binary32 5.9 against 7.6
-// us), else 16 a lane up to 8 warps (12 for the gradient: 8192 x 5120 bf16 58 us,
-// with 32 68; 8192 x 8192 85 and 79), then 32; with fewer rows than SMs, where
-// nothing but one row's latency counts, 8 a lane.  Uneven rows
-// take 8 a lane while its warps allow (66 against 60 us for 8000 x 5001 bf16
-// forward with 16), except one warp a row with 16 for 257 to 512 columns (65536 x
-// 301 bf16: 30 against 35, gradient 49 against 81), then 32 (it spills, but reads a row
+// Elements to a lane and warps to a row.  Even rows: one warp with 8 or 16 elements
+// a lane up to 512 columns; up to 1024 two warps with 16 while there are fewer than
+// 8 rows for each SM, then one with 32; from there 16 a lane up to 8 warps (12 for
+// the gradient), then 32; with fewer rows than SMs, where nothing but one row's
+// latency counts, 8 a lane.  Both sides, 16 and 32 a lane, in us:
+//   1024 columns of bf16, 257 rows: forward 2.8, 4.3, gradient 7.4, 7.9; 1000 rows:
+//   4.2, 4.6 and 9.4, 7.8; 16384 rows: 14.9, 16.6 and 29.6, 23.0.  The border is late
+//   for the gradient (32 is ahead from 608 rows) and early for the forward.
+//   Gradient, 8192 rows of bf16: 4608 columns 56, 67; 5120 58, 68; 6144 63, 72 (300
+//   rows 14.7, 15.6); binary32 5120 84, 81; 6144 107, 106.  8192 columns 85, 79.
+// Uneven rows take 8 a lane while its warps allow (8000 x 5001 bf16 forward 60 us,
+// with 16 66), except one warp a row with 16 for 257 to 512 columns (65536 x 301
+// bf16: 30 against 35, gradient 49 against 81), then 32 (it spills, but reads a row
 // once: 4000 x 12001 94 us, the long-row kernel 120).  warps > 0 where a kernel of
 // that shape takes the row (most[]: the warps its launch bounds allow with 8, 16
 // and 32 elements a lane), else 0.
@@ -1288,9 +1293,11 @@ try {
                          vector_rows(x, x_stride, rows, eb) && (!dx || vector_rows(dx, dx_stride, rows, eb));
         row_shape(rows, cols, vec, sms, kNormGradWarps, &el, &warps);
         const int64_t most = most_partials(rows, cols);
-        // Long rows: one pass over HBM once each SM has a few of them (4096 x 18944
-        // bf16 150 us, 64 rows 32, uneven 2000 x 12001 73; the two-pass kernels 215,
-        // 14 and 120).
+        // Long rows: one pass over HBM once each SM has a few of them, else the two
+        // kernels that share a row among blocks.  Both sides in us: 18944 columns of
+        // bf16, 304 rows 43, 23; 608 rows 52, 35; 1216 rows 69, 72; 2432 rows 104,
+        // 135.  12288 of binary32, 608 rows 34, 28; 912 rows 43, 43.  12001 uneven, 152
+        // rows 15, 17; 608 rows 30, 41; 2432 rows 82, 137.
         if (warps == 0 && cols <= kWideThreads * 48 && rows >= 4 * (int64_t)sms) {
             const int wide = cols <= kWideThreads * 32 ? 32 : cols <= kWideThreads * 40 ? 40 : 48;
             const void *fn = dtype == RR_FP32   ? norm_grad_wide_fn<float>(wide, vec)

@@ -244,7 +244,8 @@ __device__ __forceinline__ float adam_element(const AdamScalars &h, float scale,
 // alike go element by element.  Bound: HBM (7 streams with master weights).  One
 // rank's shard of a layer, 29M bf16 weights with masters, 130 us, 6.3 TB/s, 93 % of
 // the copy peak; 30M binary32 138 us (91 %); 7M in 61 tensors packed at any element
-// 34.6 us (84 %).  Two vectors a thread took 160 us for the shard.
+// 34.6 us (84 %); 30M whose pointers are not aligned alike 309 us with masters, 314
+// in binary32 (40 %).  Two vectors a thread took 160 us for the shard.
 template <class P, class G, bool MASTER, int CAP>
 __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ AdamArgs<CAP> a)
 {
@@ -336,6 +337,8 @@ struct Adam8Args {
     uint32_t seed, first;  // first: index in the caller's list of this launch's first tensor
 };
 
+// Xor-shifts and odd multipliers: shifts and first multiplier after C. Wellons,
+// "Prospecting for Hash Functions" (2018), with another second one.
 __host__ __device__ __forceinline__ uint32_t mix32(uint32_t x)
 {
     x ^= x >> 16;
@@ -372,7 +375,9 @@ __device__ __forceinline__ float cut_to_code(float t, uint32_t u, uint32_t half,
 // A positive root is stored as no less than the smallest code.
 __device__ __forceinline__ float floor_code(float t) { return t > 0.0f ? fmaxf(t, 0x1p-9f) : t; }
 // 32 random bits of element `step` after the one whose product with kWeyl,
-// plus the tensor's key, is `base`.
+// plus the tensor's key, is `base`.  One multiplication makes each element's bits
+// even over the seeds, not independent of other elements' of the same step: the
+// high halves of elements 58678 apart correlate at 0.5, those 305 apart at 0.07.
 constexpr uint32_t kWeyl = 0x9E3779B1u;
 __device__ __forceinline__ uint32_t dither(uint32_t base, uint32_t step)
 {
@@ -636,6 +641,13 @@ __device__ __forceinline__ void adamw8_block(const AdamScalars &h, float scale, 
 // apart from beta1, 2 more.  60M bf16 weights with masters 178 us (91 %), 60M
 // binary32 156 us (92 %); runs of 32 dealt out in turn, uneven at the end, 185 and
 // 161 (before that look).
+//
+// What a lane finds costs: 60M bf16 weights 121 us when a block's values are of one
+// size, 135 when they spread log-normally (sigma 1), 141 with one value a hundred
+// times the others in each block (values below 2^-6 of the code's range are rounded
+// again), 315 when every tenth gradient has always been 0, 293 when all have (a v of
+// 0 takes sqrt and / of their own).  Tensors off a 16-byte boundary go element by
+// element: 175, with masters 236 (aligned 171), binary32 367 (158).
 template <class P, class G, bool MASTER, int CAP>
 __global__ void __launch_bounds__(kThreads) adamw8_kernel(const __grid_constant__ Adam8Args<CAP> a)
 {

@@ -403,9 +403,11 @@ rr_status rr_allreduce_oneshot_noalloc_status(cudaStream_t stream);
  * out (examples/sharded_step.py runs the whole chain).
  *
  * They keep the conventions above except where stated here:
- *  - They run no barrier and need no signal pad.  Each is one to three kernel
- *    launches on `stream`, none cooperative, all programmatic; any number of
- *    streams may run them at once.  Calls allocate nothing and may be captured
+ *  - They run no barrier and need no signal pad.  They are kernel launches on
+ *    `stream`, none cooperative, all programmatic: one for rr_layer_norm, up to
+ *    three for its gradient, one for each 400 tensors of an AdamW list, one for
+ *    each 1200 of a norm's list and one more; any number of streams may run
+ *    them at once.  Calls allocate nothing and may be captured
  *    in a CUDA graph; scalars (learning rate, step number, ...) are then the
  *    captured ones on every replay.
  *  - They run on the current device and take its memory; the C entries do not
@@ -548,6 +550,8 @@ rr_status rr_adamw(void *const *params, const void *const *grads, float *const *
  *   h ^= h >> 16; h *= 0x7FEB352D; h ^= h >> 15
  * u = (h & 0xFFFF) for m, h >> 16 for sqrt(v); a value t = |value| / scale with
  * grid spacing q (2^-9 below 2^-6) becomes floor(t / q + (u + 1/2) / 65536) * q.
+ * Each value is rounded without bias over the seeds; the bits of two elements in
+ * one step are not independent (at some distances they correlate up to 0.5).
  *
  * exp_avg_scale, exp_avg_sq_scale: HOST arrays of device pointers to
  * ceil(sizes[i] / RR_ADAMW8_BLOCK) binary32 scales.  Other arguments as
