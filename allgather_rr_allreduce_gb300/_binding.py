@@ -46,6 +46,18 @@ class rr_adamw_hyper(ctypes.Structure):
                 ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("step", ctypes.c_int64)]
 
 
+class rr_policy_hyper(ctypes.Structure):
+    """rr_policy_hyper(clip_low, clip_high, kl_coef, inv_temperature, grad_scale)."""
+    _fields_ = [("clip_low", ctypes.c_double), ("clip_high", ctypes.c_double), ("kl_coef", ctypes.c_double),
+                ("inv_temperature", ctypes.c_double), ("grad_scale", ctypes.c_double)]
+
+
+class rr_preference_hyper(ctypes.Structure):
+    """rr_preference_hyper(beta, label_smoothing, margin, inv_temperature, grad_scale, average)."""
+    _fields_ = [("beta", ctypes.c_double), ("label_smoothing", ctypes.c_double), ("margin", ctypes.c_double),
+                ("inv_temperature", ctypes.c_double), ("grad_scale", ctypes.c_double), ("average", ctypes.c_int)]
+
+
 class RRError(RuntimeError):
     def __init__(self, status, message):
         self.status = status
@@ -95,6 +107,12 @@ def lib():
             "rr_grad_norm_workspace": [i32, ctypes.POINTER(ctypes.c_size_t)],
             "rr_adamw": [_vp] * 6 + [i32, i32, i32, ctypes.POINTER(rr_adamw_hyper), _vp, _vp],
             "rr_adamw8": [_vp] * 8 + [i32, i32, i32, ctypes.POINTER(rr_adamw_hyper), ctypes.c_uint32, _vp, _vp],
+            "rr_token_logp": [_vp] * 4 + [i64] * 3 + [ctypes.c_float, i32, _vp],
+            "rr_token_logp_backward": [_vp] * 5 + [i64] * 4 + [ctypes.c_float, i32, _vp],
+            "rr_policy_loss": [_vp] * 10 + [i64] * 4 + [ctypes.POINTER(rr_policy_hyper), i32, _vp],
+            "rr_preference_loss": [_vp] * 8 + [i64] * 4 + [i32, ctypes.POINTER(rr_preference_hyper), i32, _vp,
+                                                           ctypes.c_size_t, _vp],
+            "rr_preference_loss_workspace": [i64, i32, ctypes.POINTER(ctypes.c_size_t)],
         }
         for name, args in sig.items():
             f = getattr(l, name)
@@ -396,6 +414,49 @@ def rr_adamw8(params, grads, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scal
     _check(l.rr_adamw8(_at(p), _at(g), _at(m), _at(ms), _at(v), _at(vs), _at(w), _at(s), n, dtype_code(param_dtype),
                        dtype_code(grad_dtype), hyper, seed & 0xFFFFFFFF, _near(grad_scale, here),
                        stream_handle(stream, here)))
+
+
+def rr_token_logp(logits, targets, logp, lse, rows, vocab, logits_stride, inv_temperature, dtype, stream=None):
+    """Log-probability of each row's target; lse may be None."""
+    l, here = lib(), _here()
+    _check(l.rr_token_logp(_near(logits, here), _near(targets, here), _near(logp, here), _near(lse, here), rows, vocab,
+                           logits_stride, inv_temperature, dtype_code(dtype), stream_handle(stream, here)))
+
+
+def rr_token_logp_backward(logits, targets, lse, dlogp, dlogits, rows, vocab, logits_stride, dlogits_stride,
+                           inv_temperature, dtype, stream=None):
+    """Gradient of rr_token_logp."""
+    l, here = lib(), _here()
+    _check(l.rr_token_logp_backward(_near(logits, here), _near(targets, here), _near(lse, here), _near(dlogp, here),
+                                    _near(dlogits, here), rows, vocab, logits_stride, dlogits_stride, inv_temperature,
+                                    dtype_code(dtype), stream_handle(stream, here)))
+
+
+def rr_policy_loss(logits, targets, old_logp, ref_logp, advantages, weights, loss, token_loss, logp, dlogits, rows,
+                   vocab, logits_stride, dlogits_stride, hyper, dtype, stream=None):
+    """Clipped policy loss and its gradient; old_logp, ref_logp, weights, loss and dlogits may be None."""
+    l, here = lib(), _here()
+    _check(l.rr_policy_loss(_near(logits, here), _near(targets, here), _near(old_logp, here), _near(ref_logp, here),
+                            _near(advantages, here), _near(weights, here), _near(loss, here), _near(token_loss, here),
+                            _near(logp, here), _near(dlogits, here), rows, vocab, logits_stride, dlogits_stride, hyper,
+                            dtype_code(dtype), stream_handle(stream, here)))
+
+
+def rr_preference_loss(logits, targets, offsets, ref_logp, loss, seq_logp, logp, dlogits, rows, vocab, logits_stride,
+                       dlogits_stride, pairs, hyper, dtype, workspace, workspace_bytes, stream=None):
+    """Preference loss over pairs of sequences and its gradient; ref_logp and dlogits may be None."""
+    l, here = lib(), _here()
+    _check(l.rr_preference_loss(_near(logits, here), _near(targets, here), _near(offsets, here), _near(ref_logp, here),
+                                _near(loss, here), _near(seq_logp, here), _near(logp, here), _near(dlogits, here), rows,
+                                vocab, logits_stride, dlogits_stride, pairs, hyper, dtype_code(dtype),
+                                _near(workspace, here), workspace_bytes, stream_handle(stream, here)))
+
+
+def rr_preference_loss_workspace(rows, pairs):
+    """Bytes of workspace for rr_preference_loss."""
+    n = ctypes.c_size_t()
+    _check(lib().rr_preference_loss_workspace(rows, pairs, ctypes.byref(n)))
+    return n.value
 
 
 def bound_call(name, *args):

@@ -1,0 +1,738 @@
+// Log-probabilities of tokens, the clipped policy loss and the preference loss,
+// with their gradients (include/rr.h: rr_token_logp, rr_token_logp_backward,
+// rr_policy_loss, rr_preference_loss).
+//
+// All of them are row operators over logits x of `vocab` elements: with
+// z = x / temperature, M = max(x), s = sum of exp(z - M / temperature),
+//   logp = (x_t - M) / temperature - log(s),
+//   d logp / d x_j = (1[j = t] - exp(z_j - M / temperature) / s) / temperature.
+// A row's maximum and sum are taken in one pass (each thread keeps its own and
+// joins them at the end); a gradient needs them first, so it is a second pass
+// over the row, which then comes out of the L2.
+//
+// Times below are of one GB300 (152 SMs, measured copy 6.7 TB/s).
+#include <cmath>
+#include <cooperative_groups.h>
+
+#include "rr_step.h"
+
+namespace rr {
+
+namespace {
+
+namespace cg = cooperative_groups;
+
+#define RR_TRY(expr)                  \
+    do {                              \
+        const rr_status st_ = (expr); \
+        if (st_ != RR_OK) return st_; \
+    } while (0)
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kUnroll = 4;      // vectors a thread has in flight
+constexpr int kMostCluster = 8; // blocks that share a row
+constexpr int64_t kMaxVocab = (int64_t)1 << 31;
+constexpr int64_t kMaxRows = (int64_t)1 << 40;
+
+enum Mode { kLogp, kPolicy, kPreference };
+
+struct RowArgs {
+    const void *x;
+    const int64_t *target;
+    int64_t rows, vocab, stride;
+    float inv_t, log2_scale;  // 1 / temperature, and that over log(2)
+    float *logp, *lse;
+    // policy loss
+    const float *old_logp, *ref_logp, *advantage, *weight;
+    float low, high, kl, grad_scale;
+    float *token_loss;
+    void *dx;
+    int64_t dx_stride;
+    // preference loss: rows of [offsets[0], offsets[last]) only
+    const int64_t *offsets;
+    int last;
+};
+
+struct GradArgs {
+    const void *x;
+    const int64_t *target;
+    const float *lse, *dlogp;
+    void *dx;
+    int64_t rows, vocab, stride, dx_stride;
+    float inv_t, log2_scale;
+    const int64_t *offsets;  // NULL: all rows
+    int last;
+};
+
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// A maximum and the sum of exponentials relative to it.  An empty part, or one
+// of -inf alone, has maximum -inf and sum 0.
+struct Stat {
+    float top, sum;
+};
+// What exponents are taken relative to: -inf - -inf is no number.
+__device__ __forceinline__ float base_of(float top) { return top == -INFINITY ? 0.0f : top; }
+__device__ __forceinline__ Stat join(Stat a, Stat b, float scale)
+{
+    const float top = fmaxf(a.top, b.top), base = base_of(top);
+    return Stat{top, a.sum * exp2_fast((a.top - base) * scale) + b.sum * exp2_fast((b.top - base) * scale)};
+}
+
+template <class T, int E>
+__device__ __forceinline__ void take(Stat &s, const Pack<T, E> (&v)[kUnroll], float scale)
+{
+    float top = s.top;
+#pragma unroll
+    for (int j = 0; j < kUnroll; ++j)
+#pragma unroll
+        for (int k = 0; k < E; ++k) top = fmaxf(top, to_f32(v[j].v[k]));
+    const float base = base_of(top);
+    float2 sum = make_float2(s.sum * exp2_fast((s.top - base) * scale), 0.0f);
+    const float2 less = both(-base), by = both(scale);
+#pragma unroll
+    for (int j = 0; j < kUnroll; ++j)
+#pragma unroll
+        for (int k = 0; k < E; k += 2) {
+            const float2 t = mul2(add2(pair_f32(v[j].v + k), less), by);
+            sum = add2(sum, make_float2(exp2_fast(t.x), exp2_fast(t.y)));
+        }
+    s.top = top;
+    s.sum = sum.x + sum.y;
+}
+__device__ __forceinline__ void take(Stat &s, float x, float scale) { s = join(s, Stat{x, 1.0f}, scale); }
+
+// A row's elements as a block of a cluster takes them: vectors of 16 bytes where
+// they are aligned, single elements before and behind.
+struct Slice {
+    int64_t first, last;  // this block's elements
+    int64_t v0, v1;       // of which whole aligned vectors lie in [v0, v1)
+};
+template <class T>
+__device__ __forceinline__ Slice slice_of(const T *row, int64_t vocab, int part, int parts)
+{
+    constexpr int E = 16 / (int)sizeof(T);
+    int64_t head = (16 - (int)(reinterpret_cast<uintptr_t>(row) & 15)) % 16 / (int)sizeof(T);
+    if (head > vocab) head = vocab;
+    const int64_t n = (vocab - head) / E;
+    Slice s;
+    s.v0 = head + n * part / parts * E;
+    s.v1 = head + n * (part + 1) / parts * E;
+    s.first = part == 0 ? 0 : s.v0;
+    s.last = part == parts - 1 ? vocab : s.v1;
+    return s;
+}
+
+template <class T>
+__device__ __forceinline__ Stat row_stat(const T *row, const Slice &s, float scale)
+{
+    constexpr int E = 16 / (int)sizeof(T);
+    constexpr int64_t step = (int64_t)kThreads * E * kUnroll;
+    Stat st{-INFINITY, 0.0f};
+    Pack<T, E> v[kUnroll];
+    int64_t e = s.v0 + (int64_t)threadIdx.x * E;
+    for (; e + (kUnroll - 1) * kThreads * E < s.v1; e += step) {
+#pragma unroll
+        for (int j = 0; j < kUnroll; ++j) v[j] = *reinterpret_cast<const Pack<T, E> *>(row + e + j * kThreads * E);
+        take(st, v, scale);
+    }
+    if (e < s.v1) {
+#pragma unroll
+        for (int j = 0; j < kUnroll; ++j) {
+            if (e + j * kThreads * E < s.v1) {
+                v[j] = *reinterpret_cast<const Pack<T, E> *>(row + e + j * kThreads * E);
+            } else {
+#pragma unroll
+                for (int k = 0; k < E; ++k) v[j].v[k] = from_f32<T>(-INFINITY);
+            }
+        }
+        take(st, v, scale);
+    }
+    for (int64_t i = s.first + threadIdx.x; i < s.v0; i += kThreads) take(st, to_f32(row[i]), scale);
+    for (int64_t i = s.v1 + threadIdx.x; i < s.last; i += kThreads) take(st, to_f32(row[i]), scale);
+    return st;
+}
+
+// dx_j = -slope * exp2((x_j - base) * scale), plus slope at the target.
+template <class T>
+__device__ __forceinline__ void row_grad(const T *row, T *out, const Slice &s, int64_t target, float base, float scale,
+                                         float slope, float over)
+{
+    constexpr int E = 16 / (int)sizeof(T);
+    const float factor = -slope * over;
+    auto one = [&](int64_t i) {
+        const float g = exp2_fast((to_f32(row[i]) - base) * scale) * factor;
+        out[i] = from_f32<T>(i == target ? g + slope : g);
+    };
+    if (((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0) {
+        const float2 less = both(-base), by = both(scale), f = both(factor);
+        constexpr int64_t step = (int64_t)kThreads * E * kUnroll;
+        for (int64_t e = s.v0 + (int64_t)threadIdx.x * E; e < s.v1; e += step) {
+            Pack<T, E> v[kUnroll];
+#pragma unroll
+            for (int j = 0; j < kUnroll; ++j)
+                if (e + j * kThreads * E < s.v1) v[j] = *reinterpret_cast<const Pack<T, E> *>(row + e + j * kThreads * E);
+#pragma unroll
+            for (int j = 0; j < kUnroll; ++j) {
+                const int64_t at = e + j * kThreads * E;
+                if (at >= s.v1) break;
+#pragma unroll
+                for (int k = 0; k < E; k += 2) {
+                    const float2 t = mul2(add2(pair_f32(v[j].v + k), less), by);
+                    float2 g = mul2(make_float2(exp2_fast(t.x), exp2_fast(t.y)), f);
+                    if (target == at + k) g.x += slope;
+                    if (target == at + k + 1) g.y += slope;
+                    pair_set(v[j].v + k, g);
+                }
+                *reinterpret_cast<Pack<T, E> *>(out + at) = v[j];
+            }
+        }
+        for (int64_t i = s.first + threadIdx.x; i < s.v0; i += kThreads) one(i);
+        for (int64_t i = s.v1 + threadIdx.x; i < s.last; i += kThreads) one(i);
+    } else {
+#pragma unroll 8
+        for (int64_t i = s.first + threadIdx.x; i < s.last; i += kThreads) one(i);
+    }
+}
+
+template <class T>
+__device__ __forceinline__ void row_zero(T *out, int64_t vocab, int part, int parts)
+{
+    constexpr int E = 16 / (int)sizeof(T);
+    const Slice s = slice_of(out, vocab, part, parts);
+    for (int64_t i = s.first + threadIdx.x; i < s.v0; i += kThreads) out[i] = from_f32<T>(0.0f);
+    for (int64_t e = s.v0 + (int64_t)threadIdx.x * E; e < s.v1; e += kThreads * E)
+        *reinterpret_cast<uint4 *>(out + e) = make_uint4(0, 0, 0, 0);
+    for (int64_t i = s.v1 + threadIdx.x; i < s.last; i += kThreads) out[i] = from_f32<T>(0.0f);
+}
+
+// A row to a cluster of blocks (of one, mostly).
+template <class T, Mode MODE>
+__global__ void __launch_bounds__(kThreads, 2) row_kernel(const __grid_constant__ RowArgs a)
+{
+    stream_order();
+    const cg::cluster_group cluster = cg::this_cluster();
+    const int parts = (int)cluster.num_blocks(), part = (int)cluster.block_rank();
+    __shared__ Stat of_warp[2][kWarps];
+    __shared__ Stat of_block[2];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int64_t row = blockIdx.x / parts, end = a.rows;
+    const int64_t every = gridDim.x / parts;
+    if (MODE == kPreference) {
+        const int64_t first = a.offsets[0];
+        end = min(end, a.offsets[a.last]);
+        if (first > row) row += (first - row + every - 1) / every * every;
+    }
+    int turn = 0;
+    for (; row < end; row += every) {
+        const T *x = static_cast<const T *>(a.x) + row * a.stride;
+        T *dx = a.dx ? static_cast<T *>(a.dx) + row * a.dx_stride : nullptr;
+        const int64_t target = a.target[row];
+        if (target < 0 || target >= a.vocab) {  // the same for every block of the cluster
+            if (part == 0 && threadIdx.x == 0) {
+                a.logp[row] = 0.0f;
+                if (MODE != kPolicy && a.lse) a.lse[row] = 0.0f;
+                if (MODE == kPolicy) a.token_loss[row] = 0.0f;
+            }
+            if (MODE == kPolicy && dx) row_zero(dx, a.vocab, part, parts);
+            continue;
+        }
+        const float xt = to_f32(x[target]);
+        const Slice slice = slice_of(x, a.vocab, part, parts);
+        Stat s = row_stat(x, slice, a.log2_scale);
+#pragma unroll
+        for (int o = 16; o; o >>= 1)
+            s = join(s, Stat{__shfl_xor_sync(~0u, s.top, o), __shfl_xor_sync(~0u, s.sum, o)}, a.log2_scale);
+        if (lane == 0) of_warp[turn][warp] = s;
+        __syncthreads();
+        s = lane < kWarps ? of_warp[turn][lane] : Stat{-INFINITY, 0.0f};
+#pragma unroll
+        for (int o = 16; o; o >>= 1)
+            s = join(s, Stat{__shfl_xor_sync(~0u, s.top, o), __shfl_xor_sync(~0u, s.sum, o)}, a.log2_scale);
+        if (parts > 1) {
+            if (threadIdx.x == 0) of_block[turn] = s;
+            cluster.sync();
+            s = lane < parts ? *cluster.map_shared_rank(&of_block[turn], lane) : Stat{-INFINITY, 0.0f};
+#pragma unroll
+            for (int o = kMostCluster / 2; o; o >>= 1)
+                s = join(s, Stat{__shfl_xor_sync(~0u, s.top, o), __shfl_xor_sync(~0u, s.sum, o)}, a.log2_scale);
+            s.top = __shfl_sync(~0u, s.top, 0);
+            s.sum = __shfl_sync(~0u, s.sum, 0);
+        }
+        turn ^= 1;
+        const float log_sum = logf(s.sum), logp = (xt - s.top) * a.inv_t - log_sum;
+        const bool first = part == 0 && threadIdx.x == 0;
+        if (first) {
+            a.logp[row] = logp;
+            if (MODE != kPolicy && a.lse) a.lse[row] = s.top * a.inv_t + log_sum;
+        }
+        if (MODE == kPolicy) {
+            const float weight = a.weight ? a.weight[row] : 1.0f, adv = a.advantage[row];
+            const float ratio = a.old_logp ? expf(logp - a.old_logp[row]) : 1.0f;
+            const float free = ratio * adv, held = fminf(fmaxf(ratio, a.low), a.high) * adv;
+            const bool passes = !(free > held);  // NaN passes
+            float loss = passes ? -free : -held, slope = passes ? -free : 0.0f;
+            if (a.ref_logp) {
+                const float gap = a.ref_logp[row] - logp, back = expm1f(gap);
+                loss += a.kl * (back - gap);
+                slope -= a.kl * back;
+            }
+            if (first) a.token_loss[row] = loss * weight;
+            if (dx)
+                row_grad(x, dx, slice, target, base_of(s.top), a.log2_scale, slope * weight * a.grad_scale * a.inv_t,
+                         1.0f / s.sum);
+        }
+    }
+    if (parts > 1) cluster.sync();  // a block's shared memory stays until the others have read it
+}
+
+// The gradient of log-probabilities whose sums are known: a row to a block, or
+// to `parts` blocks that do not meet.
+template <class T>
+__global__ void __launch_bounds__(kThreads, 2) row_grad_kernel(const __grid_constant__ GradArgs a, int parts)
+{
+    stream_order();
+    int64_t first = 0, end = a.rows;
+    if (a.offsets) {
+        first = max((int64_t)0, a.offsets[0]);
+        end = min(end, a.offsets[a.last]);
+    }
+    const int64_t every = gridDim.x / parts;
+    const int part = (int)(blockIdx.x % parts);
+    // From the last row on: the sums' pass has read it last, so it may still be in the L2.
+    for (int64_t row = end - 1 - blockIdx.x / parts; row >= first; row -= every) {
+        const T *x = static_cast<const T *>(a.x) + row * a.stride;
+        T *dx = static_cast<T *>(a.dx) + row * a.dx_stride;
+        const int64_t target = a.target[row];
+        if (target < 0 || target >= a.vocab)
+            row_zero(dx, a.vocab, part, parts);
+        else
+            row_grad(x, dx, slice_of(x, a.vocab, part, parts), target, a.lse[row] / a.inv_t, a.log2_scale,
+                     a.dlogp[row] * a.inv_t, 1.0f);
+    }
+}
+
+// ---------------------------------------------------------------- pairs of sequences
+struct PairArgs {
+    const float *logp, *ref;
+    const int64_t *target, *offsets;
+    int64_t rows, vocab;
+    int pairs;
+    float beta, smoothing, margin, grad_scale;
+    bool average;
+    float *seq_logp, *loss, *slope;  // of each sequence, pair and row
+};
+
+// Sum of a block's values in binary64, the same in every thread.
+__device__ __forceinline__ double block_sum(double x, double *s)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = x;
+    __syncthreads();
+    x = 0.0;
+    for (int i = 0; i < kWarps; ++i) x += s[i];
+    return x;
+}
+
+// log(1 + exp(x)) without overflow.
+__device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x))); }
+
+// A block a pair: sums of log-probabilities, the pair's loss, the slope of every row.
+__global__ void __launch_bounds__(kThreads) pair_kernel(const __grid_constant__ PairArgs a)
+{
+    stream_order();
+    __shared__ double s[kWarps];
+    const int p = blockIdx.x;
+    int64_t lo[2], hi[2];
+    double mean[2], count[2];
+    for (int k = 0; k < 2; ++k) {
+        const int q = p + k * a.pairs;
+        lo[k] = max((int64_t)0, a.offsets[q]);
+        hi[k] = min(a.rows, a.offsets[q + 1]);
+        double sum = 0.0, n = 0.0;
+        for (int64_t i = lo[k] + threadIdx.x; i < hi[k]; i += kThreads) {
+            const int64_t t = a.target[i];
+            if (t >= 0 && t < a.vocab) {
+                sum += (double)a.logp[i];
+                n += 1.0;
+            }
+        }
+        sum = block_sum(sum, s);
+        count[k] = a.average ? fmax(1.0, block_sum(n, s)) : 1.0;
+        mean[k] = sum / count[k];
+        if (threadIdx.x == 0) a.seq_logp[q] = (float)mean[k];
+    }
+    double gap = mean[0] - mean[1];
+    if (a.ref) gap -= (double)a.ref[p] - (double)a.ref[p + a.pairs];
+    const float h = (float)((double)a.beta * gap - (double)a.margin);
+    if (threadIdx.x == 0) a.loss[p] = (1.0f - a.smoothing) * softplus(-h) + a.smoothing * softplus(h);
+    if (!a.slope) return;
+    // d loss / d h = smoothing * sigmoid(h) - (1 - smoothing) * sigmoid(-h)
+    const float e = expf(-fabsf(h)), small = e / (1.0f + e), large = 1.0f / (1.0f + e);
+    const float up = h >= 0.0f ? large : small, down = h >= 0.0f ? small : large;
+    const float dh = (a.smoothing * up - (1.0f - a.smoothing) * down) * a.beta / (float)a.pairs * a.grad_scale;
+    for (int k = 0; k < 2; ++k) {
+        const float slope = (k ? -dh : dh) / (float)count[k];
+        for (int64_t i = lo[k] + threadIdx.x; i < hi[k]; i += kThreads) a.slope[i] = slope;
+    }
+}
+
+// loss = sum / count, in one order.
+struct SumArgs {
+    const float *part;
+    int64_t n;
+    double count;
+    float *loss;
+};
+__global__ void __launch_bounds__(kThreads) sum_kernel(const __grid_constant__ SumArgs a)
+{
+    stream_order();
+    __shared__ double s[kWarps];
+    double sum = 0.0;
+    for (int64_t i = threadIdx.x; i < a.n; i += kThreads) sum += (double)a.part[i];
+    sum = block_sum(sum, s);
+    if (threadIdx.x == 0) *a.loss = (float)(sum / a.count);
+}
+
+// ---------------------------------------------------------------- host side
+struct Range {
+    const char *name;
+    const void *p;
+    int64_t bytes;
+};
+bool ranges_touch(const Range &a, const Range &b)
+{
+    if (!a.p || !b.p || a.bytes <= 0 || b.bytes <= 0) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return x < y + (uintptr_t)b.bytes && y < x + (uintptr_t)a.bytes;
+}
+// Nothing written may overlap anything else.
+template <size_t N, size_t M>
+rr_status check_apart(const Range (&out)[N], const Range (&in)[M])
+{
+    for (size_t i = 0; i < N; ++i) {
+        for (size_t j = 0; j < M; ++j)
+            if (ranges_touch(out[i], in[j])) return step_fail(RR_ERR_ALIAS, "%s overlaps %s", out[i].name, in[j].name);
+        for (size_t j = 0; j < i; ++j)
+            if (ranges_touch(out[i], out[j])) return step_fail(RR_ERR_ALIAS, "%s overlaps %s", out[i].name, out[j].name);
+    }
+    return RR_OK;
+}
+
+rr_status check_rows(int64_t rows, int64_t vocab, int64_t stride, float inv_t, rr_dtype dtype)
+{
+    if (!float_bytes(dtype)) return step_fail(RR_ERR_UNSUPPORTED_DTYPE, "dtype %d", (int)dtype);
+    if (rows < 0 || rows > kMaxRows) return step_fail(RR_ERR_INVALID_ARG, "rows %lld", (long long)rows);
+    if (vocab < 1 || vocab > kMaxVocab) return step_fail(RR_ERR_INVALID_ARG, "vocab %lld", (long long)vocab);
+    if (rows > 1 && (stride < vocab || stride > kMaxRows))
+        return step_fail(RR_ERR_INVALID_ARG, "logits_stride %lld, vocab %lld", (long long)stride, (long long)vocab);
+    if (rows > 1 && rows > INT64_MAX / 8 / stride) return step_fail(RR_ERR_INVALID_ARG, "rows %lld of logits_stride %lld", (long long)rows, (long long)stride);
+    if (!(inv_t > 0.0f && std::isfinite(inv_t))) return step_fail(RR_ERR_INVALID_ARG, "inv_temperature %g", (double)inv_t);
+    return RR_OK;
+}
+rr_status check_grad(const void *logits, const void *dlogits, int64_t rows, int64_t vocab, int64_t stride,
+                     int64_t dstride, int eb)
+{
+    if (rows > 1 && (dstride < vocab || dstride > kMaxRows || rows > INT64_MAX / 8 / dstride))
+        return step_fail(RR_ERR_INVALID_ARG, "dlogits_stride %lld, vocab %lld", (long long)dstride, (long long)vocab);
+    if (!aligned_to(dlogits, eb)) return step_fail(RR_ERR_ALIGNMENT, "dlogits not %d-byte aligned", eb);
+    const bool in_place = dlogits == logits && (dstride == stride || rows <= 1);
+    const Range out[] = {{"dlogits", dlogits, ((rows - 1) * dstride + vocab) * eb}};
+    const Range in[] = {{"logits", in_place ? nullptr : logits, ((rows - 1) * stride + vocab) * eb}};
+    return check_apart(out, in);
+}
+rr_status check_word(const char *name, const void *p, int bytes, bool needed)
+{
+    if (needed && !p) return step_fail(RR_ERR_INVALID_ARG, "%s is NULL", name);
+    if (!aligned_to(p, bytes)) return step_fail(RR_ERR_ALIGNMENT, "%s not %d-byte aligned", name, bytes);
+    return RR_OK;
+}
+
+template <Mode MODE>
+const void *row_fn(rr_dtype d)
+{
+    return d == RR_FP32 ? (const void *)row_kernel<float, MODE>
+           : d == RR_BF16 ? (const void *)row_kernel<__nv_bfloat16, MODE> : (const void *)row_kernel<__half, MODE>;
+}
+
+// Blocks that share a row: as many as keep no SM without one.
+int blocks_to_a_row(int64_t rows, int64_t vocab, int eb, int sms)
+{
+    int parts = 1;
+    while (parts < kMostCluster && rows * parts * 2 <= sms && vocab * eb / (parts * 2) >= 8192) parts *= 2;
+    return parts;
+}
+
+rr_status launch_rows(const void *fn, RowArgs &a, rr_dtype dtype, cudaStream_t stream)
+{
+    int sms = 0, fit = 0;
+    RR_TRY(step_sms(&sms));
+    RR_TRY(step_fit(fn, kThreads, 0, &fit));
+    const int parts = blocks_to_a_row(a.rows, a.vocab, float_bytes(dtype), sms);
+    int64_t clusters = a.rows;
+    if (parts == 1 && clusters > (int64_t)fit * sms) clusters = (int64_t)fit * sms;
+    cudaLaunchAttribute attr[2] = {};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)parts;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(clusters * parts));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    void *args[] = {&a};
+    const cudaError_t e = cudaLaunchKernelExC(&cfg, fn, args);
+    return e == cudaSuccess ? RR_OK : step_cuda_fail(e, "kernel launch");
+}
+
+rr_status launch_grad(GradArgs &a, rr_dtype dtype, cudaStream_t stream)
+{
+    const void *fn = dtype == RR_FP32   ? (const void *)row_grad_kernel<float>
+                     : dtype == RR_BF16 ? (const void *)row_grad_kernel<__nv_bfloat16> : (const void *)row_grad_kernel<__half>;
+    int sms = 0, fit = 0;
+    RR_TRY(step_sms(&sms));
+    RR_TRY(step_fit(fn, kThreads, 0, &fit));
+    int parts = blocks_to_a_row(a.rows, a.vocab, float_bytes(dtype), fit * sms);
+    int64_t teams = a.rows;
+    if (teams * parts > (int64_t)fit * sms) teams = (int64_t)fit * sms / parts;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(teams * parts));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    void *args[] = {&a, &parts};
+    const cudaError_t e = cudaLaunchKernelExC(&cfg, fn, args);
+    return e == cudaSuccess ? RR_OK : step_cuda_fail(e, "kernel launch");
+}
+
+float log2_scale(float inv_t) { return (float)((double)inv_t * 1.4426950408889634); }
+int64_t span(int64_t rows, int64_t stride, int64_t vocab, int eb) { return ((rows - 1) * stride + vocab) * eb; }
+
+rr_status launch_sum(const float *part, int64_t n, double count, float *loss, cudaStream_t stream)
+{
+    SumArgs a{part, n, count, loss};
+    return step_launch((const void *)sum_kernel, 1, kThreads, 0, &a, stream);
+}
+
+// Workspace of the preference loss: each row's log-sum and slope, each pair's loss.
+int64_t padded(int64_t floats) { return (floats + 3) & ~(int64_t)3; }
+
+}  // namespace
+
+}  // namespace rr
+
+using namespace rr;
+
+extern "C" rr_status rr_token_logp(const void *logits, const int64_t *targets, float *logp, float *lse, int64_t rows,
+                                   int64_t vocab, int64_t logits_stride, float inv_temperature, rr_dtype dtype,
+                                   cudaStream_t stream)
+try {
+    RR_TRY(check_rows(rows, vocab, logits_stride, inv_temperature, dtype));
+    if (rows == 0) return step_ok();
+    const int eb = float_bytes(dtype);
+    RR_TRY(check_word("logits", logits, eb, true));
+    RR_TRY(check_word("targets", targets, 8, true));
+    RR_TRY(check_word("logp", logp, 4, true));
+    RR_TRY(check_word("lse", lse, 4, false));
+    const Range out[] = {{"logp", logp, rows * 4}, {"lse", lse, rows * 4}};
+    const Range in[] = {{"logits", logits, span(rows, logits_stride, vocab, eb)}, {"targets", targets, rows * 8}};
+    RR_TRY(check_apart(out, in));
+    RowArgs a = {};
+    a.x = logits;
+    a.target = targets;
+    a.rows = rows;
+    a.vocab = vocab;
+    a.stride = logits_stride;
+    a.inv_t = inv_temperature;
+    a.log2_scale = log2_scale(inv_temperature);
+    a.logp = logp;
+    a.lse = lse;
+    RR_TRY(launch_rows(row_fn<kLogp>(dtype), a, dtype, stream));
+    return step_ok();
+} catch (...) {
+    return step_no_memory();
+}
+
+extern "C" rr_status rr_token_logp_backward(const void *logits, const int64_t *targets, const float *lse,
+                                            const float *dlogp, void *dlogits, int64_t rows, int64_t vocab,
+                                            int64_t logits_stride, int64_t dlogits_stride, float inv_temperature,
+                                            rr_dtype dtype, cudaStream_t stream)
+try {
+    RR_TRY(check_rows(rows, vocab, logits_stride, inv_temperature, dtype));
+    if (rows == 0) return step_ok();
+    const int eb = float_bytes(dtype);
+    RR_TRY(check_word("logits", logits, eb, true));
+    RR_TRY(check_word("targets", targets, 8, true));
+    RR_TRY(check_word("lse", lse, 4, true));
+    RR_TRY(check_word("dlogp", dlogp, 4, true));
+    RR_TRY(check_word("dlogits", dlogits, eb, true));
+    RR_TRY(check_grad(logits, dlogits, rows, vocab, logits_stride, dlogits_stride, eb));
+    const Range out[] = {{"dlogits", dlogits, span(rows, dlogits_stride, vocab, eb)}};
+    const Range in[] = {{"targets", targets, rows * 8}, {"lse", lse, rows * 4}, {"dlogp", dlogp, rows * 4}};
+    RR_TRY(check_apart(out, in));
+    GradArgs a{logits, targets, lse, dlogp, dlogits, rows, vocab, logits_stride, dlogits_stride, inv_temperature,
+               log2_scale(inv_temperature), nullptr, 0};
+    RR_TRY(launch_grad(a, dtype, stream));
+    return step_ok();
+} catch (...) {
+    return step_no_memory();
+}
+
+extern "C" rr_status rr_policy_loss(const void *logits, const int64_t *targets, const float *old_logp,
+                                    const float *ref_logp, const float *advantages, const float *weights, float *loss,
+                                    float *token_loss, float *logp, void *dlogits, int64_t rows, int64_t vocab,
+                                    int64_t logits_stride, int64_t dlogits_stride, const rr_policy_hyper *hyper,
+                                    rr_dtype dtype, cudaStream_t stream)
+try {
+    if (!hyper) return step_fail(RR_ERR_INVALID_ARG, "hyper is NULL");
+    const float inv_t = (float)hyper->inv_temperature;
+    RR_TRY(check_rows(rows, vocab, logits_stride, inv_t, dtype));
+    if (!(hyper->clip_low >= 0.0 && hyper->clip_high >= 0.0))
+        return step_fail(RR_ERR_INVALID_ARG, "clip_low %g, clip_high %g", hyper->clip_low, hyper->clip_high);
+    if (!std::isfinite((float)hyper->kl_coef)) return step_fail(RR_ERR_INVALID_ARG, "kl_coef %g", hyper->kl_coef);
+    if (!std::isfinite((float)hyper->grad_scale)) return step_fail(RR_ERR_INVALID_ARG, "grad_scale %g", hyper->grad_scale);
+    RR_TRY(check_word("loss", loss, 4, false));
+    if (rows == 0) {
+        if (loss) RR_TRY(launch_sum(nullptr, 0, 1.0, loss, stream));
+        return step_ok();
+    }
+    const int eb = float_bytes(dtype);
+    RR_TRY(check_word("logits", logits, eb, true));
+    RR_TRY(check_word("targets", targets, 8, true));
+    RR_TRY(check_word("old_logp", old_logp, 4, false));
+    RR_TRY(check_word("ref_logp", ref_logp, 4, false));
+    RR_TRY(check_word("advantages", advantages, 4, true));
+    RR_TRY(check_word("weights", weights, 4, false));
+    RR_TRY(check_word("token_loss", token_loss, 4, true));
+    RR_TRY(check_word("logp", logp, 4, true));
+    if (dlogits) RR_TRY(check_grad(logits, dlogits, rows, vocab, logits_stride, dlogits_stride, eb));
+    const Range out[] = {{"loss", loss, 4}, {"token_loss", token_loss, rows * 4}, {"logp", logp, rows * 4}};
+    const Range in[] = {{"logits", logits, span(rows, logits_stride, vocab, eb)}, {"targets", targets, rows * 8},
+                        {"old_logp", old_logp, rows * 4}, {"ref_logp", ref_logp, rows * 4},
+                        {"advantages", advantages, rows * 4}, {"weights", weights, rows * 4},
+                        {"dlogits", dlogits, dlogits ? span(rows, dlogits_stride, vocab, eb) : 0}};
+    RR_TRY(check_apart(out, in));
+    const Range dout[] = {{"dlogits", dlogits, dlogits ? span(rows, dlogits_stride, vocab, eb) : 0}};
+    const Range din[] = {in[1], in[2], in[3], in[4], in[5]};
+    RR_TRY(check_apart(dout, din));
+    RowArgs a = {};
+    a.x = logits;
+    a.target = targets;
+    a.rows = rows;
+    a.vocab = vocab;
+    a.stride = logits_stride;
+    a.inv_t = inv_t;
+    a.log2_scale = log2_scale(inv_t);
+    a.logp = logp;
+    a.old_logp = old_logp;
+    a.ref_logp = ref_logp;
+    a.advantage = advantages;
+    a.weight = weights;
+    a.low = (float)(1.0 - hyper->clip_low);
+    a.high = (float)(1.0 + hyper->clip_high);
+    a.kl = (float)hyper->kl_coef;
+    a.grad_scale = (float)hyper->grad_scale;
+    a.token_loss = token_loss;
+    a.dx = dlogits;
+    a.dx_stride = dlogits_stride;
+    RR_TRY(launch_rows(row_fn<kPolicy>(dtype), a, dtype, stream));
+    if (loss) RR_TRY(launch_sum(token_loss, rows, 1.0, loss, stream));
+    return step_ok();
+} catch (...) {
+    return step_no_memory();
+}
+
+extern "C" rr_status rr_preference_loss_workspace(int64_t rows, int pairs, size_t *bytes)
+{
+    if (!bytes) return step_fail(RR_ERR_INVALID_ARG, "bytes is NULL");
+    if (rows < 0 || rows > kMaxRows) return step_fail(RR_ERR_INVALID_ARG, "rows %lld", (long long)rows);
+    if (pairs < 1) return step_fail(RR_ERR_INVALID_ARG, "pairs %d", pairs);
+    *bytes = (size_t)(2 * padded(rows) + padded(pairs)) * 4;
+    return step_ok();
+}
+
+extern "C" rr_status rr_preference_loss(const void *logits, const int64_t *targets, const int64_t *offsets,
+                                        const float *ref_logp, float *loss, float *seq_logp, float *logp, void *dlogits,
+                                        int64_t rows, int64_t vocab, int64_t logits_stride, int64_t dlogits_stride,
+                                        int pairs, const rr_preference_hyper *hyper, rr_dtype dtype, void *workspace,
+                                        size_t workspace_bytes, cudaStream_t stream)
+try {
+    if (!hyper) return step_fail(RR_ERR_INVALID_ARG, "hyper is NULL");
+    const float inv_t = (float)hyper->inv_temperature;
+    RR_TRY(check_rows(rows, vocab, logits_stride, inv_t, dtype));
+    size_t need = 0;
+    RR_TRY(rr_preference_loss_workspace(rows, pairs, &need));
+    if (!std::isfinite((float)hyper->beta)) return step_fail(RR_ERR_INVALID_ARG, "beta %g", hyper->beta);
+    if (!(hyper->label_smoothing >= 0.0 && hyper->label_smoothing <= 1.0))
+        return step_fail(RR_ERR_INVALID_ARG, "label_smoothing %g", hyper->label_smoothing);
+    if (!std::isfinite((float)hyper->margin)) return step_fail(RR_ERR_INVALID_ARG, "margin %g", hyper->margin);
+    if (!std::isfinite((float)hyper->grad_scale)) return step_fail(RR_ERR_INVALID_ARG, "grad_scale %g", hyper->grad_scale);
+    const int eb = float_bytes(dtype);
+    RR_TRY(check_word("logits", logits, eb, rows > 0));
+    RR_TRY(check_word("targets", targets, 8, rows > 0));
+    RR_TRY(check_word("offsets", offsets, 8, true));
+    RR_TRY(check_word("ref_logp", ref_logp, 4, false));
+    RR_TRY(check_word("loss", loss, 4, true));
+    RR_TRY(check_word("seq_logp", seq_logp, 4, true));
+    RR_TRY(check_word("logp", logp, 4, rows > 0));
+    if (!workspace) return step_fail(RR_ERR_INVALID_ARG, "workspace is NULL");
+    if (!aligned_to(workspace, 16)) return step_fail(RR_ERR_ALIGNMENT, "workspace not 16-byte aligned");
+    if (workspace_bytes < need)
+        return step_fail(RR_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+    if (rows > 0 && dlogits) RR_TRY(check_grad(logits, dlogits, rows, vocab, logits_stride, dlogits_stride, eb));
+    const int64_t seqs = 2 * (int64_t)pairs, in_bytes = rows > 0 ? span(rows, logits_stride, vocab, eb) : 0;
+    const int64_t out_bytes = rows > 0 && dlogits ? span(rows, dlogits_stride, vocab, eb) : 0;
+    const Range out[] = {{"loss", loss, 4}, {"seq_logp", seq_logp, seqs * 4}, {"logp", logp, rows * 4},
+                         {"workspace", workspace, (int64_t)need}};
+    const Range in[] = {{"logits", logits, in_bytes}, {"targets", targets, rows * 8}, {"offsets", offsets, (seqs + 1) * 8},
+                        {"ref_logp", ref_logp, seqs * 4}, {"dlogits", dlogits, out_bytes}};
+    RR_TRY(check_apart(out, in));
+    const Range dout[] = {{"dlogits", dlogits, out_bytes}};
+    const Range din[] = {in[1], in[2], in[3]};
+    RR_TRY(check_apart(dout, din));
+
+    float *lse = static_cast<float *>(workspace), *slope = lse + padded(rows), *pair_loss = slope + padded(rows);
+    if (rows > 0) {
+        RowArgs a = {};
+        a.x = logits;
+        a.target = targets;
+        a.rows = rows;
+        a.vocab = vocab;
+        a.stride = logits_stride;
+        a.inv_t = inv_t;
+        a.log2_scale = log2_scale(inv_t);
+        a.logp = logp;
+        a.lse = lse;
+        a.offsets = offsets;
+        a.last = (int)seqs;
+        RR_TRY(launch_rows(row_fn<kPreference>(dtype), a, dtype, stream));
+    }
+    PairArgs p{logp, ref_logp, targets, offsets, rows, vocab, pairs, (float)hyper->beta, (float)hyper->label_smoothing,
+               (float)hyper->margin, (float)hyper->grad_scale, hyper->average != 0, seq_logp, pair_loss,
+               dlogits ? slope : nullptr};
+    RR_TRY(step_launch((const void *)pair_kernel, pairs, kThreads, 0, &p, stream));
+    RR_TRY(launch_sum(pair_loss, pairs, (double)pairs, loss, stream));
+    if (rows > 0 && dlogits) {
+        GradArgs g{logits, targets, lse, slope, dlogits, rows, vocab, logits_stride, dlogits_stride, inv_t,
+                   log2_scale(inv_t), offsets, (int)seqs};
+        RR_TRY(launch_grad(g, dtype, stream));
+    }
+    return step_ok();
+} catch (...) {
+    return step_no_memory();
+}

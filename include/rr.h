@@ -563,6 +563,110 @@ rr_status rr_adamw8(void *const *params, const void *const *grads, uint8_t *cons
                     rr_dtype grad_dtype, const rr_adamw_hyper *hyper, uint32_t seed,
                     const float *grad_scale, cudaStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Losses over a language model's logits.  They are training-step operators and
+ * keep the conventions above (no pad, no allocation, no atomics, capturable,
+ * element alignment, binary32 arithmetic).  Common to all of them:
+ *  - logits: `rows` rows of `vocab` elements of dtype, logits_stride elements
+ *    apart; targets: one int64 per row, the token whose probability counts.  A
+ *    row whose target lies outside [0, vocab) (-100, say) takes no part: its
+ *    logits are not read, its log-probability and loss are 0 and its gradient
+ *    is zeros.  With z = logits * inv_temperature (> 0),
+ *      logp = z[target] - log(sum of exp(z)).
+ *    -inf masks a token out; a row of nothing but -inf gives NaN, as does one
+ *    that holds +inf or NaN.
+ *  - dlogits: rows of `vocab` elements of dtype, dlogits_stride apart.  dlogits
+ *    == logits with equal strides overwrites the logits by their gradient.
+ *    Nothing else written may overlap anything (RR_ERR_ALIAS).
+ *  - Rows of 16-byte aligned starts run faster where dlogits and logits are
+ *    aligned alike.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * rr_token_logp -- the log-probability of each row's target.
+ *
+ * logp: one binary32 per row.  lse: log(sum of exp(z)) of each row for the
+ * backward (0 where the row takes no part), or NULL.  rows == 0 returns RR_OK.
+ */
+rr_status rr_token_logp(const void *logits, const int64_t *targets, float *logp, float *lse, int64_t rows,
+                        int64_t vocab, int64_t logits_stride, float inv_temperature, rr_dtype dtype,
+                        cudaStream_t stream);
+
+/*
+ * rr_token_logp_backward -- the gradient of rr_token_logp from dlogp (binary32,
+ * one per row) and the forward's lse:
+ *   dlogits[j] = inv_temperature * dlogp * (1[j == target] - exp(z[j] - lse)).
+ * With dlogp = -1 / (number of counted rows) it is a cross-entropy's gradient.
+ */
+rr_status rr_token_logp_backward(const void *logits, const int64_t *targets, const float *lse, const float *dlogp,
+                                 void *dlogits, int64_t rows, int64_t vocab, int64_t logits_stride,
+                                 int64_t dlogits_stride, float inv_temperature, rr_dtype dtype, cudaStream_t stream);
+
+/* Scalars of a policy loss. */
+typedef struct {
+    double clip_low, clip_high;  /* the ratio is clipped to [1 - clip_low, 1 + clip_high]; INFINITY: not */
+    double kl_coef;              /* weight of the KL term */
+    double inv_temperature;
+    double grad_scale;           /* factor of dlogits alone (a loss scale) */
+} rr_policy_hyper;
+
+/*
+ * rr_policy_loss -- the clipped policy loss with a KL term and its gradient, in
+ * one pass over the logits.  For each row, with ratio = exp(logp - old_logp),
+ * A = advantages and w = weights:
+ *   token_loss = w * (-min(ratio * A, clamp(ratio, 1 - clip_low, 1 + clip_high) * A)
+ *                     + kl_coef * (exp(ref_logp - logp) - (ref_logp - logp) - 1))
+ *   loss       = sum of token_loss over the rows,
+ *   dlogits    = grad_scale * d loss / d logits.
+ *
+ * old_logp: NULL takes logp itself (ratio 1, a first step on fresh rollouts; its
+ * gradient is the policy's, -A).  ref_logp: NULL leaves the KL term out.
+ * weights: NULL takes 1 (1 / tokens, or 1 / (sequences * tokens of the sequence),
+ * are usual).  All binary32, one per row.
+ * loss: one binary32, or NULL.  token_loss, logp: one binary32 per row.
+ * dlogits: NULL computes no gradient.  rows == 0 gives loss 0.
+ */
+rr_status rr_policy_loss(const void *logits, const int64_t *targets, const float *old_logp, const float *ref_logp,
+                         const float *advantages, const float *weights, float *loss, float *token_loss, float *logp,
+                         void *dlogits, int64_t rows, int64_t vocab, int64_t logits_stride, int64_t dlogits_stride,
+                         const rr_policy_hyper *hyper, rr_dtype dtype, cudaStream_t stream);
+
+/* Scalars of a preference loss. */
+typedef struct {
+    double beta, label_smoothing, margin, inv_temperature;
+    double grad_scale;  /* factor of dlogits alone (a loss scale) */
+    int average;        /* 1: sequences count by the mean of their rows, not the sum */
+} rr_preference_hyper;
+
+/*
+ * rr_preference_loss -- the preference loss over pairs of a chosen and a rejected
+ * sequence, and its gradient.  The rows of sequence k are
+ * [offsets[k], offsets[k + 1]); sequences 0 .. pairs - 1 are the chosen ones, pairs
+ * .. 2 * pairs - 1 the rejected ones in the same order.  With s[k] the sum (or mean)
+ * of the log-probabilities of a sequence's rows that take part (0 if none does):
+ *   h    = beta * ((s[p] - ref_logp[p]) - (s[pairs + p] - ref_logp[pairs + p])) - margin
+ *   loss = mean over pairs of (1 - label_smoothing) * log(1 + exp(-h))
+ *                             + label_smoothing * log(1 + exp(h)),
+ *   dlogits = grad_scale * d loss / d logits.
+ *
+ * offsets: DEVICE array of 2 * pairs + 1 int64, not decreasing, within [0, rows]
+ * (kept to that range where they are not; results are then unspecified).  Rows
+ * before the first sequence and behind the last are not read, and their logp and
+ * dlogits are left as they were.
+ * ref_logp: binary32, one per sequence, or NULL (zeros).  loss: one binary32.
+ * seq_logp: s, one binary32 per sequence.  logp: one binary32 per row.
+ * dlogits: NULL computes no gradient; otherwise the logits are read twice.
+ * workspace: see rr_preference_loss_workspace.
+ */
+rr_status rr_preference_loss(const void *logits, const int64_t *targets, const int64_t *offsets,
+                             const float *ref_logp, float *loss, float *seq_logp, float *logp, void *dlogits,
+                             int64_t rows, int64_t vocab, int64_t logits_stride, int64_t dlogits_stride, int pairs,
+                             const rr_preference_hyper *hyper, rr_dtype dtype, void *workspace,
+                             size_t workspace_bytes, cudaStream_t stream);
+
+/* Bytes of workspace rr_preference_loss needs for this many rows and pairs. */
+rr_status rr_preference_loss_workspace(int64_t rows, int pairs, size_t *bytes);
+
 /* Name of a status code (static string). */
 const char *rr_status_string(rr_status s);
 
