@@ -58,6 +58,15 @@ class rr_preference_hyper(ctypes.Structure):
                 ("inv_temperature", ctypes.c_double), ("grad_scale", ctypes.c_double), ("average", ctypes.c_int)]
 
 
+RR_MUON_SPECTRAL, RR_MUON_RMS = 0, 1
+
+
+class rr_muon_hyper(ctypes.Structure):
+    """rr_muon_hyper(lr, momentum, weight_decay, eps, nesterov, adjust)."""
+    _fields_ = [("lr", ctypes.c_double), ("momentum", ctypes.c_double), ("weight_decay", ctypes.c_double),
+                ("eps", ctypes.c_double), ("nesterov", ctypes.c_int), ("adjust", ctypes.c_int)]
+
+
 class RRError(RuntimeError):
     def __init__(self, status, message):
         self.status = status
@@ -112,6 +121,9 @@ def lib():
             "rr_policy_loss": [_vp] * 10 + [i64] * 4 + [ctypes.POINTER(rr_policy_hyper), i32, _vp],
             "rr_preference_loss": [_vp] * 8 + [i64] * 4 + [i32, ctypes.POINTER(rr_preference_hyper), i32, _vp,
                                                            ctypes.c_size_t, _vp],
+            "rr_orthogonalize": [_vp] * 4 + [i32] * 3 + [_vp, i32, ctypes.c_double, _vp, ctypes.c_size_t, _vp],
+            "rr_orthogonalize_workspace": [_vp, _vp, i32, ctypes.POINTER(ctypes.c_size_t)],
+            "rr_muon": [_vp] * 6 + [i32] * 3 + [ctypes.POINTER(rr_muon_hyper), _vp, i32, _vp, _vp, ctypes.c_size_t, _vp],
             "rr_preference_loss_workspace": [i64, i32, ctypes.POINTER(ctypes.c_size_t)],
         }
         for name, args in sig.items():
@@ -457,6 +469,49 @@ def rr_preference_loss_workspace(rows, pairs):
     n = ctypes.c_size_t()
     _check(lib().rr_preference_loss_workspace(rows, pairs, ctypes.byref(n)))
     return n.value
+
+
+def _shapes(rows, cols):
+    """rows and cols as host arrays of 64-bit integers."""
+    if len(rows) != len(cols):
+        raise ValueError(f"rows has {len(rows)} entries, cols has {len(cols)}")
+    return array.array("q", rows), array.array("q", cols)
+
+
+def _coefficients(coefs):
+    """A list of (a, b, c), one for each step, as one host array."""
+    if any(len(c) != 3 for c in coefs):
+        raise ValueError("coefs is a list of (a, b, c), one for each step")
+    return array.array("d", [v for c in coefs for v in c])
+
+
+def rr_orthogonalize(x, y, rows, cols, x_dtype, y_dtype, coefs, eps, workspace, workspace_bytes, stream=None):
+    """Newton-Schulz products on a list of matrices; coefs: a list of (a, b, c), one for each step."""
+    l, n, here = lib(), len(rows), _here()
+    (r, c), k = _shapes(rows, cols), _coefficients(coefs)
+    p, q = _pointers(x, here, n, "x"), _pointers(y, here, n, "y")
+    _check(l.rr_orthogonalize(_at(p), _at(q), _at(r), _at(c), n, dtype_code(x_dtype), dtype_code(y_dtype), _at(k),
+                              len(k) // 3, eps, _near(workspace, here), workspace_bytes, stream_handle(stream, here)))
+
+
+def rr_orthogonalize_workspace(rows, cols):
+    """Bytes of workspace for rr_orthogonalize and rr_muon."""
+    r, c = _shapes(rows, cols)
+    n = ctypes.c_size_t()
+    _check(lib().rr_orthogonalize_workspace(_at(r), _at(c), len(r), ctypes.byref(n)))
+    return n.value
+
+
+def rr_muon(params, grads, momentum, master, rows, cols, param_dtype, grad_dtype, hyper, coefs, grad_scale, workspace,
+            workspace_bytes, stream=None):
+    """One Muon step over a list of matrices; master and grad_scale may be None."""
+    l, n, here = lib(), len(rows), _here()
+    (r, c), k = _shapes(rows, cols), _coefficients(coefs)
+    p, g = _pointers(params, here, n, "params"), _pointers(grads, here, n, "grads")
+    m, w = _pointers(momentum, here, n, "momentum"), _pointers(master, here, n, "master")
+    _check(l.rr_muon(_at(p), _at(g), _at(m), _at(w), _at(r), _at(c), n, dtype_code(param_dtype), dtype_code(grad_dtype),
+                     hyper, _at(k), len(k) // 3, _near(grad_scale, here), _near(workspace, here), workspace_bytes,
+                     stream_handle(stream, here)))
 
 
 def bound_call(name, *args):

@@ -1,0 +1,879 @@
+// Orthogonalisation of matrices by Newton-Schulz products and the Muon step
+// (include/rr.h: rr_orthogonalize, rr_muon).
+//
+// With X the matrix or its transpose, whichever has the fewer rows, divided by
+// its Frobenius norm, each iteration is three products on the short side m:
+//   A = X X',  B = a I + b A + c A A,  X <- B X.
+// They run on the tensor cores (tcgen05, accumulators in TMEM) over a list of
+// matrices at once: a launch takes one product of every matrix of the list.
+//
+// Operands are pairs of binary16 pieces, v * scale = hi + lo, 22 bits together,
+// and a product is hi hi + hi lo + lo hi: the iteration amplifies what small
+// singular values are off by some hundred times, so that one bf16 piece (8 bits)
+// leaves 1 to 7 % in the result, one fp16 piece 0.2 to 0.9 %, and the pairs
+// about 1e-6, as binary32 products do.
+//
+// The tensor cores' accumulator drops what lies below its last bit at every
+// instruction of 16 values (measured 4.6e-8 of the sum each, all one way: 1.5e-4
+// after the 18944 of a long row).  So hi hi is summed over kChunk stages only and
+// then added to sums in registers, rounded to nearest; hi lo + lo hi, 2^-11 of it,
+// has an accumulator of its own for the whole depth.
+//
+// Operands live in the workspace in blocks of 128 rows x 64 columns, both pieces
+// one after the other (16 KB each), rows of 128 bytes with their 16-byte pieces
+// permuted as the tensor cores' 128-byte swizzle wants them.  A block comes to
+// shared memory by one plain bulk copy, and the same bytes serve as an operand
+// along either side: rows of K values for X X' and, column by column, K rows for
+// B X.  Sizes are padded with zeros to whole tiles of 128.
+//
+// Times below are of one GB300 (152 SMs, measured 2.01 PFLOP/s bf16).
+#include <algorithm>
+#include <cmath>
+#include <vector>
+
+#include "rr_spans.h"
+#include "rr_step.h"
+
+namespace rr {
+
+namespace {
+
+#define RR_TRY(expr)                  \
+    do {                              \
+        const rr_status st_ = (expr); \
+        if (st_ != RR_OK) return st_; \
+    } while (0)
+
+constexpr int kThreads = 256;     // of the kernels that stream
+constexpr int kTile = 128;        // rows and columns of a block's tile; a pair of blocks has twice both
+constexpr int kK = 64;            // columns of a block of an operand: the depth of a stage
+constexpr int kPiece = kTile * kK * 2;  // bytes of one piece of a block
+constexpr int kBlock = 2 * kPiece;
+constexpr int kStages = 3;
+constexpr int kChunk = 2;         // stages whose hi hi the tensor cores sum
+constexpr int kSumWarps = 8;      // warps that sum chunks and write results
+constexpr int kGemmThreads = 32 * (kSumWarps + 2);  // and one that copies, one that multiplies
+constexpr int kGemmSmem = kStages * 2 * kBlock + 1024;
+constexpr int kSumBlocks = 256;   // most partial sums of a matrix's norm
+constexpr int kCapSmall = 16, kCap = 160;
+constexpr int64_t kMaxSide = (int64_t)1 << 20;
+constexpr int kMaxSteps = 64;
+// Scales of the pieces: X, A and B hold values up to 32 in magnitude, and values
+// of 1e-4 still have all 22 bits.
+constexpr float kScale = 0x1p11f, kUnscale = 0x1p-11f;
+
+enum Kind { kSums, kSplit, kGram, kNext, kKinds };
+enum Stage { kStageGram, kStageSquare, kStageNext, kStageLast };
+
+struct Item {
+    const void *src;   // the matrix, or its gradient
+    float *momentum;   // NULL: no step, the matrix itself is orthogonalised
+    void *out;         // result or parameter
+    float *master;
+    char *x, *y, *a, *b;  // blocked operands; X and its successor swap
+    double *part;
+    int64_t size;
+    int m, n;          // short and long side
+    int mt, nt;        // tiles of them
+    float scale;       // of the step
+    bool tall;         // the matrix has n rows: X is its transpose
+};
+
+template <int CAP>
+struct Args {
+    Item item[CAP];
+    int start[kKinds][CAP + 1];  // first unit of work of each matrix; start[.][count] = all
+    int count;
+    int src_dtype, out_dtype;
+    double eps;
+    float momentum, keep;  // beta; 1 - lr * weight_decay
+    bool nesterov;
+    const float *grad_scale;
+    float ca, cb, cc;      // this iteration's coefficients
+    int stage, swap;       // swap: X is in y
+    __device__ __forceinline__ int find(int kind, int unit) const
+    {
+        int lo = 0, hi = count;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (start[kind][mid] <= unit) lo = mid;
+            else hi = mid;
+        }
+        return lo;
+    }
+};
+
+// ---------------------------------------------------------------- norm and momentum
+// Sum of a block's values in binary64, the same in every thread.
+__device__ __forceinline__ double block_sum(double x, double *s)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = x;
+    __syncthreads();
+    x = 0.0;
+    for (int i = 0; i < kThreads / 32; ++i) x += s[i];
+    return x;
+}
+__host__ __device__ __forceinline__ int sum_blocks(int64_t size)
+{
+    const int64_t n = (size + 16383) / 16384;
+    return (int)(n < kSumBlocks ? n : kSumBlocks);
+}
+__device__ __forceinline__ float update_of(float g, float m, float beta, bool nesterov)
+{
+    return nesterov ? (1.0f - beta) * g + beta * m : m;
+}
+
+// The new momentum, and the sum of squares of what is orthogonalised.  Eight
+// squares are added in binary32; such a sum outside [2^-90, 2^90] (zero aside) is
+// taken again in binary64, and so is the sum of the sums.
+template <int CAP>
+__global__ void __launch_bounds__(kThreads) sums_kernel(const __grid_constant__ Args<CAP> a)
+{
+    stream_order();
+    __shared__ double s[kThreads / 32];
+    const int i = a.find(kSums, blockIdx.x);
+    const Item &it = a.item[i];
+    const int b = blockIdx.x - a.start[kSums][i], blocks = sum_blocks(it.size);
+    const int64_t lo = it.size * b / blocks, hi = it.size * (b + 1) / blocks;
+    const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
+    const bool step = it.momentum != nullptr;
+    if (step && isnan(gs)) return;
+    double sum = 0.0;
+    for (int64_t e = lo + threadIdx.x; e < hi; e += 8 * kThreads) {
+        float v[8];
+        float part = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int64_t k = e + j * kThreads;
+            v[j] = 0.0f;
+            if (k < hi) {
+                v[j] = load_any(it.src, k, a.src_dtype);
+                if (step) {
+                    const float g = v[j] * gs, m = a.momentum * it.momentum[k] + (1.0f - a.momentum) * g;
+                    it.momentum[k] = m;
+                    v[j] = update_of(g, m, a.momentum, a.nesterov);
+                }
+            }
+            part = fmaf(v[j], v[j], part);
+        }
+        if ((part >= 0x1p-90f && part <= 0x1p90f) || part == 0.0f) {
+            // an exact zero may still be squares that vanished
+            bool zero = true;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) zero = zero && v[j] == 0.0f;
+            if (part != 0.0f || zero) {
+                sum += (double)part;
+                continue;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum += (double)v[j] * (double)v[j];
+    }
+    sum = block_sum(sum, s);
+    if (threadIdx.x == 0) it.part[b] = sum;
+}
+
+// ---------------------------------------------------------------- operands
+__device__ __forceinline__ uint32_t pack2(__half lo, __half hi)
+{
+    return (uint32_t)__half_as_ushort(lo) | (uint32_t)__half_as_ushort(hi) << 16;
+}
+// Eight scaled values as two pieces of 16 bytes.
+__device__ __forceinline__ void split8(const float *v, uint4 &hi, uint4 &lo)
+{
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const __half h0 = __float2half_rn(v[2 * k]), h1 = __float2half_rn(v[2 * k + 1]);
+        h[k] = pack2(h0, h1);
+        l[k] = pack2(__float2half_rn(v[2 * k] - __half2float(h0)), __float2half_rn(v[2 * k + 1] - __half2float(h1)));
+    }
+    hi = make_uint4(h[0], h[1], h[2], h[3]);
+    lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+// Where columns [8 c, 8 c + 8) of row r of a block's piece lie.
+__device__ __forceinline__ int chunk_at(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
+
+// X = update / (norm + eps) as pieces, a block of 128 x 64 at a time.
+template <int CAP>
+__global__ void __launch_bounds__(kThreads) split_kernel(const __grid_constant__ Args<CAP> a)
+{
+    stream_order();
+    __shared__ float tile[kTile][kK + 1];
+    __shared__ double s[kThreads / 32];
+    const int i = a.find(kSplit, blockIdx.x);
+    const Item &it = a.item[i];
+    const int u = blockIdx.x - a.start[kSplit][i], nb = it.nt * 2;
+    const int r0 = u / nb * kTile, c0 = u % nb * kK;
+    const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
+    const bool step = it.momentum != nullptr;
+    const int blocks = sum_blocks(it.size);
+    const double total = block_sum((int)threadIdx.x < blocks ? it.part[threadIdx.x] : 0.0, s);
+    const double divisor = sqrt(total) + a.eps;
+    const float by = (float)divisor;
+    const bool plain = by >= 0x1p-100f && by <= 0x1p100f;
+    // neighbouring threads along the matrix's own rows
+    for (int k = threadIdx.x; k < kTile * kK; k += kThreads) {
+        const int r = it.tall ? k % kTile : k / kK, c = it.tall ? k / kTile : k % kK;
+        float v = 0.0f;
+        if (r0 + r < it.m && c0 + c < it.n) {
+            const int64_t at = it.tall ? (int64_t)(c0 + c) * it.m + r0 + r : (int64_t)(r0 + r) * it.n + c0 + c;
+            v = load_any(it.src, at, a.src_dtype);
+            if (step) v = update_of(v * gs, it.momentum[at], a.momentum, a.nesterov);
+            v = plain ? v / by : (float)((double)v / divisor);
+        }
+        tile[r][c] = v * kScale;
+    }
+    __syncthreads();
+    char *block = it.x + (int64_t)u * kBlock;
+    for (int k = threadIdx.x; k < kTile * 8; k += kThreads) {
+        const int r = k >> 3, c = k & 7;
+        uint4 hi, lo;
+        split8(&tile[r][8 * c], hi, lo);
+        *reinterpret_cast<uint4 *>(block + chunk_at(r, c)) = hi;
+        *reinterpret_cast<uint4 *>(block + kPiece + chunk_at(r, c)) = lo;
+    }
+    asm volatile("fence.proxy.async.global;" ::: "memory");  // the products fetch it by bulk copies
+}
+
+// ---------------------------------------------------------------- products
+__device__ __forceinline__ uint32_t smem_u32(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ void mbar_init(uint32_t bar, int count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+// Arrive at the barrier of the pair's first block.
+__device__ __forceinline__ void mbar_arrive_first(uint32_t bar)
+{
+    asm volatile("{\n\t.reg .b32 first;\n\tmapa.shared::cluster.u32 first, %0, 0;\n\t"
+                 "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [first];\n\t}" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_expect(uint32_t bar, int bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool mbar_test(uint32_t bar, int parity)
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
+// Waits end after two seconds: the block then stops, and its tiles become NaN.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, int parity, volatile int *dead)
+{
+    if (mbar_test(bar, parity)) return true;
+    uint64_t t0, t;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t0));
+    for (uint32_t spins = 1; !mbar_test(bar, parity); ++spins) {
+        if ((spins & 63u) == 0) {
+            asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+            if (*dead || t - t0 > 2000000000ull) {
+                *dead = 1;
+                return false;
+            }
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ void bulk_load(uint32_t to, const void *from, int bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to),
+                 "l"(from), "r"(bytes), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void fence_tmem_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_tmem_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// A place in a ring, and the parity of the barrier phase that belongs to it.
+template <int N>
+struct Turn {
+    int at = 0, phase;
+    __device__ __forceinline__ explicit Turn(int first) : phase(first) {}
+    __device__ __forceinline__ void next()
+    {
+        if (++at == N) {
+            at = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+// An operand in shared memory, 128-byte swizzle.  Rows of K values: groups of 8
+// rows lie 1024 bytes apart.  Columns (K rows of 64 values): groups of 8 K rows
+// lie 1024 bytes apart, the next 64 columns 8192.
+__device__ __forceinline__ uint64_t operand(uint32_t at, bool columns)
+{
+    const uint64_t leading = columns ? 8192 >> 4 : 1, stride = 1024 >> 4;
+    return (uint64_t)((at & 0x3FFFF) >> 4) | leading << 16 | stride << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// fp16 operands, binary32 accumulators, 256 x 256 over two blocks; the second
+// operand by columns or by rows.
+__device__ __forceinline__ uint32_t instruction(bool columns)
+{
+    return 1u << 4 | (columns ? 1u << 16 : 0u) | (uint32_t)(2 * kTile >> 3) << 17 | (uint32_t)(2 * kTile >> 4) << 24;
+}
+__device__ __forceinline__ void mma(uint32_t acc, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                 ::"r"(acc), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add) : "memory");
+}
+// Arrives at both blocks' barriers when the products issued so far are done.
+__device__ __forceinline__ void mma_commit(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+                 "h"((uint16_t)3) : "memory");
+}
+// 32 columns of this warp's 32 rows.
+__device__ __forceinline__ void tmem_load(float (&v)[32], uint32_t at)
+{
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(at) : "memory");
+#pragma unroll
+    for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r[k]);
+}
+
+// A pair's tile of a product: which matrix, which rows and columns, how deep.
+struct Job {
+    const Item *it;
+    int ti, tj, depth;
+};
+template <int CAP>
+__device__ __forceinline__ Job job_of(const Args<CAP> &a, int unit)
+{
+    const bool next = a.stage >= kStageNext;
+    const int kind = next ? kNext : kGram, i = a.find(kind, unit);
+    const Item &it = a.item[i];
+    const int u = unit - a.start[kind][i], tiles = (it.mt + 1) / 2;
+    Job j;
+    j.it = &it;
+    if (next) {
+        j.ti = u % tiles;
+        j.tj = u / tiles;
+    } else {  // a symmetric product's tiles on and below the diagonal
+        j.ti = (int)((sqrtf(8.0f * (float)u + 1.0f) - 1.0f) * 0.5f);
+        while (j.ti * (j.ti + 1) / 2 > u) --j.ti;
+        while ((j.ti + 1) * (j.ti + 2) / 2 <= u) ++j.ti;
+        j.tj = u - j.ti * (j.ti + 1) / 2;
+    }
+    j.depth = ((a.stage == kStageGram ? it.n : it.m) + kK - 1) / kK;
+    return j;
+}
+
+// Results of one row of a tile, columns [c0, c0 + 32), to where the stage puts them.
+template <int CAP>
+__device__ __forceinline__ void finish(const Args<CAP> &a, const Item &it, float *v, int rt, int ct, int c0, int r, int wide,
+                                       char *to, bool mirror, bool skip)
+{
+    const int row = rt * kTile + r, chunk0 = c0 % kK / 8;
+    const int64_t block = ((int64_t)rt * wide + ct) * 2 + c0 / kK;
+    if (a.stage == kStageSquare) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const char *from = it.a + block * kBlock + chunk_at(r, chunk0 + q);
+            const Pack<__half, 8> hi = *reinterpret_cast<const Pack<__half, 8> *>(from);
+            const Pack<__half, 8> lo = *reinterpret_cast<const Pack<__half, 8> *>(from + kPiece);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                float &x = v[8 * q + k];
+                x = a.cc * (x * kUnscale) + a.cb * (__half2float(hi.v[k]) + __half2float(lo.v[k]));
+                if (row == ct * kTile + c0 + 8 * q + k) x += a.ca * kScale;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) v[k] *= kUnscale;
+    }
+    if (a.stage != kStageLast) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            uint4 hi, lo;
+            split8(v + 8 * q, hi, lo);
+            char *p = to + block * kBlock + chunk_at(r, chunk0 + q);
+            *reinterpret_cast<uint4 *>(p) = hi;
+            *reinterpret_cast<uint4 *>(p + kPiece) = lo;
+        }
+        if (mirror) {  // the other side of the diagonal: this row is a column there
+            char *p = to + (((int64_t)ct * wide + rt) * 2 + r / kK) * kBlock + r % 8 * 2;
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+                const __half hi = __float2half_rn(v[k]);
+                __half *q = reinterpret_cast<__half *>(p + chunk_at(c0 + k, r % kK / 8));
+                q[0] = hi;
+                q[kPiece / 2] = __float2half_rn(v[k] - __half2float(hi));
+            }
+        }
+    } else if (row < it.m && !(it.momentum && skip)) {
+        const int64_t step = it.tall ? it.m : 1;
+        int64_t at = it.tall ? (int64_t)(ct * kTile + c0) * it.m + row : (int64_t)row * it.n + ct * kTile + c0;
+#pragma unroll
+        for (int k = 0; k < 32; ++k, at += step) {
+            if (ct * kTile + c0 + k < it.n) {
+                float o = v[k] * kUnscale;
+                if (it.momentum) {
+                    const float w = it.master ? it.master[at] : load_any(it.out, at, a.out_dtype);
+                    o = a.keep * w - it.scale * o;
+                    if (it.master) it.master[at] = o;
+                }
+                store_any(it.out, at, a.out_dtype, o);
+            }
+        }
+    }
+}
+
+// Two blocks of a cluster work on a tile of 256 x 256, each on 128 rows of it.
+// Each has its rows of the first operand and half the second one's columns in
+// shared memory; the first block's thread issues the products of both.
+template <int CAP>
+__global__ void __cluster_dims__(2) __launch_bounds__(kGemmThreads, 1) product_kernel(const __grid_constant__ Args<CAP> a)
+{
+    extern __shared__ char raw[];
+    __shared__ alignas(8) uint64_t bars[3 * kStages + 4];
+    __shared__ uint32_t tmem_base;
+    __shared__ int dead_word;
+    volatile int *dead = &dead_word;
+    stream_order();
+    const uint32_t smem = (smem_u32(raw) + 1023) & ~1023u;
+    // full: a stage's copies are here; peer: the second block's are there; empty: the
+    // products have read it; done, free: accumulators of hi hi (0) and the rest (1)
+    const uint32_t full = smem_u32(bars), peer = full + 8 * kStages, empty = peer + 8 * kStages, done = empty + 8 * kStages,
+                   free = done + 16;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t rank;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(full + 8 * s, 1);
+            mbar_init(peer + 8 * s, 1);
+            mbar_init(empty + 8 * s, 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(done + 8 * s, 1);
+            mbar_init(free + 8 * s, 2 * kSumWarps);
+        }
+        dead_word = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kSumWarps + 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base)), "n"(512) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    fence_tmem_before();
+    __syncthreads();
+    cluster_sync();
+    fence_tmem_after();
+    const uint32_t tmem = tmem_base;
+    const bool next = a.stage >= kStageNext;
+    const int units = a.start[next ? kNext : kGram][a.count], first_unit = blockIdx.x / 2, every = gridDim.x / 2;
+
+    if (warp == kSumWarps && lane == 0) {
+        asm volatile("fence.proxy.async.global;" ::: "memory");
+        Turn<kStages> turn(1);
+        bool ok = true;
+        for (int unit = first_unit; unit < units && ok; unit += every) {
+            const Job j = job_of(a, unit);
+            const Item &it = *j.it;
+            const char *x = a.swap ? it.y : it.x, *sq = a.stage == kStageSquare ? it.a : it.b;
+            const int64_t xrow = (int64_t)it.nt * 2 * kBlock, mrow = (int64_t)it.mt * 2 * kBlock;
+            // the last tile may have one half: the other one's place takes what is at hand
+            const int rows = min(j.ti * 2 + (int)rank, it.mt - 1);
+            const int cols = min(j.tj * 2 + (int)rank, (next ? it.nt : it.mt) - 1);
+            const char *left = a.stage == kStageGram ? x + rows * xrow : sq + rows * mrow;
+            const char *right = a.stage == kStageGram ? x + cols * xrow : next ? x + (int64_t)cols * 2 * kBlock : sq + cols * mrow;
+            for (int k = 0; k < j.depth; ++k, turn.next()) {
+                ok = mbar_wait(empty + 8 * turn.at, turn.phase, dead);
+                if (!ok) break;
+                const uint32_t to = smem + turn.at * 2 * kBlock, bar = full + 8 * turn.at;
+                mbar_expect(bar, 2 * kBlock);
+                bulk_load(to, left + (int64_t)k * kBlock, kBlock, bar);
+                if (!next) {
+                    bulk_load(to + kBlock, right + (int64_t)k * kBlock, kBlock, bar);
+                } else {  // 64 of a block's rows are the depth; two blocks side by side, each piece apart
+                    const char *from = right + (k >> 1) * xrow + (k & 1) * (kPiece / 2);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        bulk_load(to + kBlock + q * (kPiece / 2), from + (q & 1) * kBlock + (q >> 1) * kPiece, kPiece / 2, bar);
+                }
+            }
+        }
+        // a block that gave up waits for its copies before its shared memory goes
+        for (int s = 0; s < kStages && !ok; ++s, turn.next()) {
+            volatile int late = 0;
+            mbar_wait(full + 8 * turn.at, turn.phase, &late);
+        }
+    } else if (warp == kSumWarps + 1 && lane == 0 && rank == 1) {
+        // tells the first block what has come here
+        Turn<kStages> turn(0);
+        bool ok = true;
+        for (int unit = first_unit; unit < units && ok; unit += every) {
+            const Job j = job_of(a, unit);
+            for (int k = 0; k < j.depth && ok; ++k, turn.next()) {
+                ok = mbar_wait(full + 8 * turn.at, turn.phase, dead);
+                if (ok) mbar_arrive_first(peer + 8 * turn.at);
+            }
+        }
+    } else if (warp == kSumWarps + 1 && lane == 0) {
+        const uint32_t idesc = instruction(next), sums = tmem, rest = tmem + 2 * kTile;
+        const int step = next ? 2048 : 32;
+        Turn<kStages> turn(0);
+        Turn<1> chunk(1), tile(1);
+        bool ok = true;
+        for (int unit = first_unit; unit < units && ok; unit += every) {
+            const Job j = job_of(a, unit);
+            for (int k = 0; k < j.depth; ++k, turn.next()) {
+                ok = mbar_wait(full + 8 * turn.at, turn.phase, dead) && mbar_wait(peer + 8 * turn.at, turn.phase, dead);
+                const bool begins = k % kChunk == 0;
+                if (ok && begins) {
+                    ok = mbar_wait(free, chunk.phase, dead);
+                    chunk.next();
+                }
+                if (!ok) break;
+                fence_tmem_after();
+                const uint32_t left = smem + turn.at * 2 * kBlock, right = left + kBlock;
+#pragma unroll
+                for (int q = 0; q < kK / 16; ++q)
+                    mma(sums, operand(left + q * 32, false), operand(right + q * step, next), idesc, !begins || q > 0);
+                if (k % kChunk == kChunk - 1 || k == j.depth - 1) mma_commit(done);
+                if (k == 0) {
+                    ok = mbar_wait(free + 8, tile.phase, dead);
+                    tile.next();
+                    if (!ok) break;
+                    fence_tmem_after();
+                }
+#pragma unroll
+                for (int q = 0; q < kK / 16; ++q) {
+                    mma(rest, operand(left + q * 32, false), operand(right + kPiece + q * step, next), idesc, k > 0 || q > 0);
+                    mma(rest, operand(left + kPiece + q * 32, false), operand(right + q * step, next), idesc, true);
+                }
+                mma_commit(empty + 8 * turn.at);
+            }
+            if (ok) mma_commit(done + 8);
+        }
+        // what is in flight reads shared memory: the last stages' releases show its end
+        for (int s = 0; s < kStages; ++s, turn.next()) {
+            volatile int late = 0;
+            mbar_wait(empty + 8 * turn.at, turn.phase ^ 1, &late);
+        }
+    } else if (warp < kSumWarps) {
+        const int half = warp >> 2, r = (warp & 3) * 32 + lane;  // columns of the tile, row of the block
+        const uint32_t mine = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * kTile;
+        const bool skip = a.grad_scale && isnan(*a.grad_scale);
+        Turn<1> chunk(0), tile(0);
+        for (int unit = first_unit; unit < units; unit += every) {
+            const Job j = job_of(a, unit);
+            const Item &it = *j.it;
+            float v[kTile];
+#pragma unroll
+            for (int k = 0; k < kTile; ++k) v[k] = 0.0f;
+            bool ok = true;
+            for (int k = 0; k <= j.depth; k += k + kChunk > j.depth && k < j.depth ? j.depth - k : kChunk) {
+                // chunks of hi hi, then the rest
+                const bool last = k == j.depth;
+                ok = mbar_wait(done + (last ? 8 : 0), last ? tile.phase : chunk.phase, dead) && ok;
+                if (last) tile.next();
+                else chunk.next();
+                fence_tmem_after();
+                __syncwarp();
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float t[32];
+                    tmem_load(t, mine + (last ? 2 * kTile : 0) + q * 32);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[q * 32 + e] += t[e];
+                }
+                fence_tmem_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_first(free + (last ? 8 : 0));
+            }
+            if (!ok) {
+#pragma unroll
+                for (int k = 0; k < kTile; ++k) v[k] = __int_as_float(0x7fc00000);
+            }
+            const int rt = j.ti * 2 + (int)rank, ct = j.tj * 2 + half, wide = next ? it.nt : it.mt;
+            if (rt >= it.mt || ct >= wide) continue;
+            char *to = a.stage == kStageGram ? it.a : a.stage == kStageSquare ? it.b : a.swap ? it.x : it.y;
+            // 32 columns at a time, each done with before the next one's addresses are formed
+#pragma unroll
+            for (int g = 0; g < kTile / 32; ++g) {
+                asm volatile("" ::: "memory");
+                finish(a, it, v + 32 * g, rt, ct, 32 * g, r, wide, to, !next && j.ti != j.tj, skip);
+            }
+        }
+        asm volatile("fence.proxy.async.global;" ::: "memory");  // the next product fetches it by bulk copies
+    }
+    __syncwarp();
+    fence_tmem_before();
+    __syncthreads();
+    cluster_sync();  // neither block's shared memory or barriers go before the other is done
+    if (warp == kSumWarps + 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512) : "memory");
+}
+
+// ---------------------------------------------------------------- host side
+struct Sizes {
+    int m, n, mt, nt;
+    int64_t x, sq, part;  // bytes of X, of a square, of the partial sums
+    int64_t all() const { return 2 * x + 2 * sq + part; }
+};
+Sizes sizes_of(int64_t rows, int64_t cols)
+{
+    Sizes s;
+    s.m = (int)std::min(rows, cols);
+    s.n = (int)std::max(rows, cols);
+    s.mt = (s.m + kTile - 1) / kTile;
+    s.nt = (s.n + kTile - 1) / kTile;
+    s.x = (int64_t)s.mt * s.nt * 2 * kBlock;
+    s.sq = (int64_t)s.mt * s.mt * 2 * kBlock;
+    s.part = kSumBlocks * 8;
+    return s;
+}
+
+rr_status check_shapes(const int64_t *rows, const int64_t *cols, int count)
+{
+    if (count < 0) return step_fail(RR_ERR_INVALID_ARG, "num_tensors %d", count);
+    if (count > 0 && (!rows || !cols)) return step_fail(RR_ERR_INVALID_ARG, "%s is NULL", rows ? "cols" : "rows");
+    for (int i = 0; i < count; ++i) {
+        if (rows[i] < 0 || rows[i] > kMaxSide) return step_fail(RR_ERR_INVALID_ARG, "rows[%d] is %lld", i, (long long)rows[i]);
+        if (cols[i] < 0 || cols[i] > kMaxSide) return step_fail(RR_ERR_INVALID_ARG, "cols[%d] is %lld", i, (long long)cols[i]);
+    }
+    return RR_OK;
+}
+rr_status check_pointers(const char *name, const void *const *p, const int64_t *rows, const int64_t *cols, int count,
+                         int bytes)
+{
+    if (count > 0 && !p) return step_fail(RR_ERR_INVALID_ARG, "%s is NULL", name);
+    for (int i = 0; i < count; ++i) {
+        if (rows[i] * cols[i] == 0) continue;
+        if (!p[i]) return step_fail(RR_ERR_INVALID_ARG, "%s[%d] is NULL", name, i);
+        if (!aligned_to(p[i], bytes))
+            return step_fail(RR_ERR_ALIGNMENT, "%s[%d] not aligned to its %d-byte element", name, i, bytes);
+    }
+    return RR_OK;
+}
+rr_status check_iteration(const double *coefs, int steps, double eps)
+{
+    if (steps < 0 || steps > kMaxSteps) return step_fail(RR_ERR_INVALID_ARG, "steps %d", steps);
+    if (steps == 0) return step_fail(RR_ERR_INVALID_ARG, "steps 0: there is nothing to iterate");
+    if (!coefs) return step_fail(RR_ERR_INVALID_ARG, "coefs is NULL");
+    for (int i = 0; i < 3 * steps; ++i)
+        if (!(std::fabs(coefs[i]) <= 1e6)) return step_fail(RR_ERR_INVALID_ARG, "coefs[%d] is %g", i, coefs[i]);
+    if (!(eps >= 0.0 && std::isfinite(eps))) return step_fail(RR_ERR_INVALID_ARG, "eps %g", eps);
+    return RR_OK;
+}
+rr_status check_workspace(const int64_t *rows, const int64_t *cols, int count, const void *workspace, size_t bytes,
+                          size_t *need)
+{
+    RR_TRY(rr_orthogonalize_workspace(rows, cols, count, need));
+    if (*need == 0) return RR_OK;
+    if (!workspace) return step_fail(RR_ERR_INVALID_ARG, "workspace is NULL");
+    if (!aligned_to(workspace, 16)) return step_fail(RR_ERR_ALIGNMENT, "workspace not 16-byte aligned");
+    if (bytes < *need) return step_fail(RR_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", bytes, *need);
+    return RR_OK;
+}
+
+// What both entries hand over, checked.
+struct Call {
+    const void *const *src;
+    void *const *out;
+    float *const *momentum;  // NULL: no step
+    float *const *master;
+    const int64_t *rows, *cols;
+    int count;
+    rr_dtype src_dtype, out_dtype;
+    const double *coefs;
+    int steps;
+    double eps;
+    const rr_muon_hyper *hyper;
+    const float *grad_scale;
+    char *workspace;
+};
+
+template <int CAP>
+rr_status run_lists(const Call &c, int sms, cudaStream_t stream)
+{
+    Args<CAP> a;
+    a.src_dtype = (int)c.src_dtype;
+    a.out_dtype = (int)c.out_dtype;
+    a.eps = c.eps;
+    a.momentum = c.hyper ? (float)c.hyper->momentum : 0.0f;
+    a.keep = c.hyper ? (float)(1.0 - c.hyper->lr * c.hyper->weight_decay) : 0.0f;
+    a.nesterov = c.hyper && c.hyper->nesterov;
+    a.grad_scale = c.grad_scale;
+    a.stage = a.swap = 0;
+    a.ca = a.cb = a.cc = 0.0f;
+    char *at = c.workspace;
+    int fit = 0;
+    const void *product = (const void *)product_kernel<CAP>;
+    RR_TRY(step_fit(product, kGemmThreads, kGemmSmem, &fit));
+    for (int i = 0; i < c.count;) {
+        int k = 0;
+        for (int q = 0; q < kKinds; ++q) a.start[q][0] = 0;
+        for (; i < c.count && k < CAP; ++i) {
+            if (c.rows[i] * c.cols[i] == 0) continue;
+            const Sizes s = sizes_of(c.rows[i], c.cols[i]);
+            Item &it = a.item[k];
+            it.src = c.src[i];
+            it.out = c.out[i];
+            it.momentum = c.momentum ? c.momentum[i] : nullptr;
+            it.master = c.master ? c.master[i] : nullptr;
+            it.x = at;
+            it.y = it.x + s.x;
+            it.a = it.y + s.x;
+            it.b = it.a + s.sq;
+            it.part = reinterpret_cast<double *>(it.b + s.sq);
+            at += s.all();
+            it.size = c.rows[i] * c.cols[i];
+            it.m = s.m;
+            it.n = s.n;
+            it.mt = s.mt;
+            it.nt = s.nt;
+            it.tall = c.rows[i] > c.cols[i];
+            it.scale = 0.0f;
+            if (c.hyper) {
+                const double r = (double)c.rows[i], l = (double)c.cols[i];
+                it.scale = (float)(c.hyper->lr * (c.hyper->adjust == RR_MUON_RMS ? 0.2 * std::sqrt(std::max(r, l))
+                                                                                 : std::sqrt(std::max(1.0, r / l))));
+            }
+            const int64_t mp = (s.mt + 1) / 2, np = (s.nt + 1) / 2;  // pairs' tiles
+            const int64_t units[kKinds] = {sum_blocks(it.size), (int64_t)s.mt * s.nt * 2, mp * (mp + 1) / 2, mp * np};
+            for (int q = 0; q < kKinds; ++q) {
+                if (a.start[q][k] + units[q] > INT32_MAX)
+                    return step_fail(RR_ERR_INVALID_ARG, "the list's matrices are too large for one call");
+                a.start[q][k + 1] = (int)(a.start[q][k] + units[q]);
+            }
+            ++k;
+        }
+        if (k == 0) break;
+        a.count = k;
+        RR_TRY(step_launch((const void *)sums_kernel<CAP>, a.start[kSums][k], kThreads, 0, &a, stream));
+        RR_TRY(step_launch((const void *)split_kernel<CAP>, a.start[kSplit][k], kThreads, 0, &a, stream));
+        for (int step = 0; step < c.steps; ++step) {
+            a.ca = (float)c.coefs[3 * step];
+            a.cb = (float)c.coefs[3 * step + 1];
+            a.cc = (float)c.coefs[3 * step + 2];
+            a.swap = step & 1;
+            for (int q = 0; q < 3; ++q) {
+                a.stage = q < 2 ? q : step + 1 < c.steps ? kStageNext : kStageLast;
+                const int64_t units = a.start[q < 2 ? kGram : kNext][k];
+                RR_TRY(step_launch(product, 2 * std::min<int64_t>(units, sms / 2), kGemmThreads, kGemmSmem, &a, stream));
+            }
+        }
+    }
+    return RR_OK;
+}
+
+rr_status run(const Call &c, cudaStream_t stream)
+{
+    int sms = 0;
+    RR_TRY(step_sms(&sms));
+    return c.count <= kCapSmall ? run_lists<kCapSmall>(c, sms, stream) : run_lists<kCap>(c, sms, stream);
+}
+
+template <class T>
+const void *const *plain(T *const *p) { return reinterpret_cast<const void *const *>(p); }
+
+}  // namespace
+
+}  // namespace rr
+
+using namespace rr;
+
+extern "C" rr_status rr_orthogonalize_workspace(const int64_t *rows, const int64_t *cols, int num_tensors, size_t *bytes)
+{
+    if (!bytes) return step_fail(RR_ERR_INVALID_ARG, "bytes is NULL");
+    RR_TRY(check_shapes(rows, cols, num_tensors));
+    int64_t sum = 0;
+    for (int i = 0; i < num_tensors; ++i)
+        if (rows[i] * cols[i] > 0 && __builtin_add_overflow(sum, sizes_of(rows[i], cols[i]).all(), &sum))
+            return step_fail(RR_ERR_INVALID_ARG, "the list's matrices are too large for one call");
+    *bytes = (size_t)sum;
+    return step_ok();
+}
+
+extern "C" rr_status rr_orthogonalize(const void *const *x, void *const *y, const int64_t *rows, const int64_t *cols,
+                                      int num_tensors, rr_dtype x_dtype, rr_dtype y_dtype, const double *coefs, int steps,
+                                      double eps, void *workspace, size_t workspace_bytes, cudaStream_t stream)
+try {
+    if (!float_bytes(x_dtype)) return step_fail(RR_ERR_UNSUPPORTED_DTYPE, "x_dtype %d", (int)x_dtype);
+    if (!float_bytes(y_dtype)) return step_fail(RR_ERR_UNSUPPORTED_DTYPE, "y_dtype %d", (int)y_dtype);
+    RR_TRY(check_shapes(rows, cols, num_tensors));
+    RR_TRY(check_iteration(coefs, steps, eps));
+    const int xb = float_bytes(x_dtype), yb = float_bytes(y_dtype);
+    RR_TRY(check_pointers("x", x, rows, cols, num_tensors, xb));
+    RR_TRY(check_pointers("y", plain(y), rows, cols, num_tensors, yb));
+    size_t need = 0;
+    RR_TRY(check_workspace(rows, cols, num_tensors, workspace, workspace_bytes, &need));
+    static thread_local Spans spans;
+    spans.all.clear();
+    // y[i] == x[i] of one type works in place: the matrix has been read before the result is written
+    for (int i = 0; i < num_tensors; ++i)
+        if (!(x[i] == y[i] && x_dtype == y_dtype)) spans.add(x[i], rows[i] * cols[i] * xb, false);
+    for (int i = 0; i < num_tensors; ++i) spans.add(y[i], rows[i] * cols[i] * yb, true);
+    spans.add(workspace, (int64_t)need, true);
+    if (spans.touch()) return step_fail(RR_ERR_ALIAS, "a result or the workspace overlaps another argument");
+    if (need == 0) return step_ok();
+    const Call c{x, y, nullptr, nullptr, rows, cols, num_tensors, x_dtype, y_dtype, coefs, steps, eps, nullptr, nullptr,
+                 static_cast<char *>(workspace)};
+    RR_TRY(run(c, stream));
+    return step_ok();
+} catch (...) {
+    return step_no_memory();
+}
+
+extern "C" rr_status rr_muon(void *const *params, const void *const *grads, float *const *momentum, float *const *master,
+                             const int64_t *rows, const int64_t *cols, int num_tensors, rr_dtype param_dtype,
+                             rr_dtype grad_dtype, const rr_muon_hyper *hyper, const double *coefs, int steps,
+                             const float *grad_scale, void *workspace, size_t workspace_bytes, cudaStream_t stream)
+try {
+    if (!float_bytes(param_dtype)) return step_fail(RR_ERR_UNSUPPORTED_DTYPE, "param_dtype %d", (int)param_dtype);
+    if (!float_bytes(grad_dtype)) return step_fail(RR_ERR_UNSUPPORTED_DTYPE, "grad_dtype %d", (int)grad_dtype);
+    RR_TRY(check_shapes(rows, cols, num_tensors));
+    if (!hyper) return step_fail(RR_ERR_INVALID_ARG, "hyper is NULL");
+    if (!(hyper->lr >= 0.0 && std::isfinite(hyper->lr))) return step_fail(RR_ERR_INVALID_ARG, "lr %g", hyper->lr);
+    if (!(hyper->momentum >= 0.0 && hyper->momentum < 1.0)) return step_fail(RR_ERR_INVALID_ARG, "momentum %g", hyper->momentum);
+    if (!(hyper->weight_decay >= 0.0 && std::isfinite(hyper->weight_decay)))
+        return step_fail(RR_ERR_INVALID_ARG, "weight_decay %g", hyper->weight_decay);
+    if (hyper->adjust != RR_MUON_SPECTRAL && hyper->adjust != RR_MUON_RMS)
+        return step_fail(RR_ERR_INVALID_ARG, "adjust %d", hyper->adjust);
+    RR_TRY(check_iteration(coefs, steps, hyper->eps));
+    const int pb = float_bytes(param_dtype), gb = float_bytes(grad_dtype);
+    RR_TRY(check_pointers("params", plain(params), rows, cols, num_tensors, pb));
+    RR_TRY(check_pointers("grads", grads, rows, cols, num_tensors, gb));
+    RR_TRY(check_pointers("momentum", plain(momentum), rows, cols, num_tensors, 4));
+    if (master) RR_TRY(check_pointers("master", plain(master), rows, cols, num_tensors, 4));
+    if (!aligned_to(grad_scale, 4)) return step_fail(RR_ERR_ALIGNMENT, "grad_scale not 4-byte aligned");
+    size_t need = 0;
+    RR_TRY(check_workspace(rows, cols, num_tensors, workspace, workspace_bytes, &need));
+    static thread_local Spans spans;
+    spans.all.clear();
+    for (int i = 0; i < num_tensors; ++i) spans.add(params[i], rows[i] * cols[i] * pb, true);
+    for (int i = 0; i < num_tensors; ++i) spans.add(grads[i], rows[i] * cols[i] * gb, false);
+    for (int i = 0; i < num_tensors; ++i) spans.add(momentum[i], rows[i] * cols[i] * 4, true);
+    for (int i = 0; master && i < num_tensors; ++i) spans.add(master[i], rows[i] * cols[i] * 4, true);
+    spans.add(grad_scale, 4, false);
+    spans.add(workspace, (int64_t)need, true);
+    if (spans.touch()) return step_fail(RR_ERR_ALIAS, "a parameter, state, master weight or the workspace overlaps another argument");
+    if (need == 0) return step_ok();
+    const Call c{grads, params, momentum, master, rows, cols, num_tensors, grad_dtype, param_dtype, coefs, steps,
+                 hyper->eps, hyper, grad_scale, static_cast<char *>(workspace)};
+    RR_TRY(run(c, stream));
+    return step_ok();
+} catch (...) {
+    return step_no_memory();
+}

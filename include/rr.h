@@ -563,6 +563,69 @@ rr_status rr_adamw8(void *const *params, const void *const *grads, uint8_t *cons
                     rr_dtype grad_dtype, const rr_adamw_hyper *hyper, uint32_t seed,
                     const float *grad_scale, cudaStream_t stream);
 
+/*
+ * rr_orthogonalize -- the nearest thing to an orthogonal matrix that a few
+ * Newton-Schulz products make of each matrix of a list.  With X = x / (norm(x)
+ * + eps), norm the Frobenius norm, and (a, b, c) the coefficients of a step, each
+ * of `steps` steps is
+ *   A = X X',  X = (a I + b A + c A A) X
+ * (on x's transpose where x has more rows than columns, which is the same), and
+ * y = X.  It moves the singular values toward 1 and leaves the vectors; five steps
+ * of (3.4445, -4.7750, 2.0315) leave them within about 0.3 of it.
+ *
+ * Products take their operands as pairs of binary16 values with 22 bits together
+ * and sum in binary32.  Magnitudes in X, A and the polynomial have to stay below
+ * 32 (a norm of 1 and coefficients that do not diverge keep them near 1); what
+ * leaves that range becomes infinite or NaN.  NaN and infinities in x make y NaN.
+ *
+ * x, y: HOST arrays of num_tensors (>= 0) device pointers to dense row-major
+ * matrices of rows[i] x cols[i] elements, of x_dtype and y_dtype; sides up to
+ * 2^20, empty matrices (and NULL for them) allowed.  y[i] == x[i] of one type
+ * works in place; nothing else written may overlap anything (RR_ERR_ALIAS).
+ * coefs: HOST array of 3 * steps coefficients, 1 <= steps <= 64.
+ * workspace: see rr_orthogonalize_workspace; about 8 bytes an element and 8 more
+ * for each of the short side squared.
+ * A call is 2 + 3 * steps launches for each 160 matrices.
+ */
+rr_status rr_orthogonalize(const void *const *x, void *const *y, const int64_t *rows, const int64_t *cols,
+                           int num_tensors, rr_dtype x_dtype, rr_dtype y_dtype, const double *coefs, int steps,
+                           double eps, void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Bytes of workspace rr_orthogonalize and rr_muon need for a list of these shapes. */
+rr_status rr_orthogonalize_workspace(const int64_t *rows, const int64_t *cols, int num_tensors, size_t *bytes);
+
+#define RR_MUON_SPECTRAL 0 /* steps of lr * sqrt(max(1, rows / cols)) */
+#define RR_MUON_RMS 1      /* steps of lr * 0.2 * sqrt(max(rows, cols)), of AdamW's size */
+
+/* Scalars of a Muon step. */
+typedef struct {
+    double lr, momentum, weight_decay, eps;
+    int nesterov, adjust;
+} rr_muon_hyper;
+
+/*
+ * rr_muon -- one Muon step over a list of matrices, in place: momentum, whose
+ * average is orthogonalised and subtracted from the weights.  For each matrix,
+ * with g = grad * (*grad_scale) (or grad where grad_scale is NULL) and w the master
+ * weight if there is one, else the parameter:
+ *   m = momentum * m + (1 - momentum) * g
+ *   u = nesterov ? (1 - momentum) * g + momentum * m : m
+ *   o = u orthogonalised as rr_orthogonalize does with eps and coefs
+ *   w = (1 - lr * weight_decay) * w - lr * adjust(rows, cols) * o
+ * and param = w rounded once to param_dtype.
+ *
+ * grad_scale: device binary32 word (rr_grad_norm's scale), or NULL.  When it
+ * holds NaN the step is skipped: no parameter or state is written.
+ * params, grads, momentum, master: HOST arrays of device pointers to dense
+ * row-major matrices; momentum and master binary32, master NULL for none.  Nothing
+ * written may overlap anything else (RR_ERR_ALIAS).  coefs, steps and workspace as
+ * rr_orthogonalize.
+ */
+rr_status rr_muon(void *const *params, const void *const *grads, float *const *momentum, float *const *master,
+                  const int64_t *rows, const int64_t *cols, int num_tensors, rr_dtype param_dtype, rr_dtype grad_dtype,
+                  const rr_muon_hyper *hyper, const double *coefs, int steps, const float *grad_scale, void *workspace,
+                  size_t workspace_bytes, cudaStream_t stream);
+
 /* ------------------------------------------------------------------------
  * Losses over a language model's logits.  They are training-step operators and
  * keep the conventions above (no pad, no allocation, no atomics, capturable,
