@@ -15,9 +15,9 @@
 //
 // The tensor cores' accumulator drops what lies below its last bit at every
 // instruction of 16 values (measured 4.6e-8 of the sum each, all one way: 1.5e-4
-// after the 18944 of a long row).  So hi hi is summed over kChunk stages only and
-// then added to sums in registers, rounded to nearest; hi lo + lo hi, 2^-11 of it,
-// has an accumulator of its own for the whole depth.
+// after the 18944 of a long row).  So it sums 64 values only, the small products
+// first, and is then added to sums in registers, rounded to nearest, while the next
+// 64 go to a second accumulator.
 //
 // Operands live in the workspace in blocks of 128 rows x 64 columns, both pieces
 // one after the other (16 KB each), rows of 128 bytes with their 16-byte pieces
@@ -50,8 +50,7 @@ constexpr int kK = 64;            // columns of a block of an operand: the depth
 constexpr int kPiece = kTile * kK * 2;  // bytes of one piece of a block
 constexpr int kBlock = 2 * kPiece;
 constexpr int kStages = 3;
-constexpr int kChunk = 2;         // stages whose hi hi the tensor cores sum
-constexpr int kSumWarps = 8;      // warps that sum chunks and write results
+constexpr int kSumWarps = 8;      // warps that sum the stages' products and write results
 constexpr int kGemmThreads = 32 * (kSumWarps + 2);  // and one that copies, one that multiplies
 constexpr int kGemmSmem = kStages * 2 * kBlock + 1024;
 constexpr int kSumBlocks = 256;   // most partial sums of a matrix's norm
@@ -245,11 +244,13 @@ __device__ __forceinline__ void mbar_init(uint32_t bar, int count)
 {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
-// Arrive at the barrier of the pair's first block.
+// Arrive at the barrier of the pair's first block.  Nothing but accumulators and
+// bulk copies is ordered by it, so it takes no wider scope (a release to the
+// cluster waits for the thread's stores: 1.2 times the time of a product).
 __device__ __forceinline__ void mbar_arrive_first(uint32_t bar)
 {
     asm volatile("{\n\t.reg .b32 first;\n\tmapa.shared::cluster.u32 first, %0, 0;\n\t"
-                 "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [first];\n\t}" ::"r"(bar) : "memory");
+                 "mbarrier.arrive.shared::cluster.b64 _, [first];\n\t}" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void mbar_expect(uint32_t bar, int bytes)
 {
@@ -258,7 +259,7 @@ __device__ __forceinline__ void mbar_expect(uint32_t bar, int bytes)
 __device__ __forceinline__ bool mbar_test(uint32_t bar, int parity)
 {
     uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
                  "selp.u32 %0, 1, 0, p;\n\t}"
                  : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0;
@@ -332,22 +333,19 @@ __device__ __forceinline__ void mma_commit(uint32_t bar)
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
                  "h"((uint16_t)3) : "memory");
 }
-// 32 columns of this warp's 32 rows.
-__device__ __forceinline__ void tmem_load(float (&v)[32], uint32_t at)
+// 16 columns of this warp's 32 rows.
+__device__ __forceinline__ void tmem_load(float (&v)[16], uint32_t at)
 {
-    uint32_t r[32];
+    uint32_t r[16];
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(at) : "memory");
 #pragma unroll
-    for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r[k]);
+    for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(r[k]);
 }
 
 // A pair's tile of a product: which matrix, which rows and columns, how deep.
@@ -452,7 +450,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kGemmThreads, 1) product_k
     stream_order();
     const uint32_t smem = (smem_u32(raw) + 1023) & ~1023u;
     // full: a stage's copies are here; peer: the second block's are there; empty: the
-    // products have read it; done, free: accumulators of hi hi (0) and the rest (1)
+    // products have read it; done, free: an accumulator's products are complete, have been added up
     const uint32_t full = smem_u32(bars), peer = full + 8 * kStages, empty = peer + 8 * kStages, done = empty + 8 * kStages,
                    free = done + 16;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -530,41 +528,30 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kGemmThreads, 1) product_k
             }
         }
     } else if (warp == kSumWarps + 1 && lane == 0) {
-        const uint32_t idesc = instruction(next), sums = tmem, rest = tmem + 2 * kTile;
+        const uint32_t idesc = instruction(next);
         const int step = next ? 2048 : 32;
         Turn<kStages> turn(0);
-        Turn<1> chunk(1), tile(1);
+        Turn<2> acc(1);
         bool ok = true;
         for (int unit = first_unit; unit < units && ok; unit += every) {
             const Job j = job_of(a, unit);
-            for (int k = 0; k < j.depth; ++k, turn.next()) {
-                ok = mbar_wait(full + 8 * turn.at, turn.phase, dead) && mbar_wait(peer + 8 * turn.at, turn.phase, dead);
-                const bool begins = k % kChunk == 0;
-                if (ok && begins) {
-                    ok = mbar_wait(free, chunk.phase, dead);
-                    chunk.next();
-                }
+            for (int k = 0; k < j.depth; ++k, turn.next(), acc.next()) {
+                ok = mbar_wait(free + 8 * acc.at, acc.phase, dead) && mbar_wait(full + 8 * turn.at, turn.phase, dead) &&
+                     mbar_wait(peer + 8 * turn.at, turn.phase, dead);
                 if (!ok) break;
                 fence_tmem_after();
-                const uint32_t left = smem + turn.at * 2 * kBlock, right = left + kBlock;
-#pragma unroll
-                for (int q = 0; q < kK / 16; ++q)
-                    mma(sums, operand(left + q * 32, false), operand(right + q * step, next), idesc, !begins || q > 0);
-                if (k % kChunk == kChunk - 1 || k == j.depth - 1) mma_commit(done);
-                if (k == 0) {
-                    ok = mbar_wait(free + 8, tile.phase, dead);
-                    tile.next();
-                    if (!ok) break;
-                    fence_tmem_after();
-                }
+                const uint32_t left = smem + turn.at * 2 * kBlock, right = left + kBlock, sums = tmem + acc.at * 2 * kTile;
 #pragma unroll
                 for (int q = 0; q < kK / 16; ++q) {
-                    mma(rest, operand(left + q * 32, false), operand(right + kPiece + q * step, next), idesc, k > 0 || q > 0);
-                    mma(rest, operand(left + kPiece + q * 32, false), operand(right + q * step, next), idesc, true);
+                    mma(sums, operand(left + q * 32, false), operand(right + kPiece + q * step, next), idesc, q > 0);
+                    mma(sums, operand(left + kPiece + q * 32, false), operand(right + q * step, next), idesc, true);
                 }
+#pragma unroll
+                for (int q = 0; q < kK / 16; ++q)
+                    mma(sums, operand(left + q * 32, false), operand(right + q * step, next), idesc, true);
                 mma_commit(empty + 8 * turn.at);
+                mma_commit(done + 8 * acc.at);
             }
-            if (ok) mma_commit(done + 8);
         }
         // what is in flight reads shared memory: the last stages' releases show its end
         for (int s = 0; s < kStages; ++s, turn.next()) {
@@ -575,37 +562,33 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kGemmThreads, 1) product_k
         const int half = warp >> 2, r = (warp & 3) * 32 + lane;  // columns of the tile, row of the block
         const uint32_t mine = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * kTile;
         const bool skip = a.grad_scale && isnan(*a.grad_scale);
-        Turn<1> chunk(0), tile(0);
+        Turn<2> acc(0);
         for (int unit = first_unit; unit < units; unit += every) {
-            const Job j = job_of(a, unit);
-            const Item &it = *j.it;
             float v[kTile];
 #pragma unroll
             for (int k = 0; k < kTile; ++k) v[k] = 0.0f;
             bool ok = true;
-            for (int k = 0; k <= j.depth; k += k + kChunk > j.depth && k < j.depth ? j.depth - k : kChunk) {
-                // chunks of hi hi, then the rest
-                const bool last = k == j.depth;
-                ok = mbar_wait(done + (last ? 8 : 0), last ? tile.phase : chunk.phase, dead) && ok;
-                if (last) tile.next();
-                else chunk.next();
+            for (int k = job_of(a, unit).depth; k > 0; --k, acc.next()) {
+                ok = mbar_wait(done + 8 * acc.at, acc.phase, dead) && ok;
                 fence_tmem_after();
                 __syncwarp();
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    float t[32];
-                    tmem_load(t, mine + (last ? 2 * kTile : 0) + q * 32);
+                for (int q = 0; q < kTile / 16; ++q) {
+                    float t[16];
+                    tmem_load(t, mine + acc.at * 2 * kTile + q * 16);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) v[q * 32 + e] += t[e];
+                    for (int e = 0; e < 16; ++e) v[q * 16 + e] += t[e];
                 }
                 fence_tmem_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_first(free + (last ? 8 : 0));
+                if (lane == 0) mbar_arrive_first(free + 8 * acc.at);
             }
             if (!ok) {
 #pragma unroll
                 for (int k = 0; k < kTile; ++k) v[k] = __int_as_float(0x7fc00000);
             }
+            const Job j = job_of(a, unit);
+            const Item &it = *j.it;
             const int rt = j.ti * 2 + (int)rank, ct = j.tj * 2 + half, wide = next ? it.nt : it.mt;
             if (rt >= it.mt || ct >= wide) continue;
             char *to = a.stage == kStageGram ? it.a : a.stage == kStageSquare ? it.b : a.swap ? it.x : it.y;
