@@ -29,6 +29,7 @@
 // Times below are of one GB300 (152 SMs, measured 2.01 PFLOP/s bf16).
 #include <algorithm>
 #include <cmath>
+#include <mutex>
 #include <vector>
 
 #include "rr_spans.h"
@@ -51,8 +52,16 @@ constexpr int kPiece = kTile * kK * 2;  // bytes of one piece of a block
 constexpr int kBlock = 2 * kPiece;
 constexpr int kStages = 3;
 constexpr int kSumWarps = 8;      // warps that sum the stages' products and write results
-constexpr int kGemmThreads = 32 * (kSumWarps + 2);  // and one that copies, one that multiplies
-constexpr int kGemmSmem = kStages * 2 * kBlock + 1024;
+constexpr int kGemmThreads = 32 * (kSumWarps + 4);  // and one that copies, one that multiplies, two idle
+// Registers of a summing warp's threads and of the others': the launch has 168 each.
+// (128 sums and 16 values on their way do not fit 168 with what else a thread holds:
+// they spilled, and a stage's sums took 2500 cycles where the products take 1536.)
+constexpr int kSumRegisters = 216, kOtherRegisters = 72;
+static_assert(kSumWarps * kSumRegisters + 4 * kOtherRegisters <= (kSumWarps + 4) * 168, "more than the launch has");
+constexpr int kDesk = 32 * 128;   // bytes of a summing warp's own: 32 rows of a piece, or 32 x 32 results
+// Shared memory: the stages, the warps' desks, the barriers; 1024 to start on a swizzle's boundary.
+constexpr int kDesks = kStages * 2 * kBlock, kBarriers = kDesks + kSumWarps * kDesk;
+constexpr int kGemmSmem = kBarriers + 256 + 1024;
 constexpr int kSumBlocks = 256;   // most partial sums of a matrix's norm
 constexpr int kCapSmall = 16, kCap = 160;
 constexpr int64_t kMaxSide = (int64_t)1 << 20;
@@ -375,64 +384,178 @@ __device__ __forceinline__ Job job_of(const Args<CAP> &a, int unit)
     return j;
 }
 
-// Results of one row of a tile, columns [c0, c0 + 32), to where the stage puts them.
-template <int CAP>
-__device__ __forceinline__ void finish(const Args<CAP> &a, const Item &it, float *v, int rt, int ct, int c0, int r, int wide,
-                                       char *to, bool mirror, bool skip)
+// ---------------------------------------------------------------- a tile's results
+// A warp holds 32 rows x 128 columns of a tile, a row to a lane.  Lines of memory
+// hold a row's 64 values of a piece, so lanes that went to memory each for itself
+// would touch 32 lines at a time (17 to 25 thousand cycles a tile, and 100 thousand
+// for the row-major results).  They pass through the warp's desk instead, where
+// the swizzle keeps every access free of conflicts.
+__device__ __forceinline__ void bulk_store(void *to, uint32_t from, int bytes)
 {
-    const int row = rt * kTile + r, chunk0 = c0 % kK / 8;
-    const int64_t block = ((int64_t)rt * wide + ct) * 2 + c0 / kK;
-    if (a.stage == kStageSquare) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\tcp.async.bulk.commit_group;" ::"l"(to),
+                 "r"(from), "r"(bytes) : "memory");
+}
+// The desk's last bulk store has read it.
+__device__ __forceinline__ void desk_ready(int lane)
+{
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();
+}
+__device__ __forceinline__ uint32_t halves(float x, float y)
+{
+    const __half2 h = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ float2 floats(uint32_t h) { return __half22float2(*reinterpret_cast<const __half2 *>(&h)); }
+
+// v += by * what 32 rows of a block hold: both pieces of columns [64 cb, 64 cb + 64).
+__device__ __forceinline__ void add_rows(float *v, const char *rows, char *desk, int lane, float by)
+{
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const char *from = it.a + block * kBlock + chunk_at(r, chunk0 + q);
-            const Pack<__half, 8> hi = *reinterpret_cast<const Pack<__half, 8> *>(from);
-            const Pack<__half, 8> lo = *reinterpret_cast<const Pack<__half, 8> *>(from + kPiece);
+    for (int piece = 0; piece < 2; ++piece) {
+        uint4 line[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                float &x = v[8 * q + k];
-                x = a.cc * (x * kUnscale) + a.cb * (__half2float(hi.v[k]) + __half2float(lo.v[k]));
-                if (row == ct * kTile + c0 + 8 * q + k) x += a.ca * kScale;
+        for (int i = 0; i < 8; ++i) line[i] = *reinterpret_cast<const uint4 *>(rows + piece * kPiece + i * 512 + lane * 16);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4 *>(desk + i * 512 + lane * 16) = line[i];
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            const uint4 q = *reinterpret_cast<const uint4 *>(desk + chunk_at(lane, c));
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 f = floats(w[k]);
+                v[8 * c + 2 * k] += by * f.x;
+                v[8 * c + 2 * k + 1] += by * f.y;
             }
         }
-    } else {
-#pragma unroll
-        for (int k = 0; k < 32; ++k) v[k] *= kUnscale;
     }
-    if (a.stage != kStageLast) {
+}
+// 32 rows of 64 columns to a block, piece by piece.
+__device__ __forceinline__ void store_rows(const float *v, char *rows, char *desk, int lane)
+{
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            uint4 hi, lo;
-            split8(v + 8 * q, hi, lo);
-            char *p = to + block * kBlock + chunk_at(r, chunk0 + q);
-            *reinterpret_cast<uint4 *>(p) = hi;
-            *reinterpret_cast<uint4 *>(p + kPiece) = lo;
-        }
-        if (mirror) {  // the other side of the diagonal: this row is a column there
-            char *p = to + (((int64_t)ct * wide + rt) * 2 + r / kK) * kBlock + r % 8 * 2;
+    for (int piece = 0; piece < 2; ++piece) {
+        desk_ready(lane);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) {
-                const __half hi = __float2half_rn(v[k]);
-                __half *q = reinterpret_cast<__half *>(p + chunk_at(c0 + k, r % kK / 8));
-                q[0] = hi;
-                q[kPiece / 2] = __float2half_rn(v[k] - __half2float(hi));
-            }
-        }
-    } else if (row < it.m && !(it.momentum && skip)) {
-        const int64_t step = it.tall ? it.m : 1;
-        int64_t at = it.tall ? (int64_t)(ct * kTile + c0) * it.m + row : (int64_t)row * it.n + ct * kTile + c0;
+        for (int c = 0; c < 8; ++c) {
+            uint32_t w[4];
 #pragma unroll
-        for (int k = 0; k < 32; ++k, at += step) {
-            if (ct * kTile + c0 + k < it.n) {
-                float o = v[k] * kUnscale;
-                if (it.momentum) {
-                    const float w = it.master ? it.master[at] : load_any(it.out, at, a.out_dtype);
-                    o = a.keep * w - it.scale * o;
-                    if (it.master) it.master[at] = o;
+            for (int k = 0; k < 4; ++k) {
+                const float x = v[8 * c + 2 * k], y = v[8 * c + 2 * k + 1];
+                w[k] = halves(x, y);
+                if (piece) {
+                    const float2 h = floats(w[k]);
+                    w[k] = halves(x - h.x, y - h.y);
                 }
-                store_any(it.out, at, a.out_dtype, o);
             }
+            *reinterpret_cast<uint4 *>(desk + chunk_at(lane, c)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) bulk_store(rows + piece * kPiece, smem_u32(desk), kDesk);
+    }
+}
+// 64 columns of 32 rows as 64 rows of the block across the diagonal.  Neighbouring
+// lanes join their values of a row there: even lanes take even columns.
+__device__ __forceinline__ void store_columns(const float *v, char *block, int r, int lane)
+{
+    const bool odd = lane & 1;
+    char *p = block + (r & 6) * 2;
+#pragma unroll
+    for (int c = 0; c < kK; c += 2) {
+        uint32_t w[2];  // hi and lo of columns c and c + 1
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float x = v[c + k], h = __half2float(__float2half_rn(x));
+            w[k] = halves(h, x - h);
+        }
+        const uint32_t mine = odd ? w[1] : w[0], other = __shfl_xor_sync(~0u, odd ? w[0] : w[1], 1);
+        const uint32_t first = odd ? other : mine, second = odd ? mine : other;
+        char *q = p + chunk_at(c + (int)odd, r % kK / 8);
+        *reinterpret_cast<uint32_t *>(q) = __byte_perm(first, second, 0x5410);
+        *reinterpret_cast<uint32_t *>(q + kPiece) = __byte_perm(first, second, 0x7632);
+    }
+}
+// 32 x 32 results to row-major memory, neighbouring lanes along its rows.
+template <int CAP>
+__device__ __forceinline__ void store_result(const Args<CAP> &a, const Item &it, float *v, int row0, int col0, float *desk,
+                                             int lane)
+{
+    if (!it.tall) {  // v[i] becomes row i, column `lane`
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 32; ++k) desk[lane * 32 + (k ^ lane)] = v[k];
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 32; ++k) v[k] = desk[k * 32 + (lane ^ k)];
+    }
+    // the matrix's own rows and columns
+    const int64_t wide = it.tall ? it.m : it.n, first = it.tall ? col0 : row0, along = (it.tall ? row0 : col0) + lane;
+    const int most = (int)min((int64_t)32, (it.tall ? it.n : it.m) - first);
+    if (along >= wide) return;
+    const int64_t at = first * wide + along;
+#pragma unroll
+    for (int i0 = 0; i0 < 32; i0 += 8) {
+        float w[8];
+        if (it.momentum) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i0 + i < most)
+                    w[i] = it.master ? it.master[at + (i0 + i) * wide] : load_any(it.out, at + (i0 + i) * wide, a.out_dtype);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (i0 + i >= most) continue;
+            const int64_t e = at + (i0 + i) * wide;
+            float o = v[i0 + i];
+            if (it.momentum) {
+                o = a.keep * w[i] - it.scale * o;
+                if (it.master) it.master[e] = o;
+            }
+            store_any(it.out, e, a.out_dtype, o);
+        }
+    }
+}
+
+// Sums of a tile's 32 rows and 128 columns to where the stage puts them.
+template <int CAP>
+__device__ __forceinline__ void finish(const Args<CAP> &a, const Item &it, float (&v)[kTile], int rt, int ct, int warp_row,
+                                       int wide, bool mirror, bool skip, char *desk, int lane)
+{
+    const int r = warp_row + lane;
+    if (a.stage == kStageLast) {
+        if (it.momentum && skip) return;
+#pragma unroll
+        for (int g = 0; g < kTile / 32; ++g) {
+            asm volatile("" ::: "memory");
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[32 * g + k] *= kUnscale * kUnscale;
+            if (rt * kTile + warp_row < it.m)
+                store_result(a, it, v + 32 * g, rt * kTile + warp_row, ct * kTile + 32 * g, reinterpret_cast<float *>(desk), lane);
+        }
+        return;
+    }
+    char *to = a.stage == kStageGram ? it.a : a.stage == kStageSquare ? it.b : a.swap ? it.x : it.y;
+#pragma unroll
+    for (int cb = 0; cb < 2; ++cb) {
+        asm volatile("" ::: "memory");
+        const int64_t block = (((int64_t)rt * wide + ct) * 2 + cb) * kBlock + warp_row * 128;
+        float *u = v + cb * kK;
+        const float by = a.stage == kStageSquare ? a.cc * kUnscale : kUnscale;
+#pragma unroll
+        for (int k = 0; k < kK; ++k) u[k] *= by;
+        if (a.stage == kStageSquare) {
+            desk_ready(lane);
+            add_rows(u, it.a + block, desk, lane, a.cb);
+#pragma unroll
+            for (int k = 0; k < kK; ++k)
+                if (rt * kTile + r == ct * kTile + cb * kK + k) u[k] += a.ca * kScale;
+        }
+        store_rows(u, to + block, desk, lane);
+        if (mirror) store_columns(u, to + (((int64_t)ct * wide + rt) * 2 + r / kK) * kBlock + cb * kK * 128, r, lane);
     }
 }
 
@@ -443,15 +566,13 @@ template <int CAP>
 __global__ void __cluster_dims__(2) __launch_bounds__(kGemmThreads, 1) product_kernel(const __grid_constant__ Args<CAP> a)
 {
     extern __shared__ char raw[];
-    __shared__ alignas(8) uint64_t bars[3 * kStages + 4];
-    __shared__ uint32_t tmem_base;
-    __shared__ int dead_word;
-    volatile int *dead = &dead_word;
-    stream_order();
-    const uint32_t smem = (smem_u32(raw) + 1023) & ~1023u;
+    char *base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    const uint32_t smem = smem_u32(base), bars = smem + kBarriers;
+    uint32_t *tmem_base = reinterpret_cast<uint32_t *>(base + kBarriers + 192);
+    volatile int *dead = reinterpret_cast<volatile int *>(base + kBarriers + 196);
     // full: a stage's copies are here; peer: the second block's are there; empty: the
     // products have read it; done, free: an accumulator's products are complete, have been added up
-    const uint32_t full = smem_u32(bars), peer = full + 8 * kStages, empty = peer + 8 * kStages, done = empty + 8 * kStages,
+    const uint32_t full = bars, peer = full + 8 * kStages, empty = peer + 8 * kStages, done = empty + 8 * kStages,
                    free = done + 16;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t rank;
@@ -466,100 +587,26 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kGemmThreads, 1) product_k
             mbar_init(done + 8 * s, 1);
             mbar_init(free + 8 * s, 2 * kSumWarps);
         }
-        dead_word = 0;
+        *dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kSumWarps + 1) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base)), "n"(512) : "memory");
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(bars + 192), "n"(512) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     fence_tmem_before();
     __syncthreads();
     cluster_sync();
+    stream_order();
     fence_tmem_after();
-    const uint32_t tmem = tmem_base;
+    const uint32_t tmem = *tmem_base;
     const bool next = a.stage >= kStageNext;
     const int units = a.start[next ? kNext : kGram][a.count], first_unit = blockIdx.x / 2, every = gridDim.x / 2;
 
-    if (warp == kSumWarps && lane == 0) {
-        asm volatile("fence.proxy.async.global;" ::: "memory");
-        Turn<kStages> turn(1);
-        bool ok = true;
-        for (int unit = first_unit; unit < units && ok; unit += every) {
-            const Job j = job_of(a, unit);
-            const Item &it = *j.it;
-            const char *x = a.swap ? it.y : it.x, *sq = a.stage == kStageSquare ? it.a : it.b;
-            const int64_t xrow = (int64_t)it.nt * 2 * kBlock, mrow = (int64_t)it.mt * 2 * kBlock;
-            // the last tile may have one half: the other one's place takes what is at hand
-            const int rows = min(j.ti * 2 + (int)rank, it.mt - 1);
-            const int cols = min(j.tj * 2 + (int)rank, (next ? it.nt : it.mt) - 1);
-            const char *left = a.stage == kStageGram ? x + rows * xrow : sq + rows * mrow;
-            const char *right = a.stage == kStageGram ? x + cols * xrow : next ? x + (int64_t)cols * 2 * kBlock : sq + cols * mrow;
-            for (int k = 0; k < j.depth; ++k, turn.next()) {
-                ok = mbar_wait(empty + 8 * turn.at, turn.phase, dead);
-                if (!ok) break;
-                const uint32_t to = smem + turn.at * 2 * kBlock, bar = full + 8 * turn.at;
-                mbar_expect(bar, 2 * kBlock);
-                bulk_load(to, left + (int64_t)k * kBlock, kBlock, bar);
-                if (!next) {
-                    bulk_load(to + kBlock, right + (int64_t)k * kBlock, kBlock, bar);
-                } else {  // 64 of a block's rows are the depth; two blocks side by side, each piece apart
-                    const char *from = right + (k >> 1) * xrow + (k & 1) * (kPiece / 2);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        bulk_load(to + kBlock + q * (kPiece / 2), from + (q & 1) * kBlock + (q >> 1) * kPiece, kPiece / 2, bar);
-                }
-            }
-        }
-        // a block that gave up waits for its copies before its shared memory goes
-        for (int s = 0; s < kStages && !ok; ++s, turn.next()) {
-            volatile int late = 0;
-            mbar_wait(full + 8 * turn.at, turn.phase, &late);
-        }
-    } else if (warp == kSumWarps + 1 && lane == 0 && rank == 1) {
-        // tells the first block what has come here
-        Turn<kStages> turn(0);
-        bool ok = true;
-        for (int unit = first_unit; unit < units && ok; unit += every) {
-            const Job j = job_of(a, unit);
-            for (int k = 0; k < j.depth && ok; ++k, turn.next()) {
-                ok = mbar_wait(full + 8 * turn.at, turn.phase, dead);
-                if (ok) mbar_arrive_first(peer + 8 * turn.at);
-            }
-        }
-    } else if (warp == kSumWarps + 1 && lane == 0) {
-        const uint32_t idesc = instruction(next);
-        const int step = next ? 2048 : 32;
-        Turn<kStages> turn(0);
-        Turn<2> acc(1);
-        bool ok = true;
-        for (int unit = first_unit; unit < units && ok; unit += every) {
-            const Job j = job_of(a, unit);
-            for (int k = 0; k < j.depth; ++k, turn.next(), acc.next()) {
-                ok = mbar_wait(free + 8 * acc.at, acc.phase, dead) && mbar_wait(full + 8 * turn.at, turn.phase, dead) &&
-                     mbar_wait(peer + 8 * turn.at, turn.phase, dead);
-                if (!ok) break;
-                fence_tmem_after();
-                const uint32_t left = smem + turn.at * 2 * kBlock, right = left + kBlock, sums = tmem + acc.at * 2 * kTile;
-#pragma unroll
-                for (int q = 0; q < kK / 16; ++q) {
-                    mma(sums, operand(left + q * 32, false), operand(right + kPiece + q * step, next), idesc, q > 0);
-                    mma(sums, operand(left + kPiece + q * 32, false), operand(right + q * step, next), idesc, true);
-                }
-#pragma unroll
-                for (int q = 0; q < kK / 16; ++q)
-                    mma(sums, operand(left + q * 32, false), operand(right + q * step, next), idesc, true);
-                mma_commit(empty + 8 * turn.at);
-                mma_commit(done + 8 * acc.at);
-            }
-        }
-        // what is in flight reads shared memory: the last stages' releases show its end
-        for (int s = 0; s < kStages; ++s, turn.next()) {
-            volatile int late = 0;
-            mbar_wait(empty + 8 * turn.at, turn.phase ^ 1, &late);
-        }
-    } else if (warp < kSumWarps) {
-        const int half = warp >> 2, r = (warp & 3) * 32 + lane;  // columns of the tile, row of the block
+    if (warp < kSumWarps) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegisters));
+        const int half = warp >> 2;  // of the tile's columns
+        char *desk = base + kDesks + warp * kDesk;
         const uint32_t mine = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * kTile;
         const bool skip = a.grad_scale && isnan(*a.grad_scale);
         Turn<2> acc(0);
@@ -591,15 +638,90 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kGemmThreads, 1) product_k
             const Item &it = *j.it;
             const int rt = j.ti * 2 + (int)rank, ct = j.tj * 2 + half, wide = next ? it.nt : it.mt;
             if (rt >= it.mt || ct >= wide) continue;
-            char *to = a.stage == kStageGram ? it.a : a.stage == kStageSquare ? it.b : a.swap ? it.x : it.y;
-            // 32 columns at a time, each done with before the next one's addresses are formed
-#pragma unroll
-            for (int g = 0; g < kTile / 32; ++g) {
-                asm volatile("" ::: "memory");
-                finish(a, it, v + 32 * g, rt, ct, 32 * g, r, wide, to, !next && j.ti != j.tj, skip);
+            finish(a, it, v, rt, ct, (warp & 3) * 32, wide, !next && j.ti != j.tj, skip, desk, lane);
+        }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        asm volatile("fence.proxy.async.global;" ::: "memory");  // the next product fetches it by bulk copies
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegisters));
+        if (warp == kSumWarps && lane == 0) {
+            asm volatile("fence.proxy.async.global;" ::: "memory");
+            Turn<kStages> turn(1);
+            bool ok = true;
+            for (int unit = first_unit; unit < units && ok; unit += every) {
+                const Job j = job_of(a, unit);
+                const Item &it = *j.it;
+                const char *x = a.swap ? it.y : it.x, *sq = a.stage == kStageSquare ? it.a : it.b;
+                const int64_t xrow = (int64_t)it.nt * 2 * kBlock, mrow = (int64_t)it.mt * 2 * kBlock;
+                // the last tile may have one half: the other one's place takes what is at hand
+                const int rows = min(j.ti * 2 + (int)rank, it.mt - 1);
+                const int cols = min(j.tj * 2 + (int)rank, (next ? it.nt : it.mt) - 1);
+                const char *left = a.stage == kStageGram ? x + rows * xrow : sq + rows * mrow;
+                const char *right = a.stage == kStageGram ? x + cols * xrow : next ? x + (int64_t)cols * 2 * kBlock : sq + cols * mrow;
+                for (int k = 0; k < j.depth; ++k, turn.next()) {
+                    ok = mbar_wait(empty + 8 * turn.at, turn.phase, dead);
+                    if (!ok) break;
+                    const uint32_t to = smem + turn.at * 2 * kBlock, bar = full + 8 * turn.at;
+                    mbar_expect(bar, 2 * kBlock);
+                    bulk_load(to, left + (int64_t)k * kBlock, kBlock, bar);
+                    if (!next) {
+                        bulk_load(to + kBlock, right + (int64_t)k * kBlock, kBlock, bar);
+                    } else {  // 64 of a block's rows are the depth; two blocks side by side, each piece apart
+                        const char *from = right + (k >> 1) * xrow + (k & 1) * (kPiece / 2);
+    #pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            bulk_load(to + kBlock + q * (kPiece / 2), from + (q & 1) * kBlock + (q >> 1) * kPiece, kPiece / 2, bar);
+                    }
+                }
+            }
+            // a block that gave up waits for its copies before its shared memory goes
+            for (int s = 0; s < kStages && !ok; ++s, turn.next()) {
+                volatile int late = 0;
+                mbar_wait(full + 8 * turn.at, turn.phase, &late);
+            }
+        } else if (warp == kSumWarps + 1 && lane == 0 && rank == 1) {
+            // tells the first block what has come here
+            Turn<kStages> turn(0);
+            bool ok = true;
+            for (int unit = first_unit; unit < units && ok; unit += every) {
+                const Job j = job_of(a, unit);
+                for (int k = 0; k < j.depth && ok; ++k, turn.next()) {
+                    ok = mbar_wait(full + 8 * turn.at, turn.phase, dead);
+                    if (ok) mbar_arrive_first(peer + 8 * turn.at);
+                }
+            }
+        } else if (warp == kSumWarps + 1 && lane == 0) {
+            const uint32_t idesc = instruction(next);
+            const int step = next ? 2048 : 32;
+            Turn<kStages> turn(0);
+            Turn<2> acc(1);
+            bool ok = true;
+            for (int unit = first_unit; unit < units && ok; unit += every) {
+                const Job j = job_of(a, unit);
+                for (int k = 0; k < j.depth; ++k, turn.next(), acc.next()) {
+                    ok = mbar_wait(free + 8 * acc.at, acc.phase, dead) && mbar_wait(full + 8 * turn.at, turn.phase, dead) &&
+                         mbar_wait(peer + 8 * turn.at, turn.phase, dead);
+                    if (!ok) break;
+                    fence_tmem_after();
+                    const uint32_t left = smem + turn.at * 2 * kBlock, right = left + kBlock, sums = tmem + acc.at * 2 * kTile;
+    #pragma unroll
+                    for (int q = 0; q < kK / 16; ++q) {
+                        mma(sums, operand(left + q * 32, false), operand(right + kPiece + q * step, next), idesc, q > 0);
+                        mma(sums, operand(left + kPiece + q * 32, false), operand(right + q * step, next), idesc, true);
+                    }
+    #pragma unroll
+                    for (int q = 0; q < kK / 16; ++q)
+                        mma(sums, operand(left + q * 32, false), operand(right + q * step, next), idesc, true);
+                    mma_commit(empty + 8 * turn.at);
+                    mma_commit(done + 8 * acc.at);
+                }
+            }
+            // what is in flight reads shared memory: the last stages' releases show its end
+            for (int s = 0; s < kStages; ++s, turn.next()) {
+                volatile int late = 0;
+                mbar_wait(empty + 8 * turn.at, turn.phase ^ 1, &late);
             }
         }
-        asm volatile("fence.proxy.async.global;" ::: "memory");  // the next product fetches it by bulk copies
     }
     __syncwarp();
     fence_tmem_before();
@@ -687,6 +809,26 @@ struct Call {
     char *workspace;
 };
 
+// The products' kernel takes nearly all of an SM's shared memory, more than
+// step_fit asks for; asked for once on each device.
+template <int CAP>
+rr_status product_ready()
+{
+    static std::mutex mu;
+    static std::vector<char> ready;
+    int dev = -1;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return step_cuda_fail(e, "cudaGetDevice");
+    std::lock_guard<std::mutex> lock(mu);
+    if ((int)ready.size() <= dev) ready.resize(dev + 1, 0);
+    if (!ready[dev]) {
+        e = cudaFuncSetAttribute((const void *)product_kernel<CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem);
+        if (e != cudaSuccess) return step_cuda_fail(e, "cudaFuncSetAttribute(maxDynamicSharedMemorySize)");
+        ready[dev] = 1;
+    }
+    return RR_OK;
+}
+
 template <int CAP>
 rr_status run_lists(const Call &c, int sms, cudaStream_t stream)
 {
@@ -701,9 +843,8 @@ rr_status run_lists(const Call &c, int sms, cudaStream_t stream)
     a.stage = a.swap = 0;
     a.ca = a.cb = a.cc = 0.0f;
     char *at = c.workspace;
-    int fit = 0;
     const void *product = (const void *)product_kernel<CAP>;
-    RR_TRY(step_fit(product, kGemmThreads, kGemmSmem, &fit));
+    RR_TRY(product_ready<CAP>());
     for (int i = 0; i < c.count;) {
         int k = 0;
         for (int q = 0; q < kKinds; ++q) a.start[q][0] = 0;
