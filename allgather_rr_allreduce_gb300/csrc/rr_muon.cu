@@ -324,11 +324,12 @@ __device__ __forceinline__ uint64_t operand(uint32_t at, bool columns)
     const uint64_t leading = columns ? 8192 >> 4 : 1, stride = 1024 >> 4;
     return (uint64_t)((at & 0x3FFFF) >> 4) | leading << 16 | stride << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
-// fp16 operands, binary32 accumulators, 256 x 256 over two blocks; the second
-// operand by columns or by rows.
-__device__ __forceinline__ uint32_t instruction(bool columns)
+// fp16 operands, each by rows or by columns, binary32 accumulators, 256 x 256 over
+// two blocks.
+__device__ __forceinline__ uint32_t instruction(bool left_columns, bool right_columns)
 {
-    return 1u << 4 | (columns ? 1u << 16 : 0u) | (uint32_t)(2 * kTile >> 3) << 17 | (uint32_t)(2 * kTile >> 4) << 24;
+    return 1u << 4 | (left_columns ? 1u << 15 : 0u) | (right_columns ? 1u << 16 : 0u) | (uint32_t)(2 * kTile >> 3) << 17 |
+           (uint32_t)(2 * kTile >> 4) << 24;
 }
 __device__ __forceinline__ void mma(uint32_t acc, uint64_t a, uint64_t b, uint32_t idesc, bool add)
 {
@@ -458,47 +459,18 @@ __device__ __forceinline__ void store_rows(const float *v, char *rows, char *des
         if (lane == 0) bulk_store(rows + piece * kPiece, smem_u32(desk), kDesk);
     }
 }
-// 64 columns of 32 rows as 64 rows of the block across the diagonal.  Neighbouring
-// lanes join their values of a row there: even lanes take even columns.
-__device__ __forceinline__ void store_columns(const float *v, char *block, int r, int lane)
-{
-    const bool odd = lane & 1;
-    char *p = block + (r & 6) * 2;
-#pragma unroll
-    for (int c = 0; c < kK; c += 2) {
-        uint32_t w[2];  // hi and lo of columns c and c + 1
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const float x = v[c + k], h = __half2float(__float2half_rn(x));
-            w[k] = halves(h, x - h);
-        }
-        const uint32_t mine = odd ? w[1] : w[0], other = __shfl_xor_sync(~0u, odd ? w[0] : w[1], 1);
-        const uint32_t first = odd ? other : mine, second = odd ? mine : other;
-        char *q = p + chunk_at(c + (int)odd, r % kK / 8);
-        *reinterpret_cast<uint32_t *>(q) = __byte_perm(first, second, 0x5410);
-        *reinterpret_cast<uint32_t *>(q + kPiece) = __byte_perm(first, second, 0x7632);
-    }
-}
-// 32 x 32 results to row-major memory, neighbouring lanes along its rows.
+// 32 x 32 results on the desk (value of row r, column c at r * 32 + (c ^ r)) to
+// row-major memory, neighbouring lanes along its rows.
 template <int CAP>
-__device__ __forceinline__ void store_result(const Args<CAP> &a, const Item &it, float *v, int row0, int col0, float *desk,
-                                             int lane)
+__device__ __forceinline__ void store_result(const Args<CAP> &a, const Item &it, int row0, int col0, const float *desk, int lane)
 {
-    if (!it.tall) {  // v[i] becomes row i, column `lane`
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < 32; ++k) desk[lane * 32 + (k ^ lane)] = v[k];
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < 32; ++k) v[k] = desk[k * 32 + (lane ^ k)];
-    }
     // the matrix's own rows and columns
     const int64_t wide = it.tall ? it.m : it.n, first = it.tall ? col0 : row0, along = (it.tall ? row0 : col0) + lane;
     const int most = (int)min((int64_t)32, (it.tall ? it.n : it.m) - first);
     if (along >= wide) return;
     const int64_t at = first * wide + along;
-#pragma unroll
-    for (int i0 = 0; i0 < 32; i0 += 8) {
+#pragma unroll 1
+    for (int i0 = 0; i0 < most; i0 += 8) {
         float w[8];
         if (it.momentum) {
 #pragma unroll
@@ -508,9 +480,9 @@ __device__ __forceinline__ void store_result(const Args<CAP> &a, const Item &it,
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            if (i0 + i >= most) continue;
+            if (i0 + i >= most) break;
             const int64_t e = at + (i0 + i) * wide;
-            float o = v[i0 + i];
+            float o = it.tall ? desk[lane * 32 + ((i0 + i) ^ lane)] : desk[(i0 + i) * 32 + (lane ^ (i0 + i))];
             if (it.momentum) {
                 o = a.keep * w[i] - it.scale * o;
                 if (it.master) it.master[e] = o;
@@ -523,18 +495,24 @@ __device__ __forceinline__ void store_result(const Args<CAP> &a, const Item &it,
 // Sums of a tile's 32 rows and 128 columns to where the stage puts them.
 template <int CAP>
 __device__ __forceinline__ void finish(const Args<CAP> &a, const Item &it, float (&v)[kTile], int rt, int ct, int warp_row,
-                                       int wide, bool mirror, bool skip, char *desk, int lane)
+                                       int wide, bool skip, char *desk, int lane)
 {
     const int r = warp_row + lane;
     if (a.stage == kStageLast) {
         if (it.momentum && skip) return;
+        if (rt * kTile + warp_row >= it.m) return;
+        float *d = reinterpret_cast<float *>(desk);
+#pragma unroll 1
+        for (int g = 0; g < kTile / 32; ++g) {  // one copy of the loop over memory
+            __syncwarp();
 #pragma unroll
-        for (int g = 0; g < kTile / 32; ++g) {
-            asm volatile("" ::: "memory");
+            for (int h = 0; h < kTile / 32; ++h)
+                if (g == h) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) v[32 * g + k] *= kUnscale * kUnscale;
-            if (rt * kTile + warp_row < it.m)
-                store_result(a, it, v + 32 * g, rt * kTile + warp_row, ct * kTile + 32 * g, reinterpret_cast<float *>(desk), lane);
+                    for (int k = 0; k < 32; ++k) d[lane * 32 + (k ^ lane)] = v[32 * h + k] * (kUnscale * kUnscale);
+                }
+            __syncwarp();
+            store_result(a, it, rt * kTile + warp_row, ct * kTile + 32 * g, d, lane);
         }
         return;
     }
@@ -555,8 +533,26 @@ __device__ __forceinline__ void finish(const Args<CAP> &a, const Item &it, float
                 if (rt * kTile + r == ct * kTile + cb * kK + k) u[k] += a.ca * kScale;
         }
         store_rows(u, to + block, desk, lane);
-        if (mirror) store_columns(u, to + (((int64_t)ct * wide + rt) * 2 + r / kK) * kBlock + cb * kK * 128, r, lane);
     }
+}
+
+// Of a symmetric matrix the pairs' tiles on and below the diagonal are stored.  The
+// block of rows `tile`, columns of K block k, that lies above is the transpose of one
+// below: it is fetched by columns.
+__device__ __forceinline__ bool above(int tile, int k) { return tile / 2 < k / 4; }
+// Both pieces of 128 rows and a K block, from a blocked matrix `wide` tiles across.
+__device__ __forceinline__ void fetch_rows(uint32_t to, const char *m, int wide, int tile, int k, uint32_t bar)
+{
+    bulk_load(to, m + ((int64_t)tile * wide * 2 + k) * kBlock, kBlock, bar);
+}
+// The same of its transpose: 64 of a block's rows are the depth; two blocks side by
+// side, each piece apart.
+__device__ __forceinline__ void fetch_columns(uint32_t to, const char *m, int wide, int tile, int k, uint32_t bar)
+{
+    const char *from = m + ((int64_t)(k >> 1) * wide + tile) * 2 * kBlock + (k & 1) * (kPiece / 2);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        bulk_load(to + q * (kPiece / 2), from + (q & 1) * kBlock + (q >> 1) * kPiece, kPiece / 2, bar);
 }
 
 // Two blocks of a cluster work on a tile of 256 x 256, each on 128 rows of it.
@@ -570,17 +566,16 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kGemmThreads, 1) product_k
     const uint32_t smem = smem_u32(base), bars = smem + kBarriers;
     uint32_t *tmem_base = reinterpret_cast<uint32_t *>(base + kBarriers + 192);
     volatile int *dead = reinterpret_cast<volatile int *>(base + kBarriers + 196);
-    // full: a stage's copies are here; peer: the second block's are there; empty: the
-    // products have read it; done, free: an accumulator's products are complete, have been added up
-    const uint32_t full = bars, peer = full + 8 * kStages, empty = peer + 8 * kStages, done = empty + 8 * kStages,
-                   free = done + 16;
+    // full: a stage's copies are here, in the first block the second one's too; empty:
+    // the products have read it; done, free: an accumulator's products are complete,
+    // have been added up
+    const uint32_t full = bars, empty = full + 8 * kStages, done = empty + 8 * kStages, free = done + 16;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t rank;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(full + 8 * s, 1);
-            mbar_init(peer + 8 * s, 1);
+            mbar_init(full + 8 * s, rank == 0 ? 2 : 1);
             mbar_init(empty + 8 * s, 1);
         }
         for (int s = 0; s < 2; ++s) {
@@ -638,7 +633,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kGemmThreads, 1) product_k
             const Item &it = *j.it;
             const int rt = j.ti * 2 + (int)rank, ct = j.tj * 2 + half, wide = next ? it.nt : it.mt;
             if (rt >= it.mt || ct >= wide) continue;
-            finish(a, it, v, rt, ct, (warp & 3) * 32, wide, !next && j.ti != j.tj, skip, desk, lane);
+            finish(a, it, v, rt, ct, (warp & 3) * 32, wide, skip, desk, lane);
         }
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         asm volatile("fence.proxy.async.global;" ::: "memory");  // the next product fetches it by bulk copies
@@ -652,26 +647,21 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kGemmThreads, 1) product_k
                 const Job j = job_of(a, unit);
                 const Item &it = *j.it;
                 const char *x = a.swap ? it.y : it.x, *sq = a.stage == kStageSquare ? it.a : it.b;
-                const int64_t xrow = (int64_t)it.nt * 2 * kBlock, mrow = (int64_t)it.mt * 2 * kBlock;
                 // the last tile may have one half: the other one's place takes what is at hand
                 const int rows = min(j.ti * 2 + (int)rank, it.mt - 1);
                 const int cols = min(j.tj * 2 + (int)rank, (next ? it.nt : it.mt) - 1);
-                const char *left = a.stage == kStageGram ? x + rows * xrow : sq + rows * mrow;
-                const char *right = a.stage == kStageGram ? x + cols * xrow : next ? x + (int64_t)cols * 2 * kBlock : sq + cols * mrow;
                 for (int k = 0; k < j.depth; ++k, turn.next()) {
                     ok = mbar_wait(empty + 8 * turn.at, turn.phase, dead);
                     if (!ok) break;
-                    const uint32_t to = smem + turn.at * 2 * kBlock, bar = full + 8 * turn.at;
+                    const uint32_t left = smem + turn.at * 2 * kBlock, right = left + kBlock, bar = full + 8 * turn.at;
                     mbar_expect(bar, 2 * kBlock);
-                    bulk_load(to, left + (int64_t)k * kBlock, kBlock, bar);
-                    if (!next) {
-                        bulk_load(to + kBlock, right + (int64_t)k * kBlock, kBlock, bar);
-                    } else {  // 64 of a block's rows are the depth; two blocks side by side, each piece apart
-                        const char *from = right + (k >> 1) * xrow + (k & 1) * (kPiece / 2);
-    #pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            bulk_load(to + kBlock + q * (kPiece / 2), from + (q & 1) * kBlock + (q >> 1) * kPiece, kPiece / 2, bar);
-                    }
+                    if (a.stage == kStageGram) fetch_rows(left, x, it.nt, rows, k, bar);
+                    else if (above(j.ti * 2, k)) fetch_columns(left, sq, it.mt, rows, k, bar);
+                    else fetch_rows(left, sq, it.mt, rows, k, bar);
+                    if (a.stage == kStageGram) fetch_rows(right, x, it.nt, cols, k, bar);
+                    else if (next) fetch_columns(right, x, it.nt, cols, k, bar);
+                    else if (above(j.tj * 2, k)) fetch_columns(right, sq, it.mt, cols, k, bar);
+                    else fetch_rows(right, sq, it.mt, cols, k, bar);
                 }
             }
             // a block that gave up waits for its copies before its shared memory goes
@@ -687,31 +677,33 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kGemmThreads, 1) product_k
                 const Job j = job_of(a, unit);
                 for (int k = 0; k < j.depth && ok; ++k, turn.next()) {
                     ok = mbar_wait(full + 8 * turn.at, turn.phase, dead);
-                    if (ok) mbar_arrive_first(peer + 8 * turn.at);
+                    if (ok) mbar_arrive_first(full + 8 * turn.at);
                 }
             }
         } else if (warp == kSumWarps + 1 && lane == 0) {
-            const uint32_t idesc = instruction(next);
-            const int step = next ? 2048 : 32;
             Turn<kStages> turn(0);
             Turn<2> acc(1);
             bool ok = true;
             for (int unit = first_unit; unit < units && ok; unit += every) {
                 const Job j = job_of(a, unit);
                 for (int k = 0; k < j.depth; ++k, turn.next(), acc.next()) {
-                    ok = mbar_wait(free + 8 * acc.at, acc.phase, dead) && mbar_wait(full + 8 * turn.at, turn.phase, dead) &&
-                         mbar_wait(peer + 8 * turn.at, turn.phase, dead);
+                    const bool lc = a.stage != kStageGram && above(j.ti * 2, k);
+                    const bool rc = next || (a.stage == kStageSquare && above(j.tj * 2, k));
+                    const uint32_t left = smem + turn.at * 2 * kBlock, right = left + kBlock, sums = tmem + acc.at * 2 * kTile;
+                    const uint32_t idesc = instruction(lc, rc);
+                    const uint64_t lh = operand(left, lc), ll = operand(left + kPiece, lc), rh = operand(right, rc),
+                                   rl = operand(right + kPiece, rc);
+                    const int lstep = (lc ? 2048 : 32) >> 4, rstep = (rc ? 2048 : 32) >> 4;  // 16 values on
+                    ok = mbar_wait(free + 8 * acc.at, acc.phase, dead) && mbar_wait(full + 8 * turn.at, turn.phase, dead);
                     if (!ok) break;
                     fence_tmem_after();
-                    const uint32_t left = smem + turn.at * 2 * kBlock, right = left + kBlock, sums = tmem + acc.at * 2 * kTile;
-    #pragma unroll
+#pragma unroll
                     for (int q = 0; q < kK / 16; ++q) {
-                        mma(sums, operand(left + q * 32, false), operand(right + kPiece + q * step, next), idesc, q > 0);
-                        mma(sums, operand(left + kPiece + q * 32, false), operand(right + q * step, next), idesc, true);
+                        mma(sums, lh + q * lstep, rl + q * rstep, idesc, q > 0);
+                        mma(sums, ll + q * lstep, rh + q * rstep, idesc, true);
                     }
-    #pragma unroll
-                    for (int q = 0; q < kK / 16; ++q)
-                        mma(sums, operand(left + q * 32, false), operand(right + q * step, next), idesc, true);
+#pragma unroll
+                    for (int q = 0; q < kK / 16; ++q) mma(sums, lh + q * lstep, rh + q * rstep, idesc, true);
                     mma_commit(empty + 8 * turn.at);
                     mma_commit(done + 8 * acc.at);
                 }
