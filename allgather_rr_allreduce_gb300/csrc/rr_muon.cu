@@ -46,11 +46,10 @@ namespace {
     } while (0)
 
 constexpr int kThreads = 256;     // of the kernels that stream
-constexpr int kTile = 128;        // rows and columns of a block's tile; a pair of blocks has twice both
+constexpr int kTile = 128;        // rows and columns of a block's tile in memory
 constexpr int kK = 64;            // columns of a block of an operand: the depth of a stage
 constexpr int kPiece = kTile * kK * 2;  // bytes of one piece of a block
 constexpr int kBlock = 2 * kPiece;
-constexpr int kStages = 3;
 constexpr int kSumWarps = 8;      // warps that sum the stages' products and write results
 constexpr int kGemmThreads = 32 * (kSumWarps + 4);  // and one that copies, one that multiplies, two idle
 // Registers of a summing warp's threads and of the others': the launch has 168 each.
@@ -59,10 +58,19 @@ constexpr int kGemmThreads = 32 * (kSumWarps + 4);  // and one that copies, one 
 constexpr int kSumRegisters = 216, kOtherRegisters = 72;
 static_assert(kSumWarps * kSumRegisters + 4 * kOtherRegisters <= (kSumWarps + 4) * 168, "more than the launch has");
 constexpr int kDesk = 32 * 128;   // bytes of a summing warp's own: 32 rows of a piece, or 32 x 32 results
-// Shared memory: the stages, the warps' desks, the barriers; 1024 to start on a swizzle's boundary.
-constexpr int kDesks = kStages * 2 * kBlock, kBarriers = kDesks + kSumWarps * kDesk;
-constexpr int kGemmSmem = kBarriers + 256 + 1024;
-constexpr int kSumBlocks = 256;   // most partial sums of a matrix's norm
+
+// A pair of blocks works on 256 rows x N columns.  256 columns read least; 128
+// where there are few tiles, or where they fill the last wave of pairs better.
+template <int N>
+struct Shape {
+    static constexpr int half = N / 2;                       // columns of the right operand that a block holds
+    static constexpr int right = half * kK * 4;              // bytes of them, both pieces
+    static constexpr int stage = kBlock + right;
+    static constexpr int stages = N == 256 ? 3 : 4;
+    static constexpr int desks = stages * stage, barriers = desks + kSumWarps * kDesk;
+    static constexpr int smem = barriers + 256 + 1024;       // 1024 to start on a swizzle's boundary
+};
+constexpr int kSumBlocks = 1024;  // most partial sums of a matrix's norm
 constexpr int kCapSmall = 16, kCap = 160;
 constexpr int64_t kMaxSide = (int64_t)1 << 20;
 constexpr int kMaxSteps = 64;
@@ -70,7 +78,7 @@ constexpr int kMaxSteps = 64;
 // of 1e-4 still have all 22 bits.
 constexpr float kScale = 0x1p11f, kUnscale = 0x1p-11f;
 
-enum Kind { kSums, kSplit, kGram, kNext, kKinds };
+enum Kind { kSums, kSplit, kGram256, kNext256, kGram128, kNext128, kKinds };
 enum Stage { kStageGram, kStageSquare, kStageNext, kStageLast };
 
 struct Item {
@@ -134,9 +142,32 @@ __device__ __forceinline__ float update_of(float g, float m, float beta, bool ne
     return nesterov ? (1.0f - beta) * g + beta * m : m;
 }
 
+// Four consecutive elements, aligned to their size.
+__device__ __forceinline__ void load4(float *v, const void *p, int64_t i, int dtype)
+{
+    if (dtype == RR_FP32) {
+        const float4 x = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
+        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+    } else {
+        const uint2 x = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + i);
+        const uint32_t w[2] = {x.x, x.y};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float2 f = dtype == RR_BF16 ? __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[k]))
+                                              : __half22float2(*reinterpret_cast<const __half2 *>(&w[k]));
+            v[2 * k] = f.x;
+            v[2 * k + 1] = f.y;
+        }
+    }
+}
+__device__ __forceinline__ bool aligned4(const void *p, int dtype)
+{
+    return (reinterpret_cast<uintptr_t>(p) & (dtype == RR_FP32 ? 15 : 7)) == 0;
+}
+
 // The new momentum, and the sum of squares of what is orthogonalised.  Eight
 // squares are added in binary32; such a sum outside [2^-90, 2^90] (zero aside) is
-// taken again in binary64, and so is the sum of the sums.
+// taken again in binary64, and so is the sum of the sums.  Bound: HBM.
 template <int CAP>
 __global__ void __launch_bounds__(kThreads) sums_kernel(const __grid_constant__ Args<CAP> a)
 {
@@ -145,40 +176,59 @@ __global__ void __launch_bounds__(kThreads) sums_kernel(const __grid_constant__ 
     const int i = a.find(kSums, blockIdx.x);
     const Item &it = a.item[i];
     const int b = blockIdx.x - a.start[kSums][i], blocks = sum_blocks(it.size);
-    const int64_t lo = it.size * b / blocks, hi = it.size * (b + 1) / blocks;
+    const int64_t lo = it.size * b / blocks & ~(int64_t)7, hi = b + 1 == blocks ? it.size : it.size * (b + 1) / blocks & ~(int64_t)7;
     const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
     const bool step = it.momentum != nullptr;
     if (step && isnan(gs)) return;
+    const bool vec = aligned4(it.src, a.src_dtype) && aligned4(it.momentum, RR_FP32);
     double sum = 0.0;
-    for (int64_t e = lo + threadIdx.x; e < hi; e += 8 * kThreads) {
-        float v[8];
+    for (int64_t e = lo + (vec ? 4 * threadIdx.x : threadIdx.x); e < hi; e += 8 * kThreads) {
+        float v[8], m[8];
         float part = 0.0f;
+        const bool whole = vec && e + 4 * kThreads + 4 <= hi;
+        auto at = [&](int j) { return e + (vec ? (j & 3) + (j >> 2) * 4 * kThreads : (int64_t)j * kThreads); };
+        if (whole) {
+            load4(v, it.src, e, a.src_dtype);
+            load4(v + 4, it.src, e + 4 * kThreads, a.src_dtype);
+            if (step) {
+                load4(m, it.momentum, e, RR_FP32);
+                load4(m + 4, it.momentum, e + 4 * kThreads, RR_FP32);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                v[j] = at(j) < hi ? load_any(it.src, at(j), a.src_dtype) : 0.0f;
+                m[j] = step && at(j) < hi ? it.momentum[at(j)] : 0.0f;
+            }
+        }
+        if (step) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float g = v[j] * gs;
+                m[j] = a.momentum * m[j] + (1.0f - a.momentum) * g;
+                v[j] = update_of(g, m[j], a.momentum, a.nesterov);
+            }
+            if (whole) {
+                *reinterpret_cast<float4 *>(it.momentum + e) = make_float4(m[0], m[1], m[2], m[3]);
+                *reinterpret_cast<float4 *>(it.momentum + e + 4 * kThreads) = make_float4(m[4], m[5], m[6], m[7]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (at(j) < hi) it.momentum[at(j)] = m[j];
+            }
+        }
+        bool zero = true;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int64_t k = e + j * kThreads;
-            v[j] = 0.0f;
-            if (k < hi) {
-                v[j] = load_any(it.src, k, a.src_dtype);
-                if (step) {
-                    const float g = v[j] * gs, m = a.momentum * it.momentum[k] + (1.0f - a.momentum) * g;
-                    it.momentum[k] = m;
-                    v[j] = update_of(g, m, a.momentum, a.nesterov);
-                }
-            }
             part = fmaf(v[j], v[j], part);
+            zero = zero && v[j] == 0.0f;
         }
-        if ((part >= 0x1p-90f && part <= 0x1p90f) || part == 0.0f) {
-            // an exact zero may still be squares that vanished
-            bool zero = true;
+        if (zero || (part >= 0x1p-90f && part <= 0x1p90f)) {
+            sum += (double)part;
+        } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) zero = zero && v[j] == 0.0f;
-            if (part != 0.0f || zero) {
-                sum += (double)part;
-                continue;
-            }
+            for (int j = 0; j < 8; ++j) sum += (double)v[j] * (double)v[j];
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum += (double)v[j] * (double)v[j];
     }
     sum = block_sum(sum, s);
     if (threadIdx.x == 0) it.part[b] = sum;
@@ -205,12 +255,12 @@ __device__ __forceinline__ void split8(const float *v, uint4 &hi, uint4 &lo)
 // Where columns [8 c, 8 c + 8) of row r of a block's piece lie.
 __device__ __forceinline__ int chunk_at(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
 
-// X = update / (norm + eps) as pieces, a block of 128 x 64 at a time.
+// X = update / (norm + eps) as pieces, a block of 128 x 64 at a time.  Bound: HBM.
 template <int CAP>
 __global__ void __launch_bounds__(kThreads) split_kernel(const __grid_constant__ Args<CAP> a)
 {
     stream_order();
-    __shared__ float tile[kTile][kK + 1];
+    __shared__ float tile[kK][kTile + 1];  // of a matrix whose transpose is X
     __shared__ double s[kThreads / 32];
     const int i = a.find(kSplit, blockIdx.x);
     const Item &it = a.item[i];
@@ -219,28 +269,68 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const __grid_constant__
     const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
     const bool step = it.momentum != nullptr;
     const int blocks = sum_blocks(it.size);
-    const double total = block_sum((int)threadIdx.x < blocks ? it.part[threadIdx.x] : 0.0, s);
+    double total = 0.0;
+    for (int k = threadIdx.x; k < blocks; k += kThreads) total += it.part[k];
+    total = block_sum(total, s);
     const double divisor = sqrt(total) + a.eps;
     const float by = (float)divisor;
     const bool plain = by >= 0x1p-100f && by <= 0x1p100f;
-    // neighbouring threads along the matrix's own rows
-    for (int k = threadIdx.x; k < kTile * kK; k += kThreads) {
-        const int r = it.tall ? k % kTile : k / kK, c = it.tall ? k / kTile : k % kK;
-        float v = 0.0f;
-        if (r0 + r < it.m && c0 + c < it.n) {
-            const int64_t at = it.tall ? (int64_t)(c0 + c) * it.m + r0 + r : (int64_t)(r0 + r) * it.n + c0 + c;
-            v = load_any(it.src, at, a.src_dtype);
-            if (step) v = update_of(v * gs, it.momentum[at], a.momentum, a.nesterov);
-            v = plain ? v / by : (float)((double)v / divisor);
-        }
-        tile[r][c] = v * kScale;
-    }
-    __syncthreads();
+    auto scaled = [&](float g, float m) {
+        const float v = step ? update_of(g * gs, m, a.momentum, a.nesterov) : g;
+        return (plain ? v / by : (float)((double)v / divisor)) * kScale;
+    };
     char *block = it.x + (int64_t)u * kBlock;
+    const bool vec = it.n % 8 == 0 && !it.tall && aligned4(it.src, a.src_dtype) && aligned4(it.momentum, RR_FP32);
+    if (it.tall) {  // neighbouring threads along the matrix's own rows
+        for (int k0 = threadIdx.x; k0 < kTile * kK; k0 += 8 * kThreads) {
+            float v[8], m[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int k = k0 + j * kThreads, r = k % kTile, c = k / kTile;
+                const bool in = r0 + r < it.m && c0 + c < it.n;
+                const int64_t at = (int64_t)(c0 + c) * it.m + r0 + r;
+                v[j] = in ? load_any(it.src, at, a.src_dtype) : 0.0f;
+                m[j] = in && step ? it.momentum[at] : 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int k = k0 + j * kThreads, r = k % kTile, c = k / kTile;
+                tile[c][r] = r0 + r < it.m && c0 + c < it.n ? scaled(v[j], m[j]) : 0.0f;
+            }
+        }
+        __syncthreads();
+    }
+#pragma unroll 2
     for (int k = threadIdx.x; k < kTile * 8; k += kThreads) {
-        const int r = k >> 3, c = k & 7;
+        const int r = k >> 3, c = k & 7, col = c0 + 8 * c;
+        float v[8];
+        if (it.tall) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = tile[8 * c + e][r];
+        } else {
+            const bool row = r0 + r < it.m;
+            const int64_t at = (int64_t)(r0 + r) * it.n + col;
+            float m[8];
+            if (vec && row && col < it.n) {
+                load4(v, it.src, at, a.src_dtype);
+                load4(v + 4, it.src, at + 4, a.src_dtype);
+                if (step) {
+                    load4(m, it.momentum, at, RR_FP32);
+                    load4(m + 4, it.momentum, at + 4, RR_FP32);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const bool in = row && col + e < it.n;
+                    v[e] = in ? load_any(it.src, at + e, a.src_dtype) : 0.0f;
+                    m[e] = in && step ? it.momentum[at + e] : 0.0f;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = row && col + e < it.n ? scaled(v[e], m[e]) : 0.0f;
+        }
         uint4 hi, lo;
-        split8(&tile[r][8 * c], hi, lo);
+        split8(v, hi, lo);
         *reinterpret_cast<uint4 *>(block + chunk_at(r, c)) = hi;
         *reinterpret_cast<uint4 *>(block + kPiece + chunk_at(r, c)) = lo;
     }
@@ -269,6 +359,15 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, int parity)
 {
     uint32_t ok;
     asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
+// Whether the phase is over, without waiting.
+__device__ __forceinline__ bool mbar_done(uint32_t bar, int parity)
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
                  "selp.u32 %0, 1, 0, p;\n\t}"
                  : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0;
@@ -324,11 +423,12 @@ __device__ __forceinline__ uint64_t operand(uint32_t at, bool columns)
     const uint64_t leading = columns ? 8192 >> 4 : 1, stride = 1024 >> 4;
     return (uint64_t)((at & 0x3FFFF) >> 4) | leading << 16 | stride << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
-// fp16 operands, each by rows or by columns, binary32 accumulators, 256 x 256 over
+// fp16 operands, each by rows or by columns, binary32 accumulators, 256 x N over
 // two blocks.
+template <int N>
 __device__ __forceinline__ uint32_t instruction(bool left_columns, bool right_columns)
 {
-    return 1u << 4 | (left_columns ? 1u << 15 : 0u) | (right_columns ? 1u << 16 : 0u) | (uint32_t)(2 * kTile >> 3) << 17 |
+    return 1u << 4 | (left_columns ? 1u << 15 : 0u) | (right_columns ? 1u << 16 : 0u) | (uint32_t)(N >> 3) << 17 |
            (uint32_t)(2 * kTile >> 4) << 24;
 }
 __device__ __forceinline__ void mma(uint32_t acc, uint64_t a, uint64_t b, uint32_t idesc, bool add)
@@ -358,16 +458,16 @@ __device__ __forceinline__ void tmem_load(float (&v)[16], uint32_t at)
     for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(r[k]);
 }
 
-// A pair's tile of a product: which matrix, which rows and columns, how deep.
+// A pair's tile of a product: which matrix, which 256 rows and N columns, how deep.
 struct Job {
     const Item *it;
     int ti, tj, depth;
 };
-template <int CAP>
+template <int N, int CAP>
 __device__ __forceinline__ Job job_of(const Args<CAP> &a, int unit)
 {
     const bool next = a.stage >= kStageNext;
-    const int kind = next ? kNext : kGram, i = a.find(kind, unit);
+    const int kind = N == 256 ? (next ? kNext256 : kGram256) : (next ? kNext128 : kGram128), i = a.find(kind, unit);
     const Item &it = a.item[i];
     const int u = unit - a.start[kind][i], tiles = (it.mt + 1) / 2;
     Job j;
@@ -375,33 +475,24 @@ __device__ __forceinline__ Job job_of(const Args<CAP> &a, int unit)
     if (next) {
         j.ti = u % tiles;
         j.tj = u / tiles;
-    } else {  // a symmetric product's tiles on and below the diagonal
-        j.ti = (int)((sqrtf(8.0f * (float)u + 1.0f) - 1.0f) * 0.5f);
-        while (j.ti * (j.ti + 1) / 2 > u) --j.ti;
-        while ((j.ti + 1) * (j.ti + 2) / 2 <= u) ++j.ti;
-        j.tj = u - j.ti * (j.ti + 1) / 2;
+    } else {  // a symmetric product's squares of 256 on and below the diagonal, N columns at a time
+        constexpr int per = 256 / N;
+        const int t = u / per;
+        j.ti = (int)((sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
+        while (j.ti * (j.ti + 1) / 2 > t) --j.ti;
+        while ((j.ti + 1) * (j.ti + 2) / 2 <= t) ++j.ti;
+        j.tj = (t - j.ti * (j.ti + 1) / 2) * per + u % per;
     }
     j.depth = ((a.stage == kStageGram ? it.n : it.m) + kK - 1) / kK;
     return j;
 }
 
 // ---------------------------------------------------------------- a tile's results
-// A warp holds 32 rows x 128 columns of a tile, a row to a lane.  Lines of memory
-// hold a row's 64 values of a piece, so lanes that went to memory each for itself
-// would touch 32 lines at a time (17 to 25 thousand cycles a tile, and 100 thousand
-// for the row-major results).  They pass through the warp's desk instead, where
-// the swizzle keeps every access free of conflicts.
-__device__ __forceinline__ void bulk_store(void *to, uint32_t from, int bytes)
-{
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\tcp.async.bulk.commit_group;" ::"l"(to),
-                 "r"(from), "r"(bytes) : "memory");
-}
-// The desk's last bulk store has read it.
-__device__ __forceinline__ void desk_ready(int lane)
-{
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-    __syncwarp();
-}
+// A warp holds 32 rows of a tile, a row to a lane.  Lines of memory hold a row's 64
+// values of a piece, so lanes that went to memory each for itself would touch 32
+// lines at a time (17 to 25 thousand cycles a tile, and 100 thousand for row-major
+// results).  Values pass through the warp's desk instead, where the swizzle keeps
+// every access free of conflicts, and go on by whole lines.
 __device__ __forceinline__ uint32_t halves(float x, float y)
 {
     const __half2 h = __floats2half2_rn(x, y);
@@ -409,37 +500,42 @@ __device__ __forceinline__ uint32_t halves(float x, float y)
 }
 __device__ __forceinline__ float2 floats(uint32_t h) { return __half22float2(*reinterpret_cast<const __half2 *>(&h)); }
 
-// v += by * what 32 rows of a block hold: both pieces of columns [64 cb, 64 cb + 64).
-__device__ __forceinline__ void add_rows(float *v, const char *rows, char *desk, int lane, float by)
+// One piece of 32 rows of a block, by whole lines.
+struct Lines {
+    uint4 line[8];
+    __device__ __forceinline__ void load(const char *rows, int lane)
+    {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) line[i] = *reinterpret_cast<const uint4 *>(rows + i * 512 + lane * 16);
+    }
+};
+// v += by * that piece, 64 columns of the lane's row; `next` is under way meanwhile.
+__device__ __forceinline__ void add_rows(float *v, Lines &from, const char *next, char *desk, int lane, float by)
 {
+    __syncwarp();
 #pragma unroll
-    for (int piece = 0; piece < 2; ++piece) {
-        uint4 line[8];
+    for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4 *>(desk + i * 512 + lane * 16) = from.line[i];
+    __syncwarp();
+    if (next) from.load(next, lane);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) line[i] = *reinterpret_cast<const uint4 *>(rows + piece * kPiece + i * 512 + lane * 16);
-        __syncwarp();
+    for (int c = 0; c < 8; ++c) {
+        asm volatile("" ::: "memory");  // a chunk at a time: registers are short
+        const uint4 q = *reinterpret_cast<const uint4 *>(desk + chunk_at(lane, c));
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4 *>(desk + i * 512 + lane * 16) = line[i];
-        __syncwarp();
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            const uint4 q = *reinterpret_cast<const uint4 *>(desk + chunk_at(lane, c));
-            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float2 f = floats(w[k]);
-                v[8 * c + 2 * k] += by * f.x;
-                v[8 * c + 2 * k + 1] += by * f.y;
-            }
+        for (int k = 0; k < 4; ++k) {
+            const float2 f = floats(w[k]);
+            v[8 * c + 2 * k] += by * f.x;
+            v[8 * c + 2 * k + 1] += by * f.y;
         }
     }
 }
-// 32 rows of 64 columns to a block, piece by piece.
+// 64 columns of 32 rows to a block, piece by piece.
 __device__ __forceinline__ void store_rows(const float *v, char *rows, char *desk, int lane)
 {
 #pragma unroll
     for (int piece = 0; piece < 2; ++piece) {
-        desk_ready(lane);
+        __syncwarp();
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
             uint32_t w[4];
@@ -454,127 +550,151 @@ __device__ __forceinline__ void store_rows(const float *v, char *rows, char *des
             }
             *reinterpret_cast<uint4 *>(desk + chunk_at(lane, c)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) bulk_store(rows + piece * kPiece, smem_u32(desk), kDesk);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (i % 4 == 0) asm volatile("" ::: "memory");
+            *reinterpret_cast<uint4 *>(rows + piece * kPiece + i * 512 + lane * 16) =
+                *reinterpret_cast<const uint4 *>(desk + i * 512 + lane * 16);
+        }
     }
 }
 // 32 x 32 results on the desk (value of row r, column c at r * 32 + (c ^ r)) to
 // row-major memory, neighbouring lanes along its rows.
-template <int CAP>
-__device__ __forceinline__ void store_result(const Args<CAP> &a, const Item &it, int row0, int col0, const float *desk, int lane)
+template <class T>
+__device__ __forceinline__ void store_result(const Item &it, float keep, int row0, int col0, const float *desk, int lane)
 {
     // the matrix's own rows and columns
     const int64_t wide = it.tall ? it.m : it.n, first = it.tall ? col0 : row0, along = (it.tall ? row0 : col0) + lane;
-    const int most = (int)min((int64_t)32, (it.tall ? it.n : it.m) - first);
-    if (along >= wide) return;
-    const int64_t at = first * wide + along;
+    const int most = along < wide ? (int)min((int64_t)32, (it.tall ? it.n : it.m) - first) : 0;
+    T *out = static_cast<T *>(it.out) + first * wide + along;
+    float *master = it.master ? it.master + first * wide + along : nullptr;
 #pragma unroll 1
     for (int i0 = 0; i0 < most; i0 += 8) {
-        float w[8];
-        if (it.momentum) {
+        float w[8], o[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i0 + i < most)
-                    w[i] = it.master ? it.master[at + (i0 + i) * wide] : load_any(it.out, at + (i0 + i) * wide, a.out_dtype);
+        for (int i = 0; i < 8; ++i) {
+            const int k = i0 + i;
+            o[i] = it.tall ? desk[lane * 32 + (k ^ lane)] : desk[k * 32 + (lane ^ k)];
+            if (it.momentum && k < most) w[i] = master ? master[i * wide] : to_f32(out[i * wide]);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            if (i0 + i >= most) break;
-            const int64_t e = at + (i0 + i) * wide;
-            float o = it.tall ? desk[lane * 32 + ((i0 + i) ^ lane)] : desk[(i0 + i) * 32 + (lane ^ (i0 + i))];
-            if (it.momentum) {
-                o = a.keep * w[i] - it.scale * o;
-                if (it.master) it.master[e] = o;
+            if (i0 + i < most) {
+                if (it.momentum) {
+                    o[i] = keep * w[i] - it.scale * o[i];
+                    if (master) master[i * wide] = o[i];
+                }
+                out[i * wide] = from_f32<T>(o[i]);
             }
-            store_any(it.out, e, a.out_dtype, o);
         }
+        out += 8 * wide;
+        if (master) master += 8 * wide;
     }
 }
 
-// Sums of a tile's 32 rows and 128 columns to where the stage puts them.
-template <int CAP>
-__device__ __forceinline__ void finish(const Args<CAP> &a, const Item &it, float (&v)[kTile], int rt, int ct, int warp_row,
-                                       int wide, bool skip, char *desk, int lane)
+// Sums of 32 rows (from row0 on) and M columns (from block column cb0 on) of a
+// product to where the stage puts them.
+template <int M, int CAP>
+__device__ __forceinline__ void finish(const Args<CAP> &a, const Item &it, float (&v)[M], int row0, int cb0, int wide, bool skip,
+                                       char *desk, int lane)
 {
-    const int r = warp_row + lane;
     if (a.stage == kStageLast) {
-        if (it.momentum && skip) return;
-        if (rt * kTile + warp_row >= it.m) return;
+        if ((it.momentum && skip) || row0 >= it.m) return;
         float *d = reinterpret_cast<float *>(desk);
 #pragma unroll 1
-        for (int g = 0; g < kTile / 32; ++g) {  // one copy of the loop over memory
+        for (int g = 0; g < M / 32; ++g) {  // one copy of the loop over memory
             __syncwarp();
 #pragma unroll
-            for (int h = 0; h < kTile / 32; ++h)
+            for (int h = 0; h < M / 32; ++h)
                 if (g == h) {
 #pragma unroll
                     for (int k = 0; k < 32; ++k) d[lane * 32 + (k ^ lane)] = v[32 * h + k] * (kUnscale * kUnscale);
                 }
             __syncwarp();
-            store_result(a, it, rt * kTile + warp_row, ct * kTile + 32 * g, d, lane);
+            const int col0 = cb0 * kK + 32 * g;
+            if (a.out_dtype == RR_FP32) store_result<float>(it, a.keep, row0, col0, d, lane);
+            else if (a.out_dtype == RR_BF16) store_result<__nv_bfloat16>(it, a.keep, row0, col0, d, lane);
+            else store_result<__half>(it, a.keep, row0, col0, d, lane);
         }
         return;
     }
     char *to = a.stage == kStageGram ? it.a : a.stage == kStageSquare ? it.b : a.swap ? it.x : it.y;
+    const int64_t block0 = ((int64_t)(row0 / kTile) * wide * 2 + cb0) * kBlock + row0 % kTile * 128;
+    const bool square = a.stage == kStageSquare;
 #pragma unroll
-    for (int cb = 0; cb < 2; ++cb) {
+    for (int cb = 0; cb < M / kK; ++cb) {
         asm volatile("" ::: "memory");
-        const int64_t block = (((int64_t)rt * wide + ct) * 2 + cb) * kBlock + warp_row * 128;
+        if (cb0 + cb >= wide * 2) break;
+        const int64_t block = block0 + cb * kBlock;
         float *u = v + cb * kK;
-        const float by = a.stage == kStageSquare ? a.cc * kUnscale : kUnscale;
+        const float by = square ? a.cc * kUnscale : kUnscale;
 #pragma unroll
         for (int k = 0; k < kK; ++k) u[k] *= by;
-        if (a.stage == kStageSquare) {
-            desk_ready(lane);
-            add_rows(u, it.a + block, desk, lane, a.cb);
+        if (square) {
+            Lines from;
+            from.load(it.a + block, lane);
+            add_rows(u, from, it.a + block + kPiece, desk, lane, a.cb);
+            add_rows(u, from, nullptr, desk, lane, a.cb);
 #pragma unroll
             for (int k = 0; k < kK; ++k)
-                if (rt * kTile + r == ct * kTile + cb * kK + k) u[k] += a.ca * kScale;
+                if (row0 + lane == (cb0 + cb) * kK + k) u[k] += a.ca * kScale;
         }
         store_rows(u, to + block, desk, lane);
     }
 }
 
-// Of a symmetric matrix the pairs' tiles on and below the diagonal are stored.  The
-// block of rows `tile`, columns of K block k, that lies above is the transpose of one
-// below: it is fetched by columns.
-__device__ __forceinline__ bool above(int tile, int k) { return tile / 2 < k / 4; }
-// Both pieces of 128 rows and a K block, from a blocked matrix `wide` tiles across.
-__device__ __forceinline__ void fetch_rows(uint32_t to, const char *m, int wide, int tile, int k, uint32_t bar)
+// Of a symmetric matrix the squares of 256 on and below the diagonal are stored.  The
+// rows of such a square `band`, columns of K block k, that lie above are the transpose
+// of some below: they are fetched by columns.
+__device__ __forceinline__ bool above(int band, int k) { return band < k / 4; }
+// Both pieces of R rows (64 or 128, the `at`th such) and a K block, from a blocked
+// matrix `wide` tiles across.
+template <int R>
+__device__ __forceinline__ void fetch_rows(uint32_t to, const char *m, int wide, int at, int k, uint32_t bar)
 {
-    bulk_load(to, m + ((int64_t)tile * wide * 2 + k) * kBlock, kBlock, bar);
+    constexpr int per = kTile / R;
+    const char *from = m + ((int64_t)(at / per) * wide * 2 + k) * kBlock + at % per * (R * 128);
+    if (R == kTile) {
+        bulk_load(to, from, kBlock, bar);
+    } else {
+        bulk_load(to, from, R * 128, bar);
+        bulk_load(to + R * 128, from + kPiece, R * 128, bar);
+    }
 }
-// The same of its transpose: 64 of a block's rows are the depth; two blocks side by
-// side, each piece apart.
-__device__ __forceinline__ void fetch_columns(uint32_t to, const char *m, int wide, int tile, int k, uint32_t bar)
+// The same of its transpose: 64 of a block's rows are the depth, and R columns are
+// one block or two side by side; each piece apart.
+template <int R>
+__device__ __forceinline__ void fetch_columns(uint32_t to, const char *m, int wide, int at, int k, uint32_t bar)
 {
-    const char *from = m + ((int64_t)(k >> 1) * wide + tile) * 2 * kBlock + (k & 1) * (kPiece / 2);
+    constexpr int cbs = R / kK;
+    const char *from = m + ((int64_t)(k >> 1) * wide * 2 + at * cbs) * kBlock + (k & 1) * (kPiece / 2);
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-        bulk_load(to + q * (kPiece / 2), from + (q & 1) * kBlock + (q >> 1) * kPiece, kPiece / 2, bar);
+    for (int q = 0; q < 2 * cbs; ++q)
+        bulk_load(to + q * (kPiece / 2), from + q % cbs * kBlock + q / cbs * kPiece, kPiece / 2, bar);
 }
 
-// Two blocks of a cluster work on a tile of 256 x 256, each on 128 rows of it.
+// Two blocks of a cluster work on a tile of 256 x N, each on 128 rows of it.
 // Each has its rows of the first operand and half the second one's columns in
 // shared memory; the first block's thread issues the products of both.
-template <int CAP>
+template <int N, int CAP>
 __global__ void __cluster_dims__(2) __launch_bounds__(kGemmThreads, 1) product_kernel(const __grid_constant__ Args<CAP> a)
 {
+    using S = Shape<N>;
     extern __shared__ char raw[];
     char *base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-    const uint32_t smem = smem_u32(base), bars = smem + kBarriers;
-    uint32_t *tmem_base = reinterpret_cast<uint32_t *>(base + kBarriers + 192);
-    volatile int *dead = reinterpret_cast<volatile int *>(base + kBarriers + 196);
+    const uint32_t smem = smem_u32(base), bars = smem + S::barriers;
+    uint32_t *tmem_base = reinterpret_cast<uint32_t *>(base + S::barriers + 192);
+    volatile int *dead = reinterpret_cast<volatile int *>(base + S::barriers + 196);
     // full: a stage's copies are here, in the first block the second one's too; empty:
     // the products have read it; done, free: an accumulator's products are complete,
     // have been added up
-    const uint32_t full = bars, empty = full + 8 * kStages, done = empty + 8 * kStages, free = done + 16;
+    const uint32_t full = bars, empty = full + 8 * S::stages, done = empty + 8 * S::stages, free = done + 16;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t rank;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
+        for (int s = 0; s < S::stages; ++s) {
             mbar_init(full + 8 * s, rank == 0 ? 2 : 1);
             mbar_init(empty + 8 * s, 1);
         }
@@ -586,7 +706,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kGemmThreads, 1) product_k
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kSumWarps + 1) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(bars + 192), "n"(512) : "memory");
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(bars + 192), "n"(2 * N) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     fence_tmem_before();
@@ -596,28 +716,28 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kGemmThreads, 1) product_k
     fence_tmem_after();
     const uint32_t tmem = *tmem_base;
     const bool next = a.stage >= kStageNext;
-    const int units = a.start[next ? kNext : kGram][a.count], first_unit = blockIdx.x / 2, every = gridDim.x / 2;
+    const int units = a.start[N == 256 ? (next ? kNext256 : kGram256) : (next ? kNext128 : kGram128)][a.count], first_unit = blockIdx.x / 2, every = gridDim.x / 2;
 
     if (warp < kSumWarps) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegisters));
         const int half = warp >> 2;  // of the tile's columns
-        char *desk = base + kDesks + warp * kDesk;
-        const uint32_t mine = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * kTile;
+        char *desk = base + S::desks + warp * kDesk;
+        const uint32_t mine = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * S::half;
         const bool skip = a.grad_scale && isnan(*a.grad_scale);
         Turn<2> acc(0);
         for (int unit = first_unit; unit < units; unit += every) {
-            float v[kTile];
+            float v[S::half];
 #pragma unroll
-            for (int k = 0; k < kTile; ++k) v[k] = 0.0f;
+            for (int k = 0; k < S::half; ++k) v[k] = 0.0f;
             bool ok = true;
-            for (int k = job_of(a, unit).depth; k > 0; --k, acc.next()) {
+            for (int k = job_of<N>(a, unit).depth; k > 0; --k, acc.next()) {
                 ok = mbar_wait(done + 8 * acc.at, acc.phase, dead) && ok;
                 fence_tmem_after();
                 __syncwarp();
 #pragma unroll
-                for (int q = 0; q < kTile / 16; ++q) {
+                for (int q = 0; q < S::half / 16; ++q) {
                     float t[16];
-                    tmem_load(t, mine + acc.at * 2 * kTile + q * 16);
+                    tmem_load(t, mine + acc.at * N + q * 16);
 #pragma unroll
                     for (int e = 0; e < 16; ++e) v[q * 16 + e] += t[e];
                 }
@@ -627,74 +747,73 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kGemmThreads, 1) product_k
             }
             if (!ok) {
 #pragma unroll
-                for (int k = 0; k < kTile; ++k) v[k] = __int_as_float(0x7fc00000);
+                for (int k = 0; k < S::half; ++k) v[k] = __int_as_float(0x7fc00000);
             }
-            const Job j = job_of(a, unit);
+            const Job j = job_of<N>(a, unit);
             const Item &it = *j.it;
-            const int rt = j.ti * 2 + (int)rank, ct = j.tj * 2 + half, wide = next ? it.nt : it.mt;
-            if (rt >= it.mt || ct >= wide) continue;
-            finish(a, it, v, rt, ct, (warp & 3) * 32, wide, skip, desk, lane);
+            const int rt = j.ti * 2 + (int)rank, cb = (j.tj * 2 + half) * (S::half / kK), wide = next ? it.nt : it.mt;
+            if (rt < it.mt && cb < wide * 2) finish(a, it, v, rt * kTile + (warp & 3) * 32, cb, wide, skip, desk, lane);
         }
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         asm volatile("fence.proxy.async.global;" ::: "memory");  // the next product fetches it by bulk copies
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegisters));
         if (warp == kSumWarps && lane == 0) {
             asm volatile("fence.proxy.async.global;" ::: "memory");
-            Turn<kStages> turn(1);
+            Turn<S::stages> turn(1);
             bool ok = true;
             for (int unit = first_unit; unit < units && ok; unit += every) {
-                const Job j = job_of(a, unit);
+                const Job j = job_of<N>(a, unit);
                 const Item &it = *j.it;
                 const char *x = a.swap ? it.y : it.x, *sq = a.stage == kStageSquare ? it.a : it.b;
                 // the last tile may have one half: the other one's place takes what is at hand
                 const int rows = min(j.ti * 2 + (int)rank, it.mt - 1);
-                const int cols = min(j.tj * 2 + (int)rank, (next ? it.nt : it.mt) - 1);
+                // columns of the right operand by S::half
+                const int cols = min(j.tj * 2 + (int)rank, (next ? it.nt : it.mt) * (kTile / S::half) - 1);
                 for (int k = 0; k < j.depth; ++k, turn.next()) {
                     ok = mbar_wait(empty + 8 * turn.at, turn.phase, dead);
                     if (!ok) break;
-                    const uint32_t left = smem + turn.at * 2 * kBlock, right = left + kBlock, bar = full + 8 * turn.at;
-                    mbar_expect(bar, 2 * kBlock);
-                    if (a.stage == kStageGram) fetch_rows(left, x, it.nt, rows, k, bar);
-                    else if (above(j.ti * 2, k)) fetch_columns(left, sq, it.mt, rows, k, bar);
-                    else fetch_rows(left, sq, it.mt, rows, k, bar);
-                    if (a.stage == kStageGram) fetch_rows(right, x, it.nt, cols, k, bar);
-                    else if (next) fetch_columns(right, x, it.nt, cols, k, bar);
-                    else if (above(j.tj * 2, k)) fetch_columns(right, sq, it.mt, cols, k, bar);
-                    else fetch_rows(right, sq, it.mt, cols, k, bar);
+                    const uint32_t left = smem + turn.at * S::stage, right = left + kBlock, bar = full + 8 * turn.at;
+                    mbar_expect(bar, S::stage);
+                    if (a.stage == kStageGram) fetch_rows<kTile>(left, x, it.nt, rows, k, bar);
+                    else if (above(j.ti, k)) fetch_columns<kTile>(left, sq, it.mt, rows, k, bar);
+                    else fetch_rows<kTile>(left, sq, it.mt, rows, k, bar);
+                    if (a.stage == kStageGram) fetch_rows<S::half>(right, x, it.nt, cols, k, bar);
+                    else if (next) fetch_columns<S::half>(right, x, it.nt, cols, k, bar);
+                    else if (above(j.tj * N / 256, k)) fetch_columns<S::half>(right, sq, it.mt, cols, k, bar);
+                    else fetch_rows<S::half>(right, sq, it.mt, cols, k, bar);
                 }
             }
             // a block that gave up waits for its copies before its shared memory goes
-            for (int s = 0; s < kStages && !ok; ++s, turn.next()) {
+            for (int s = 0; s < S::stages && !ok; ++s, turn.next()) {
                 volatile int late = 0;
                 mbar_wait(full + 8 * turn.at, turn.phase, &late);
             }
         } else if (warp == kSumWarps + 1 && lane == 0 && rank == 1) {
             // tells the first block what has come here
-            Turn<kStages> turn(0);
+            Turn<S::stages> turn(0);
             bool ok = true;
             for (int unit = first_unit; unit < units && ok; unit += every) {
-                const Job j = job_of(a, unit);
+                const Job j = job_of<N>(a, unit);
                 for (int k = 0; k < j.depth && ok; ++k, turn.next()) {
                     ok = mbar_wait(full + 8 * turn.at, turn.phase, dead);
                     if (ok) mbar_arrive_first(full + 8 * turn.at);
                 }
             }
         } else if (warp == kSumWarps + 1 && lane == 0) {
-            Turn<kStages> turn(0);
+            Turn<S::stages> turn(0);
             Turn<2> acc(1);
-            bool ok = true;
+            bool ok = true, ready = false;
             for (int unit = first_unit; unit < units && ok; unit += every) {
-                const Job j = job_of(a, unit);
+                const Job j = job_of<N>(a, unit);
                 for (int k = 0; k < j.depth; ++k, turn.next(), acc.next()) {
-                    const bool lc = a.stage != kStageGram && above(j.ti * 2, k);
-                    const bool rc = next || (a.stage == kStageSquare && above(j.tj * 2, k));
-                    const uint32_t left = smem + turn.at * 2 * kBlock, right = left + kBlock, sums = tmem + acc.at * 2 * kTile;
-                    const uint32_t idesc = instruction(lc, rc);
+                    const bool lc = a.stage != kStageGram && above(j.ti, k);
+                    const bool rc = next || (a.stage == kStageSquare && above(j.tj * N / 256, k));
+                    const uint32_t left = smem + turn.at * S::stage, right = left + kBlock, sums = tmem + acc.at * N;
+                    const uint32_t idesc = instruction<N>(lc, rc);
                     const uint64_t lh = operand(left, lc), ll = operand(left + kPiece, lc), rh = operand(right, rc),
-                                   rl = operand(right + kPiece, rc);
+                                   rl = operand(right + S::right / 2, rc);
                     const int lstep = (lc ? 2048 : 32) >> 4, rstep = (rc ? 2048 : 32) >> 4;  // 16 values on
-                    ok = mbar_wait(free + 8 * acc.at, acc.phase, dead) && mbar_wait(full + 8 * turn.at, turn.phase, dead);
+                    if (!ready) ok = mbar_wait(free + 8 * acc.at, acc.phase, dead) && mbar_wait(full + 8 * turn.at, turn.phase, dead);
                     if (!ok) break;
                     fence_tmem_after();
 #pragma unroll
@@ -702,6 +821,12 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kGemmThreads, 1) product_k
                         mma(sums, lh + q * lstep, rl + q * rstep, idesc, q > 0);
                         mma(sums, ll + q * lstep, rh + q * rstep, idesc, true);
                     }
+                    // looks at the next stage while there are products to run (1670 -> 1550 cycles a stage)
+                    Turn<S::stages> turn1 = turn;
+                    Turn<2> acc1 = acc;
+                    turn1.next();
+                    acc1.next();
+                    ready = mbar_done(free + 8 * acc1.at, acc1.phase) && mbar_done(full + 8 * turn1.at, turn1.phase);
 #pragma unroll
                     for (int q = 0; q < kK / 16; ++q) mma(sums, lh + q * lstep, rh + q * rstep, idesc, true);
                     mma_commit(empty + 8 * turn.at);
@@ -709,7 +834,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kGemmThreads, 1) product_k
                 }
             }
             // what is in flight reads shared memory: the last stages' releases show its end
-            for (int s = 0; s < kStages; ++s, turn.next()) {
+            for (int s = 0; s < S::stages; ++s, turn.next()) {
                 volatile int late = 0;
                 mbar_wait(empty + 8 * turn.at, turn.phase ^ 1, &late);
             }
@@ -719,7 +844,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kGemmThreads, 1) product_k
     fence_tmem_before();
     __syncthreads();
     cluster_sync();  // neither block's shared memory or barriers go before the other is done
-    if (warp == kSumWarps + 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512) : "memory");
+    if (warp == kSumWarps + 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(2 * N) : "memory");
 }
 
 // ---------------------------------------------------------------- host side
@@ -803,7 +928,7 @@ struct Call {
 
 // The products' kernel takes nearly all of an SM's shared memory, more than
 // step_fit asks for; asked for once on each device.
-template <int CAP>
+template <int N, int CAP>
 rr_status product_ready()
 {
     static std::mutex mu;
@@ -814,11 +939,21 @@ rr_status product_ready()
     std::lock_guard<std::mutex> lock(mu);
     if ((int)ready.size() <= dev) ready.resize(dev + 1, 0);
     if (!ready[dev]) {
-        e = cudaFuncSetAttribute((const void *)product_kernel<CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem);
+        e = cudaFuncSetAttribute((const void *)product_kernel<N, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<N>::smem);
         if (e != cudaSuccess) return step_cuda_fail(e, "cudaFuncSetAttribute(maxDynamicSharedMemorySize)");
         ready[dev] = 1;
     }
     return RR_OK;
+}
+template <int N, int CAP>
+rr_status launch_product(Args<CAP> &a, int64_t units, int64_t pairs, cudaStream_t stream)
+{
+    return step_launch((const void *)product_kernel<N, CAP>, 2 * std::min(units, pairs), kGemmThreads, Shape<N>::smem, &a, stream);
+}
+// Whether tiles of 128 columns take less: a wave of them is 0.55 of a wave of 256.
+bool narrow_tiles(int64_t wide_units, int64_t narrow_units, int64_t pairs)
+{
+    return 11 * ((narrow_units + pairs - 1) / pairs) < 20 * ((wide_units + pairs - 1) / pairs);
 }
 
 template <int CAP>
@@ -835,8 +970,9 @@ rr_status run_lists(const Call &c, int sms, cudaStream_t stream)
     a.stage = a.swap = 0;
     a.ca = a.cb = a.cc = 0.0f;
     char *at = c.workspace;
-    const void *product = (const void *)product_kernel<CAP>;
-    RR_TRY(product_ready<CAP>());
+    RR_TRY((product_ready<256, CAP>()));
+    RR_TRY((product_ready<128, CAP>()));
+    const int64_t pairs = std::max(1, sms / 2);
     for (int i = 0; i < c.count;) {
         int k = 0;
         for (int q = 0; q < kKinds; ++q) a.start[q][0] = 0;
@@ -867,7 +1003,8 @@ rr_status run_lists(const Call &c, int sms, cudaStream_t stream)
                                                                                  : std::sqrt(std::max(1.0, r / l))));
             }
             const int64_t mp = (s.mt + 1) / 2, np = (s.nt + 1) / 2;  // pairs' tiles
-            const int64_t units[kKinds] = {sum_blocks(it.size), (int64_t)s.mt * s.nt * 2, mp * (mp + 1) / 2, mp * np};
+            const int64_t units[kKinds] = {sum_blocks(it.size), (int64_t)s.mt * s.nt * 2, mp * (mp + 1) / 2, mp * np,
+                                           mp * (mp + 1), mp * s.nt};
             for (int q = 0; q < kKinds; ++q) {
                 if (a.start[q][k] + units[q] > INT32_MAX)
                     return step_fail(RR_ERR_INVALID_ARG, "the list's matrices are too large for one call");
@@ -886,8 +1023,9 @@ rr_status run_lists(const Call &c, int sms, cudaStream_t stream)
             a.swap = step & 1;
             for (int q = 0; q < 3; ++q) {
                 a.stage = q < 2 ? q : step + 1 < c.steps ? kStageNext : kStageLast;
-                const int64_t units = a.start[q < 2 ? kGram : kNext][k];
-                RR_TRY(step_launch(product, 2 * std::min<int64_t>(units, sms / 2), kGemmThreads, kGemmSmem, &a, stream));
+                const int64_t wide = a.start[q < 2 ? kGram256 : kNext256][k], narrow = a.start[q < 2 ? kGram128 : kNext128][k];
+                RR_TRY((narrow_tiles(wide, narrow, pairs) ? launch_product<128>(a, narrow, pairs, stream)
+                                                          : launch_product<256>(a, wide, pairs, stream)));
             }
         }
     }

@@ -57,10 +57,9 @@ def test_orthogonalize(rr, shape, kind):
     again, = orthogonalize(rr, [x])
     assert torch.equal(y, again)
     flipped, = orthogonalize(rr, [x.t().contiguous()])
-    if shape[0] != shape[1]:  # the same products on the short side
-        assert torch.equal(flipped.t(), y)
-    else:
-        near(flipped.t(), want, tol, U["fp32"], "transposed")
+    # The same products on the short side, but not bit for bit: squares are added in the
+    # order of memory, eight at a time in binary32, so the norms may differ by 4u.
+    near(flipped.t(), want, tol, U["fp32"], "transposed")
 
 
 @pytest.mark.parametrize("xdt", ["bf16", "fp16", "fp32"])
