@@ -57,7 +57,9 @@ constexpr int kGemmThreads = 32 * (kSumWarps + 4);  // and one that copies, one 
 // they spilled, and a stage's sums took 2500 cycles where the products take 1536.)
 constexpr int kSumRegisters = 216, kOtherRegisters = 72;
 static_assert(kSumWarps * kSumRegisters + 4 * kOtherRegisters <= (kSumWarps + 4) * 168, "more than the launch has");
-constexpr int kDesk = 32 * 128;   // bytes of a summing warp's own: 32 rows of a piece, or 32 x 32 results
+constexpr int kDesk = 32 * 128;   // bytes of a summing warp's own: 32 x 32 sums
+
+enum Kind { kSums, kSplit, kGram256, kNext256, kGram128, kNext128, kKinds };
 
 // A pair of blocks works on 256 rows x N columns.  256 columns read least; 128
 // where there are few tiles, or where they fill the last wave of pairs better.
@@ -69,6 +71,7 @@ struct Shape {
     static constexpr int stages = N == 256 ? 3 : 4;
     static constexpr int desks = stages * stage, barriers = desks + kSumWarps * kDesk;
     static constexpr int smem = barriers + 256 + 1024;       // 1024 to start on a swizzle's boundary
+    static constexpr __device__ int units(bool next) { return N == 256 ? (next ? kNext256 : kGram256) : (next ? kNext128 : kGram128); }
 };
 constexpr int kSumBlocks = 1024;  // most partial sums of a matrix's norm
 constexpr int kCapSmall = 16, kCap = 160;
@@ -78,7 +81,6 @@ constexpr int kMaxSteps = 64;
 // of 1e-4 still have all 22 bits.
 constexpr float kScale = 0x1p11f, kUnscale = 0x1p-11f;
 
-enum Kind { kSums, kSplit, kGram256, kNext256, kGram128, kNext128, kKinds };
 enum Stage { kStageGram, kStageSquare, kStageNext, kStageLast };
 
 struct Item {
@@ -235,19 +237,21 @@ __global__ void __launch_bounds__(kThreads) sums_kernel(const __grid_constant__ 
 }
 
 // ---------------------------------------------------------------- operands
-__device__ __forceinline__ uint32_t pack2(__half lo, __half hi)
+__device__ __forceinline__ uint32_t halves(float2 v)
 {
-    return (uint32_t)__half_as_ushort(lo) | (uint32_t)__half_as_ushort(hi) << 16;
+    const __half2 h = __float22half2_rn(v);
+    return *reinterpret_cast<const uint32_t *>(&h);
 }
+__device__ __forceinline__ float2 floats(uint32_t h) { return __half22float2(*reinterpret_cast<const __half2 *>(&h)); }
 // Eight scaled values as two pieces of 16 bytes.
-__device__ __forceinline__ void split8(const float *v, uint4 &hi, uint4 &lo)
+__device__ __forceinline__ void split8(const float2 (&v)[4], uint4 &hi, uint4 &lo)
 {
     uint32_t h[4], l[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        const __half h0 = __float2half_rn(v[2 * k]), h1 = __float2half_rn(v[2 * k + 1]);
-        h[k] = pack2(h0, h1);
-        l[k] = pack2(__float2half_rn(v[2 * k] - __half2float(h0)), __float2half_rn(v[2 * k + 1] - __half2float(h1)));
+        h[k] = halves(v[k]);
+        const float2 f = floats(h[k]);
+        l[k] = halves(add2(v[k], make_float2(-f.x, -f.y)));
     }
     hi = make_uint4(h[0], h[1], h[2], h[3]);
     lo = make_uint4(l[0], l[1], l[2], l[3]);
@@ -330,7 +334,7 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const __grid_constant__
             for (int e = 0; e < 8; ++e) v[e] = row && col + e < it.n ? scaled(v[e], m[e]) : 0.0f;
         }
         uint4 hi, lo;
-        split8(v, hi, lo);
+        split8({make_float2(v[0], v[1]), make_float2(v[2], v[3]), make_float2(v[4], v[5]), make_float2(v[6], v[7])}, hi, lo);
         *reinterpret_cast<uint4 *>(block + chunk_at(r, c)) = hi;
         *reinterpret_cast<uint4 *>(block + kPiece + chunk_at(r, c)) = lo;
     }
@@ -467,7 +471,7 @@ template <int N, int CAP>
 __device__ __forceinline__ Job job_of(const Args<CAP> &a, int unit)
 {
     const bool next = a.stage >= kStageNext;
-    const int kind = N == 256 ? (next ? kNext256 : kGram256) : (next ? kNext128 : kGram128), i = a.find(kind, unit);
+    const int kind = Shape<N>::units(next), i = a.find(kind, unit);
     const Item &it = a.item[i];
     const int u = unit - a.start[kind][i], tiles = (it.mt + 1) / 2;
     Job j;
@@ -491,105 +495,81 @@ __device__ __forceinline__ Job job_of(const Args<CAP> &a, int unit)
 // A warp holds 32 rows of a tile, a row to a lane.  Lines of memory hold a row's 64
 // values of a piece, so lanes that went to memory each for itself would touch 32
 // lines at a time (17 to 25 thousand cycles a tile, and 100 thousand for row-major
-// results).  Values pass through the warp's desk instead, where the swizzle keeps
-// every access free of conflicts, and go on by whole lines.
-__device__ __forceinline__ uint32_t halves(float x, float y)
-{
-    const __half2 h = __floats2half2_rn(x, y);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-__device__ __forceinline__ float2 floats(uint32_t h) { return __half22float2(*reinterpret_cast<const __half2 *>(&h)); }
+// results).  Values pass through the warp's desk instead, 32 x 32 at a time: value of
+// row r, column c at r * 32 + (c ^ r), free of conflicts along both.  What follows is
+// written as loops: instructions run once come from the L2 at some 75 cycles each.
 
-// One piece of 32 rows of a block, by whole lines.
-struct Lines {
-    uint4 line[8];
-    __device__ __forceinline__ void load(const char *rows, int lane)
-    {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) line[i] = *reinterpret_cast<const uint4 *>(rows + i * 512 + lane * 16);
-    }
-};
-// v += by * that piece, 64 columns of the lane's row; `next` is under way meanwhile.
-__device__ __forceinline__ void add_rows(float *v, Lines &from, const char *next, char *desk, int lane, float by)
-{
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4 *>(desk + i * 512 + lane * 16) = from.line[i];
-    __syncwarp();
-    if (next) from.load(next, lane);
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        asm volatile("" ::: "memory");  // a chunk at a time: registers are short
-        const uint4 q = *reinterpret_cast<const uint4 *>(desk + chunk_at(lane, c));
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float2 f = floats(w[k]);
-            v[8 * c + 2 * k] += by * f.x;
-            v[8 * c + 2 * k + 1] += by * f.y;
-        }
-    }
-}
-// 64 columns of 32 rows to a block, piece by piece.
-__device__ __forceinline__ void store_rows(const float *v, char *rows, char *desk, int lane)
-{
-#pragma unroll
-    for (int piece = 0; piece < 2; ++piece) {
-        __syncwarp();
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float x = v[8 * c + 2 * k], y = v[8 * c + 2 * k + 1];
-                w[k] = halves(x, y);
-                if (piece) {
-                    const float2 h = floats(w[k]);
-                    w[k] = halves(x - h.x, y - h.y);
-                }
-            }
-            *reinterpret_cast<uint4 *>(desk + chunk_at(lane, c)) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (i % 4 == 0) asm volatile("" ::: "memory");
-            *reinterpret_cast<uint4 *>(rows + piece * kPiece + i * 512 + lane * 16) =
-                *reinterpret_cast<const uint4 *>(desk + i * 512 + lane * 16);
-        }
-    }
-}
-// 32 x 32 results on the desk (value of row r, column c at r * 32 + (c ^ r)) to
-// row-major memory, neighbouring lanes along its rows.
+// 32 x 32 results to row-major memory, neighbouring lanes along its rows.
 template <class T>
 __device__ __forceinline__ void store_result(const Item &it, float keep, int row0, int col0, const float *desk, int lane)
 {
     // the matrix's own rows and columns
     const int64_t wide = it.tall ? it.m : it.n, first = it.tall ? col0 : row0, along = (it.tall ? row0 : col0) + lane;
     const int most = along < wide ? (int)min((int64_t)32, (it.tall ? it.n : it.m) - first) : 0;
+    // row k of the desk, this lane's column, or the other way round
+    const int base = it.tall ? lane * 32 : 0, by = it.tall ? 0 : 32;
     T *out = static_cast<T *>(it.out) + first * wide + along;
+    if (!it.momentum) {
+#pragma unroll 4
+        for (int k = 0; k < most; ++k, out += wide) *out = from_f32<T>(desk[base + k * by + (k ^ lane)] * (kUnscale * kUnscale));
+        return;
+    }
     float *master = it.master ? it.master + first * wide + along : nullptr;
+    const float step = it.scale * (kUnscale * kUnscale);
 #pragma unroll 1
-    for (int i0 = 0; i0 < most; i0 += 8) {
-        float w[8], o[8];
+    for (int k0 = 0; k0 < most; k0 += 8) {
+        float w[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int k = i0 + i;
-            o[i] = it.tall ? desk[lane * 32 + (k ^ lane)] : desk[k * 32 + (lane ^ k)];
-            if (it.momentum && k < most) w[i] = master ? master[i * wide] : to_f32(out[i * wide]);
-        }
+        for (int i = 0; i < 8; ++i)
+            if (k0 + i < most) w[i] = master ? master[i * wide] : to_f32(out[i * wide]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (i0 + i < most) {
-                if (it.momentum) {
-                    o[i] = keep * w[i] - it.scale * o[i];
-                    if (master) master[i * wide] = o[i];
-                }
-                out[i * wide] = from_f32<T>(o[i]);
+        for (int i = 0; i < 8; ++i)
+            if (k0 + i < most) {
+                w[i] = keep * w[i] - step * desk[base + (k0 + i) * by + ((k0 + i) ^ lane)];
+                if (master) master[i * wide] = w[i];
+                out[i * wide] = from_f32<T>(w[i]);
             }
-        }
         out += 8 * wide;
         if (master) master += 8 * wide;
+    }
+}
+
+// 32 x 32 sums to a block, as pieces; of a square, c * sum + b * A + a * I.
+// Four lanes have 64 bytes of a row.
+template <int CAP>
+__device__ __forceinline__ void store_pieces(const Args<CAP> &a, const Item &it, char *to, int64_t at, int chunk0, int diagonal,
+                                             const float *desk, int lane)
+{
+    const bool square = a.stage == kStageSquare;
+    const float2 by = both(square ? a.cc * kUnscale : kUnscale), cb = both(a.cb);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + (lane >> 2), c = (lane & 3) * 8;
+        const int64_t e = at + chunk_at(r, chunk0 + (lane & 3));  // rows begin at a multiple of 8
+        uint4 hi, lo;
+        if (square) {
+            hi = *reinterpret_cast<const uint4 *>(it.a + e);
+            lo = *reinterpret_cast<const uint4 *>(it.a + e + kPiece);
+        }
+        const float *row = desk + r * 32;
+        float2 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = mul2(make_float2(row[(c + 2 * k) ^ r], row[(c + 2 * k + 1) ^ r]), by);
+        if (square) {
+            const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w}, l[4] = {lo.x, lo.y, lo.z, lo.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = fma2(add2(floats(h[k]), floats(l[k])), cb, v[k]);
+            if (diagonal == 0) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (r == c + 2 * k) v[k].x += a.ca * kScale;
+                    if (r == c + 2 * k + 1) v[k].y += a.ca * kScale;
+                }
+            }
+        }
+        split8(v, hi, lo);
+        *reinterpret_cast<uint4 *>(to + e) = hi;
+        *reinterpret_cast<uint4 *>(to + e + kPiece) = lo;
     }
 }
 
@@ -597,50 +577,31 @@ __device__ __forceinline__ void store_result(const Item &it, float keep, int row
 // product to where the stage puts them.
 template <int M, int CAP>
 __device__ __forceinline__ void finish(const Args<CAP> &a, const Item &it, float (&v)[M], int row0, int cb0, int wide, bool skip,
-                                       char *desk, int lane)
+                                       float *desk, int lane)
 {
-    if (a.stage == kStageLast) {
-        if ((it.momentum && skip) || row0 >= it.m) return;
-        float *d = reinterpret_cast<float *>(desk);
-#pragma unroll 1
-        for (int g = 0; g < M / 32; ++g) {  // one copy of the loop over memory
-            __syncwarp();
-#pragma unroll
-            for (int h = 0; h < M / 32; ++h)
-                if (g == h) {
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) d[lane * 32 + (k ^ lane)] = v[32 * h + k] * (kUnscale * kUnscale);
-                }
-            __syncwarp();
-            const int col0 = cb0 * kK + 32 * g;
-            if (a.out_dtype == RR_FP32) store_result<float>(it, a.keep, row0, col0, d, lane);
-            else if (a.out_dtype == RR_BF16) store_result<__nv_bfloat16>(it, a.keep, row0, col0, d, lane);
-            else store_result<__half>(it, a.keep, row0, col0, d, lane);
-        }
-        return;
-    }
+    if (a.stage == kStageLast && ((it.momentum && skip) || row0 >= it.m)) return;
     char *to = a.stage == kStageGram ? it.a : a.stage == kStageSquare ? it.b : a.swap ? it.x : it.y;
     const int64_t block0 = ((int64_t)(row0 / kTile) * wide * 2 + cb0) * kBlock + row0 % kTile * 128;
-    const bool square = a.stage == kStageSquare;
+#pragma unroll 1
+    for (int g = 0; g < M / 32; ++g) {
+        if (cb0 + g / 2 >= wide * 2) break;
+        __syncwarp();
 #pragma unroll
-    for (int cb = 0; cb < M / kK; ++cb) {
-        asm volatile("" ::: "memory");
-        if (cb0 + cb >= wide * 2) break;
-        const int64_t block = block0 + cb * kBlock;
-        float *u = v + cb * kK;
-        const float by = square ? a.cc * kUnscale : kUnscale;
+        for (int h = 0; h < M / 32; ++h)
+            if (g == h) {
 #pragma unroll
-        for (int k = 0; k < kK; ++k) u[k] *= by;
-        if (square) {
-            Lines from;
-            from.load(it.a + block, lane);
-            add_rows(u, from, it.a + block + kPiece, desk, lane, a.cb);
-            add_rows(u, from, nullptr, desk, lane, a.cb);
-#pragma unroll
-            for (int k = 0; k < kK; ++k)
-                if (row0 + lane == (cb0 + cb) * kK + k) u[k] += a.ca * kScale;
-        }
-        store_rows(u, to + block, desk, lane);
+                for (int k = 0; k < 32; ++k) desk[lane * 32 + (k ^ lane)] = v[32 * h + k];
+            }
+        __syncwarp();
+        const int col0 = cb0 * kK + 32 * g;
+        if (a.stage != kStageLast)
+            store_pieces(a, it, to, block0 + g / 2 * kBlock, g % 2 * 4, col0 - row0, desk, lane);
+        else if (a.out_dtype == RR_FP32)
+            store_result<float>(it, a.keep, row0, col0, desk, lane);
+        else if (a.out_dtype == RR_BF16)
+            store_result<__nv_bfloat16>(it, a.keep, row0, col0, desk, lane);
+        else
+            store_result<__half>(it, a.keep, row0, col0, desk, lane);
     }
 }
 
@@ -712,16 +673,21 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kGemmThreads, 1) product_k
     fence_tmem_before();
     __syncthreads();
     cluster_sync();
+    if (blockIdx.x / 2 < a.start[S::units(a.stage >= kStageNext)][a.count]) {
+        // the table of matrices comes to the SM while the stage before runs
+        const Job j = job_of<N>(a, blockIdx.x / 2);
+        asm volatile("" ::"l"(j.it->x), "l"(j.it->b), "l"(j.it->out), "r"(j.ti + j.tj + j.depth));
+    }
     stream_order();
     fence_tmem_after();
     const uint32_t tmem = *tmem_base;
     const bool next = a.stage >= kStageNext;
-    const int units = a.start[N == 256 ? (next ? kNext256 : kGram256) : (next ? kNext128 : kGram128)][a.count], first_unit = blockIdx.x / 2, every = gridDim.x / 2;
+    const int units = a.start[S::units(next)][a.count], first_unit = blockIdx.x / 2, every = gridDim.x / 2;
 
     if (warp < kSumWarps) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegisters));
         const int half = warp >> 2;  // of the tile's columns
-        char *desk = base + S::desks + warp * kDesk;
+        float *desk = reinterpret_cast<float *>(base + S::desks + warp * kDesk);
         const uint32_t mine = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * S::half;
         const bool skip = a.grad_scale && isnan(*a.grad_scale);
         Turn<2> acc(0);
