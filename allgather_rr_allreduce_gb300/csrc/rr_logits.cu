@@ -28,7 +28,8 @@ namespace cg = cooperative_groups;
         if (st_ != RR_OK) return st_; \
     } while (0)
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
+constexpr int kBlocks = 4;      // blocks of an SM: one's loads run while another joins its sums
 constexpr int kWarps = kThreads / 32;
 constexpr int kUnroll = 4;      // vectors a thread has in flight
 constexpr int kMostCluster = 8; // blocks that share a row
@@ -54,6 +55,13 @@ struct RowArgs {
     int last;
 };
 
+// loss = sum / count, in one order.
+struct SumArgs {
+    const float *part;
+    int64_t n;
+    double count;
+    float *loss;
+};
 struct GradArgs {
     const void *x;
     const int64_t *target;
@@ -63,6 +71,7 @@ struct GradArgs {
     float inv_t, log2_scale;
     const int64_t *offsets;  // NULL: all rows
     int last;
+    SumArgs sum;             // of the pairs' losses, by the first block; loss NULL: none
 };
 
 __device__ __forceinline__ float exp2_fast(float x)
@@ -85,14 +94,34 @@ __device__ __forceinline__ Stat join(Stat a, Stat b, float scale)
     return Stat{top, a.sum * exp2_fast((a.top - base) * scale) + b.sum * exp2_fast((b.top - base) * scale)};
 }
 
-template <class T, int E>
-__device__ __forceinline__ void take(Stat &s, const Pack<T, E> (&v)[kUnroll], float scale)
+// The largest of a thread's elements (a NaN among them may be passed over: the sum
+// of exponentials keeps it).
+__device__ __forceinline__ float largest(const Pack<float, 4> (&v)[kUnroll])
 {
-    float top = s.top;
+    float top = -INFINITY;
 #pragma unroll
     for (int j = 0; j < kUnroll; ++j)
 #pragma unroll
-        for (int k = 0; k < E; ++k) top = fmaxf(top, to_f32(v[j].v[k]));
+        for (int k = 0; k < 4; ++k) top = fmaxf(top, v[j].v[k]);
+    return top;
+}
+template <class T2, class T>
+__device__ __forceinline__ float largest_pairs(const Pack<T, 8> (&v)[kUnroll])
+{
+    T2 top = *reinterpret_cast<const T2 *>(v[0].v);
+#pragma unroll
+    for (int j = 0; j < kUnroll; ++j)
+#pragma unroll
+        for (int k = j == 0 ? 2 : 0; k < 8; k += 2) top = __hmax2(top, *reinterpret_cast<const T2 *>(v[j].v + k));
+    return fmaxf(to_f32(top.x), to_f32(top.y));
+}
+__device__ __forceinline__ float largest(const Pack<__half, 8> (&v)[kUnroll]) { return largest_pairs<__half2>(v); }
+__device__ __forceinline__ float largest(const Pack<__nv_bfloat16, 8> (&v)[kUnroll]) { return largest_pairs<__nv_bfloat162>(v); }
+
+template <class T, int E>
+__device__ __forceinline__ void take(Stat &s, const Pack<T, E> (&v)[kUnroll], float scale)
+{
+    const float top = fmaxf(s.top, largest(v));
     const float base = base_of(top);
     float2 sum = make_float2(s.sum * exp2_fast((s.top - base) * scale), 0.0f);
     const float2 less = both(-base), by = both(scale);
@@ -111,21 +140,21 @@ __device__ __forceinline__ void take(Stat &s, float x, float scale) { s = join(s
 // A row's elements as a block of a cluster takes them: vectors of 16 bytes where
 // they are aligned, single elements before and behind.
 struct Slice {
-    int64_t first, last;  // this block's elements
-    int64_t v0, v1;       // of which whole aligned vectors lie in [v0, v1)
+    uint32_t first, last;  // this block's elements
+    uint32_t v0, v1;       // of which whole aligned vectors lie in [v0, v1)
 };
 template <class T>
 __device__ __forceinline__ Slice slice_of(const T *row, int64_t vocab, int part, int parts)
 {
     constexpr int E = 16 / (int)sizeof(T);
-    int64_t head = (16 - (int)(reinterpret_cast<uintptr_t>(row) & 15)) % 16 / (int)sizeof(T);
-    if (head > vocab) head = vocab;
-    const int64_t n = (vocab - head) / E;
+    uint32_t head = (16 - (int)(reinterpret_cast<uintptr_t>(row) & 15)) % 16 / (int)sizeof(T);
+    if (head > (uint32_t)vocab) head = (uint32_t)vocab;
+    const uint32_t n = ((uint32_t)vocab - head) / E, each = n / parts, more = n % parts;
     Slice s;
-    s.v0 = head + n * part / parts * E;
-    s.v1 = head + n * (part + 1) / parts * E;
+    s.v0 = head + (part * each + min((uint32_t)part, more)) * E;
+    s.v1 = s.v0 + (each + ((uint32_t)part < more ? 1 : 0)) * E;
     s.first = part == 0 ? 0 : s.v0;
-    s.last = part == parts - 1 ? vocab : s.v1;
+    s.last = part == parts - 1 ? (uint32_t)vocab : s.v1;
     return s;
 }
 
@@ -133,10 +162,10 @@ template <class T>
 __device__ __forceinline__ Stat row_stat(const T *row, const Slice &s, float scale)
 {
     constexpr int E = 16 / (int)sizeof(T);
-    constexpr int64_t step = (int64_t)kThreads * E * kUnroll;
+    constexpr uint32_t step = kThreads * E * kUnroll;
     Stat st{-INFINITY, 0.0f};
     Pack<T, E> v[kUnroll];
-    int64_t e = s.v0 + (int64_t)threadIdx.x * E;
+    uint32_t e = s.v0 + threadIdx.x * E;
     for (; e + (kUnroll - 1) * kThreads * E < s.v1; e += step) {
 #pragma unroll
         for (int j = 0; j < kUnroll; ++j) v[j] = *reinterpret_cast<const Pack<T, E> *>(row + e + j * kThreads * E);
@@ -154,51 +183,99 @@ __device__ __forceinline__ Stat row_stat(const T *row, const Slice &s, float sca
         }
         take(st, v, scale);
     }
-    for (int64_t i = s.first + threadIdx.x; i < s.v0; i += kThreads) take(st, to_f32(row[i]), scale);
-    for (int64_t i = s.v1 + threadIdx.x; i < s.last; i += kThreads) take(st, to_f32(row[i]), scale);
+    // fewer than a vector each
+    if (s.first + threadIdx.x < s.v0) take(st, to_f32(row[s.first + threadIdx.x]), scale);
+    if (s.v1 + threadIdx.x < s.last) take(st, to_f32(row[s.v1 + threadIdx.x]), scale);
     return st;
 }
 
-// dx_j = -slope * exp2((x_j - base) * scale), plus slope at the target.
+// 16 bytes that lie `by` bytes into 32: by is a multiple of 2, the same for all lanes.
+__device__ __forceinline__ uint4 cut_out(uint4 x, uint4 y, uint32_t by)
+{
+    uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    if (by & 8) {
+#pragma unroll
+        for (int k = 0; k < 6; ++k) w[k] = w[k + 2];
+    }
+    if (by & 4) {
+#pragma unroll
+        for (int k = 0; k < 5; ++k) w[k] = w[k + 1];
+    }
+    const uint32_t bits = (by & 2) * 8;
+    return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits), __funnelshift_r(w[2], w[3], bits),
+                      __funnelshift_r(w[3], w[4], bits));
+}
+
+// dx_j = -slope * exp2((x_j - base) * scale) * over, plus slope at the target.
 template <class T>
-__device__ __forceinline__ void row_grad(const T *row, T *out, const Slice &s, int64_t target, float base, float scale,
-                                         float slope, float over)
+__device__ __forceinline__ void row_grad(const T *row, T *out, const Slice &s, int64_t vocab, int64_t target, float base,
+                                         float scale, float slope, float over)
 {
     constexpr int E = 16 / (int)sizeof(T);
     const float factor = -slope * over;
-    auto one = [&](int64_t i) {
+    const uint32_t t = (uint32_t)target;
+    auto one = [&](uint32_t i) {
         const float g = exp2_fast((to_f32(row[i]) - base) * scale) * factor;
-        out[i] = from_f32<T>(i == target ? g + slope : g);
+        out[i] = from_f32<T>(i == t ? g + slope : g);
     };
-    if (((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0) {
-        const float2 less = both(-base), by = both(scale), f = both(factor);
-        constexpr int64_t step = (int64_t)kThreads * E * kUnroll;
-        for (int64_t e = s.v0 + (int64_t)threadIdx.x * E; e < s.v1; e += step) {
+    const float2 less = both(-base), by = both(scale), f = both(factor);
+    auto vector = [&](Pack<T, E> &v, uint32_t at) {
+#pragma unroll
+        for (int k = 0; k < E; k += 2) {
+            const float2 z = mul2(add2(pair_f32(v.v + k), less), by);
+            pair_set(v.v + k, mul2(make_float2(exp2_fast(z.x), exp2_fast(z.y)), f));
+        }
+        if (t - at < E) {  // the target's place, from its own element
+#pragma unroll
+            for (int k = 0; k < E; ++k)
+                if (t - at == k) v.v[k] = from_f32<T>(exp2_fast((to_f32(row[t]) - base) * scale) * factor + slope);
+        }
+        *reinterpret_cast<Pack<T, E> *>(out + at) = v;
+    };
+    const uint32_t shift = (uint32_t)(reinterpret_cast<uintptr_t>(row) - reinterpret_cast<uintptr_t>(out)) & 15;
+    constexpr uint32_t step = kThreads * E * kUnroll;
+    if (shift == 0) {
+        for (uint32_t e = s.v0 + threadIdx.x * E; e < s.v1; e += step) {
             Pack<T, E> v[kUnroll];
 #pragma unroll
             for (int j = 0; j < kUnroll; ++j)
                 if (e + j * kThreads * E < s.v1) v[j] = *reinterpret_cast<const Pack<T, E> *>(row + e + j * kThreads * E);
 #pragma unroll
-            for (int j = 0; j < kUnroll; ++j) {
-                const int64_t at = e + j * kThreads * E;
-                if (at >= s.v1) break;
-#pragma unroll
-                for (int k = 0; k < E; k += 2) {
-                    const float2 t = mul2(add2(pair_f32(v[j].v + k), less), by);
-                    float2 g = mul2(make_float2(exp2_fast(t.x), exp2_fast(t.y)), f);
-                    if (target == at + k) g.x += slope;
-                    if (target == at + k + 1) g.y += slope;
-                    pair_set(v[j].v + k, g);
-                }
-                *reinterpret_cast<Pack<T, E> *>(out + at) = v[j];
-            }
+            for (int j = 0; j < kUnroll; ++j)
+                if (e + j * kThreads * E < s.v1) vector(v[j], e + j * kThreads * E);
         }
-        for (int64_t i = s.first + threadIdx.x; i < s.v0; i += kThreads) one(i);
-        for (int64_t i = s.v1 + threadIdx.x; i < s.last; i += kThreads) one(i);
-    } else {
-#pragma unroll 8
-        for (int64_t i = s.first + threadIdx.x; i < s.last; i += kThreads) one(i);
+        if (s.first + threadIdx.x < s.v0) one(s.first + threadIdx.x);
+        if (s.v1 + threadIdx.x < s.last) one(s.v1 + threadIdx.x);
+        return;
     }
+    // The rows are aligned to different places: whole vectors of the output are cut out
+    // of two neighbours of the input (8 rows of 2049 x 50021: element by element 188 us,
+    // so 95).  In place it does not come here.
+    const Slice o = slice_of(out + s.first, s.last - s.first, 0, 1);  // this block's part, from its first element on
+    uint32_t v0 = s.first + o.v0, v1 = s.first + o.v1;
+    // both neighbours have to lie in the row
+    const uint32_t lead = shift / (uint32_t)sizeof(T);
+    if (v0 < lead && v0 < v1) v0 += E;
+    while (v0 < v1 && v1 + (E - lead) > (uint32_t)vocab) v1 -= E;
+    constexpr int U = kUnroll / 2;
+    for (uint32_t e = v0 + threadIdx.x * E; e < v1; e += kThreads * E * U) {
+        uint4 x[U], y[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+            if (e + j * kThreads * E < v1) {
+                x[j] = *reinterpret_cast<const uint4 *>(row + (e + j * kThreads * E - lead));
+                y[j] = *reinterpret_cast<const uint4 *>(row + (e + j * kThreads * E - lead + E));
+            }
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+            if (e + j * kThreads * E < v1) {
+                const uint4 q = cut_out(x[j], y[j], shift);
+                Pack<T, E> v = *reinterpret_cast<const Pack<T, E> *>(&q);
+                vector(v, e + j * kThreads * E);
+            }
+    }
+    for (uint32_t i = s.first + threadIdx.x; i < v0; i += kThreads) one(i);
+    for (uint32_t i = v1 + threadIdx.x; i < s.last; i += kThreads) one(i);
 }
 
 template <class T>
@@ -206,15 +283,15 @@ __device__ __forceinline__ void row_zero(T *out, int64_t vocab, int part, int pa
 {
     constexpr int E = 16 / (int)sizeof(T);
     const Slice s = slice_of(out, vocab, part, parts);
-    for (int64_t i = s.first + threadIdx.x; i < s.v0; i += kThreads) out[i] = from_f32<T>(0.0f);
-    for (int64_t e = s.v0 + (int64_t)threadIdx.x * E; e < s.v1; e += kThreads * E)
+    if (s.first + threadIdx.x < s.v0) out[s.first + threadIdx.x] = from_f32<T>(0.0f);
+    for (uint32_t e = s.v0 + threadIdx.x * E; e < s.v1; e += kThreads * E)
         *reinterpret_cast<uint4 *>(out + e) = make_uint4(0, 0, 0, 0);
-    for (int64_t i = s.v1 + threadIdx.x; i < s.last; i += kThreads) out[i] = from_f32<T>(0.0f);
+    if (s.v1 + threadIdx.x < s.last) out[s.v1 + threadIdx.x] = from_f32<T>(0.0f);
 }
 
 // A row to a cluster of blocks (of one, mostly).
 template <class T, Mode MODE>
-__global__ void __launch_bounds__(kThreads, 2) row_kernel(const __grid_constant__ RowArgs a)
+__global__ void __launch_bounds__(kThreads, kBlocks) row_kernel(const __grid_constant__ RowArgs a)
 {
     stream_order();
     const cg::cluster_group cluster = cg::this_cluster();
@@ -285,19 +362,42 @@ __global__ void __launch_bounds__(kThreads, 2) row_kernel(const __grid_constant_
             }
             if (first) a.token_loss[row] = loss * weight;
             if (dx)
-                row_grad(x, dx, slice, target, base_of(s.top), a.log2_scale, slope * weight * a.grad_scale * a.inv_t,
+                row_grad(x, dx, slice, a.vocab, target, base_of(s.top), a.log2_scale, slope * weight * a.grad_scale * a.inv_t,
                          1.0f / s.sum);
         }
     }
     if (parts > 1) cluster.sync();  // a block's shared memory stays until the others have read it
 }
 
+// Sum of a block's values in binary64, the same in every thread.
+__device__ __forceinline__ double block_sum(double x, double *s)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = x;
+    __syncthreads();
+    x = 0.0;
+    for (int i = 0; i < kWarps; ++i) x += s[i];
+    return x;
+}
+
+__device__ __forceinline__ void take_sum(const SumArgs &a, double *s)
+{
+    double sum = 0.0;
+    for (int64_t i = threadIdx.x; i < a.n; i += kThreads) sum += (double)a.part[i];
+    sum = block_sum(sum, s);
+    if (threadIdx.x == 0) *a.loss = (float)(sum / a.count);
+}
+
 // The gradient of log-probabilities whose sums are known: a row to a block, or
 // to `parts` blocks that do not meet.
 template <class T>
-__global__ void __launch_bounds__(kThreads, 2) row_grad_kernel(const __grid_constant__ GradArgs a, int parts)
+__global__ void __launch_bounds__(kThreads, kBlocks) row_grad_kernel(const __grid_constant__ GradArgs a, int parts)
 {
     stream_order();
+    __shared__ double s[kWarps];
+    if (blockIdx.x == 0 && a.sum.loss) take_sum(a.sum, s);
     int64_t first = 0, end = a.rows;
     if (a.offsets) {
         first = max((int64_t)0, a.offsets[0]);
@@ -313,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 2) row_grad_kernel(const __grid_cons
         if (target < 0 || target >= a.vocab)
             row_zero(dx, a.vocab, part, parts);
         else
-            row_grad(x, dx, slice_of(x, a.vocab, part, parts), target, a.lse[row] / a.inv_t, a.log2_scale,
+            row_grad(x, dx, slice_of(x, a.vocab, part, parts), a.vocab, target, a.lse[row] / a.inv_t, a.log2_scale,
                      a.dlogp[row] * a.inv_t, 1.0f);
     }
 }
@@ -328,19 +428,6 @@ struct PairArgs {
     bool average;
     float *seq_logp, *loss, *slope;  // of each sequence, pair and row
 };
-
-// Sum of a block's values in binary64, the same in every thread.
-__device__ __forceinline__ double block_sum(double x, double *s)
-{
-#pragma unroll
-    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = x;
-    __syncthreads();
-    x = 0.0;
-    for (int i = 0; i < kWarps; ++i) x += s[i];
-    return x;
-}
 
 // log(1 + exp(x)) without overflow.
 __device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x))); }
@@ -385,21 +472,11 @@ __global__ void __launch_bounds__(kThreads) pair_kernel(const __grid_constant__ 
     }
 }
 
-// loss = sum / count, in one order.
-struct SumArgs {
-    const float *part;
-    int64_t n;
-    double count;
-    float *loss;
-};
 __global__ void __launch_bounds__(kThreads) sum_kernel(const __grid_constant__ SumArgs a)
 {
     stream_order();
     __shared__ double s[kWarps];
-    double sum = 0.0;
-    for (int64_t i = threadIdx.x; i < a.n; i += kThreads) sum += (double)a.part[i];
-    sum = block_sum(sum, s);
-    if (threadIdx.x == 0) *a.loss = (float)(sum / a.count);
+    take_sum(a, s);
 }
 
 // ---------------------------------------------------------------- host side
@@ -463,22 +540,27 @@ const void *row_fn(rr_dtype d)
            : d == RR_BF16 ? (const void *)row_kernel<__nv_bfloat16, MODE> : (const void *)row_kernel<__half, MODE>;
 }
 
-// Blocks that share a row: as many as keep no SM without one.
-int blocks_to_a_row(int64_t rows, int64_t vocab, int eb, int sms)
+// Blocks that share a row: as many as all fit at once where rows are few; with a
+// second pass (the policy loss's gradient) at least so many that the rows under way
+// stay in the L2 until then (without a gradient too: the loss is the same).
+constexpr int64_t kRowsInL2 = (int64_t)40 << 20;
+int blocks_to_a_row(int64_t rows, int64_t vocab, int eb, int64_t blocks, bool again)
 {
     int parts = 1;
-    while (parts < kMostCluster && rows * parts * 2 <= sms && vocab * eb / (parts * 2) >= 8192) parts *= 2;
+    while (parts < kMostCluster && vocab * eb / (parts * 2) >= 8192 &&
+           (rows * parts * 2 <= blocks || (again && blocks / parts * vocab * eb > kRowsInL2)))
+        parts *= 2;
     return parts;
 }
 
-rr_status launch_rows(const void *fn, RowArgs &a, rr_dtype dtype, cudaStream_t stream)
+rr_status launch_rows(const void *fn, RowArgs &a, rr_dtype dtype, bool again, cudaStream_t stream)
 {
     int sms = 0, fit = 0;
     RR_TRY(step_sms(&sms));
     RR_TRY(step_fit(fn, kThreads, 0, &fit));
-    const int parts = blocks_to_a_row(a.rows, a.vocab, float_bytes(dtype), sms);
+    const int parts = blocks_to_a_row(a.rows, a.vocab, float_bytes(dtype), (int64_t)fit * sms, again);
     int64_t clusters = a.rows;
-    if (parts == 1 && clusters > (int64_t)fit * sms) clusters = (int64_t)fit * sms;
+    if (clusters > (int64_t)fit * sms / parts) clusters = (int64_t)fit * sms / parts;
     cudaLaunchAttribute attr[2] = {};
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -503,7 +585,7 @@ rr_status launch_grad(GradArgs &a, rr_dtype dtype, cudaStream_t stream)
     int sms = 0, fit = 0;
     RR_TRY(step_sms(&sms));
     RR_TRY(step_fit(fn, kThreads, 0, &fit));
-    int parts = blocks_to_a_row(a.rows, a.vocab, float_bytes(dtype), fit * sms);
+    int parts = blocks_to_a_row(a.rows, a.vocab, float_bytes(dtype), (int64_t)fit * sms, false);
     int64_t teams = a.rows;
     if (teams * parts > (int64_t)fit * sms) teams = (int64_t)fit * sms / parts;
     cudaLaunchAttribute attr = {};
@@ -562,7 +644,7 @@ try {
     a.log2_scale = log2_scale(inv_temperature);
     a.logp = logp;
     a.lse = lse;
-    RR_TRY(launch_rows(row_fn<kLogp>(dtype), a, dtype, stream));
+    RR_TRY(launch_rows(row_fn<kLogp>(dtype), a, dtype, false, stream));
     return step_ok();
 } catch (...) {
     return step_no_memory();
@@ -586,7 +668,7 @@ try {
     const Range in[] = {{"targets", targets, rows * 8}, {"lse", lse, rows * 4}, {"dlogp", dlogp, rows * 4}};
     RR_TRY(check_apart(out, in));
     GradArgs a{logits, targets, lse, dlogp, dlogits, rows, vocab, logits_stride, dlogits_stride, inv_temperature,
-               log2_scale(inv_temperature), nullptr, 0};
+               log2_scale(inv_temperature), nullptr, 0, {}};
     RR_TRY(launch_grad(a, dtype, stream));
     return step_ok();
 } catch (...) {
@@ -650,7 +732,7 @@ try {
     a.token_loss = token_loss;
     a.dx = dlogits;
     a.dx_stride = dlogits_stride;
-    RR_TRY(launch_rows(row_fn<kPolicy>(dtype), a, dtype, stream));
+    RR_TRY(launch_rows(row_fn<kPolicy>(dtype), a, dtype, true, stream));
     if (loss) RR_TRY(launch_sum(token_loss, rows, 1.0, loss, stream));
     return step_ok();
 } catch (...) {
@@ -720,16 +802,17 @@ try {
         a.lse = lse;
         a.offsets = offsets;
         a.last = (int)seqs;
-        RR_TRY(launch_rows(row_fn<kPreference>(dtype), a, dtype, stream));
+        RR_TRY(launch_rows(row_fn<kPreference>(dtype), a, dtype, false, stream));
     }
     PairArgs p{logp, ref_logp, targets, offsets, rows, vocab, pairs, (float)hyper->beta, (float)hyper->label_smoothing,
                (float)hyper->margin, (float)hyper->grad_scale, hyper->average != 0, seq_logp, pair_loss,
                dlogits ? slope : nullptr};
     RR_TRY(step_launch((const void *)pair_kernel, pairs, kThreads, 0, &p, stream));
-    RR_TRY(launch_sum(pair_loss, pairs, (double)pairs, loss, stream));
-    if (rows > 0 && dlogits) {
+    if (rows == 0 || !dlogits) {
+        RR_TRY(launch_sum(pair_loss, pairs, (double)pairs, loss, stream));
+    } else {
         GradArgs g{logits, targets, lse, slope, dlogits, rows, vocab, logits_stride, dlogits_stride, inv_t,
-                   log2_scale(inv_t), offsets, (int)seqs};
+                   log2_scale(inv_t), offsets, (int)seqs, {pair_loss, pairs, (double)pairs, loss}};
         RR_TRY(launch_grad(g, dtype, stream));
     }
     return step_ok();

@@ -4,7 +4,7 @@ Bounds (u = 2^-24).  A term exp(z_j - max) has its exponent rounded three times
 (difference, factor, product): relative 3u |z_j - max|, and ex2.approx adds 4u.
 A thread rescales its sum whenever its maximum moves, and the joins of threads,
 warps and blocks do so 15 times more: at most `chunks + 16` factors of 4u each.
-A thread adds vocab / 1024 terms to each of two sums (a warp's lanes and the
+A thread of 256 adds vocab / 512 terms to each of two sums (a warp's lanes and the
 blocks' join: 16 more): u each.  What the sum is off by, relative, is what its
 logarithm is off by, and logf and the differences around it add a few u."""
 import torch
@@ -45,9 +45,9 @@ class Reference:
         picked = (self.z.gather(1, self.at) - top).view(-1)
         self.logp = torch.where(self.counts, picked - total.log().view(-1), 0.0)
         per = 16 // x.element_size()
-        factors = -(-self.vocab // (512 * per * 4)) + ROW_FACTORS
+        factors = -(-self.vocab // (256 * per * 4)) + ROW_FACTORS
         first = torch.where(self.p > 0, self.p * gap, 0.0).sum(1)
-        self.sum_tol = u * (4 * (factors + 1) + 3 * first + self.vocab / 1024 + 16)
+        self.sum_tol = u * (4 * (factors + 1) + 3 * first + self.vocab / 512 + 16)
         log_total = total.log().view(-1).abs()
         self.logp_tol = self.sum_tol + u * (2 * log_total + 3 * picked.abs() + 2 * self.logp.abs()) + u
         self.lse_tol = self.sum_tol + u * (2 * log_total + 3 * top.view(-1).abs() + 2 * self.lse.abs()) + u
