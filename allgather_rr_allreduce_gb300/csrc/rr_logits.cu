@@ -207,7 +207,10 @@ __device__ __forceinline__ uint4 cut_out(uint4 x, uint4 y, uint32_t by)
 }
 
 // dx_j = -slope * exp2((x_j - base) * scale) * over, plus slope at the target.
-template <class T>
+// LAST: rows of other blocks wait in the L2 for this pass, so what it has read and
+// written leaves the L2 first (policy loss of 8192 x 131072 bf16 935 -> 837 us; the
+// gradient by itself is slower for it, 547 -> 559 us of a preference loss).
+template <bool LAST, class T>
 __device__ __forceinline__ void row_grad(const T *row, T *out, const Slice &s, int64_t vocab, int64_t target, float base,
                                          float scale, float slope, float over)
 {
@@ -230,7 +233,8 @@ __device__ __forceinline__ void row_grad(const T *row, T *out, const Slice &s, i
             for (int k = 0; k < E; ++k)
                 if (t - at == k) v.v[k] = from_f32<T>(exp2_fast((to_f32(row[t]) - base) * scale) * factor + slope);
         }
-        *reinterpret_cast<Pack<T, E> *>(out + at) = v;
+        if (LAST) __stcs(reinterpret_cast<uint4 *>(out + at), *reinterpret_cast<const uint4 *>(v.v));
+        else *reinterpret_cast<Pack<T, E> *>(out + at) = v;
     };
     const uint32_t shift = (uint32_t)(reinterpret_cast<uintptr_t>(row) - reinterpret_cast<uintptr_t>(out)) & 15;
     constexpr uint32_t step = kThreads * E * kUnroll;
@@ -239,7 +243,10 @@ __device__ __forceinline__ void row_grad(const T *row, T *out, const Slice &s, i
             Pack<T, E> v[kUnroll];
 #pragma unroll
             for (int j = 0; j < kUnroll; ++j)
-                if (e + j * kThreads * E < s.v1) v[j] = *reinterpret_cast<const Pack<T, E> *>(row + e + j * kThreads * E);
+                if (e + j * kThreads * E < s.v1) {
+                    if (LAST) *reinterpret_cast<uint4 *>(v[j].v) = __ldcs(reinterpret_cast<const uint4 *>(row + e + j * kThreads * E));
+                    else v[j] = *reinterpret_cast<const Pack<T, E> *>(row + e + j * kThreads * E);
+                }
 #pragma unroll
             for (int j = 0; j < kUnroll; ++j)
                 if (e + j * kThreads * E < s.v1) vector(v[j], e + j * kThreads * E);
@@ -362,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) row_kernel(const __grid_con
             }
             if (first) a.token_loss[row] = loss * weight;
             if (dx)
-                row_grad(x, dx, slice, a.vocab, target, base_of(s.top), a.log2_scale, slope * weight * a.grad_scale * a.inv_t,
+                row_grad<true>(x, dx, slice, a.vocab, target, base_of(s.top), a.log2_scale, slope * weight * a.grad_scale * a.inv_t,
                          1.0f / s.sum);
         }
     }
@@ -413,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) row_grad_kernel(const __gri
         if (target < 0 || target >= a.vocab)
             row_zero(dx, a.vocab, part, parts);
         else
-            row_grad(x, dx, slice_of(x, a.vocab, part, parts), a.vocab, target, a.lse[row] / a.inv_t, a.log2_scale,
+            row_grad<false>(x, dx, slice_of(x, a.vocab, part, parts), a.vocab, target, a.lse[row] / a.inv_t, a.log2_scale,
                      a.dlogp[row] * a.inv_t, 1.0f);
     }
 }
@@ -542,8 +549,10 @@ const void *row_fn(rr_dtype d)
 
 // Blocks that share a row: as many as all fit at once where rows are few; with a
 // second pass (the policy loss's gradient) at least so many that the rows under way
-// stay in the L2 until then (without a gradient too: the loss is the same).
-constexpr int64_t kRowsInL2 = (int64_t)40 << 20;
+// stay in the L2 until then (without a gradient too: the loss is the same).  8192 x
+// 131072 bf16: 85 MB of them 837 us, 160 MB 904, 43 MB 1039 (blocks that share a row
+// wait for one another).
+constexpr int64_t kRowsInL2 = (int64_t)85 << 20;
 int blocks_to_a_row(int64_t rows, int64_t vocab, int eb, int64_t blocks, bool again)
 {
     int parts = 1;
