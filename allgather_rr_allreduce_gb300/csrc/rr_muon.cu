@@ -666,11 +666,6 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kGemmThreads, 1) product_k
         *dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == kSumWarps + 1) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(bars + 192), "n"(2 * N) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-    }
-    fence_tmem_before();
     __syncthreads();
     cluster_sync();
     if (blockIdx.x / 2 < a.start[S::units(a.stage >= kStageNext)][a.count]) {
@@ -679,6 +674,15 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kGemmThreads, 1) product_k
         asm volatile("" ::"l"(j.it->x), "l"(j.it->b), "l"(j.it->out), "r"(j.ti + j.tj + j.depth));
     }
     stream_order();
+    // Only now: accumulators held while waiting could be what a kernel before waits for.
+    // (The first block's products wait for the second's copies, whose arrival the warp
+    // that has made room there passes on.)
+    if (warp == kSumWarps + 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(bars + 192), "n"(2 * N) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    fence_tmem_before();
+    __syncthreads();
     fence_tmem_after();
     const uint32_t tmem = *tmem_base;
     const bool next = a.stage >= kStageNext;

@@ -92,7 +92,7 @@ def test_step(rr, kind):
     logits, _ = forward(rr, net.p, x)
     rr.rr_token_logp(logits, target, old, None, ROWS, VOCAB, VOCAB, 1.0, "fp32")
     ref.copy_(old + 0.1 * torch.randn(ROWS, generator=g, **CUDA))
-    first = torch.log_softmax(plain_logits(want.p, x.double()), 1).gather(1, at).view(-1)
+    first = torch.log_softmax(plain_logits(want.p, x.double()), 1).gather(1, at).view(-1).detach()
     assert float((old - torch.where(counts, first, 0.0)).abs().max()) < 1e-4
     seq_ref = torch.stack([ref[a:b][counts[a:b]].sum() for a, b in zip(offsets.tolist(), offsets.tolist()[1:])])
     loss, token, lp = torch.empty(1, **CUDA), torch.empty(ROWS, **CUDA), torch.empty(ROWS, **CUDA)

@@ -120,6 +120,7 @@ def test_policy_refusals(rr, status, text, kw):
 
 @pytest.mark.parametrize("status,text,kw", ROWS + [
     ("RR_ERR_INVALID_ARG", "pairs", dict(pairs=0)),
+    ("RR_ERR_INVALID_ARG", "pairs", dict(pairs=(1 << 24) + 1)),
     ("RR_ERR_INVALID_ARG", "inv_temperature", dict(hyper=(0.1, 0.0, 0.0, -1.0, 1.0, 0))),
     ("RR_ERR_INVALID_ARG", "beta", dict(hyper=(NAN, 0.0, 0.0, 1.0, 1.0, 0))),
     ("RR_ERR_INVALID_ARG", "label_smoothing", dict(hyper=(0.1, 1.5, 0.0, 1.0, 1.0, 0))),
