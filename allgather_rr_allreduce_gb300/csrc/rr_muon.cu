@@ -349,7 +349,8 @@ __device__ __forceinline__ void mbar_init(uint32_t bar, int count)
 }
 // Arrive at the barrier of the pair's first block.  Nothing but accumulators and
 // bulk copies is ordered by it, so it takes no wider scope (a release to the
-// cluster waits for the thread's stores: 1.2 times the time of a product).
+// cluster waits for the thread's stores: with it a layer's attention weights took 5.8
+// ms where they took 4.7 without).
 __device__ __forceinline__ void mbar_arrive_first(uint32_t bar)
 {
     asm volatile("{\n\t.reg .b32 first;\n\tmapa.shared::cluster.u32 first, %0, 0;\n\t"
@@ -363,15 +364,6 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, int parity)
 {
     uint32_t ok;
     asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-                 "selp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-    return ok != 0;
-}
-// Whether the phase is over, without waiting.
-__device__ __forceinline__ bool mbar_done(uint32_t bar, int parity)
-{
-    uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
                  "selp.u32 %0, 1, 0, p;\n\t}"
                  : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0;
@@ -496,8 +488,9 @@ __device__ __forceinline__ Job job_of(const Args<CAP> &a, int unit)
 // values of a piece, so lanes that went to memory each for itself would touch 32
 // lines at a time (17 to 25 thousand cycles a tile, and 100 thousand for row-major
 // results).  Values pass through the warp's desk instead, 32 x 32 at a time: value of
-// row r, column c at r * 32 + (c ^ r), free of conflicts along both.  What follows is
-// written as loops: instructions run once come from the L2 at some 75 cycles each.
+// row r, column c at r * 32 + (c ^ r), free of conflicts along both.  What is left is
+// the rate at which an SM stores, some 32 bytes a cycle: 4 to 5 thousand cycles for the
+// 128 KB of a tile of 256 columns, against 86 thousand of products at a depth of 3584.
 
 // 32 x 32 results to row-major memory, neighbouring lanes along its rows.
 template <class T>
@@ -635,6 +628,11 @@ __device__ __forceinline__ void fetch_columns(uint32_t to, const char *m, int wi
         bulk_load(to + q * (kPiece / 2), from + q % cbs * kBlock + q / cbs * kPiece, kPiece / 2, bar);
 }
 
+// Bound: the tensor cores.  Both sides of a feed-forward product (3584 x 18944): X X'
+// 0.82 ms, 1.90 PFLOP/s of binary16 products (of 2.01 measured for cuBLAS in bf16); the
+// square 0.17; B X 1.54 ms, 1.89 PFLOP/s.  Sums in registers run beside the products
+// (three stages of 64 KB come from the L2 at 43 bytes a cycle); results do not, see above.
+//
 // Two blocks of a cluster work on a tile of 256 x N, each on 128 rows of it.
 // Each has its rows of the first operand and half the second one's columns in
 // shared memory; the first block's thread issues the products of both.
@@ -772,7 +770,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kGemmThreads, 1) product_k
         } else if (warp == kSumWarps + 1 && lane == 0) {
             Turn<S::stages> turn(0);
             Turn<2> acc(1);
-            bool ok = true, ready = false;
+            bool ok = true;
             for (int unit = first_unit; unit < units && ok; unit += every) {
                 const Job j = job_of<N>(a, unit);
                 for (int k = 0; k < j.depth; ++k, turn.next(), acc.next()) {
@@ -783,7 +781,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kGemmThreads, 1) product_k
                     const uint64_t lh = operand(left, lc), ll = operand(left + kPiece, lc), rh = operand(right, rc),
                                    rl = operand(right + S::right / 2, rc);
                     const int lstep = (lc ? 2048 : 32) >> 4, rstep = (rc ? 2048 : 32) >> 4;  // 16 values on
-                    if (!ready) ok = mbar_wait(free + 8 * acc.at, acc.phase, dead) && mbar_wait(full + 8 * turn.at, turn.phase, dead);
+                    ok = mbar_wait(free + 8 * acc.at, acc.phase, dead) && mbar_wait(full + 8 * turn.at, turn.phase, dead);
                     if (!ok) break;
                     fence_tmem_after();
 #pragma unroll
@@ -791,12 +789,6 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kGemmThreads, 1) product_k
                         mma(sums, lh + q * lstep, rl + q * rstep, idesc, q > 0);
                         mma(sums, ll + q * lstep, rh + q * rstep, idesc, true);
                     }
-                    // looks at the next stage while there are products to run (1670 -> 1550 cycles a stage)
-                    Turn<S::stages> turn1 = turn;
-                    Turn<2> acc1 = acc;
-                    turn1.next();
-                    acc1.next();
-                    ready = mbar_done(free + 8 * acc1.at, acc1.phase) && mbar_done(full + 8 * turn1.at, turn1.phase);
 #pragma unroll
                     for (int q = 0; q < kK / 16; ++q) mma(sums, lh + q * lstep, rh + q * rstep, idesc, true);
                     mma_commit(empty + 8 * turn.at);
@@ -920,10 +912,13 @@ rr_status launch_product(Args<CAP> &a, int64_t units, int64_t pairs, cudaStream_
 {
     return step_launch((const void *)product_kernel<N, CAP>, 2 * std::min(units, pairs), kGemmThreads, Shape<N>::smem, &a, stream);
 }
-// Whether tiles of 128 columns take less: a wave of them is 0.55 of a wave of 256.
+// Whether tiles of 128 columns take less: a wave of them is 0.77 of a wave of 256
+// (they read more for each product).  Five steps of square matrices, us at 256 and 128
+// columns throughout: four of 512 260, 203; 1024 351, 283; 2048 586, 601 (518 as chosen
+// here); 2560 888, 1189; 3584 2001, 2649; eight of 1024 x 4096 1703, 2074.
 bool narrow_tiles(int64_t wide_units, int64_t narrow_units, int64_t pairs)
 {
-    return 11 * ((narrow_units + pairs - 1) / pairs) < 20 * ((wide_units + pairs - 1) / pairs);
+    return 77 * ((narrow_units + pairs - 1) / pairs) < 100 * ((wide_units + pairs - 1) / pairs);
 }
 
 template <int CAP>
