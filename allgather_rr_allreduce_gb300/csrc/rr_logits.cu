@@ -8,7 +8,12 @@
 //   d logp / d x_j = (1[j = t] - exp(z_j - M / temperature) / s) / temperature.
 // A row's maximum and sum are taken in one pass (each thread keeps its own and
 // joins them at the end); a gradient needs them first, so it is a second pass
-// over the row, which then comes out of the L2.
+// over the row, which then comes mostly out of the L2.
+//
+// Bound: HBM.  12288 x 50021 fp16 log-probabilities 192 us (89 % of the copy peak), the
+// gradient of 4096 x 32768 bf16 85 (91 %), a policy loss with its gradient of 8192 x
+// 131072 bf16 837 (74 %; 87 by the traffic, as a quarter of the rows is read twice), a
+// preference loss of 4000 rows x 131072 547 (two reads and a write, 92 %).
 //
 // Times below are of one GB300 (152 SMs, measured copy 6.7 TB/s).
 #include <cmath>

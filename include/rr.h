@@ -585,7 +585,8 @@ rr_status rr_adamw8(void *const *params, const void *const *grads, uint8_t *cons
  * coefs: HOST array of 3 * steps coefficients, 1 <= steps <= 64.
  * workspace: see rr_orthogonalize_workspace; about 8 bytes an element and 8 more
  * for each of the short side squared.
- * A call is 2 + 3 * steps launches for each 160 matrices.
+ * A call is 2 + 3 * steps launches for each 160 matrices.  Every wait in them is
+ * bounded; a block whose wait ran out (two seconds) leaves NaN in its results.
  */
 rr_status rr_orthogonalize(const void *const *x, void *const *y, const int64_t *rows, const int64_t *cols,
                            int num_tensors, rr_dtype x_dtype, rr_dtype y_dtype, const double *coefs, int steps,
@@ -674,8 +675,8 @@ typedef struct {
 } rr_policy_hyper;
 
 /*
- * rr_policy_loss -- the clipped policy loss with a KL term and its gradient, in
- * one pass over the logits.  For each row, with ratio = exp(logp - old_logp),
+ * rr_policy_loss -- the clipped policy loss with a KL term and its gradient, a row
+ * at a time (its second reading comes out of the L2).  For each row, with ratio = exp(logp - old_logp),
  * A = advantages and w = weights:
  *   token_loss = w * (-min(ratio * A, clamp(ratio, 1 - clip_low, 1 + clip_high) * A)
  *                     + kl_coef * (exp(ref_logp - logp) - (ref_logp - logp) - 1))
@@ -687,7 +688,8 @@ typedef struct {
  * weights: NULL takes 1 (1 / tokens, or 1 / (sequences * tokens of the sequence),
  * are usual).  All binary32, one per row.
  * loss: one binary32, or NULL.  token_loss, logp: one binary32 per row.
- * dlogits: NULL computes no gradient.  rows == 0 gives loss 0.
+ * dlogits: NULL computes no gradient; the losses are the same bit for bit.  rows ==
+ * 0 gives loss 0.
  */
 rr_status rr_policy_loss(const void *logits, const int64_t *targets, const float *old_logp, const float *ref_logp,
                          const float *advantages, const float *weights, float *loss, float *token_loss, float *logp,
