@@ -80,6 +80,10 @@ struct GradArgs {
     SumArgs sum;             // of the pairs' losses, by the first block; loss NULL: none
 };
 
+// An offset kept to the rows on both sides: what rows are counted from must not
+// wrap where a thread's number or a stretch of rows is added to it.
+__device__ __forceinline__ int64_t row_within(int64_t offset, int64_t rows) { return min(max(offset, (int64_t)0), rows); }
+
 __device__ __forceinline__ float exp2_fast(float x)
 {
     float y;
@@ -315,8 +319,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) row_kernel(const __grid_con
     int64_t row = blockIdx.x / parts, end = a.rows;
     const int64_t every = gridDim.x / parts;
     if (MODE == kPreference) {
-        const int64_t first = a.offsets[0];
-        end = min(end, a.offsets[a.last]);
+        const int64_t first = row_within(a.offsets[0], a.rows);
+        end = row_within(a.offsets[a.last], a.rows);
         if (first > row) row += (first - row + every - 1) / every * every;
     }
     int turn = 0;
@@ -413,8 +417,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) row_grad_kernel(const __gri
     if (blockIdx.x == 0 && a.sum.loss) take_sum(a.sum, s);
     int64_t first = 0, end = a.rows;
     if (a.offsets) {
-        first = max((int64_t)0, a.offsets[0]);
-        end = min(end, a.offsets[a.last]);
+        first = row_within(a.offsets[0], a.rows);
+        end = row_within(a.offsets[a.last], a.rows);
     }
     const int64_t every = gridDim.x / parts;
     const int part = (int)(blockIdx.x % parts);
@@ -455,8 +459,8 @@ __global__ void __launch_bounds__(kThreads) pair_kernel(const __grid_constant__ 
     double mean[2], count[2];
     for (int k = 0; k < 2; ++k) {
         const int q = p + k * a.pairs;
-        lo[k] = max((int64_t)0, a.offsets[q]);
-        hi[k] = min(a.rows, a.offsets[q + 1]);
+        lo[k] = row_within(a.offsets[q], a.rows);
+        hi[k] = row_within(a.offsets[q + 1], a.rows);
         double sum = 0.0, n = 0.0;
         for (int64_t i = lo[k] + threadIdx.x; i < hi[k]; i += kThreads) {
             const int64_t t = a.target[i];
