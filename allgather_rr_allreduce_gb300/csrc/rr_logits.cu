@@ -56,9 +56,11 @@ struct RowArgs {
     float *token_loss;
     void *dx;
     int64_t dx_stride;
-    // preference loss: rows of [offsets[0], offsets[last]) only
+    // preference loss: rows of [offsets[0], offsets[last]) only; what the gradient takes
+    // probabilities from
     const int64_t *offsets;
     int last;
+    float *base, *over;
 };
 
 // loss = sum / count, in one order.
@@ -71,7 +73,9 @@ struct SumArgs {
 struct GradArgs {
     const void *x;
     const int64_t *target;
-    const float *lse, *dlogp;
+    const float *lse;          // or each row's maximum and 1 / sum:
+    const float *base, *over;
+    const float *dlogp;
     void *dx;
     int64_t rows, vocab, stride, dx_stride;
     float inv_t, log2_scale;
@@ -331,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) row_kernel(const __grid_con
         if (target < 0 || target >= a.vocab) {  // the same for every block of the cluster
             if (part == 0 && threadIdx.x == 0) {
                 a.logp[row] = 0.0f;
-                if (MODE != kPolicy && a.lse) a.lse[row] = 0.0f;
+                if (MODE == kLogp && a.lse) a.lse[row] = 0.0f;
                 if (MODE == kPolicy) a.token_loss[row] = 0.0f;
             }
             if (MODE == kPolicy && dx) row_zero(dx, a.vocab, part, parts);
@@ -364,7 +368,11 @@ __global__ void __launch_bounds__(kThreads, kBlocks) row_kernel(const __grid_con
         const bool first = part == 0 && threadIdx.x == 0;
         if (first) {
             a.logp[row] = logp;
-            if (MODE != kPolicy && a.lse) a.lse[row] = s.top * a.inv_t + log_sum;
+            if (MODE == kLogp && a.lse) a.lse[row] = s.top * a.inv_t + log_sum;
+            if (MODE == kPreference) {
+                a.base[row] = base_of(s.top);
+                a.over[row] = 1.0f / s.sum;
+            }
         }
         if (MODE == kPolicy) {
             const float weight = a.weight ? a.weight[row] : 1.0f, adv = a.advantage[row];
@@ -408,7 +416,10 @@ __device__ __forceinline__ void take_sum(const SumArgs &a, double *s)
 }
 
 // The gradient of log-probabilities whose sums are known: a row to a block, or
-// to `parts` blocks that do not meet.
+// to `parts` blocks that do not meet.  exp(z - lse) carries lse's rounding, 1e-5 of
+// a probability where logits lie around 1000; it is what rr_token_logp_backward's
+// caller hands over.  The preference loss keeps the maximum and the sum apart
+// (3e-7 wherever logits lie).
 template <class T>
 __global__ void __launch_bounds__(kThreads, kBlocks) row_grad_kernel(const __grid_constant__ GradArgs a, int parts)
 {
@@ -430,8 +441,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks) row_grad_kernel(const __gri
         if (target < 0 || target >= a.vocab)
             row_zero(dx, a.vocab, part, parts);
         else
-            row_grad<false>(x, dx, slice_of(x, a.vocab, part, parts), a.vocab, target, a.lse[row] / a.inv_t, a.log2_scale,
-                     a.dlogp[row] * a.inv_t, 1.0f);
+            row_grad<false>(x, dx, slice_of(x, a.vocab, part, parts), a.vocab, target,
+                            a.lse ? a.lse[row] / a.inv_t : a.base[row], a.log2_scale, a.dlogp[row] * a.inv_t,
+                            a.lse ? 1.0f : a.over[row]);
     }
 }
 
@@ -630,7 +642,7 @@ rr_status launch_sum(const float *part, int64_t n, double count, float *loss, cu
     return step_launch((const void *)sum_kernel, 1, kThreads, 0, &a, stream);
 }
 
-// Workspace of the preference loss: each row's log-sum and slope, each pair's loss.
+// Workspace of the preference loss: each row's maximum, 1 / sum and slope, each pair's loss.
 int64_t padded(int64_t floats) { return (floats + 3) & ~(int64_t)3; }
 
 }  // namespace
@@ -686,7 +698,7 @@ try {
     const Range out[] = {{"dlogits", dlogits, span(rows, dlogits_stride, vocab, eb)}};
     const Range in[] = {{"targets", targets, rows * 8}, {"lse", lse, rows * 4}, {"dlogp", dlogp, rows * 4}};
     RR_TRY(check_apart(out, in));
-    GradArgs a{logits, targets, lse, dlogp, dlogits, rows, vocab, logits_stride, dlogits_stride, inv_temperature,
+    GradArgs a{logits, targets, lse, nullptr, nullptr, dlogp, dlogits, rows, vocab, logits_stride, dlogits_stride, inv_temperature,
                log2_scale(inv_temperature), nullptr, 0, {}};
     RR_TRY(launch_grad(a, dtype, stream));
     return step_ok();
@@ -763,7 +775,7 @@ extern "C" rr_status rr_preference_loss_workspace(int64_t rows, int pairs, size_
     if (!bytes) return step_fail(RR_ERR_INVALID_ARG, "bytes is NULL");
     if (rows < 0 || rows > kMaxRows) return step_fail(RR_ERR_INVALID_ARG, "rows %lld", (long long)rows);
     if (pairs < 1 || pairs > kMaxPairs) return step_fail(RR_ERR_INVALID_ARG, "pairs %d", pairs);
-    *bytes = (size_t)(2 * padded(rows) + padded(pairs)) * 4;
+    *bytes = (size_t)(3 * padded(rows) + padded(pairs)) * 4;
     return step_ok();
 }
 
@@ -807,7 +819,8 @@ try {
     const Range din[] = {in[1], in[2], in[3]};
     RR_TRY(check_apart(dout, din));
 
-    float *lse = static_cast<float *>(workspace), *slope = lse + padded(rows), *pair_loss = slope + padded(rows);
+    float *base = static_cast<float *>(workspace), *over = base + padded(rows), *slope = over + padded(rows);
+    float *pair_loss = slope + padded(rows);
     if (rows > 0) {
         RowArgs a = {};
         a.x = logits;
@@ -818,7 +831,8 @@ try {
         a.inv_t = inv_t;
         a.log2_scale = log2_scale(inv_t);
         a.logp = logp;
-        a.lse = lse;
+        a.base = base;
+        a.over = over;
         a.offsets = offsets;
         a.last = (int)seqs;
         RR_TRY(launch_rows(row_fn<kPreference>(dtype), a, dtype, false, stream));
@@ -830,7 +844,7 @@ try {
     if (rows == 0 || !dlogits) {
         RR_TRY(launch_sum(pair_loss, pairs, (double)pairs, loss, stream));
     } else {
-        GradArgs g{logits, targets, lse, slope, dlogits, rows, vocab, logits_stride, dlogits_stride, inv_t,
+        GradArgs g{logits, targets, nullptr, base, over, slope, dlogits, rows, vocab, logits_stride, dlogits_stride, inv_t,
                    log2_scale(inv_t), offsets, (int)seqs, {pair_loss, pairs, (double)pairs, loss}};
         RR_TRY(launch_grad(g, dtype, stream));
     }
