@@ -84,6 +84,14 @@ struct GradArgs {
     SumArgs sum;             // of the pairs' losses, by the first block; loss NULL: none
 };
 
+// A product in which a factor of 0 leaves out what it multiplies, also where that is
+// infinite (a masked target, or what binary32 does not hold).  NaN stays NaN.
+__device__ __forceinline__ float times(float x, float y)
+{
+    const float p = x * y;
+    return (x == 0.0f && y == y) || (y == 0.0f && x == x) ? 0.0f : p;
+}
+
 // An offset kept to the rows on both sides: what rows are counted from must not
 // wrap where a thread's number or a stretch of rows is added to it.
 __device__ __forceinline__ int64_t row_within(int64_t offset, int64_t rows) { return min(max(offset, (int64_t)0), rows); }
@@ -489,7 +497,7 @@ __global__ void __launch_bounds__(kThreads) pair_kernel(const __grid_constant__ 
     double gap = mean[0] - mean[1];
     if (a.ref) gap -= (double)a.ref[p] - (double)a.ref[p + a.pairs];
     const float h = (float)((double)a.beta * gap - (double)a.margin);
-    if (threadIdx.x == 0) a.loss[p] = (1.0f - a.smoothing) * softplus(-h) + a.smoothing * softplus(h);
+    if (threadIdx.x == 0) a.loss[p] = times(1.0f - a.smoothing, softplus(-h)) + times(a.smoothing, softplus(h));
     if (!a.slope) return;
     // d loss / d h = smoothing * sigmoid(h) - (1 - smoothing) * sigmoid(-h)
     const float e = expf(-fabsf(h)), small = e / (1.0f + e), large = 1.0f / (1.0f + e);

@@ -713,6 +713,8 @@ typedef struct {
  *   loss = mean over pairs of (1 - label_smoothing) * log(1 + exp(-h))
  *                             + label_smoothing * log(1 + exp(h)),
  *   dlogits = grad_scale * d loss / d logits.
+ * A term whose factor is 0 is left out, also where it is infinite (a masked target in
+ * a rejected sequence without label smoothing costs nothing).
  *
  * offsets: DEVICE array of 2 * pairs + 1 int64, not decreasing, within [0, rows]
  * (kept to that range where they are not; results are then unspecified).  Rows
