@@ -385,18 +385,23 @@ __global__ void __launch_bounds__(kThreads, kBlocks) row_kernel(const __grid_con
         if (MODE == kPolicy) {
             const float weight = a.weight ? a.weight[row] : 1.0f, adv = a.advantage[row];
             const float ratio = a.old_logp ? expf(logp - a.old_logp[row]) : 1.0f;
-            const float free = ratio * adv, held = fminf(fmaxf(ratio, a.low), a.high) * adv;
+            const float free = times(ratio, adv), held = times(fminf(fmaxf(ratio, a.low), a.high), adv);
             const bool passes = !(free > held);  // NaN passes
-            float loss = passes ? -free : -held, slope = passes ? -free : 0.0f;
+            const float loss = passes ? -free : -held, slope = passes ? -free : 0.0f;
+            float apart = 0.0f, pull = 0.0f;  // of the KL term
             if (a.ref_logp) {
                 const float gap = a.ref_logp[row] - logp, back = expm1f(gap);
-                loss += a.kl * (back - gap);
-                slope -= a.kl * back;
+                apart = times(a.kl, back < INFINITY ? back - gap : back);  // of a masked target both are infinite
+                pull = times(a.kl, back);
             }
-            if (first) a.token_loss[row] = loss * weight;
+            // without a factor the parts are 0 each: infinite ones do not meet first
+            if (first)
+                a.token_loss[row] = weight == 0.0f ? times(loss, 0.0f) + times(apart, 0.0f) : (loss + apart) * weight;
             if (dx)
-                row_grad<true>(x, dx, slice, a.vocab, target, base_of(s.top), a.log2_scale, slope * weight * a.grad_scale * a.inv_t,
-                         1.0f / s.sum);
+                row_grad<true>(x, dx, slice, a.vocab, target, base_of(s.top), a.log2_scale,
+                               weight == 0.0f || a.grad_scale == 0.0f ? times(slope, 0.0f) + times(pull, 0.0f)
+                                                                      : (slope - pull) * weight * a.grad_scale * a.inv_t,
+                               1.0f / s.sum);
         }
     }
     if (parts > 1) cluster.sync();  // a block's shared memory stays until the others have read it

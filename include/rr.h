@@ -682,6 +682,8 @@ typedef struct {
  *                     + kl_coef * (exp(ref_logp - logp) - (ref_logp - logp) - 1))
  *   loss       = sum of token_loss over the rows,
  *   dlogits    = grad_scale * d loss / d logits.
+ * A factor of 0 (an advantage, a weight, kl_coef, grad_scale) leaves out what it
+ * multiplies, also where that is infinite in binary32; NaN stays NaN.
  *
  * old_logp: NULL takes logp itself (ratio 1, a first step on fresh rollouts; its
  * gradient is the policy's, -A).  ref_logp: NULL leaves the KL term out.
