@@ -41,6 +41,9 @@ constexpr int kMostCluster = 8; // blocks that share a row
 constexpr int64_t kMaxVocab = (int64_t)1 << 31;
 constexpr int64_t kMaxRows = (int64_t)1 << 40;
 constexpr int kMaxPairs = 1 << 24;
+// So that neither 1 / (temperature * log(2)) nor a log-sum times the temperature
+// leaves binary32's range.
+constexpr float kMinInvT = 0x1p-120f, kMaxInvT = 0x1p127f;
 
 enum Mode { kLogp, kPolicy, kPreference };
 
@@ -554,7 +557,7 @@ rr_status check_rows(int64_t rows, int64_t vocab, int64_t stride, float inv_t, r
     if (rows > 1 && (stride < vocab || stride > kMaxRows))
         return step_fail(RR_ERR_INVALID_ARG, "logits_stride %lld, vocab %lld", (long long)stride, (long long)vocab);
     if (rows > 1 && rows > INT64_MAX / 8 / stride) return step_fail(RR_ERR_INVALID_ARG, "rows %lld of logits_stride %lld", (long long)rows, (long long)stride);
-    if (!(inv_t > 0.0f && std::isfinite(inv_t))) return step_fail(RR_ERR_INVALID_ARG, "inv_temperature %g", (double)inv_t);
+    if (!(inv_t >= kMinInvT && inv_t <= kMaxInvT)) return step_fail(RR_ERR_INVALID_ARG, "inv_temperature %g", (double)inv_t);
     return RR_OK;
 }
 rr_status check_grad(const void *logits, const void *dlogits, int64_t rows, int64_t vocab, int64_t stride,

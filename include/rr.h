@@ -635,7 +635,7 @@ rr_status rr_muon(void *const *params, const void *const *grads, float *const *m
  *    apart; targets: one int64 per row, the token whose probability counts.  A
  *    row whose target lies outside [0, vocab) (-100, say) takes no part: its
  *    logits are not read, its log-probability and loss are 0 and its gradient
- *    is zeros.  With z = logits * inv_temperature (> 0),
+ *    is zeros.  With z = logits * inv_temperature (2^-120 to 2^127),
  *      logp = z[target] - log(sum of exp(z)).
  *    -inf masks a token out; a row of nothing but -inf gives NaN, as does one
  *    that holds +inf or NaN.
