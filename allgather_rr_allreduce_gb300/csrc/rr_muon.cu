@@ -32,6 +32,7 @@
 #include <mutex>
 #include <vector>
 
+#include "rr_ring.h"
 #include "rr_spans.h"
 #include "rr_step.h"
 
@@ -397,20 +398,6 @@ __device__ __forceinline__ void cluster_sync()
 __device__ __forceinline__ void fence_tmem_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_tmem_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// A place in a ring, and the parity of the barrier phase that belongs to it.
-template <int N>
-struct Turn {
-    int at = 0, phase;
-    __device__ __forceinline__ explicit Turn(int first) : phase(first) {}
-    __device__ __forceinline__ void next()
-    {
-        if (++at == N) {
-            at = 0;
-            phase ^= 1;
-        }
-    }
-};
-
 // An operand in shared memory, 128-byte swizzle.  Rows of K values: groups of 8
 // rows lie 1024 bytes apart.  Columns (K rows of 64 values): groups of 8 K rows
 // lie 1024 bytes apart, the next 64 columns 8192.
@@ -693,26 +680,29 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kGemmThreads, 1) product_k
         const uint32_t mine = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * S::half;
         const bool skip = a.grad_scale && isnan(*a.grad_scale);
         Turn<2> acc(0);
+        bool ok = true;
         for (int unit = first_unit; unit < units; unit += every) {
             float v[S::half];
 #pragma unroll
             for (int k = 0; k < S::half; ++k) v[k] = 0.0f;
-            bool ok = true;
-            for (int k = job_of<N>(a, unit).depth; k > 0; --k, acc.next()) {
-                ok = mbar_wait(done + 8 * acc.at, acc.phase, dead) && ok;
-                fence_tmem_after();
-                __syncwarp();
+            ok = take_turns(
+                ok, acc, job_of<N>(a, unit).depth,
+                [&](const Turn<2> &t) { return __all_sync(~0u, mbar_wait(done + 8 * t.at, t.phase, dead)) != 0; },
+                [&](const Turn<2> &t) {
+                    fence_tmem_after();
 #pragma unroll
-                for (int q = 0; q < S::half / 16; ++q) {
-                    float t[16];
-                    tmem_load(t, mine + acc.at * N + q * 16);
+                    for (int q = 0; q < S::half / 16; ++q) {
+                        float x[16];
+                        tmem_load(x, mine + t.at * N + q * 16);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) v[q * 16 + e] += t[e];
-                }
-                fence_tmem_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_first(free + 8 * acc.at);
-            }
+                        for (int e = 0; e < 16; ++e) v[q * 16 + e] += x[e];
+                    }
+                    fence_tmem_before();
+                    __syncwarp();
+                },
+                [&](const Turn<2> &t) {
+                    if (lane == 0) mbar_arrive_first(free + 8 * t.at);
+                });
             if (!ok) {
 #pragma unroll
                 for (int k = 0; k < S::half; ++k) v[k] = __int_as_float(0x7fc00000);
@@ -751,8 +741,8 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kGemmThreads, 1) product_k
                     else fetch_rows<S::half>(right, sq, it.mt, cols, k, bar);
                 }
             }
-            // a block that gave up waits for its copies before its shared memory goes
-            for (int s = 0; s < S::stages && !ok; ++s, turn.next()) {
+            // a block waits for its copies before its shared memory goes, whichever thread gave up
+            for (int s = 0; s < S::stages; ++s, turn.next()) {
                 volatile int late = 0;
                 mbar_wait(full + 8 * turn.at, turn.phase, &late);
             }
