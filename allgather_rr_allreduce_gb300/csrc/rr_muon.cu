@@ -105,7 +105,7 @@ struct Args {
     int count;
     int src_dtype, out_dtype;
     double eps;
-    float momentum, keep;  // beta; 1 - lr * weight_decay
+    float momentum, fresh, keep;  // beta; 1 - beta and 1 - lr * weight_decay, formed in binary64
     bool nesterov;
     const float *grad_scale;
     float ca, cb, cc;      // this iteration's coefficients
@@ -140,9 +140,9 @@ __host__ __device__ __forceinline__ int sum_blocks(int64_t size)
     const int64_t n = (size + 16383) / 16384;
     return (int)(n < kSumBlocks ? n : kSumBlocks);
 }
-__device__ __forceinline__ float update_of(float g, float m, float beta, bool nesterov)
+__device__ __forceinline__ float update_of(float g, float m, float beta, float fresh, bool nesterov)
 {
-    return nesterov ? (1.0f - beta) * g + beta * m : m;
+    return nesterov ? fresh * g + beta * m : m;
 }
 
 // Four consecutive elements, aligned to their size.
@@ -208,8 +208,8 @@ __global__ void __launch_bounds__(kThreads) sums_kernel(const __grid_constant__ 
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float g = v[j] * gs;
-                m[j] = a.momentum * m[j] + (1.0f - a.momentum) * g;
-                v[j] = update_of(g, m[j], a.momentum, a.nesterov);
+                m[j] = a.momentum * m[j] + a.fresh * g;
+                v[j] = update_of(g, m[j], a.momentum, a.fresh, a.nesterov);
             }
             if (whole) {
                 *reinterpret_cast<float4 *>(it.momentum + e) = make_float4(m[0], m[1], m[2], m[3]);
@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const __grid_constant__
     const float by = (float)divisor;
     const bool plain = by >= 0x1p-100f && by <= 0x1p100f;
     auto scaled = [&](float g, float m) {
-        const float v = step ? update_of(g * gs, m, a.momentum, a.nesterov) : g;
+        const float v = step ? update_of(g * gs, m, a.momentum, a.fresh, a.nesterov) : g;
         return (plain ? v / by : (float)((double)v / divisor)) * kScale;
     };
     char *block = it.x + (int64_t)u * kBlock;
@@ -919,6 +919,7 @@ rr_status run_lists(const Call &c, int sms, cudaStream_t stream)
     a.out_dtype = (int)c.out_dtype;
     a.eps = c.eps;
     a.momentum = c.hyper ? (float)c.hyper->momentum : 0.0f;
+    a.fresh = c.hyper ? (float)(1.0 - c.hyper->momentum) : 0.0f;
     a.keep = c.hyper ? (float)(1.0 - c.hyper->lr * c.hyper->weight_decay) : 0.0f;
     a.nesterov = c.hyper && c.hyper->nesterov;
     a.grad_scale = c.grad_scale;
