@@ -687,9 +687,10 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kGemmThreads, 1) product_k
             for (int k = 0; k < S::half; ++k) v[k] = 0.0f;
             ok = take_turns(
                 ok, acc, job_of<N>(a, unit).depth,
-                [&](const Turn<2> &t) { return __all_sync(~0u, mbar_wait(done + 8 * t.at, t.phase, dead)) != 0; },
+                [&](const Turn<2> &t) { return mbar_wait(done + 8 * t.at, t.phase, dead); },
                 [&](const Turn<2> &t) {
                     fence_tmem_after();
+                    __syncwarp();
 #pragma unroll
                     for (int q = 0; q < S::half / 16; ++q) {
                         float x[16];
@@ -700,7 +701,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kGemmThreads, 1) product_k
                     fence_tmem_before();
                     __syncwarp();
                 },
-                [&](const Turn<2> &t) {
+                [&](const Turn<2> &t) {  // by lane 0 for the warp
                     if (lane == 0) mbar_arrive_first(free + 8 * t.at);
                 });
             if (!ok) {

@@ -25,19 +25,19 @@ struct Turn {
 };
 
 // Waits for `depth` turns one after the other, takes each and lets it go again.
-// `ok` is what became of the turns before: once a wait has run out, nothing later
-// counts, in this stretch or in one after it.  A barrier's parity tells a phase from
-// the next one only, so one that stands still would look complete again two phases
-// on; and a place that was not taken is not let go, or others would lose what lies
-// there.
+// `ok` is what became of a thread's turns before: once a wait has run out, nothing
+// later counts, in this stretch or in one after it.  A barrier's parity tells a phase
+// from the next one only, so one that stands still would look complete again two
+// phases on; and what a thread was too late for it does not let go, or others would
+// lose what lies there.  It takes all turns, as the threads of its warp take them
+// together (what it takes then is no use, and ok says so).
 template <int N, class Wait, class Take, class Release>
 RR_HD bool take_turns(bool ok, Turn<N> &turn, int depth, Wait wait, Take take, Release release)
 {
-    for (; ok && depth > 0; --depth, turn.next()) {
-        ok = wait(turn);
-        if (!ok) break;
+    for (; depth > 0; --depth, turn.next()) {
+        ok = ok && wait(turn);
         take(turn);
-        release(turn);
+        if (ok) release(turn);
     }
     return ok;
 }
