@@ -168,6 +168,9 @@ __device__ __forceinline__ bool aligned4(const void *p, int dtype)
     return (reinterpret_cast<uintptr_t>(p) & (dtype == RR_FP32 ? 15 : 7)) == 0;
 }
 
+// A step whose gradient scale is NaN is skipped: every kernel of it leaves at once,
+// and reads and writes nothing else.
+//
 // The new momentum, and the sum of squares of what is orthogonalised.  Eight
 // squares are added in binary32; such a sum outside [2^-90, 2^90] (zero aside) is
 // taken again in binary64, and so is the sum of the sums.  Bound: HBM.
@@ -273,6 +276,7 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const __grid_constant__
     const int r0 = u / nb * kTile, c0 = u % nb * kK;
     const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
     const bool step = it.momentum != nullptr;
+    if (step && isnan(gs)) return;
     const int blocks = sum_blocks(it.size);
     double total = 0.0;
     for (int k = threadIdx.x; k < blocks; k += kThreads) total += it.part[k];
@@ -556,10 +560,10 @@ __device__ __forceinline__ void store_pieces(const Args<CAP> &a, const Item &it,
 // Sums of 32 rows (from row0 on) and M columns (from block column cb0 on) of a
 // product to where the stage puts them.
 template <int M, int CAP>
-__device__ __forceinline__ void finish(const Args<CAP> &a, const Item &it, float (&v)[M], int row0, int cb0, int wide, bool skip,
-                                       float *desk, int lane)
+__device__ __forceinline__ void finish(const Args<CAP> &a, const Item &it, float (&v)[M], int row0, int cb0, int wide, float *desk,
+                                       int lane)
 {
-    if (a.stage == kStageLast && ((it.momentum && skip) || row0 >= it.m)) return;
+    if (a.stage == kStageLast && row0 >= it.m) return;
     char *to = a.stage == kStageGram ? it.a : a.stage == kStageSquare ? it.b : a.swap ? it.x : it.y;
     const int64_t block0 = ((int64_t)(row0 / kTile) * wide * 2 + cb0) * kBlock + row0 % kTile * 128;
 #pragma unroll 1
@@ -673,12 +677,14 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kGemmThreads, 1) product_k
     const bool next = a.stage >= kStageNext;
     const int units = a.start[S::units(next)][a.count], first_unit = blockIdx.x / 2, every = gridDim.x / 2;
 
-    if (warp < kSumWarps) {
+    // (Read here: on its way while the accumulators are made it cost every launch 0.1 us.)
+    if (a.grad_scale && isnan(*a.grad_scale)) {
+        // a step that is skipped
+    } else if (warp < kSumWarps) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegisters));
         const int half = warp >> 2;  // of the tile's columns
         float *desk = reinterpret_cast<float *>(base + S::desks + warp * kDesk);
         const uint32_t mine = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * S::half;
-        const bool skip = a.grad_scale && isnan(*a.grad_scale);
         Turn<2> acc(0);
         bool ok = true;
         for (int unit = first_unit; unit < units; unit += every) {
@@ -711,7 +717,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kGemmThreads, 1) product_k
             const Job j = job_of<N>(a, unit);
             const Item &it = *j.it;
             const int rt = j.ti * 2 + (int)rank, cb = (j.tj * 2 + half) * (S::half / kK), wide = next ? it.nt : it.mt;
-            if (rt < it.mt && cb < wide * 2) finish(a, it, v, rt * kTile + (warp & 3) * 32, cb, wide, skip, desk, lane);
+            if (rt < it.mt && cb < wide * 2) finish(a, it, v, rt * kTile + (warp & 3) * 32, cb, wide, desk, lane);
         }
         asm volatile("fence.proxy.async.global;" ::: "memory");  // the next product fetches it by bulk copies
     } else {
