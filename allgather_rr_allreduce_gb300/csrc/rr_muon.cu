@@ -825,6 +825,16 @@ Sizes sizes_of(int64_t rows, int64_t cols)
     return s;
 }
 
+// A matrix's units of work in each kind of launch.
+struct Units {
+    int64_t of[kKinds];
+};
+Units units_of(const Sizes &s)
+{
+    const int64_t mp = (s.mt + 1) / 2, np = (s.nt + 1) / 2;  // pairs' tiles
+    return {{sum_blocks((int64_t)s.m * s.n), (int64_t)s.mt * s.nt * 2, mp * (mp + 1) / 2, mp * np, mp * (mp + 1), mp * s.nt}};
+}
+
 rr_status check_shapes(const int64_t *rows, const int64_t *cols, int count)
 {
     if (count < 0) return step_fail(RR_ERR_INVALID_ARG, "num_tensors %d", count);
@@ -833,6 +843,24 @@ rr_status check_shapes(const int64_t *rows, const int64_t *cols, int count)
         if (rows[i] < 0 || rows[i] > kMaxSide) return step_fail(RR_ERR_INVALID_ARG, "rows[%d] is %lld", i, (long long)rows[i]);
         if (cols[i] < 0 || cols[i] > kMaxSide) return step_fail(RR_ERR_INVALID_ARG, "cols[%d] is %lld", i, (long long)cols[i]);
     }
+    return RR_OK;
+}
+// The list as run_lists works through it, kCap matrices at a time (empty ones aside):
+// whether each table's launches can count their units; the workspace's bytes.
+rr_status check_list(const int64_t *rows, const int64_t *cols, int count, size_t *bytes)
+{
+    Units all = {};
+    int64_t sum = 0;
+    for (int i = 0, k = 0; i < count; ++i) {
+        if (rows[i] * cols[i] == 0) continue;
+        if (k++ % kCap == 0) all = {};
+        const Sizes s = sizes_of(rows[i], cols[i]);
+        const Units units = units_of(s);
+        bool fits = !__builtin_add_overflow(sum, s.all(), &sum);
+        for (int q = 0; q < kKinds; ++q) fits = fits && (all.of[q] += units.of[q]) <= INT32_MAX;
+        if (!fits) return step_fail(RR_ERR_INVALID_ARG, "the list's matrices are too large for one call");
+    }
+    *bytes = (size_t)sum;
     return RR_OK;
 }
 rr_status check_pointers(const char *name, const void *const *p, const int64_t *rows, const int64_t *cols, int count,
@@ -965,14 +993,8 @@ rr_status run_lists(const Call &c, int sms, cudaStream_t stream)
                 it.scale = (float)(c.hyper->lr * (c.hyper->adjust == RR_MUON_RMS ? 0.2 * std::sqrt(std::max(r, l))
                                                                                  : std::sqrt(std::max(1.0, r / l))));
             }
-            const int64_t mp = (s.mt + 1) / 2, np = (s.nt + 1) / 2;  // pairs' tiles
-            const int64_t units[kKinds] = {sum_blocks(it.size), (int64_t)s.mt * s.nt * 2, mp * (mp + 1) / 2, mp * np,
-                                           mp * (mp + 1), mp * s.nt};
-            for (int q = 0; q < kKinds; ++q) {
-                if (a.start[q][k] + units[q] > INT32_MAX)
-                    return step_fail(RR_ERR_INVALID_ARG, "the list's matrices are too large for one call");
-                a.start[q][k + 1] = (int)(a.start[q][k] + units[q]);
-            }
+            const Units units = units_of(s);
+            for (int q = 0; q < kKinds; ++q) a.start[q][k + 1] = (int)(a.start[q][k] + units.of[q]);  // see check_list
             ++k;
         }
         if (k == 0) break;
@@ -1015,11 +1037,7 @@ extern "C" rr_status rr_orthogonalize_workspace(const int64_t *rows, const int64
 {
     if (!bytes) return step_fail(RR_ERR_INVALID_ARG, "bytes is NULL");
     RR_TRY(check_shapes(rows, cols, num_tensors));
-    int64_t sum = 0;
-    for (int i = 0; i < num_tensors; ++i)
-        if (rows[i] * cols[i] > 0 && __builtin_add_overflow(sum, sizes_of(rows[i], cols[i]).all(), &sum))
-            return step_fail(RR_ERR_INVALID_ARG, "the list's matrices are too large for one call");
-    *bytes = (size_t)sum;
+    RR_TRY(check_list(rows, cols, num_tensors, bytes));
     return step_ok();
 }
 

@@ -580,7 +580,8 @@ rr_status rr_adamw8(void *const *params, const void *const *grads, uint8_t *cons
  *
  * x, y: HOST arrays of num_tensors (>= 0) device pointers to dense row-major
  * matrices of rows[i] x cols[i] elements, of x_dtype and y_dtype; sides up to
- * 2^20, empty matrices (and NULL for them) allowed.  y[i] == x[i] of one type
+ * 2^20, empty matrices (and NULL for them) allowed; 160 matrices in a row of more
+ * than 2^31 - 1 blocks of 128 x 64 together are refused.  y[i] == x[i] of one type
  * works in place; nothing else written may overlap anything (RR_ERR_ALIAS).
  * coefs: HOST array of 3 * steps coefficients, 1 <= steps <= 64.
  * workspace: see rr_orthogonalize_workspace; about 8 bytes an element and 8 more
