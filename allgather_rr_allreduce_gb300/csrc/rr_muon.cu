@@ -846,21 +846,27 @@ rr_status check_shapes(const int64_t *rows, const int64_t *cols, int count)
     return RR_OK;
 }
 // The list as run_lists works through it, kCap matrices at a time (empty ones aside):
-// whether each table's launches can count their units; the workspace's bytes.
+// whether each table's launches can count their units; bytes: of the largest table's
+// workspace, as the tables come one after the other.
 rr_status check_list(const int64_t *rows, const int64_t *cols, int count, size_t *bytes)
 {
     Units all = {};
-    int64_t sum = 0;
+    int64_t sum = 0, most = 0;
     for (int i = 0, k = 0; i < count; ++i) {
         if (rows[i] * cols[i] == 0) continue;
-        if (k++ % kCap == 0) all = {};
+        if (k++ % kCap == 0) {
+            all = {};
+            sum = 0;
+        }
         const Sizes s = sizes_of(rows[i], cols[i]);
         const Units units = units_of(s);
-        bool fits = !__builtin_add_overflow(sum, s.all(), &sum);
+        bool fits = true;
         for (int q = 0; q < kKinds; ++q) fits = fits && (all.of[q] += units.of[q]) <= INT32_MAX;
+        sum += s.all();  // of fewer than 2^31 blocks
+        most = std::max(most, sum);
         if (!fits) return step_fail(RR_ERR_INVALID_ARG, "the list's matrices are too large for one call");
     }
-    *bytes = (size_t)sum;
+    *bytes = (size_t)most;
     return RR_OK;
 }
 rr_status check_pointers(const char *name, const void *const *p, const int64_t *rows, const int64_t *cols, int count,
@@ -960,12 +966,12 @@ rr_status run_lists(const Call &c, int sms, cudaStream_t stream)
     a.grad_scale = c.grad_scale;
     a.stage = a.swap = 0;
     a.ca = a.cb = a.cc = 0.0f;
-    char *at = c.workspace;
     RR_TRY((product_ready<256, CAP>()));
     RR_TRY((product_ready<128, CAP>()));
     const int64_t pairs = std::max(1, sms / 2);
     for (int i = 0; i < c.count;) {
         int k = 0;
+        char *at = c.workspace;
         for (int q = 0; q < kKinds; ++q) a.start[q][0] = 0;
         for (; i < c.count && k < CAP; ++i) {
             if (c.rows[i] * c.cols[i] == 0) continue;

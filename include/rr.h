@@ -585,7 +585,7 @@ rr_status rr_adamw8(void *const *params, const void *const *grads, uint8_t *cons
  * works in place; nothing else written may overlap anything (RR_ERR_ALIAS).
  * coefs: HOST array of 3 * steps coefficients, 1 <= steps <= 64.
  * workspace: see rr_orthogonalize_workspace; about 8 bytes an element and 8 more
- * for each of the short side squared.
+ * for each of the short side squared, of the 160 matrices in a row that need most.
  * A call is 2 + 3 * steps launches for each 160 matrices.  Every wait in them is
  * bounded; a block whose wait ran out (two seconds) leaves NaN in its results.
  */
