@@ -410,24 +410,11 @@ __global__ void __launch_bounds__(kThreads, kBlocks) row_kernel(const __grid_con
     if (parts > 1) cluster.sync();  // a block's shared memory stays until the others have read it
 }
 
-// Sum of a block's values in binary64, the same in every thread.
-__device__ __forceinline__ double block_sum(double x, double *s)
-{
-#pragma unroll
-    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = x;
-    __syncthreads();
-    x = 0.0;
-    for (int i = 0; i < kWarps; ++i) x += s[i];
-    return x;
-}
-
 __device__ __forceinline__ void take_sum(const SumArgs &a, double *s)
 {
     double sum = 0.0;
     for (int64_t i = threadIdx.x; i < a.n; i += kThreads) sum += (double)a.part[i];
-    sum = block_sum(sum, s);
+    sum = block_sum64<kWarps>(sum, s);
     if (threadIdx.x == 0) *a.loss = (float)(sum / a.count);
 }
 
@@ -497,8 +484,8 @@ __global__ void __launch_bounds__(kThreads) pair_kernel(const __grid_constant__ 
                 n += 1.0;
             }
         }
-        sum = block_sum(sum, s);
-        count[k] = a.average ? fmax(1.0, block_sum(n, s)) : 1.0;
+        sum = block_sum64<kWarps>(sum, s);
+        count[k] = a.average ? fmax(1.0, block_sum64<kWarps>(n, s)) : 1.0;
         mean[k] = sum / count[k];
         if (threadIdx.x == 0) a.seq_logp[q] = (float)mean[k];
     }

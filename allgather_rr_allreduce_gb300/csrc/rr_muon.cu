@@ -123,18 +123,6 @@ struct Args {
 };
 
 // ---------------------------------------------------------------- norm and momentum
-// Sum of a block's values in binary64, the same in every thread.
-__device__ __forceinline__ double block_sum(double x, double *s)
-{
-#pragma unroll
-    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = x;
-    __syncthreads();
-    x = 0.0;
-    for (int i = 0; i < kThreads / 32; ++i) x += s[i];
-    return x;
-}
 __host__ __device__ __forceinline__ int sum_blocks(int64_t size)
 {
     const int64_t n = (size + 16383) / 16384;
@@ -236,7 +224,7 @@ __global__ void __launch_bounds__(kThreads) sums_kernel(const __grid_constant__ 
             for (int j = 0; j < 8; ++j) sum += (double)v[j] * (double)v[j];
         }
     }
-    sum = block_sum(sum, s);
+    sum = block_sum64<kThreads / 32>(sum, s);
     if (threadIdx.x == 0) it.part[b] = sum;
 }
 
@@ -280,7 +268,7 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const __grid_constant__
     const int blocks = sum_blocks(it.size);
     double total = 0.0;
     for (int k = threadIdx.x; k < blocks; k += kThreads) total += it.part[k];
-    total = block_sum(total, s);
+    total = block_sum64<kThreads / 32>(total, s);
     const double divisor = sqrt(total) + a.eps;
     const float by = (float)divisor;
     const bool plain = by >= 0x1p-100f && by <= 0x1p100f;

@@ -1,5 +1,5 @@
 // Whether the device memory of a call's arguments overlaps where it must not
-// (host code of rr_optim.cu).
+// (host code of rr_optim.cu and rr_muon.cu).
 #pragma once
 
 #include <algorithm>

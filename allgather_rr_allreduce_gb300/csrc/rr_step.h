@@ -1,4 +1,4 @@
-// Shared by the training-step operators (rr_layer_norm.cu, rr_optim.cu):
+// Shared by the training-step operators (rr_layer_norm.cu, rr_optim.cu, rr_logits.cu, rr_muon.cu):
 // errors, launches, element loads and reductions.  Not part of the public ABI.
 #pragma once
 
@@ -157,6 +157,20 @@ struct Compensated {
     // Of a sum that is not finite nothing was rounded off.
     __device__ __forceinline__ float value() const { return fabsf(hi) < __int_as_float(0x7f800000) ? hi + lo : hi; }
 };
+
+// Sum of a block's values in binary64, the same in every thread; s: a word for each of its warps.
+template <int WARPS>
+__device__ __forceinline__ double block_sum64(double x, double *s)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = x;
+    __syncthreads();
+    x = 0.0;
+    for (int i = 0; i < WARPS; ++i) x += s[i];
+    return x;
+}
 
 __device__ __forceinline__ float warp_sum(float x)
 {
