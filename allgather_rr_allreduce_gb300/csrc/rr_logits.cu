@@ -11,9 +11,13 @@
 // over the row, which then comes mostly out of the L2.
 //
 // Bound: HBM.  12288 x 50021 fp16 log-probabilities 192 us (89 % of the copy peak), the
-// gradient of 4096 x 32768 bf16 85 (91 %), a policy loss with its gradient of 8192 x
-// 131072 bf16 837 (74 %; 87 by the traffic, as a quarter of the rows is read twice), a
-// preference loss of 4000 rows x 131072 547 (two reads and a write, 92 %).
+// gradient of 4096 x 32768 bf16 84 (92 %), a policy loss with its gradient of 8192 x
+// 131072 bf16 838 (74 % by one read and a write; some rows are read twice, a quarter of
+// 2048 in a profile), a preference loss of 4821 rows x 131072, 3866 of them counted, 551
+// (two reads and a write, 89 %).  Rows of 1000 to 4096 columns are far from it: a block
+// has a few vectors a thread and two joins to wait for (65536 x 1000 bf16
+// log-probabilities 252 us, 8 %, and with the policy's gradient 402; 65536 x 4096 310 and
+// 526).
 //
 // Times below are of one GB300 (152 SMs, measured copy 6.7 TB/s).
 #include <cmath>
@@ -321,7 +325,8 @@ __device__ __forceinline__ void row_zero(T *out, int64_t vocab, int part, int pa
     if (s.v1 + threadIdx.x < s.last) out[s.v1 + threadIdx.x] = from_f32<T>(0.0f);
 }
 
-// A row to a cluster of blocks (of one, mostly).
+// A row to a cluster of blocks (of one, mostly).  The policy loss spills 20 to 40 bytes
+// a thread at its 64 registers.
 template <class T, Mode MODE>
 __global__ void __launch_bounds__(kThreads, kBlocks) row_kernel(const __grid_constant__ RowArgs a)
 {
@@ -576,7 +581,11 @@ const void *row_fn(rr_dtype d)
 // second pass (the policy loss's gradient) at least so many that the rows under way
 // stay in the L2 until then (without a gradient too: the loss is the same).  8192 x
 // 131072 bf16: 85 MB of them 837 us, 160 MB 904, 43 MB 1039 (blocks that share a row
-// wait for one another).
+// wait for one another).  The border rests on that one vocabulary: bf16 rows of 73297
+// columns and more get two blocks (8192 x 100000 658 us, 74 % of the copy peak by one
+// read and a write; x 146000 1012, 71 %), of 146594 and more four, which is too many
+// (x 152064 1405, 53 %; x 200064 1861), and binary32 rows of 73297 and more as well
+// (4096 x 65536 419, 77 %; x 128256 1139, 55 %).
 constexpr int64_t kRowsInL2 = (int64_t)85 << 20;
 int blocks_to_a_row(int64_t rows, int64_t vocab, int eb, int64_t blocks, bool again)
 {

@@ -19,6 +19,12 @@
 // first, and is then added to sums in registers, rounded to nearest, while the next
 // 64 go to a second accumulator.
 //
+// Next to products in binary32 that leaves fewer bits in three places: operands have
+// 22 bits for 24, the product of the two low pieces is dropped, and what lies below
+// 2^-36 is (half the smallest binary16 over the scale: elements of X under 1e-4 lose
+// bits).  Results are 0.5 to 1.7 times as far from 64 bits as binary32 products leave
+// them.
+//
 // Operands live in the workspace in blocks of 128 rows x 64 columns, both pieces
 // one after the other (16 KB each), rows of 128 bytes with their 16-byte pieces
 // permuted as the tensor cores' 128-byte swizzle wants them.  A block comes to
@@ -609,7 +615,9 @@ __device__ __forceinline__ void fetch_columns(uint32_t to, const char *m, int wi
 
 // Bound: the tensor cores.  Both sides of a feed-forward product (3584 x 18944): X X'
 // 0.82 ms, 1.90 PFLOP/s of binary16 products (of 2.01 measured for cuBLAS in bf16); the
-// square 0.17; B X 1.54 ms, 1.89 PFLOP/s.  Sums in registers run beside the products
+// square 0.17; B X 1.54 ms, 1.89 PFLOP/s: launches by themselves, at 2.07 GHz.  Five steps
+// take 13.5 ms so, and 15.0 call after call, at the 1.6 GHz that the power limit leaves
+// (1.63 PFLOP/s, cuBLAS 1.77).  Sums in registers run beside the products
 // (three stages of 64 KB come from the L2 at 43 bytes a cycle); results do not, see above.
 //
 // Two blocks of a cluster work on a tile of 256 x N, each on 128 rows of it.

@@ -573,10 +573,13 @@ rr_status rr_adamw8(void *const *params, const void *const *grads, uint8_t *cons
  * y = X.  It moves the singular values toward 1 and leaves the vectors; five steps
  * of (3.4445, -4.7750, 2.0315) leave them within about 0.3 of it.
  *
- * Products take their operands as pairs of binary16 values with 22 bits together
- * and sum in binary32.  Magnitudes in X, A and the polynomial have to stay below
- * 32 (a norm of 1 and coefficients that do not diverge keep them near 1); what
- * leaves that range becomes infinite or NaN.  NaN and infinities in x make y NaN.
+ * Products take their operands as pairs of binary16 values with 22 bits together,
+ * to 2^-36 absolute (an element of X below 1e-4 has fewer bits), and sum in binary32.
+ * Magnitudes in X, A and the polynomial have to stay below 32 (a norm of 1 and
+ * coefficients that do not diverge keep them near 1); what leaves that range becomes
+ * infinite or NaN.  NaN and infinities in x make y NaN.  The norm's squares are added
+ * in memory's order, eight at a time in binary32 and those sums in binary64, so a
+ * matrix and its transpose may differ in their last bits.
  *
  * x, y: HOST arrays of num_tensors (>= 0) device pointers to dense row-major
  * matrices of rows[i] x cols[i] elements, of x_dtype and y_dtype; sides up to
@@ -587,7 +590,8 @@ rr_status rr_adamw8(void *const *params, const void *const *grads, uint8_t *cons
  * workspace: see rr_orthogonalize_workspace; about 8 bytes an element and 8 more
  * for each of the short side squared, of the 160 matrices in a row that need most.
  * A call is 2 + 3 * steps launches for each 160 matrices.  Every wait in them is
- * bounded; a block whose wait ran out (two seconds) leaves NaN in its results.
+ * bounded; a block whose wait ran out (two seconds) leaves NaN in its results from
+ * there on.
  */
 rr_status rr_orthogonalize(const void *const *x, void *const *y, const int64_t *rows, const int64_t *cols,
                            int num_tensors, rr_dtype x_dtype, rr_dtype y_dtype, const double *coefs, int steps,
@@ -617,7 +621,7 @@ typedef struct {
  * and param = w rounded once to param_dtype.
  *
  * grad_scale: device binary32 word (rr_grad_norm's scale), or NULL.  When it
- * holds NaN the step is skipped: no parameter or state is written.
+ * holds NaN the step is skipped: no parameter, state or workspace is written.
  * params, grads, momentum, master: HOST arrays of device pointers to dense
  * row-major matrices; momentum and master binary32, master NULL for none.  Nothing
  * written may overlap anything else (RR_ERR_ALIAS).  coefs, steps and workspace as
