@@ -22,8 +22,8 @@
 // Next to products in binary32 that leaves fewer bits in three places: operands have
 // 22 bits for 24, the product of the two low pieces is dropped, and what lies below
 // 2^-36 is (half the smallest binary16 over the scale: elements of X under 1e-4 lose
-// bits).  Results are 0.5 to 1.7 times as far from 64 bits as binary32 products leave
-// them.
+// bits).  Results are 0.5 to 2.2 times as far from 64 bits as binary32 products leave
+// them (4e-6 at most on drawn matrices of 32 to 8192 a side).
 //
 // Operands live in the workspace in blocks of 128 rows x 64 columns, both pieces
 // one after the other (16 KB each), rows of 128 bytes with their 16-byte pieces
